@@ -275,7 +275,7 @@ def work(case):
         expert = 3 * H * I + 4 * 3 * H * I // BLOCK**2
         return {"bytes": _touched(c) * expert + 4 * H * E + 4 * T * H, "flops": 2 * T * H * E + 6 * T * k * H * I}
     T, H = c["T"], c["H"]
-    per = 2 * (4 if c["residual"] == "fp32" else 2) if c["branch"] else (8 if c["residual"] == "fp32" else 4)
+    per = (4 if c["residual"] == "fp32" else 2) * (2 if c["branch"] else 1)
     per += 2 + (2 if c["branch"] else 0) + (2 if c["gate"] == "element" else 0)
     row = 2 * H * (1 + c["post"] + (c["gate"] == "channel")) + (2 * T if c["gate"] == "token" else 0)
     return {"bytes": T * H * per + row, "flops": 12 * T * H}
