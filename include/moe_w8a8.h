@@ -439,6 +439,87 @@ MOE_W8A8_API moe_status_t moe_w8a8_fp8_forward_host(const uint16_t* x_host, cons
 MOE_W8A8_API int moe_w8a8_host_chunks(int64_t T, int64_t H, int64_t I, int64_t E);
 
 /* ---------------------------------------------------------------------------
+ * Block-scaled FP8 (E4M3).  Activations carry one scale for each row and 128
+ * input channels, found in the call; weights one for each 128 output x 128
+ * input channels, found once.  The last block of a dimension may be shorter.
+ * A block's scale is s = amax * (1/448) (one binary32 product with the rounded
+ * reciprocal) and its codes are the E4M3 values nearest to the binary32
+ * quotients v / s, ties to even, saturated at +-448; a block of zeros has s = 0 and codes 0.  A NaN or an infinity
+ * makes its block's scale non-finite and the results that use it NaN.  The
+ * product is
+ *   y[m][n] = sum_b s_x[m][b] * s_w[n / 128][b] * sum_{k in b} q_x[m][k] * q_w[n][k]
+ * with exact E4M3 products summed in binary32 and each block's sum scaled
+ * before it is added.  Scale factors of one block instead of a whole row: an
+ * outlier channel costs precision in its own 128 channels only.  (Block scales
+ * for the E4M3 operands of "DeepSeek V4 950 FP8 inference on H100", sections
+ * 2.1-2.4.)
+ *
+ * moe_w8a8_fp8_block_quantize_weights: w fp32 [groups][rows][K] to
+ *   w_q      E4M3 [groups][rows][K]
+ *   w_scale  fp32 [groups][ceil(rows / 128)][ceil(K / 128)]
+ * rows and K multiples of 16 in [16, 65536]; groups == 0 is a no-op.  Call it
+ * with groups = E for an expert tensor, 1 for a linear layer.
+ *
+ * moe_w8a8_fp8_block_linear: y = x W^T.
+ *   x        bf16 [M][K]
+ *   w_q      E4M3 [N][K], w_scale fp32 [ceil(N / 128)][ceil(K / 128)]
+ *   y        bf16 [M][N], rounded once
+ *   workspace >= moe_w8a8_fp8_block_linear_workspace_size(M, N, K) bytes, 256-byte
+ *            aligned, its first 256 bytes zeroed once by the caller
+ * Supported: 0 <= M <= 2^20; N, K multiples of 16 in [16, 65536].  M == 0 is a
+ * no-op that reads no pointer.  Errors as moe_w8a8_linear; while
+ * moe_w8a8_set_gemm_path forces a kernel, MOE_ERR_NOT_IMPLEMENTED.
+ * ------------------------------------------------------------------------- */
+MOE_W8A8_API moe_status_t moe_w8a8_fp8_block_quantize_weights(const float* w, int64_t groups, int64_t rows,
+                                                              int64_t K, uint8_t* w_q, float* w_scale,
+                                                              void* stream);
+MOE_W8A8_API size_t moe_w8a8_fp8_block_linear_workspace_size(int64_t M, int64_t N, int64_t K);
+MOE_W8A8_API moe_status_t moe_w8a8_fp8_block_linear(const uint16_t* x, const uint8_t* w_q, const float* w_scale,
+                                                    int64_t M, int64_t N, int64_t K, uint16_t* y, void* workspace,
+                                                    size_t workspace_bytes, void* stream);
+
+/* moe_w8a8_fp8_block_forward: the whole MoE layer (top of this file) with
+ * block-scaled FP8 products.  Arguments, shapes and errors as
+ * moe_w8a8_fp8_forward, with
+ *   w13_scale fp32 [E][2I / 128][H / 128], w2_scale fp32 [E][H / 128][I / 128]
+ *   workspace >= moe_w8a8_fp8_block_workspace_size(T, H, I, E, top_k) bytes
+ * Router, top-k, slots and combine are those of the other forms; x is
+ * quantised per token and 128 channels, h per slot and 128 channels. */
+MOE_W8A8_API size_t moe_w8a8_fp8_block_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k);
+MOE_W8A8_API moe_status_t moe_w8a8_fp8_block_forward(const uint16_t* x, const float* router_w,
+                                                     const float* router_bias, const uint8_t* w13_q,
+                                                     const float* w13_scale, const uint8_t* w2_q,
+                                                     const float* w2_scale, int64_t T, int64_t H, int64_t I,
+                                                     int64_t E, int64_t top_k, uint16_t* y, void* workspace,
+                                                     size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_w8a8_norm_residual -- the norms around a block: the norm after it, its
+ * gate, the residual scale and addition, and the norm before the next block,
+ * in one pass.  Per row of H channels, in binary32:
+ *   b     = branch * rsqrt(mean(branch^2) + eps) * post_w   (post_w NULL: b = branch)
+ *   r     = x + scale * gate * b                            (branch NULL: r = x)
+ *   n     = r * rsqrt(mean(r^2) + eps) * pre_w              (from the unrounded r)
+ *
+ *   x         [T][H], bf16, or fp32 when x_fp32 != 0
+ *   branch    bf16 [T][H], or NULL: x_out is not written, x is only normed
+ *   post_w    bf16 [H], or NULL
+ *   gate      bf16; gate_form 0: none, 1: [H], one a channel, 2: [T], one a
+ *             token, 3: [T][H]
+ *   pre_w     bf16 [H], or NULL: n_out is not written
+ *   x_out     r as x's type; may be x itself
+ *   n_out     n, bf16 [T][H]
+ * Supported: 0 <= T <= 2^20; H a multiple of 8 in [8, 16384].  T == 0 is a
+ * no-op.  Errors: MOE_ERR_INVALID_ARG also where neither branch nor pre_w is
+ * given, where post_w or a gate is given without a branch, and for a gate_form
+ * outside 0..3 or an eps that is negative or NaN.  No workspace, one launch.
+ * ------------------------------------------------------------------------- */
+MOE_W8A8_API moe_status_t moe_w8a8_norm_residual(const void* x, int x_fp32, const uint16_t* branch,
+                                                 const uint16_t* post_w, const uint16_t* gate, int gate_form,
+                                                 float scale, const uint16_t* pre_w, float eps, int64_t T, int64_t H,
+                                                 void* x_out, uint16_t* n_out, void* stream);
+
+/* ---------------------------------------------------------------------------
  * moe_w8a8_device_error -- synchronise `stream`, then read and clear the
  * sticky device error word in the first bytes of `workspace`.  Returns
  * MOE_OK, MOE_ERR_DEVICE_TIMEOUT (a pipeline wait inside a kernel gave up;

@@ -24,6 +24,8 @@ __all__ = [
     "fused_supported", "linear_workspace_size", "linear",
     "device_error", "set_wait_timeout_ns", "set_gemm_path", "GEMM_PATHS", "version",
     "fp8_quantize_weights", "fp8_forward", "fp8_forward_debug", "fp8_forward_host",
+    "fp8_block_quantize_weights", "fp8_block_linear_workspace_size", "fp8_block_linear", "fp8_block_workspace_size",
+    "fp8_block_forward", "norm_residual",
 ]
 
 
@@ -415,3 +417,138 @@ def fp8_forward_host(x_host, router_w, router_bias, w13_q, w13_scale, w2_q, w2_s
     return _forward_host(_lib.load().moe_w8a8_fp8_forward_host, "moe_w8a8_fp8_forward_host", torch.uint8, x_host,
                          router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, top_k, y_host, x_dev, y_dev,
                          workspace, stream, copy_stream, chunks)
+
+
+# ---- block-scaled FP8 (E4M3, a scale per 128 channels) ---------------------
+
+BLOCK = 128  # input channels, and output channels of a weight, that share a scale
+
+
+def _blocks(n):
+    return -(-n // BLOCK)
+
+
+def fp8_block_quantize_weights(w, stream=None):
+    """E4M3 quantisation of fp32 ``w [rows, K]`` or ``[groups, rows, K]`` with one
+    scale per 128 x 128 block -> (codes as uint8, as ``w``; fp32 scales
+    [..., ceil(rows / 128), ceil(K / 128)])."""
+    torch = _torch()
+    if w.dim() not in (2, 3):
+        raise ValueError(f"w: expected 2 or 3 dimensions, got {w.dim()}")
+    _need(w, torch.float32, w.shape, "w")
+    groups, (rows, K) = (1 if w.dim() == 2 else w.shape[0]), w.shape[-2:]
+    q = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
+    s = torch.empty((*w.shape[:-2], _blocks(rows), _blocks(K)), dtype=torch.float32, device=w.device)
+    _lib.check(_lib.load().moe_w8a8_fp8_block_quantize_weights(_ptr(w), groups, rows, K, _ptr(q), _ptr(s),
+                                                               _stream(stream)),
+               "moe_w8a8_fp8_block_quantize_weights")
+    return q, s
+
+
+def fp8_block_linear_workspace_size(M, N, K) -> int:
+    n = _lib.load().moe_w8a8_fp8_block_linear_workspace_size(M, N, K)
+    if n == 0:
+        raise MoeError(-2, "moe_w8a8_fp8_block_linear_workspace_size")
+    return int(n)
+
+
+def fp8_block_linear(x, w_q, w_scale, workspace=None, out=None, stream=None):
+    """Block-scaled FP8 linear layer: bf16 x [M, K], E4M3 w_q [N, K] (uint8), fp32
+    w_scale [ceil(N / 128), ceil(K / 128)] -> bf16 [M, N]."""
+    torch = _torch()
+    M, K = x.shape
+    N = w_q.shape[0]
+    _need(x, torch.bfloat16, (M, K), "x")
+    _need(w_q, torch.uint8, (N, K), "w_q")
+    _need(w_scale, torch.float32, (_blocks(N), _blocks(K)), "w_scale")
+    if workspace is None:
+        workspace = new_workspace(fp8_block_linear_workspace_size(M, N, K), x.device)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    else:
+        _need(out, torch.bfloat16, (M, N), "out")
+    _lib.check(_lib.load().moe_w8a8_fp8_block_linear(
+        _ptr(x), _ptr(w_q), _ptr(w_scale), M, N, K, _ptr(out), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)), "moe_w8a8_fp8_block_linear")
+    return out
+
+
+def fp8_block_workspace_size(T, H, I, E, top_k) -> int:
+    n = _lib.load().moe_w8a8_fp8_block_workspace_size(T, H, I, E, top_k)
+    if n == 0:
+        raise MoeError(-2, "moe_w8a8_fp8_block_workspace_size")
+    return int(n)
+
+
+def fp8_block_forward(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, top_k, workspace=None, out=None,
+                      stream=None):
+    """The MoE layer with block-scaled FP8 products: bf16 x [T, H] -> bf16 y [T, H];
+    w13_q [E, 2I, H] and w2_q [E, H, I] E4M3 (uint8) with fp32 scales
+    [E, 2I / 128, H / 128] and [E, H / 128, I / 128]."""
+    torch = _torch()
+    T, H = x.shape
+    E = router_w.shape[1]
+    I = w2_q.shape[2] if w2_q.dim() == 3 else 0
+    _need(x, torch.bfloat16, (T, H), "x")
+    _need(router_w, torch.float32, (H, E), "router_w")
+    if router_bias is not None:
+        _need(router_bias, torch.float32, (E,), "router_bias")
+    _need(w13_q, torch.uint8, (E, 2 * I, H), "w13_q")
+    _need(w13_scale, torch.float32, (E, 2 * I // BLOCK, H // BLOCK), "w13_scale")
+    _need(w2_q, torch.uint8, (E, H, I), "w2_q")
+    _need(w2_scale, torch.float32, (E, H // BLOCK, I // BLOCK), "w2_scale")
+    if workspace is None:
+        workspace = new_workspace(fp8_block_workspace_size(T, H, I, E, top_k), x.device)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    else:
+        _need(out, torch.bfloat16, (T, H), "out")
+    _lib.check(_lib.load().moe_w8a8_fp8_block_forward(
+        _ptr(x), _ptr(router_w), _ptr(router_bias), _ptr(w13_q), _ptr(w13_scale), _ptr(w2_q), _ptr(w2_scale),
+        T, H, I, E, top_k, _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream(stream)), "moe_w8a8_fp8_block_forward")
+    return out
+
+
+# ---- the norms around a block ----------------------------------------------
+
+def norm_residual(x, branch=None, post_w=None, gate=None, scale=1.0, pre_w=None, eps=1e-6, x_out=None, n_out=None,
+                  stream=None):
+    """The norm after a block, its gate, the residual addition and the norm before
+    the next block, in one pass over x [T, H] (bf16 or fp32):
+
+        b = rms_norm(branch) * post_w       (post_w None: b = branch)
+        r = x + scale * gate * b            (branch None: r = x)
+        n = rms_norm(r) * pre_w             (pre_w None: n is None)
+
+    branch, weights and gate are bf16; gate is [H], [T, 1] or [T, H].  Returns
+    (r, n): r in x's type (x itself without a branch; ``x_out`` may be x), n bf16."""
+    torch = _torch()
+    T, H = x.shape
+    if x.dtype is not torch.float32:
+        _need(x, torch.bfloat16, (T, H), "x")
+    else:
+        _need(x, torch.float32, (T, H), "x")
+    form = 0
+    if branch is not None:
+        _need(branch, torch.bfloat16, (T, H), "branch")
+        if x_out is None:
+            x_out = torch.empty_like(x)
+        else:
+            _need(x_out, x.dtype, (T, H), "x_out")
+    if post_w is not None:
+        _need(post_w, torch.bfloat16, (H,), "post_w")
+    if gate is not None:
+        form = 1 if gate.dim() == 1 else 2 if gate.dim() == 2 and gate.shape[1] == 1 and H != 1 else 3
+        _need(gate, torch.bfloat16, ((H,), (T, 1), (T, H))[form - 1], "gate")
+    if pre_w is not None:
+        _need(pre_w, torch.bfloat16, (H,), "pre_w")
+        if n_out is None:
+            n_out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        else:
+            _need(n_out, torch.bfloat16, (T, H), "n_out")
+    _lib.check(_lib.load().moe_w8a8_norm_residual(
+        _ptr(x), x.dtype is torch.float32, _ptr(branch), _ptr(post_w), _ptr(gate), form, scale, _ptr(pre_w), eps,
+        T, H, _ptr(x_out) if branch is not None else None, _ptr(n_out) if pre_w is not None else None,
+        _stream(stream)), "moe_w8a8_norm_residual")
+    return (x_out if branch is not None else x), (n_out if pre_w is not None else None)

@@ -51,6 +51,12 @@ EXPORTS = (
     "moe_w8a8_forward_smooth",
     "moe_w8a8_forward_fused",
     "moe_w8a8_fused_supported",
+    "moe_w8a8_fp8_block_quantize_weights",
+    "moe_w8a8_fp8_block_linear_workspace_size",
+    "moe_w8a8_fp8_block_linear",
+    "moe_w8a8_fp8_block_workspace_size",
+    "moe_w8a8_fp8_block_forward",
+    "moe_w8a8_norm_residual",
 )
 
 
@@ -91,7 +97,7 @@ def open_library(path: str):
 
 
 def _declare(lib) -> None:
-    i64, vp, sz, i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+    i64, vp, sz, i32, f32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
     decl = {
         "moe_w8a8_status_string": ([i32], ctypes.c_char_p),
         "moe_w8a8_version": ([], i32),
@@ -124,6 +130,12 @@ def _declare(lib) -> None:
         "moe_w8a8_forward_fused": ([vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, sz, vp,
                                     ctypes.POINTER(DebugBuffers)], i32),
         "moe_w8a8_fused_supported": ([i64, i64, i64, i64, i64], i32),
+        "moe_w8a8_fp8_block_quantize_weights": ([vp, i64, i64, i64, vp, vp, vp], i32),
+        "moe_w8a8_fp8_block_linear_workspace_size": ([i64, i64, i64], sz),
+        "moe_w8a8_fp8_block_linear": ([vp, vp, vp, i64, i64, i64, vp, vp, sz, vp], i32),
+        "moe_w8a8_fp8_block_workspace_size": ([i64, i64, i64, i64, i64], sz),
+        "moe_w8a8_fp8_block_forward": ([vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, sz, vp], i32),
+        "moe_w8a8_norm_residual": ([vp, i32, vp, vp, vp, i32, f32, vp, f32, i64, i64, vp, vp, vp], i32),
     }
     for name, (args, res) in decl.items():
         fn = getattr(lib, name)

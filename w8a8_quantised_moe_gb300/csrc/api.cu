@@ -20,8 +20,7 @@
 #include <cstring>
 #include <vector>
 
-#include "moe_w8a8.h"
-#include "internal.h"
+#include "api_common.h"
 
 namespace moe {
 
@@ -50,10 +49,6 @@ bool pdl_env_off() {
     return off;
 }
 
-size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // The dp4a GEMM's scheduling words in a workspace's error region (the GEMM
 // leaves them zero).  Taken by the one-kernel layer, whose gate/up GEMM phase
 // they shortened (decode layer: 122.5 -> 118.7 us); the separate dp4a
@@ -63,22 +58,13 @@ unsigned int* sched_words(int* err) {
     return reinterpret_cast<unsigned int*>(reinterpret_cast<char*>(err) + kSchedOffset);
 }
 
-moe_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
-bool moe_shape_ok(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
-    if (T < 0 || T > (int64_t(1) << 20)) return false;
-    if (H < 128 || H > 16384 || H % 128) return false;
-    if (I < 128 || I > 16384 || I % 128) return false;
-    if (E < 1 || E > kMaxExperts) return false;
-    if (k < 1 || k > kMaxTopK || k > E) return false;
-    return true;
-}
-
 }  // namespace
 
 bool pdl_default() { return t_events == nullptr && !pdl_env_off(); }
 
 uint64_t current_timeout_ns() { return g_timeout_ns.load(); }
+
+bool gemm_path_forced() { return g_gemm_path.load() >= 0; }
 
 bool injected(InjectFault f) {
     const char* v = std::getenv("MOE_INJECT");
@@ -180,11 +166,6 @@ LinLayout lin_layout(int64_t M, int64_t N, int64_t K) {
 using namespace moe;
 
 namespace {
-
-template <typename T>
-T* at(void* base, size_t off) {
-    return reinterpret_cast<T*>(static_cast<char*>(base) + off);
-}
 
 moe_status_t forward_impl(const uint16_t* x, const float* router_w, const float* router_bias,
                           const int8_t* w13_q, const float* w13_scale, const int8_t* w2_q,

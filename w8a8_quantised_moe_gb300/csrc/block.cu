@@ -1,0 +1,133 @@
+// block.cu -- quantisers of the block-scaled FP8 operators.
+//
+// A block's scale is s = amax * (1/448) (one binary32 product with the rounded
+// reciprocal) and its codes are the E4M3 values nearest to the binary32 quotients x / s, ties to the even
+// mantissa, saturated at +-448; a block of zeros has s = 0 and codes 0.
+// Activations: a block is 128 channels of one row, so a row needs no
+// reduction across its blocks.  Weights: a block is 128 x 128.
+#include <cuda_bf16.h>
+
+#include "block.h"
+#include "block_dev.cuh"
+
+namespace moe {
+namespace {
+
+// One CTA of 256 threads per 128 x 128 weight block, held in registers (16
+// float4 a thread): one read of the fp32 weights, one write of the codes.
+__global__ void __launch_bounds__(256) quantize_weights_block_kernel(const float* __restrict__ w, int64_t n_blocks,
+                                                                     int rows, int K, uint8_t* __restrict__ q,
+                                                                     float* __restrict__ s_out) {
+    __shared__ float red[8];
+    const int nb = blocks_of(rows), kb = blocks_of(K);
+    const int c4 = threadIdx.x & 31, r0 = threadIdx.x >> 5;  // this thread's float4 column and first row
+    for (int64_t b = blockIdx.x; b < n_blocks; b += gridDim.x) {
+        const int64_t g = b / ((int64_t)nb * kb);
+        const int rb = (int)(b / kb % nb), cb = (int)(b % kb);
+        const int col = cb * kBlk + c4 * 4;
+        const size_t base = ((size_t)g * rows + (size_t)rb * kBlk) * K + col;
+        float4 v[16];
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int r = r0 + 8 * i;
+            v[i] = (rb * kBlk + r < rows && col < K) ? __ldcs(reinterpret_cast<const float4*>(w + base + (size_t)r * K))
+                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+            amax = amax_nan(amax_nan(amax_nan(amax_nan(amax, v[i].x), v[i].y), v[i].z), v[i].w);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) amax = amax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+        __syncthreads();  // red of the previous block has been read
+        if (c4 == 0) red[r0] = amax;
+        __syncthreads();
+        amax = red[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) amax = amax_nan(amax, red[i]);
+        const float s = block_scale(amax);
+        if (threadIdx.x == 0) s_out[b] = s;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int r = r0 + 8 * i;
+            if (rb * kBlk + r < rows && col < K)
+                *reinterpret_cast<uint32_t*>(q + base + (size_t)r * K) =
+                    e4m3_quot4(v[i].x, v[i].y, v[i].z, v[i].w, s);
+        }
+    }
+}
+
+// A warp per (row, 256 channels): lanes 0-15 and 16-31 hold a block each, 8
+// channels a lane.  SLOTS: the row is a token whose codes go to its k slots.
+template <bool SLOTS>
+__global__ void __launch_bounds__(256) quantize_rows_block_kernel(
+    const uint16_t* __restrict__ x, int M, int K, uint8_t* __restrict__ q, float* __restrict__ s_out,
+    const int32_t* __restrict__ topk_ids, const int32_t* __restrict__ rank, const int32_t* __restrict__ base, int E,
+    int k, int32_t* __restrict__ slot_of, int32_t* __restrict__ slot_token, int* __restrict__ error) {
+    const int lane = threadIdx.x & 31;
+    const int kb = blocks_of(K), parts = (kb + 1) / 2;
+    const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int r = (int)(item / parts), part = (int)(item % parts);
+    const int col = part * 256 + lane * 8;
+    pdl_wait();
+    pdl_trigger();
+    if (r >= M) return;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (col < K) v = __ldg(reinterpret_cast<const uint4*>(x + (size_t)r * K + col));
+    int my_slot = r;
+    if (SLOTS && lane < k) {
+        const int e = topk_ids[(size_t)r * k + lane];
+        my_slot = in_range(e, 0, E, error) ? base[(size_t)(r / kRouterTokens) * E + e] + rank[(size_t)r * k + lane]
+                                           : -1;  // -1: out of range (checked build), its writes skipped
+        if (my_slot >= 0 && !in_range(my_slot, 0, (long long)M * k, error)) my_slot = -1;
+        if (part == 0) {
+            slot_of[(size_t)r * k + lane] = my_slot;
+            if (!kChecked || my_slot >= 0) slot_token[my_slot] = r;
+        }
+    }
+    float f[8];
+    bf16x8_to_f32(v, f);
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = amax_nan(amax, f[i]);
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) amax = amax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    const float s = block_scale(amax);
+    const uint2 c = make_uint2(e4m3_quot4(f[0], f[1], f[2], f[3], s), e4m3_quot4(f[4], f[5], f[6], f[7], s));
+    const int n = SLOTS ? k : 1;
+    for (int j = 0; j < n; ++j) {
+        const int row = SLOTS ? __shfl_sync(0xffffffffu, my_slot, j) : r;
+        if (col < K && (!kChecked || row >= 0)) {
+            *reinterpret_cast<uint2*>(q + (size_t)row * K + col) = c;
+            if ((lane & 15) == 0) s_out[(size_t)row * kb + part * 2 + (lane >> 4)] = s;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_weights_block(const float* w, int64_t groups, int rows, int K, uint8_t* q, float* s,
+                                          cudaStream_t st) {
+    const int64_t n = groups * blocks_of(rows) * blocks_of(K);
+    if (n == 0) return cudaSuccess;
+    const int64_t cap = (int64_t)num_sms() * 8;
+    return launch_kernel(quantize_weights_block_kernel, dim3((unsigned)(n < cap ? n : cap)), dim3(256), 0, st, false,
+                         w, n, rows, K, q, s);
+}
+
+cudaError_t launch_quantize_block(const uint16_t* x, int M, int K, uint8_t* q, float* s, cudaStream_t st, bool pdl) {
+    if (M == 0) return cudaSuccess;
+    const int64_t items = (int64_t)M * ((blocks_of(K) + 1) / 2);
+    return launch_kernel(quantize_rows_block_kernel<false>, dim3((unsigned)((items + 7) / 8)), dim3(256), 0, st, pdl,
+                         x, M, K, q, s, nullptr, nullptr, nullptr, 0, 1, nullptr, nullptr, nullptr);
+}
+
+cudaError_t launch_permute_quant_block(const uint16_t* x, const int32_t* topk_ids, const int32_t* rank,
+                                       const int32_t* base, int T, int H, int E, int k, int32_t* slot_of,
+                                       int32_t* slot_token, uint8_t* q, float* s, int* error, cudaStream_t st,
+                                       bool pdl) {
+    if (T == 0) return cudaSuccess;
+    const int64_t items = (int64_t)T * ((blocks_of(H) + 1) / 2);
+    return launch_kernel(quantize_rows_block_kernel<true>, dim3((unsigned)((items + 7) / 8)), dim3(256), 0, st, pdl,
+                         x, T, H, q, s, topk_ids, rank, base, E, k, slot_of, slot_token, error);
+}
+
+}  // namespace moe

@@ -1,0 +1,431 @@
+// gemm_block.cu -- the grouped block-scaled FP8 product on the tcgen05 tensor
+// cores:
+//
+//   D[r][n] = sum_b sx[r][b] * sw[n / 128][b] * (sum_{k in block b} a[r][k] * w[n][k])
+//
+// with E4M3 a and w (their products are exact in binary32).  The tensor cores
+// accumulate one 128-channel block at a time in tensor memory; the scales
+// differ from block to block, so the block's partial sums go to registers,
+// where they are multiplied by the block's scale and added to binary32 sums.
+//
+// Tile: 128 activation rows (the MMA's M, one TMEM lane each) x 256 weight
+// rows (N) in two halves of 128.  With rows on the lanes a thread's scale is
+// one value per half and block: sx of its row times sw of the half.  GateUp's
+// halves are 128 gate rows and the 128 up rows of the same channels, so the
+// tile holds whole scale blocks of h: each thread applies silu(gate) * up to
+// its 64 + 64 columns and h leaves the kernel as E4M3 codes with their scale,
+// never as binary32.
+//   warp 0     TMA producer (ring of kNS stages: activation rows and both
+//              halves' weight rows, 128 bytes of K each)
+//   warp 1     TMEM allocator and MMA issuer: four K = 32 MMAs a block into one
+//              of two 256-column TMEM buffers
+//   warps 2-9  scale and sum the blocks, then the epilogue: warp w has lanes
+//              32 (w % 4).., and columns 64 ((w - 2) / 4).. of each half
+// Persistent grid, tiles dealt round-robin with a group's row blocks next to
+// each other (they share weight tiles in L2).  Every wait is bounded (ptx.cuh).
+#include <mutex>
+
+#include "block.h"
+#include "block_dev.cuh"
+#include "gemm_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBgRows = 128;       // activation rows per tile
+constexpr int kBgCols = 256;       // weight rows per tile
+constexpr int kBgNS = 4;           // stages
+constexpr int kBgThreads = 320;
+constexpr int kBgEpi0 = 2;         // first epilogue warp
+constexpr int kBgEpiWarps = 8;
+constexpr int kBgStageA = kBgRows * kBlk;
+constexpr int kBgStageB = kBgCols * kBlk;
+constexpr int kBgStage = kBgStageA + kBgStageB;
+constexpr int kBgOffBars = kBgNS * kBgStage;
+constexpr int kBgNumBars = 2 * kBgNS + 4 + 2 + 4;  // full, empty, acc_full/empty[2], teardown, stall, pair[4]
+constexpr int kBgOffTiles = kBgOffBars + kBgNumBars * 8;
+constexpr int kBgOffXch = kBgOffTiles + (kMaxExperts + 1) * 4 * 2;
+constexpr int kBgOffMisc = kBgOffXch + 2 * 2 * kBgRows * 4;  // row maxima [2 tiles][2 warps][rows]
+constexpr int kBgSmem = kBgOffMisc + 64 + 1024;              // + alignment slack
+static_assert(kBgOffTiles % 8 == 0 && kBgOffXch % 8 == 0 && kBgOffMisc % 8 == 0, "alignment");
+static_assert(kBgSmem <= 232448, "shared memory budget");
+
+__device__ __forceinline__ void bg_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor of kind::f8f6f4: E4M3 A and B (format 0), fp32 D.
+__host__ __device__ constexpr uint32_t bg_idesc(uint32_t M, uint32_t N) {
+    return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// Waits for this warp's tensor-memory loads; the registers pass through, so
+// that no use of them moves above the wait.
+__device__ __forceinline__ void bg_wait_ld(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15])::"memory");
+}
+
+// Box heights of the activation maps: the smallest that covers a tile's rows.
+__host__ __device__ constexpr int bg_box_rows(int i) { return i == 0 ? 32 : i == 1 ? 64 : kBgRows; }
+__device__ __forceinline__ int bg_box_index(int nvalid) { return nvalid <= 32 ? 0 : nvalid <= 64 ? 1 : 2; }
+
+__device__ __forceinline__ void bg_decode_tile(const Tiles& t, int tile, int& g, int& cb, int& row0, int& nvalid) {
+    g = last_le(t.tile_start, t.n_groups, tile);
+    const int local = tile - t.tile_start[g];
+    const int rows = t.row_start[g + 1] - t.row_start[g];
+    const int ntb = (rows + kBgRows - 1) / kBgRows;
+    cb = local / ntb;
+    const int tb = local - cb * ntb;
+    row0 = t.row_start[g] + tb * kBgRows;
+    nvalid = min(kBgRows, t.row_start[g + 1] - row0);
+}
+
+template <int EPI>
+__global__ void __launch_bounds__(kBgThreads, 1)
+    block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a0,
+                      const __grid_constant__ CUtensorMap tmap_a1, const __grid_constant__ CUtensorMap tmap_a2,
+                      const BlockGemmArgs args) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBgOffBars);
+    uint64_t* full = bars;              // [NS] the stage landed
+    uint64_t* empty = full + kBgNS;     // [NS] the MMAs of the stage completed
+    uint64_t* acc_full = empty + kBgNS; // [2] a block's partial sums are in tensor memory
+    uint64_t* acc_empty = acc_full + 2; // [2] the 8 epilogue warps have read them
+    uint64_t* teardown = acc_empty + 2;
+    uint64_t* stall_bar = teardown + 1; // test hook: nothing arrives on it
+    uint64_t* pair_bar = stall_bar + 1; // [4] the two warps of a lane quarter
+    int* tile_start = reinterpret_cast<int*>(smem + kBgOffTiles);
+    int* row_start = tile_start + (kMaxExperts + 1);
+    float* xch = reinterpret_cast<float*>(smem + kBgOffXch);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBgOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kBgOffMisc + 8);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_groups = args.n_groups;
+    const int nkb = blocks_of(args.K);
+    const int n_cb = EPI == (int)BlockEpi::GateUp ? args.up_offset / kBlk : (args.w_rows + kBgCols - 1) / kBgCols;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kBgNS; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int d = 0; d < 2; ++d) {
+            mbar_init(&acc_full[d], 1);
+            mbar_init(&acc_empty[d], kBgEpiWarps);
+        }
+        mbar_init(teardown, 1);
+        mbar_init(stall_bar, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&pair_bar[i], 2);
+        *abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmap_w);
+        tma_prefetch_desc(&tmap_a2);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    pdl_wait();  // the previous kernel's outputs (offsets, codes, scales) are visible from here
+    pdl_trigger();
+    if (warp == 2) {  // tile table: tiles of group g = ceil(rows_g / 128) * n_cb
+        int carry = 0;
+        bool bad = false;  // checked build: an offset out of order or range
+        for (int base = 0; base < n_groups; base += 32) {
+            const int g = base + lane;
+            int r0 = 0, r1 = 0;
+            if (g < n_groups) {
+                r0 = args.offsets ? args.offsets[g] : 0;
+                r1 = args.offsets ? args.offsets[g + 1] : args.total_rows;
+                if (!group_rows_ok(r0, r1, args.total_rows, args.error)) {
+                    bad = true;
+                    r0 = r1 = 0;
+                }
+                row_start[g] = r0;
+                if (g == n_groups - 1) row_start[n_groups] = r1;
+            }
+            const int v = (g < n_groups) ? ((r1 - r0 + kBgRows - 1) / kBgRows) * n_cb : 0;
+            int incl = v;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += o;
+            }
+            if (g < n_groups) tile_start[g] = carry + incl - v;
+            carry += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) tile_start[n_groups] = carry;
+        if (kChecked && __any_sync(0xffffffffu, bad)) {  // an empty, consistent table: no tile runs
+            for (int g = lane; g <= n_groups; g += 32) {
+                row_start[g] = 0;
+                tile_start[g] = 0;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int total_tiles = tile_start[n_groups];
+    const Tiles tiles{tile_start, row_start, n_groups};
+    const WaitCtl ctl{abort_flag, args.error, args.timeout_ns, 0u};
+    // halves of a tile that hold weight rows (GateUp: always both)
+    auto halves_of = [&](int cb) {
+        return EPI == (int)BlockEpi::GateUp || args.w_rows - cb * kBgCols > kBlk ? 2 : 1;
+    };
+
+    if (warp == 0) {
+        // ---------------------------------------------------------- producer
+        // lanes 0-2 issue one box each (both halves' weight rows, activation
+        // rows) in the same warp instruction; lane 0 owns the waits
+        if (lane < 3) {
+            uint32_t it = 0;
+            int ok = 1;
+            if (lane == 0) ok = !args.stall || mbar_wait(stall_bar, 0, ctl);  // the test hook's wait runs out
+            ok = __shfl_sync(0x7u, ok, 0);
+            for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
+                int g, cb, row0, nvalid;
+                bg_decode_tile(tiles, tile, g, cb, row0, nvalid);
+                const int halves = halves_of(cb);
+                int wrow0, wrow1;  // first weight row of each half
+                if (EPI == (int)BlockEpi::GateUp) {
+                    wrow0 = g * args.w_rows + cb * kBlk;
+                    wrow1 = wrow0 + args.up_offset;
+                } else {
+                    wrow0 = g * args.w_rows + cb * kBgCols;
+                    wrow1 = wrow0 + kBlk;
+                }
+                const int bi = bg_box_index(nvalid);
+                const CUtensorMap* ma = bi == 0 ? &tmap_a0 : bi == 1 ? &tmap_a1 : &tmap_a2;
+                const uint32_t bytes = (uint32_t)((bg_box_rows(bi) + halves * kBlk) * kBlk);
+                const CUtensorMap* map = lane == 2 ? ma : &tmap_w;
+                const int row = lane == 0 ? wrow0 : lane == 1 ? wrow1 : row0;
+                const int off = lane == 2 ? 0 : kBgStageA + lane * (kBlk * kBlk);
+                for (int kb = 0; kb < nkb; ++kb, ++it) {
+                    const uint32_t s = it % kBgNS, ph = (it / kBgNS) & 1u;
+                    if (lane == 0) {
+                        ok = mbar_wait(&empty[s], ph ^ 1u, ctl);
+                        if (ok) mbar_arrive_expect_tx(&full[s], bytes);
+                    }
+                    ok = __shfl_sync(0x7u, ok, 0);
+                    if (!ok) break;
+                    if (lane != 1 || halves == 2) tma_load_2d(smem + s * kBgStage + off, map, &full[s], kb * kBlk, row);
+                }
+            }
+            // drain: every fill issued must land before the CTA may exit
+            if (lane == 0)
+                for (uint32_t s = 0; s < (uint32_t)kBgNS && s < it; ++s) {
+                    const uint32_t last = it - 1 - ((it - 1 - s) % kBgNS);
+                    mbar_wait_drain(&full[s], (last / kBgNS) & 1u);
+                }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
+                int g, cb, row0, nvalid;
+                bg_decode_tile(tiles, tile, g, cb, row0, nvalid);
+                const uint32_t idesc = bg_idesc(kBgRows, (uint32_t)(halves_of(cb) * kBlk));
+                for (int kb = 0; kb < nkb; ++kb, ++it) {
+                    const uint32_t s = it % kBgNS, d = it & 1u;
+                    if (!mbar_wait(&acc_empty[d], ((it >> 1) & 1u) ^ 1u, ctl) ||
+                        !mbar_wait(&full[s], (it / kBgNS) & 1u, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a_base = smem_u32(smem + s * kBgStage);
+                    const uint64_t a_desc = smem_desc_sw128(a_base), b_desc = smem_desc_sw128(a_base + kBgStageA);
+#pragma unroll
+                    for (int ks = 0; ks < kBlk / 32; ++ks)  // 32 bytes of K per MMA
+                        bg_mma(tmem + d * kBgCols, a_desc + (uint64_t)(ks * 2), b_desc + (uint64_t)(ks * 2), idesc,
+                               ks != 0 ? 1u : 0u);
+                    mma_commit(&empty[s]);
+                    mma_commit(&acc_full[d]);
+                }
+            }
+            mma_commit(teardown);
+            mbar_wait_drain(teardown, 0);
+        }
+    } else {
+        // ------------------------------------- block sums and the epilogue
+        const int q = warp & 3;
+        const int w2 = (warp - kBgEpi0) >> 2;  // which 64 columns of each half
+        const int row = q * 32 + lane;         // TMEM lane = row of the tile
+        const uint32_t col_addr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(w2 * 64);
+        const int nb = blocks_of(args.w_rows);
+        uint32_t it = 0, tl = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x, ++tl) {
+            int g, cb, row0, nvalid;
+            bg_decode_tile(tiles, tile, g, cb, row0, nvalid);
+            const int r = row0 + min(row, nvalid - 1);
+            const float* sx = args.act_scale + (size_t)r * nkb;
+            const int b0 = EPI == (int)BlockEpi::GateUp ? cb : 2 * cb;
+            const int b1 = EPI == (int)BlockEpi::GateUp ? cb + args.up_offset / kBlk : min(2 * cb + 1, nb - 1);
+            const float* sw0 = args.w_scale + ((size_t)g * nb + b0) * nkb;
+            const float* sw1 = args.w_scale + ((size_t)g * nb + b1) * nkb;
+            f32x2 acc[2][32];  // [half][column pair]
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[0][j] = acc[1][j] = 0ull;
+            float x_next = __ldg(sx), w0_next = __ldg(sw0), w1_next = __ldg(sw1);
+            for (int kb = 0; kb < nkb; ++kb, ++it) {
+                const float s0 = __fmul_rn(x_next, w0_next), s1 = __fmul_rn(x_next, w1_next);
+                const f32x2 sc[2] = {pack2(s0, s0), pack2(s1, s1)};
+                if (kb + 1 < nkb) {
+                    x_next = __ldg(sx + kb + 1);
+                    w0_next = __ldg(sw0 + kb + 1);
+                    w1_next = __ldg(sw1 + kb + 1);
+                }
+                const uint32_t d = it & 1u;
+                if (!warp_wait(&acc_full[d], (it >> 1) & 1u, ctl)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t a = col_addr + d * kBgCols;
+                uint32_t v[2][16];  // the next 16 columns load while these are summed
+                tmem_ld_16(a, v[0]);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    bg_wait_ld(v[c & 1]);
+                    if (c < 7) tmem_ld_16(a + ((c + 1) >> 2) * kBlk + ((c + 1) & 3) * 16, v[(c + 1) & 1]);
+                    if (c == 7) {  // every column is in registers: release the buffer
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&acc_empty[d]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        fma2(acc[c >> 2][(c & 3) * 8 + j],
+                             pack2(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])), sc[c >> 2]);
+                }
+            }
+            if (!ok) break;
+            if (EPI == (int)BlockEpi::GateUp) {
+                float amax = 0.f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    float g0, g1, u0, u1;
+                    unpack2(acc[0][j], g0, g1);
+                    unpack2(acc[1][j], u0, u1);
+                    g0 = silu_mul(g0, u0);
+                    g1 = silu_mul(g1, u1);
+                    amax = amax_nan(amax_nan(amax, g0), g1);
+                    acc[0][j] = pack2(g0, g1);
+                }
+                // the row's other 64 columns are the partner warp's
+                float* mine = xch + (tl & 1u) * 2 * kBgRows;
+                mine[w2 * kBgRows + row] = amax;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pair_bar[q]);
+                if (!warp_wait(&pair_bar[q], tl & 1u, ctl)) break;
+                amax = amax_nan(amax, mine[(w2 ^ 1) * kBgRows + row]);
+                const float s = block_scale(amax);
+                // the quotient as a product with 1 / s: h is rounded already,
+                // see silu_mul
+                const float inv = s == 0.f ? 0.f : __fdiv_rn(1.0f, s);
+                if (row < nvalid) {
+                    const int n_ch = args.up_offset;
+                    uint4* out = reinterpret_cast<uint4*>(args.q_out + (size_t)r * n_ch + cb * kBlk + w2 * 64);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t c4[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float h0, h1, h2, h3;
+                            unpack2(acc[0][i * 8 + j * 2], h0, h1);
+                            unpack2(acc[0][i * 8 + j * 2 + 1], h2, h3);
+                            c4[j] = e4m3_pair(h0 * inv, h1 * inv) | (e4m3_pair(h2 * inv, h3 * inv) << 16);
+                        }
+                        out[i] = make_uint4(c4[0], c4[1], c4[2], c4[3]);
+                    }
+                    if (w2 == 0) args.s_out[(size_t)r * (n_ch / kBlk) + cb] = s;
+                }
+            } else if (row < nvalid) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int col = cb * kBgCols + half * kBlk + w2 * 64;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {  // 8 columns a step; w_rows is a multiple of 16
+                        if (col + i * 8 < args.w_rows) {
+                            float f[8];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) unpack2(acc[half][i * 4 + j], f[2 * j], f[2 * j + 1]);
+                            const size_t at = (size_t)r * args.w_rows + col + i * 8;
+                            if (EPI == (int)BlockEpi::F32) {
+                                float4* out = reinterpret_cast<float4*>(static_cast<float*>(args.out) + at);
+                                out[0] = make_float4(f[0], f[1], f[2], f[3]);
+                                out[1] = make_float4(f[4], f[5], f[6], f[7]);
+                            } else {
+                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.out) + at) =
+                                    make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]),
+                                               bf16_pair(f[6], f[7]));
+                            }
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int EPI>
+cudaError_t launch_block_impl(const BlockGemmArgs& args, cudaStream_t st, bool pdl) {
+    auto kern = block_gemm_kernel<EPI>;
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [&] {
+        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBgSmem);
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    CUtensorMap tw, ta[3];
+    if (!make_tensor_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, args.w, args.K,
+                            (uint64_t)args.n_groups * args.w_rows, kBlk, kBlk, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    for (int i = 0; i < 3; ++i)
+        if (!make_tensor_map_2d(&ta[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, args.act, args.K, (uint64_t)args.total_rows,
+                                kBlk, bg_box_rows(i), CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    const int n_cb = EPI == (int)BlockEpi::GateUp ? args.up_offset / kBlk : (args.w_rows + kBgCols - 1) / kBgCols;
+    const long max_tiles = ((long)(args.total_rows + kBgRows - 1) / kBgRows + args.n_groups - 1) * n_cb;
+    long grid = num_sms();
+    if (max_tiles < grid) grid = max_tiles;
+    if (grid < 1) grid = 1;
+    return launch_kernel(kern, dim3((unsigned)grid), dim3(kBgThreads), kBgSmem, st, pdl, tw, ta[0], ta[1], ta[2],
+                         args);
+}
+
+}  // namespace
+
+cudaError_t launch_block_gemm(BlockEpi epi, const BlockGemmArgs& args, cudaStream_t st, bool pdl) {
+    if (args.total_rows == 0) return cudaSuccess;
+    switch (epi) {
+        case BlockEpi::GateUp: return launch_block_impl<0>(args, st, pdl);
+        case BlockEpi::F32: return launch_block_impl<1>(args, st, pdl);
+        case BlockEpi::BF16: return launch_block_impl<2>(args, st, pdl);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace moe
