@@ -83,7 +83,8 @@ def test_linear(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (3, 16, 8192), (8, 2064, 7184), (40, 1024, 4112), (1003, 528, 1488),
-                                   (520, 4112, 144), (2100, 1040, 256)])
+                                   (520, 4112, 144), (2100, 1040, 256),
+                                   (16, 512, 16400), (100, 272, 8208), (128, 2064, 4096), (2, 128, 65536)])
 def test_linear_long(M, N, K):
     g = gen(M + K)
     check_linear(activations(g, M, K), *weight(g, N, K))
@@ -264,11 +265,12 @@ def test_layer_on_a_side_stream_with_no_tokens_between():
     assert torch.equal(out, want)
 
 
-def test_a_wait_that_runs_out_is_reported(monkeypatch):
+@pytest.mark.parametrize("M", [20, 400])
+def test_a_wait_that_runs_out_is_reported(monkeypatch, M):
     """The test hook makes the tensor-core product's producer wait for nothing."""
     g = gen(11)
-    x, (w_q, w_s) = activations(g, 400, 512), weight(g, 512, 512)
-    ws = moe.new_workspace(moe.fp8_block_linear_workspace_size(400, 512, 512))
+    x, (w_q, w_s) = activations(g, M, 512), weight(g, 512, 512)
+    ws = moe.new_workspace(moe.fp8_block_linear_workspace_size(M, 512, 512))
     want = moe.fp8_block_linear(x, w_q, w_s, workspace=ws)
     prev = moe.set_wait_timeout_ns(2_000_000)
     try:

@@ -48,7 +48,7 @@ def _need(t, dtype, shape, name):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_cuda or not t.is_contiguous():
+    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
         raise ValueError(f"{name}: expected contiguous cuda {dtype} {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
 
@@ -420,12 +420,19 @@ def fp8_forward_host(x_host, router_w, router_bias, w13_q, w13_scale, w2_q, w2_s
 
 
 # ---- block-scaled FP8 (E4M3, a scale per 128 channels) ---------------------
+# A decode step calls these with a few microseconds of GPU work each, so their
+# argument handling is kept short.
 
 BLOCK = 128  # input channels, and output channels of a weight, that share a scale
 
 
 def _blocks(n):
     return -(-n // BLOCK)
+
+
+def _raw_stream(stream, t):
+    """The stream's handle: ``stream``, or the current one of t's device."""
+    return _torch()._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def fp8_block_quantize_weights(w, stream=None):
@@ -439,8 +446,8 @@ def fp8_block_quantize_weights(w, stream=None):
     groups, (rows, K) = (1 if w.dim() == 2 else w.shape[0]), w.shape[-2:]
     q = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
     s = torch.empty((*w.shape[:-2], _blocks(rows), _blocks(K)), dtype=torch.float32, device=w.device)
-    _lib.check(_lib.load().moe_w8a8_fp8_block_quantize_weights(_ptr(w), groups, rows, K, _ptr(q), _ptr(s),
-                                                               _stream(stream)),
+    _lib.check(_lib.load().moe_w8a8_fp8_block_quantize_weights(w.data_ptr(), groups, rows, K, q.data_ptr(),
+                                                               s.data_ptr(), _raw_stream(stream, w)),
                "moe_w8a8_fp8_block_quantize_weights")
     return q, s
 
@@ -468,8 +475,8 @@ def fp8_block_linear(x, w_q, w_scale, workspace=None, out=None, stream=None):
     else:
         _need(out, torch.bfloat16, (M, N), "out")
     _lib.check(_lib.load().moe_w8a8_fp8_block_linear(
-        _ptr(x), _ptr(w_q), _ptr(w_scale), M, N, K, _ptr(out), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)), "moe_w8a8_fp8_block_linear")
+        x.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), M, N, K, out.data_ptr(), workspace.data_ptr(),
+        workspace.nbytes, _raw_stream(stream, x)), "moe_w8a8_fp8_block_linear")
     return out
 
 
@@ -500,13 +507,13 @@ def fp8_block_forward(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale
     if workspace is None:
         workspace = new_workspace(fp8_block_workspace_size(T, H, I, E, top_k), x.device)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        out = torch.empty_like(x)
     else:
         _need(out, torch.bfloat16, (T, H), "out")
     _lib.check(_lib.load().moe_w8a8_fp8_block_forward(
-        _ptr(x), _ptr(router_w), _ptr(router_bias), _ptr(w13_q), _ptr(w13_scale), _ptr(w2_q), _ptr(w2_scale),
-        T, H, I, E, top_k, _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _stream(stream)), "moe_w8a8_fp8_block_forward")
+        x.data_ptr(), router_w.data_ptr(), _ptr(router_bias), w13_q.data_ptr(), w13_scale.data_ptr(), w2_q.data_ptr(),
+        w2_scale.data_ptr(), T, H, I, E, top_k, out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        _raw_stream(stream, x)), "moe_w8a8_fp8_block_forward")
     return out
 
 
@@ -524,31 +531,31 @@ def norm_residual(x, branch=None, post_w=None, gate=None, scale=1.0, pre_w=None,
     branch, weights and gate are bf16; gate is [H], [T, 1] or [T, H].  Returns
     (r, n): r in x's type (x itself without a branch; ``x_out`` may be x), n bf16."""
     torch = _torch()
-    T, H = x.shape
-    if x.dtype is not torch.float32:
-        _need(x, torch.bfloat16, (T, H), "x")
-    else:
-        _need(x, torch.float32, (T, H), "x")
-    form = 0
+    bf16 = torch.bfloat16
+    fp32 = x.dtype is torch.float32
+    T, H = shape = x.shape
+    _need(x, torch.float32 if fp32 else bf16, shape, "x")
+    form, r, n = 0, x, None
     if branch is not None:
-        _need(branch, torch.bfloat16, (T, H), "branch")
+        _need(branch, bf16, shape, "branch")
         if x_out is None:
-            x_out = torch.empty_like(x)
+            r = torch.empty_like(x)
         else:
-            _need(x_out, x.dtype, (T, H), "x_out")
+            r = x_out
+            _need(r, x.dtype, shape, "x_out")
     if post_w is not None:
-        _need(post_w, torch.bfloat16, (H,), "post_w")
+        _need(post_w, bf16, (H,), "post_w")
     if gate is not None:
-        form = 1 if gate.dim() == 1 else 2 if gate.dim() == 2 and gate.shape[1] == 1 and H != 1 else 3
-        _need(gate, torch.bfloat16, ((H,), (T, 1), (T, H))[form - 1], "gate")
+        form = 1 if gate.dim() == 1 else 2 if gate.dim() == 2 and gate.shape[1] == 1 else 3
+        _need(gate, bf16, ((H,), (T, 1), shape)[form - 1], "gate")
     if pre_w is not None:
-        _need(pre_w, torch.bfloat16, (H,), "pre_w")
+        _need(pre_w, bf16, (H,), "pre_w")
         if n_out is None:
-            n_out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+            n = torch.empty_like(x, dtype=bf16)
         else:
-            _need(n_out, torch.bfloat16, (T, H), "n_out")
+            n = n_out
+            _need(n, bf16, shape, "n_out")
     _lib.check(_lib.load().moe_w8a8_norm_residual(
-        _ptr(x), x.dtype is torch.float32, _ptr(branch), _ptr(post_w), _ptr(gate), form, scale, _ptr(pre_w), eps,
-        T, H, _ptr(x_out) if branch is not None else None, _ptr(n_out) if pre_w is not None else None,
-        _stream(stream)), "moe_w8a8_norm_residual")
-    return (x_out if branch is not None else x), (n_out if pre_w is not None else None)
+        x.data_ptr(), fp32, _ptr(branch), _ptr(post_w), _ptr(gate), form, scale, _ptr(pre_w), eps, T, H,
+        r.data_ptr(), _ptr(n), _raw_stream(stream, x)), "moe_w8a8_norm_residual")
+    return r, n

@@ -98,9 +98,12 @@ moe_status_t moe_w8a8_fp8_block_linear(const uint16_t* x, const uint8_t* w_q, co
     if (workspace_bytes < L.total || injected(kInjectWsShort)) return MOE_ERR_WORKSPACE_TOO_SMALL;
     if (gemm_path_forced()) return MOE_ERR_NOT_IMPLEMENTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool pdl = pdl_default();
+    uint8_t* q_x = at<uint8_t>(workspace, L.q_x);
+    float* s_x = at<float>(workspace, L.s_x);
     BlockGemmArgs g{};
-    g.act = at<uint8_t>(workspace, L.q_x);
-    g.act_scale = at<float>(workspace, L.s_x);
+    g.act = q_x;
+    g.act_scale = s_x;
     g.w = w_q;
     g.w_scale = w_scale;
     g.K = (int)K;
@@ -111,10 +114,12 @@ moe_status_t moe_w8a8_fp8_block_linear(const uint16_t* x, const uint8_t* w_q, co
     g.error = at<int>(workspace, L.err);
     g.timeout_ns = current_timeout_ns();
     g.stall = injected(kInjectStall) ? 1 : 0;
-    cudaError_t e = launch_quantize_block(x, (int)M, (int)K, at<uint8_t>(workspace, L.q_x),
-                                          at<float>(workspace, L.s_x), st, false);
-    if (e == cudaSuccess) e = launch_block_gemm(BlockEpi::BF16, g, st, pdl_default());
-    return from_cuda(e);
+    const bool few = block_linear_few_supported((int)M, (int)N, (int)K);
+    if (!few || !block_linear_few_fused((int)M)) {
+        const cudaError_t e = launch_quantize_block(x, (int)M, (int)K, q_x, s_x, st, pdl);
+        if (e != cudaSuccess) return from_cuda(e);
+    }
+    return from_cuda(few ? launch_block_linear_few(g, x, st, pdl) : launch_block_gemm(BlockEpi::BF16, g, st, pdl));
 }
 
 size_t moe_w8a8_fp8_block_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k) {

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(256) quantize_rows_block_kernel(
     pdl_trigger();
     if (r >= M) return;
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (col < K) v = __ldg(reinterpret_cast<const uint4*>(x + (size_t)r * K + col));
+    if (col < K) v = *reinterpret_cast<const uint4*>(x + (size_t)r * K + col);
     int my_slot = r;
     if (SLOTS && lane < k) {
         const int e = topk_ids[(size_t)r * k + lane];
@@ -83,15 +83,9 @@ __global__ void __launch_bounds__(256) quantize_rows_block_kernel(
             if (!kChecked || my_slot >= 0) slot_token[my_slot] = r;
         }
     }
-    float f[8];
+    float f[8], s;
     bf16x8_to_f32(v, f);
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = amax_nan(amax, f[i]);
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) amax = amax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    const float s = block_scale(amax);
-    const uint2 c = make_uint2(e4m3_quot4(f[0], f[1], f[2], f[3], s), e4m3_quot4(f[4], f[5], f[6], f[7], s));
+    const uint2 c = quant8(f, s);
     const int n = SLOTS ? k : 1;
     for (int j = 0; j < n; ++j) {
         const int row = SLOTS ? __shfl_sync(0xffffffffu, my_slot, j) : r;

@@ -42,6 +42,13 @@ struct BlockGemmArgs {
 // Tensor-core product (gemm_block.cu).
 cudaError_t launch_block_gemm(BlockEpi epi, const BlockGemmArgs& args, cudaStream_t st, bool pdl);
 
+// The linear layer for few rows (linear_block_few.cu): g as for
+// launch_block_gemm with BlockEpi::BF16 and one group.  Where
+// block_linear_few_fused, x is quantised in the launch and g.act is not read.
+bool block_linear_few_fused(int M);
+bool block_linear_few_supported(int M, int N, int K);
+cudaError_t launch_block_linear_few(const BlockGemmArgs& g, const uint16_t* x, cudaStream_t st, bool pdl);
+
 // Weights fp32 [groups][rows][K] to E4M3 codes and scales per 128 x 128 block.
 cudaError_t launch_quantize_weights_block(const float* w, int64_t groups, int rows, int K, uint8_t* q, float* s,
                                           cudaStream_t st);

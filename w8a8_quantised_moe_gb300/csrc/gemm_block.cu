@@ -50,21 +50,6 @@ constexpr int kBgSmem = kBgOffMisc + 64 + 1024;              // + alignment slac
 static_assert(kBgOffTiles % 8 == 0 && kBgOffXch % 8 == 0 && kBgOffMisc % 8 == 0, "alignment");
 static_assert(kBgSmem <= 232448, "shared memory budget");
 
-__device__ __forceinline__ void bg_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// Instruction descriptor of kind::f8f6f4: E4M3 A and B (format 0), fp32 D.
-__host__ __device__ constexpr uint32_t bg_idesc(uint32_t M, uint32_t N) {
-    return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-
 // Waits for this warp's tensor-memory loads; the registers pass through, so
 // that no use of them moves above the wait.
 __device__ __forceinline__ void bg_wait_ld(uint32_t (&r)[16]) {
@@ -237,7 +222,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
             for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
                 int g, cb, row0, nvalid;
                 bg_decode_tile(tiles, tile, g, cb, row0, nvalid);
-                const uint32_t idesc = bg_idesc(kBgRows, (uint32_t)(halves_of(cb) * kBlk));
+                const uint32_t idesc = idesc_e4m3(kBgRows, (uint32_t)(halves_of(cb) * kBlk));
                 for (int kb = 0; kb < nkb; ++kb, ++it) {
                     const uint32_t s = it % kBgNS, d = it & 1u;
                     if (!mbar_wait(&acc_empty[d], ((it >> 1) & 1u) ^ 1u, ctl) ||
@@ -250,7 +235,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
                     const uint64_t a_desc = smem_desc_sw128(a_base), b_desc = smem_desc_sw128(a_base + kBgStageA);
 #pragma unroll
                     for (int ks = 0; ks < kBlk / 32; ++ks)  // 32 bytes of K per MMA
-                        bg_mma(tmem + d * kBgCols, a_desc + (uint64_t)(ks * 2), b_desc + (uint64_t)(ks * 2), idesc,
+                        mma_e4m3(tmem + d * kBgCols, a_desc + (uint64_t)(ks * 2), b_desc + (uint64_t)(ks * 2), idesc,
                                ks != 0 ? 1u : 0u);
                     mma_commit(&empty[s]);
                     mma_commit(&acc_full[d]);
