@@ -1,11 +1,12 @@
-// block.cu -- quantisers of the block-scaled FP8 operators.
+// block.cu -- quantisers and the combine of the block-scaled FP8 operators.
 //
 // A block's scale is s = amax * (1/448) (one binary32 product with the rounded
-// reciprocal) and its codes are the E4M3 values nearest to the binary32 quotients x / s, ties to the even
-// mantissa, saturated at +-448; a block of zeros has s = 0 and codes 0.
+// reciprocal) and its codes are the E4M3 values nearest to the binary32
+// quotients x / s, ties to the even mantissa, saturated at +-448; a block of
+// zeros has s = 0 and codes 0.
 // Activations: a block is 128 channels of one row, so a row needs no
 // reduction across its blocks.  Weights: a block is 128 x 128.
-#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "block.h"
 #include "block_dev.cuh"
@@ -55,23 +56,28 @@ __global__ void __launch_bounds__(256) quantize_weights_block_kernel(const float
     }
 }
 
-// A warp per (row, 256 channels): lanes 0-15 and 16-31 hold a block each, 8
-// channels a lane.  SLOTS: the row is a token whose codes go to its k slots.
-template <bool SLOTS>
+// A warp per (row, 256 V channels): V vectors of 8 channels a lane, all in
+// flight; lanes 0-15 and 16-31 hold a block of a vector each.  SLOTS: the row
+// is a token whose codes go to its k slots.
+template <bool SLOTS, int V>
 __global__ void __launch_bounds__(256) quantize_rows_block_kernel(
     const uint16_t* __restrict__ x, int M, int K, uint8_t* __restrict__ q, float* __restrict__ s_out,
     const int32_t* __restrict__ topk_ids, const int32_t* __restrict__ rank, const int32_t* __restrict__ base, int E,
     int k, int32_t* __restrict__ slot_of, int32_t* __restrict__ slot_token, int* __restrict__ error) {
     const int lane = threadIdx.x & 31;
-    const int kb = blocks_of(K), parts = (kb + 1) / 2;
+    const int kb = blocks_of(K), parts = (kb + 2 * V - 1) / (2 * V);
     const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int r = (int)(item / parts), part = (int)(item % parts);
-    const int col = part * 256 + lane * 8;
+    const int r = (int)(item / parts), part = (int)(item - (int64_t)r * parts);
+    const int col = part * 256 * V + lane * 8;
     pdl_wait();
     pdl_trigger();
     if (r >= M) return;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (col < K) v = *reinterpret_cast<const uint4*>(x + (size_t)r * K + col);
+    uint4 v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = col + i * 256;
+        v[i] = c < K ? *reinterpret_cast<const uint4*>(x + (size_t)r * K + c) : make_uint4(0u, 0u, 0u, 0u);
+    }
     int my_slot = r;
     if (SLOTS && lane < k) {
         const int e = topk_ids[(size_t)r * k + lane];
@@ -83,17 +89,74 @@ __global__ void __launch_bounds__(256) quantize_rows_block_kernel(
             if (!kChecked || my_slot >= 0) slot_token[my_slot] = r;
         }
     }
-    float f[8], s;
-    bf16x8_to_f32(v, f);
-    const uint2 c = quant8(f, s);
     const int n = SLOTS ? k : 1;
-    for (int j = 0; j < n; ++j) {
-        const int row = SLOTS ? __shfl_sync(0xffffffffu, my_slot, j) : r;
-        if (col < K && (!kChecked || row >= 0)) {
-            *reinterpret_cast<uint2*>(q + (size_t)row * K + col) = c;
-            if ((lane & 15) == 0) s_out[(size_t)row * kb + part * 2 + (lane >> 4)] = s;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = col + i * 256;
+        float f[8], s;
+        bf16x8_to_f32(v[i], f);
+        const uint2 code = quant8(f, s);
+        for (int j = 0; j < n; ++j) {
+            const int row = SLOTS ? __shfl_sync(0xffffffffu, my_slot, j) : r;
+            if (c < K && (!kChecked || row >= 0)) {
+                *reinterpret_cast<uint2*>(q + (size_t)row * K + c) = code;
+                if ((lane & 15) == 0) s_out[(size_t)row * kb + c / kBlk] = s;
+            }
         }
     }
+}
+
+// A warp per (token, 256 columns): the token's k rows are all in flight before
+// the sum, which runs in top-k order.
+template <int KMAX>
+__global__ void __launch_bounds__(256) combine_half_kernel(const uint16_t* __restrict__ o,
+                                                           const float* __restrict__ o_scale,
+                                                           const int32_t* __restrict__ slot_of,
+                                                           const float* __restrict__ topk_w, int T, int H, int k,
+                                                           uint16_t* __restrict__ y, int* __restrict__ error) {
+    const int lane = threadIdx.x & 31;
+    const int parts = (H + 255) / 256;
+    const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int t = (int)(item / parts), col = (int)(item - (int64_t)t * parts) * 256 + lane * 8;
+    pdl_wait();
+    pdl_trigger();
+    if (t >= T || col >= H) return;
+    uint4 v[KMAX];
+    float w[KMAX];
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+        v[j] = make_uint4(0u, 0u, 0u, 0u);
+        w[j] = 0.f;
+        if (j >= k) continue;
+        const int slot = slot_of[(size_t)t * k + j];
+        if (!in_range(slot, 0, (long long)T * k, error)) continue;  // checked build: contributes nothing
+        v[j] = *reinterpret_cast<const uint4*>(o + (size_t)slot * H + col);
+        w[j] = topk_w[(size_t)t * k + j] * o_scale[(size_t)slot * (H / 32) + col / 32];
+    }
+    float a[8] = {};
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+        const __half2* h = reinterpret_cast<const __half2*>(&v[j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(h[i]);
+            a[2 * i] = fmaf(w[j], f.x, a[2 * i]);
+            a[2 * i + 1] = fmaf(w[j], f.y, a[2 * i + 1]);
+        }
+    }
+    *reinterpret_cast<uint4*>(y + (size_t)t * H + col) =
+        make_uint4(bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3]), bf16_pair(a[4], a[5]), bf16_pair(a[6], a[7]));
+}
+
+// Four vectors a lane where that still leaves work for every SM, else one.
+template <bool SLOTS, typename... Args>
+cudaError_t launch_quantize_rows(cudaStream_t st, bool pdl, const uint16_t* x, int M, int K, Args... args) {
+    const int v4 = (blocks_of(K) + 7) / 8, v1 = (blocks_of(K) + 1) / 2;
+    const bool wide = (int64_t)M * v4 >= 32LL * num_sms();
+    const int64_t items = (int64_t)M * (wide ? v4 : v1);
+    const dim3 grid((unsigned)((items + 7) / 8)), block(256);
+    return wide ? launch_kernel(quantize_rows_block_kernel<SLOTS, 4>, grid, block, 0, st, pdl, x, M, K, args...)
+                : launch_kernel(quantize_rows_block_kernel<SLOTS, 1>, grid, block, 0, st, pdl, x, M, K, args...);
 }
 
 }  // namespace
@@ -109,9 +172,8 @@ cudaError_t launch_quantize_weights_block(const float* w, int64_t groups, int ro
 
 cudaError_t launch_quantize_block(const uint16_t* x, int M, int K, uint8_t* q, float* s, cudaStream_t st, bool pdl) {
     if (M == 0) return cudaSuccess;
-    const int64_t items = (int64_t)M * ((blocks_of(K) + 1) / 2);
-    return launch_kernel(quantize_rows_block_kernel<false>, dim3((unsigned)((items + 7) / 8)), dim3(256), 0, st, pdl,
-                         x, M, K, q, s, nullptr, nullptr, nullptr, 0, 1, nullptr, nullptr, nullptr);
+    return launch_quantize_rows<false>(st, pdl, x, M, K, q, s, nullptr, nullptr, nullptr, 0, 1, nullptr, nullptr,
+                                       nullptr);
 }
 
 cudaError_t launch_permute_quant_block(const uint16_t* x, const int32_t* topk_ids, const int32_t* rank,
@@ -119,9 +181,22 @@ cudaError_t launch_permute_quant_block(const uint16_t* x, const int32_t* topk_id
                                        int32_t* slot_token, uint8_t* q, float* s, int* error, cudaStream_t st,
                                        bool pdl) {
     if (T == 0) return cudaSuccess;
-    const int64_t items = (int64_t)T * ((blocks_of(H) + 1) / 2);
-    return launch_kernel(quantize_rows_block_kernel<true>, dim3((unsigned)((items + 7) / 8)), dim3(256), 0, st, pdl,
-                         x, T, H, q, s, topk_ids, rank, base, E, k, slot_of, slot_token, error);
+    return launch_quantize_rows<true>(st, pdl, x, T, H, q, s, topk_ids, rank, base, E, k, slot_of, slot_token, error);
+}
+
+cudaError_t launch_combine_half(const uint16_t* o, const float* o_scale, const int32_t* slot_of, const float* topk_w,
+                                int T, int H, int k, uint16_t* y, int* error, cudaStream_t st, bool pdl) {
+    if (T == 0) return cudaSuccess;
+    const int64_t items = (int64_t)T * ((H + 255) / 256);
+    const dim3 grid((unsigned)((items + 7) / 8)), block(256);
+    if (k <= 2)
+        return launch_kernel(combine_half_kernel<2>, grid, block, 0, st, pdl, o, o_scale, slot_of, topk_w, T, H, k, y,
+                             error);
+    if (k <= 4)
+        return launch_kernel(combine_half_kernel<4>, grid, block, 0, st, pdl, o, o_scale, slot_of, topk_w, T, H, k, y,
+                             error);
+    return launch_kernel(combine_half_kernel<8>, grid, block, 0, st, pdl, o, o_scale, slot_of, topk_w, T, H, k, y,
+                         error);
 }
 
 }  // namespace moe

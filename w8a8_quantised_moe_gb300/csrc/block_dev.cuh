@@ -80,6 +80,23 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return r;
 }
 
+// Two fp16 (lo in the low half), each rounded to nearest even.
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Scale s = 2^(e - 14), amax in [2^e, 2^(e + 1)), and inv = 1 / s: v * inv is
+// below 2^15, so it fits fp16, and what lies 2^-28 below the largest still has
+// fp16's full 11 bits: an eighth of bf16's rounding error for the same bytes.  A
+// NaN or an infinity keeps the scale 1 and stays what it is.
+__device__ __forceinline__ void half_scale(float amax, float& s, float& inv) {
+    const uint32_t e = min(max(__float_as_uint(amax) >> 23, 16u), 254u);
+    const bool finite = amax < INFINITY;
+    s = finite ? __uint_as_float((e - 14) << 23) : 1.f;
+    inv = finite ? __uint_as_float((268 - e) << 23) : 1.f;
+}
+
 // h = g / (1 + exp(-g)) * u.  The exponential and the quotient are the fast
 // forms (about 2 ulp each): h is rounded to a 4-bit significand next, and a
 // code that such an error moves lies as close to its neighbour as to h.
@@ -88,7 +105,7 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 }
 
 // Two binary32 values in one 64-bit register, and the packed multiply-add on
-// them (two rounded FMAs in one instruction: twice the rate of fma.rn.f32).
+// them (two rounded FMAs).
 using f32x2 = unsigned long long;
 __device__ __forceinline__ f32x2 pack2(float lo, float hi) {
     f32x2 r;

@@ -1,5 +1,5 @@
 // gemm_block.cu -- the grouped block-scaled FP8 product on the tcgen05 tensor
-// cores:
+// cores, for groups of many rows:
 //
 //   D[r][n] = sum_b sx[r][b] * sw[n / 128][b] * (sum_{k in block b} a[r][k] * w[n][k])
 //
@@ -8,21 +8,30 @@
 // differ from block to block, so the block's partial sums go to registers,
 // where they are multiplied by the block's scale and added to binary32 sums.
 //
-// Tile: 128 activation rows (the MMA's M, one TMEM lane each) x 256 weight
-// rows (N) in two halves of 128.  With rows on the lanes a thread's scale is
-// one value per half and block: sx of its row times sw of the half.  GateUp's
-// halves are 128 gate rows and the 128 up rows of the same channels, so the
-// tile holds whole scale blocks of h: each thread applies silu(gate) * up to
-// its 64 + 64 columns and h leaves the kernel as E4M3 codes with their scale,
-// never as binary32.
-//   warp 0     TMA producer (ring of kNS stages: activation rows and both
-//              halves' weight rows, 128 bytes of K each)
-//   warp 1     TMEM allocator and MMA issuer: four K = 32 MMAs a block into one
-//              of two 256-column TMEM buffers
-//   warps 2-9  scale and sum the blocks, then the epilogue: warp w has lanes
-//              32 (w % 4).., and columns 64 ((w - 2) / 4).. of each half
-// Persistent grid, tiles dealt round-robin with a group's row blocks next to
-// each other (they share weight tiles in L2).  Every wait is bounded (ptx.cuh).
+// Tile: 128 activation rows (the MMA's M, one TMEM lane each) x 256 weight rows
+// (N) in two halves of 128.  With rows on the lanes a thread's scale is one value
+// per half and block: sx of its row times sw of the half.  GateUp's halves are
+// 128 gate rows and the 128 up rows of the same channels, so the tile holds
+// whole scale blocks of h: each thread applies silu(gate) * up to its 64 + 64
+// columns and h leaves the kernel as E4M3 codes with their scale, never as
+// binary32.
+//   warp 0      TMA producer (ring of kBgNS stages: activation rows and both
+//               halves' weight rows, 128 bytes of K each)
+//   warp 1      TMEM allocator and MMA issuer: four K = 32 MMAs a block into one
+//               of two 256-column TMEM buffers
+//   warps 4-11  scale and sum the blocks, then the epilogue
+// Persistent grid, tiles dealt round-robin.  Every wait is bounded (ptx.cuh).
+//
+// What bounds it: 8192^3 takes 489 us beside its quantiser, 1040 clocks a block
+// of a tile, of which the MMAs are 512.  With the sums cut to a quarter of the
+// columns a block took 780, without the operands' loads as well 670.  The sums
+// are a chain for each warp (wait for the MMAs 180 clocks, eight tensor-memory
+// loads of 16 columns 650, and their multiply-adds, 80 to 100 a clock and SM,
+// partly behind them) on two buffers, all that tensor memory holds.  Tried and
+// slower: CTA pairs that share the weights (less to load, the same chain: 562),
+// two MMA-issuing threads (525), sixteen epilogue warps (639), loads of 32
+// columns (522 to 697 with the registers the compiler then lacks), scalar
+// multiply-adds (642 against 611).
 #include <mutex>
 
 #include "block.h"
@@ -32,23 +41,20 @@
 namespace moe {
 namespace {
 
-constexpr int kBgRows = 128;       // activation rows per tile
-constexpr int kBgCols = 256;       // weight rows per tile
-constexpr int kBgNS = 4;           // stages
-constexpr int kBgThreads = 320;
-constexpr int kBgEpi0 = 2;         // first epilogue warp
+constexpr int kBgRows = 128;     // activation rows of a CTA
+constexpr int kBgCols = 256;     // weight rows of a tile
+constexpr int kBgThreads = 384;  // producer, MMA issuer, two idle and 8 epilogue warps
+constexpr int kBgEpi0 = 4;       // first epilogue warp
 constexpr int kBgEpiWarps = 8;
-constexpr int kBgStageA = kBgRows * kBlk;
-constexpr int kBgStageB = kBgCols * kBlk;
-constexpr int kBgStage = kBgStageA + kBgStageB;
-constexpr int kBgOffBars = kBgNS * kBgStage;
-constexpr int kBgNumBars = 2 * kBgNS + 4 + 2 + 4;  // full, empty, acc_full/empty[2], teardown, stall, pair[4]
-constexpr int kBgOffTiles = kBgOffBars + kBgNumBars * 8;
-constexpr int kBgOffXch = kBgOffTiles + (kMaxExperts + 1) * 4 * 2;
-constexpr int kBgOffMisc = kBgOffXch + 2 * 2 * kBgRows * 4;  // row maxima [2 tiles][2 warps][rows]
-constexpr int kBgSmem = kBgOffMisc + 64 + 1024;              // + alignment slack
-static_assert(kBgOffTiles % 8 == 0 && kBgOffXch % 8 == 0 && kBgOffMisc % 8 == 0, "alignment");
-static_assert(kBgSmem <= 232448, "shared memory budget");
+constexpr int kBgHalf = kBlk * kBlk;         // bytes of 128 rows x 128 channels
+constexpr int kBgStaging = 32 * 64;          // per epilogue warp: 32 rows x 64 bytes
+constexpr int kBgXch = 2 * 2 * kBgRows * 4;  // row maxima [2 tiles][2 warps][rows]
+
+// The launch gives every thread 168 registers; the epilogue warps hold 128 sums
+// and their next columns each, so the first four warps pass them theirs: 128 x
+// 40 + 256 x 232 = 384 x 168.
+__device__ __forceinline__ void bg_regs_few() { asm volatile("setmaxnreg.dec.sync.aligned.u32 40;"); }
+__device__ __forceinline__ void bg_regs_many() { asm volatile("setmaxnreg.inc.sync.aligned.u32 232;"); }
 
 // Waits for this warp's tensor-memory loads; the registers pass through, so
 // that no use of them moves above the wait.
@@ -59,20 +65,259 @@ __device__ __forceinline__ void bg_wait_ld(uint32_t (&r)[16]) {
                    "+r"(r[15])::"memory");
 }
 
-// Box heights of the activation maps: the smallest that covers a tile's rows.
-__host__ __device__ constexpr int bg_box_rows(int i) { return i == 0 ? 32 : i == 1 ? 64 : kBgRows; }
-__device__ __forceinline__ int bg_box_index(int nvalid) { return nvalid <= 32 ? 0 : nvalid <= 64 ? 1 : 2; }
+// An epilogue warp: 32 lanes' rows x columns 64 w2 .. of each half.
+struct BgWarp {
+    int q, w2, row, lane;  // lane quarter, column half, row of the CTA's 128
+    __device__ __forceinline__ BgWarp(int warp, int ln) : q(warp & 3), w2((warp - kBgEpi0) >> 2), lane(ln) {
+        row = q * 32 + lane;
+    }
+    // its columns of a 256-column buffer at `tmem`
+    __device__ __forceinline__ uint32_t addr(uint32_t tmem) const {
+        return tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(w2 * 64);
+    }
+};
 
-__device__ __forceinline__ void bg_decode_tile(const Tiles& t, int tile, int& g, int& cb, int& row0, int& nvalid) {
+// Adds the block's sums at `a` (this warp's columns), times the halves' scales,
+// to acc[half][column pair]; the next 16 columns load while 16 are summed.
+// `release` runs once every column is in registers.
+template <class Release>
+__device__ __forceinline__ void bg_add_block(f32x2 (&acc)[2][32], uint32_t a, float s0, float s1, Release release) {
+    const f32x2 sc[2] = {pack2(s0, s0), pack2(s1, s1)};
+    uint32_t v[2][16];
+    tmem_ld_16(a, v[0]);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        bg_wait_ld(v[c & 1]);
+        if (c < 7) tmem_ld_16(a + ((c + 1) >> 2) * kBlk + ((c + 1) & 3) * 16, v[(c + 1) & 1]);
+        if (c == 7) release();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            fma2(acc[c >> 2][(c & 3) * 8 + j],
+                 pack2(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])), sc[c >> 2]);
+    }
+}
+
+// The scales that an epilogue thread applies, read one block ahead: its row's
+// (blocks of a row are next to each other: seven of eight reads hit L1) and the
+// weights' two.  Measured at 8192^3, us: this 522; the rows' scales stored block
+// by block, one line a warp and block, 617; staged in shared memory by a fourth
+// warp or by the producer's copies, behind barriers of their own, 608 and 728.
+struct BgScales {
+    const float *sx, *sw0, *sw1;
+    float x, w0, w1;
+    template <int EPI>
+    __device__ __forceinline__ void start(const BlockGemmArgs& a, int g, int cb, int r, int nkb) {
+        const int nb = blocks_of(a.w_rows);
+        const int b0 = EPI == (int)BlockEpi::GateUp ? cb : 2 * cb;
+        const int b1 = EPI == (int)BlockEpi::GateUp ? cb + a.up_offset / kBlk : min(2 * cb + 1, nb - 1);
+        sx = a.act_scale + (size_t)r * nkb;
+        sw0 = a.w_scale + ((size_t)g * nb + b0) * nkb;
+        sw1 = a.w_scale + ((size_t)g * nb + b1) * nkb;
+        x = __ldg(sx);
+        w0 = __ldg(sw0);
+        w1 = __ldg(sw1);
+    }
+    __device__ __forceinline__ void next(int kb, int nkb, float& s0, float& s1) {
+        s0 = __fmul_rn(x, w0);
+        s1 = __fmul_rn(x, w1);
+        if (kb + 1 < nkb) {
+            x = __ldg(sx + kb + 1);
+            w0 = __ldg(sw0 + kb + 1);
+            w1 = __ldg(sw1 + kb + 1);
+        }
+    }
+};
+
+// The warp's 32 rows x 64 bytes (v: this lane's row) to memory through shared
+// memory, so that an instruction writes whole 64-byte pieces of 8 rows instead
+// of 16 bytes of 32.  dst: row 0's piece; rows from `rows` on are not written.
+__device__ __forceinline__ void bg_store_rows(uint8_t* staging, const uint4 (&v)[4], int lane, uint8_t* dst,
+                                              size_t stride, int rows) {
+    __syncwarp();  // the previous piece has been read
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4*>(staging + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)) = v[c];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2), c = lane & 3;
+        if (r < rows)
+            *reinterpret_cast<uint4*>(dst + (size_t)r * stride + c * 16) =
+                *reinterpret_cast<const uint4*>(staging + r * 64 + ((c ^ (r >> 1 & 3)) << 4));
+    }
+}
+
+// What a tile's sums become.  row0: the CTA's first row; nvalid: its rows; cb:
+// channel block (GateUp) or 256-column block.  Returns false when a wait gave up.
+template <int EPI>
+__device__ __forceinline__ bool bg_output(const BlockGemmArgs& args, f32x2 (&acc)[2][32], const BgWarp& w, int row0,
+                                          int nvalid, int cb, float* xch, uint64_t* pair_bar, uint32_t tl,
+                                          uint8_t* staging, const WaitCtl& ctl) {
+    const int rows = min(32, nvalid - w.q * 32);  // of this warp; may be negative
+    const size_t r0 = (size_t)row0 + w.q * 32;
+    if constexpr (EPI == (int)BlockEpi::GateUp) {
+        float amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            float g0, g1, u0, u1;
+            unpack2(acc[0][j], g0, g1);
+            unpack2(acc[1][j], u0, u1);
+            g0 = silu_mul(g0, u0);
+            g1 = silu_mul(g1, u1);
+            amax = amax_nan(amax_nan(amax, g0), g1);
+            acc[0][j] = pack2(g0, g1);
+        }
+        // the row's other 64 columns are the partner warp's
+        float* mine = xch + (tl & 1u) * 2 * kBgRows;
+        mine[w.w2 * kBgRows + w.row] = amax;
+        __syncwarp();
+        if (w.lane == 0) mbar_arrive(&pair_bar[w.q]);
+        if (!warp_wait(&pair_bar[w.q], tl & 1u, ctl)) return false;
+        amax = amax_nan(amax, mine[(w.w2 ^ 1) * kBgRows + w.row]);
+        const float s = block_scale(amax);
+        // the quotient as a product with 1 / s: h is rounded already, see silu_mul
+        const float inv = s == 0.f ? 0.f : __fdiv_rn(1.0f, s);
+        const int n_ch = args.up_offset;
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t c4[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float h0, h1, h2, h3;
+                unpack2(acc[0][i * 8 + j * 2], h0, h1);
+                unpack2(acc[0][i * 8 + j * 2 + 1], h2, h3);
+                c4[j] = e4m3_pair(h0 * inv, h1 * inv) | (e4m3_pair(h2 * inv, h3 * inv) << 16);
+            }
+            v[i] = make_uint4(c4[0], c4[1], c4[2], c4[3]);
+        }
+        bg_store_rows(staging, v, w.lane, args.q_out + r0 * n_ch + cb * kBlk + w.w2 * 64, n_ch, rows);
+        if (w.w2 == 0 && w.lane < rows) args.s_out[(r0 + w.lane) * (n_ch / kBlk) + cb] = s;
+    } else {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int col = cb * kBgCols + half * kBlk + w.w2 * 64;
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {  // 32 columns: 64 bytes
+                const int c0 = col + p * 32;
+                if (c0 >= args.w_rows) continue;
+                float inv = 1.f;
+                if (EPI == (int)BlockEpi::Half) {
+                    float amax = 0.f, s;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float a, b;
+                        unpack2(acc[half][p * 16 + j], a, b);
+                        amax = amax_nan(amax_nan(amax, a), b);
+                    }
+                    half_scale(amax, s, inv);
+                    if (w.lane < rows) args.s_out[(r0 + w.lane) * (args.w_rows / 32) + c0 / 32] = s;
+                }
+                uint4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t c4[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float a, b;
+                        unpack2(acc[half][p * 16 + i * 4 + j], a, b);
+                        c4[j] = EPI == (int)BlockEpi::Half ? half_pair(a * inv, b * inv) : bf16_pair(a, b);
+                    }
+                    v[i] = make_uint4(c4[0], c4[1], c4[2], c4[3]);
+                }
+                uint8_t* dst = static_cast<uint8_t*>(args.out) + (r0 * args.w_rows + c0) * 2;
+                if (c0 + 32 <= args.w_rows) {
+                    bg_store_rows(staging, v, w.lane, dst, (size_t)args.w_rows * 2, rows);
+                } else if (w.lane < rows) {  // the last 16 columns of a matrix
+                    uint4* d = reinterpret_cast<uint4*>(dst + (size_t)w.lane * args.w_rows * 2);
+                    d[0] = v[0];
+                    d[1] = v[1];
+                }
+            }
+        }
+    }
+    return true;
+}
+
+// Tile table of a launch, by one warp: group g has ceil(rows_g / rows_tile) *
+// n_cb tiles.
+__device__ __forceinline__ void bg_tile_table(const BlockGemmArgs& args, int rows_tile, int n_cb, int* tile_start,
+                                              int* row_start, int lane) {
+    const int n = args.n_groups;
+    int carry = 0;
+    bool bad = false;  // checked build: an offset out of order or range
+    for (int base = 0; base < n; base += 32) {
+        const int g = base + lane;
+        int r0 = 0, r1 = 0;
+        if (g < n) {
+            r0 = args.offsets ? args.offsets[g] : 0;
+            r1 = args.offsets ? args.offsets[g + 1] : args.total_rows;
+            if (!group_rows_ok(r0, r1, args.total_rows, args.error)) {
+                bad = true;
+                r0 = r1 = 0;
+            }
+            row_start[g] = r0;
+            if (g == n - 1) row_start[n] = r1;
+        }
+        const int v = (g < n) ? ((r1 - r0 + rows_tile - 1) / rows_tile) * n_cb : 0;
+        int incl = v;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += o;
+        }
+        if (g < n) tile_start[g] = carry + incl - v;
+        carry += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) tile_start[n] = carry;
+    if (kChecked && __any_sync(0xffffffffu, bad)) {  // an empty, consistent table: no tile runs
+        for (int g = lane; g <= n; g += 32) {
+            row_start[g] = 0;
+            tile_start[g] = 0;
+        }
+    }
+}
+
+// Tile -> group, column block, first row, valid rows (row blocks fastest, so
+// that a group's row blocks run together and share weight tiles in L2).
+__device__ __forceinline__ void bg_decode_tile(const Tiles& t, int tile, int rows_tile, int& g, int& cb, int& row0,
+                                               int& nvalid) {
     g = last_le(t.tile_start, t.n_groups, tile);
     const int local = tile - t.tile_start[g];
     const int rows = t.row_start[g + 1] - t.row_start[g];
-    const int ntb = (rows + kBgRows - 1) / kBgRows;
+    const int ntb = (rows + rows_tile - 1) / rows_tile;
     cb = local / ntb;
-    const int tb = local - cb * ntb;
-    row0 = t.row_start[g] + tb * kBgRows;
-    nvalid = min(kBgRows, t.row_start[g + 1] - row0);
+    row0 = t.row_start[g] + (local - cb * ntb) * rows_tile;
+    nvalid = min(rows_tile, t.row_start[g + 1] - row0);
 }
+
+template <int EPI>
+__host__ __device__ inline int bg_col_blocks(const BlockGemmArgs& a) {
+    return EPI == (int)BlockEpi::GateUp ? a.up_offset / kBlk : (a.w_rows + kBgCols - 1) / kBgCols;
+}
+
+// First weight row of a tile's halves.
+template <int EPI>
+__device__ __forceinline__ int bg_weight_row(const BlockGemmArgs& a, int g, int cb, int half) {
+    return EPI == (int)BlockEpi::GateUp ? g * a.w_rows + half * a.up_offset + cb * kBlk
+                                        : g * a.w_rows + cb * kBgCols + half * kBlk;
+}
+
+constexpr int kBgNS = 4;  // stages
+constexpr int kBgStage = 3 * kBgHalf;
+constexpr int kBgOffBars = kBgNS * kBgStage;
+constexpr int kBgNumBars = 2 * kBgNS + 4 + 2 + 4;  // full, empty, acc_full/empty[2], teardown, stall, pair[4]
+constexpr int kBgOffTiles = kBgOffBars + kBgNumBars * 8;
+constexpr int kBgOffXch = (kBgOffTiles + (kMaxExperts + 1) * 4 * 2 + 15) / 16 * 16;
+constexpr int kBgOffStaging = kBgOffXch + kBgXch;
+constexpr int kBgOffMisc = kBgOffStaging + kBgEpiWarps * kBgStaging;
+constexpr int kBgSmem = kBgOffMisc + 64 + 1024;  // + alignment slack
+static_assert(kBgOffTiles % 8 == 0, "alignment");
+static_assert(kBgSmem <= 232448, "shared memory budget");
+
+// Box heights of the activation maps: the smallest that covers a tile's rows.
+__host__ __device__ constexpr int bg_box_rows(int i) { return i == 0 ? 32 : i == 1 ? 64 : kBgRows; }
+__device__ __forceinline__ int bg_box_index(int nvalid) { return nvalid <= 32 ? 0 : nvalid <= 64 ? 1 : 2; }
 
 template <int EPI>
 __global__ void __launch_bounds__(kBgThreads, 1)
@@ -85,7 +330,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     uint64_t* full = bars;              // [NS] the stage landed
     uint64_t* empty = full + kBgNS;     // [NS] the MMAs of the stage completed
     uint64_t* acc_full = empty + kBgNS; // [2] a block's partial sums are in tensor memory
-    uint64_t* acc_empty = acc_full + 2; // [2] the 8 epilogue warps have read them
+    uint64_t* acc_empty = acc_full + 2; // [2] the epilogue warps have read them
     uint64_t* teardown = acc_empty + 2;
     uint64_t* stall_bar = teardown + 1; // test hook: nothing arrives on it
     uint64_t* pair_bar = stall_bar + 1; // [4] the two warps of a lane quarter
@@ -96,9 +341,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kBgOffMisc + 8);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_groups = args.n_groups;
     const int nkb = blocks_of(args.K);
-    const int n_cb = EPI == (int)BlockEpi::GateUp ? args.up_offset / kBlk : (args.w_rows + kBgCols - 1) / kBgCols;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kBgNS; ++s) {
@@ -123,246 +366,121 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     }
     pdl_wait();  // the previous kernel's outputs (offsets, codes, scales) are visible from here
     pdl_trigger();
-    if (warp == 2) {  // tile table: tiles of group g = ceil(rows_g / 128) * n_cb
-        int carry = 0;
-        bool bad = false;  // checked build: an offset out of order or range
-        for (int base = 0; base < n_groups; base += 32) {
-            const int g = base + lane;
-            int r0 = 0, r1 = 0;
-            if (g < n_groups) {
-                r0 = args.offsets ? args.offsets[g] : 0;
-                r1 = args.offsets ? args.offsets[g + 1] : args.total_rows;
-                if (!group_rows_ok(r0, r1, args.total_rows, args.error)) {
-                    bad = true;
-                    r0 = r1 = 0;
-                }
-                row_start[g] = r0;
-                if (g == n_groups - 1) row_start[n_groups] = r1;
-            }
-            const int v = (g < n_groups) ? ((r1 - r0 + kBgRows - 1) / kBgRows) * n_cb : 0;
-            int incl = v;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += o;
-            }
-            if (g < n_groups) tile_start[g] = carry + incl - v;
-            carry += __shfl_sync(0xffffffffu, incl, 31);
-        }
-        if (lane == 0) tile_start[n_groups] = carry;
-        if (kChecked && __any_sync(0xffffffffu, bad)) {  // an empty, consistent table: no tile runs
-            for (int g = lane; g <= n_groups; g += 32) {
-                row_start[g] = 0;
-                tile_start[g] = 0;
-            }
-        }
-    }
+    if (warp == 2) bg_tile_table(args, kBgRows, bg_col_blocks<EPI>(args), tile_start, row_start, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int total_tiles = tile_start[n_groups];
-    const Tiles tiles{tile_start, row_start, n_groups};
+    const int total_tiles = tile_start[args.n_groups];
+    const Tiles tiles{tile_start, row_start, args.n_groups};
     const WaitCtl ctl{abort_flag, args.error, args.timeout_ns, 0u};
     // halves of a tile that hold weight rows (GateUp: always both)
     auto halves_of = [&](int cb) {
         return EPI == (int)BlockEpi::GateUp || args.w_rows - cb * kBgCols > kBlk ? 2 : 1;
     };
 
-    if (warp == 0) {
-        // ---------------------------------------------------------- producer
-        // lanes 0-2 issue one box each (both halves' weight rows, activation
-        // rows) in the same warp instruction; lane 0 owns the waits
-        if (lane < 3) {
-            uint32_t it = 0;
-            int ok = 1;
-            if (lane == 0) ok = !args.stall || mbar_wait(stall_bar, 0, ctl);  // the test hook's wait runs out
-            ok = __shfl_sync(0x7u, ok, 0);
-            for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
-                int g, cb, row0, nvalid;
-                bg_decode_tile(tiles, tile, g, cb, row0, nvalid);
-                const int halves = halves_of(cb);
-                int wrow0, wrow1;  // first weight row of each half
-                if (EPI == (int)BlockEpi::GateUp) {
-                    wrow0 = g * args.w_rows + cb * kBlk;
-                    wrow1 = wrow0 + args.up_offset;
-                } else {
-                    wrow0 = g * args.w_rows + cb * kBgCols;
-                    wrow1 = wrow0 + kBlk;
-                }
-                const int bi = bg_box_index(nvalid);
-                const CUtensorMap* ma = bi == 0 ? &tmap_a0 : bi == 1 ? &tmap_a1 : &tmap_a2;
-                const uint32_t bytes = (uint32_t)((bg_box_rows(bi) + halves * kBlk) * kBlk);
-                const CUtensorMap* map = lane == 2 ? ma : &tmap_w;
-                const int row = lane == 0 ? wrow0 : lane == 1 ? wrow1 : row0;
-                const int off = lane == 2 ? 0 : kBgStageA + lane * (kBlk * kBlk);
-                for (int kb = 0; kb < nkb; ++kb, ++it) {
-                    const uint32_t s = it % kBgNS, ph = (it / kBgNS) & 1u;
-                    if (lane == 0) {
-                        ok = mbar_wait(&empty[s], ph ^ 1u, ctl);
-                        if (ok) mbar_arrive_expect_tx(&full[s], bytes);
+    if (warp < kBgEpi0) {
+        bg_regs_few();
+        if (warp == 0) {
+            // ---------------------------------------------------------- producer
+            // lanes 0-2 issue one box each (both halves' weight rows, activation
+            // rows) in the same warp instruction; lane 0 owns the waits
+            if (lane < 3) {
+                uint32_t it = 0;
+                int ok = 1;
+                if (lane == 0) ok = !args.stall || mbar_wait(stall_bar, 0, ctl);  // the test hook's wait runs out
+                ok = __shfl_sync(0x7u, ok, 0);
+                for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
+                    int g, cb, row0, nvalid;
+                    bg_decode_tile(tiles, tile, kBgRows, g, cb, row0, nvalid);
+                    const int halves = halves_of(cb);
+                    const int bi = bg_box_index(nvalid);
+                    const CUtensorMap* ma = bi == 0 ? &tmap_a0 : bi == 1 ? &tmap_a1 : &tmap_a2;
+                    const uint32_t bytes = (uint32_t)((bg_box_rows(bi) + halves * kBlk) * kBlk);
+                    const CUtensorMap* map = lane == 2 ? ma : &tmap_w;
+                    const int row = lane == 2 ? row0 : bg_weight_row<EPI>(args, g, cb, lane);
+                    const int off = lane == 2 ? 0 : (1 + lane) * kBgHalf;
+                    for (int kb = 0; kb < nkb; ++kb, ++it) {
+                        const uint32_t s = it % kBgNS, ph = (it / kBgNS) & 1u;
+                        if (lane == 0) {
+                            ok = mbar_wait(&empty[s], ph ^ 1u, ctl);
+                            if (ok) mbar_arrive_expect_tx(&full[s], bytes);
+                        }
+                        ok = __shfl_sync(0x7u, ok, 0);
+                        if (!ok) break;
+                        if (lane != 1 || halves == 2)
+                            tma_load_2d(smem + s * kBgStage + off, map, &full[s], kb * kBlk, row);
                     }
-                    ok = __shfl_sync(0x7u, ok, 0);
-                    if (!ok) break;
-                    if (lane != 1 || halves == 2) tma_load_2d(smem + s * kBgStage + off, map, &full[s], kb * kBlk, row);
                 }
+                // drain: every fill issued must land before the CTA may exit
+                if (lane == 0)
+                    for (uint32_t s = 0; s < (uint32_t)kBgNS && s < it; ++s) {
+                        const uint32_t last = it - 1 - ((it - 1 - s) % kBgNS);
+                        mbar_wait_drain(&full[s], (last / kBgNS) & 1u);
+                    }
             }
-            // drain: every fill issued must land before the CTA may exit
-            if (lane == 0)
-                for (uint32_t s = 0; s < (uint32_t)kBgNS && s < it; ++s) {
-                    const uint32_t last = it - 1 - ((it - 1 - s) % kBgNS);
-                    mbar_wait_drain(&full[s], (last / kBgNS) & 1u);
-                }
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
-                int g, cb, row0, nvalid;
-                bg_decode_tile(tiles, tile, g, cb, row0, nvalid);
-                const uint32_t idesc = idesc_e4m3(kBgRows, (uint32_t)(halves_of(cb) * kBlk));
-                for (int kb = 0; kb < nkb; ++kb, ++it) {
-                    const uint32_t s = it % kBgNS, d = it & 1u;
-                    if (!mbar_wait(&acc_empty[d], ((it >> 1) & 1u) ^ 1u, ctl) ||
-                        !mbar_wait(&full[s], (it / kBgNS) & 1u, ctl)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t a_base = smem_u32(smem + s * kBgStage);
-                    const uint64_t a_desc = smem_desc_sw128(a_base), b_desc = smem_desc_sw128(a_base + kBgStageA);
+        } else if (warp == 1) {
+            // ------------------------------------------------------ MMA issuer
+            if (lane == 0) {
+                uint32_t it = 0;
+                bool ok = true;
+                for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
+                    int g, cb, row0, nvalid;
+                    bg_decode_tile(tiles, tile, kBgRows, g, cb, row0, nvalid);
+                    const uint32_t idesc = idesc_e4m3(kBgRows, (uint32_t)(halves_of(cb) * kBlk));
+                    for (int kb = 0; kb < nkb; ++kb, ++it) {
+                        const uint32_t s = it % kBgNS, d = it & 1u;
+                        if (!mbar_wait(&acc_empty[d], ((it >> 1) & 1u) ^ 1u, ctl) ||
+                            !mbar_wait(&full[s], (it / kBgNS) & 1u, ctl)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t a_base = smem_u32(smem + s * kBgStage);
+                        const uint64_t a_desc = smem_desc_sw128(a_base), b_desc = smem_desc_sw128(a_base + kBgHalf);
 #pragma unroll
-                    for (int ks = 0; ks < kBlk / 32; ++ks)  // 32 bytes of K per MMA
-                        mma_e4m3(tmem + d * kBgCols, a_desc + (uint64_t)(ks * 2), b_desc + (uint64_t)(ks * 2), idesc,
-                               ks != 0 ? 1u : 0u);
-                    mma_commit(&empty[s]);
-                    mma_commit(&acc_full[d]);
+                        for (int ks = 0; ks < kBlk / 32; ++ks)  // 32 bytes of K per MMA
+                            mma_e4m3(tmem + d * kBgCols, a_desc + (uint64_t)(ks * 2), b_desc + (uint64_t)(ks * 2), idesc,
+                                     ks != 0 ? 1u : 0u);
+                        mma_commit(&empty[s]);
+                        mma_commit(&acc_full[d]);
+                    }
                 }
+                mma_commit(teardown);
+                mbar_wait_drain(teardown, 0);
             }
-            mma_commit(teardown);
-            mbar_wait_drain(teardown, 0);
         }
     } else {
+        bg_regs_many();
         // ------------------------------------- block sums and the epilogue
-        const int q = warp & 3;
-        const int w2 = (warp - kBgEpi0) >> 2;  // which 64 columns of each half
-        const int row = q * 32 + lane;         // TMEM lane = row of the tile
-        const uint32_t col_addr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(w2 * 64);
-        const int nb = blocks_of(args.w_rows);
-        uint32_t it = 0, tl = 0;
+        const BgWarp w(warp, lane);
+        uint8_t* staging = smem + kBgOffStaging + (warp - kBgEpi0) * kBgStaging;
+        uint32_t it = 0, tl = 0;  // blocks, tiles
         bool ok = true;
         for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x, ++tl) {
             int g, cb, row0, nvalid;
-            bg_decode_tile(tiles, tile, g, cb, row0, nvalid);
-            const int r = row0 + min(row, nvalid - 1);
-            const float* sx = args.act_scale + (size_t)r * nkb;
-            const int b0 = EPI == (int)BlockEpi::GateUp ? cb : 2 * cb;
-            const int b1 = EPI == (int)BlockEpi::GateUp ? cb + args.up_offset / kBlk : min(2 * cb + 1, nb - 1);
-            const float* sw0 = args.w_scale + ((size_t)g * nb + b0) * nkb;
-            const float* sw1 = args.w_scale + ((size_t)g * nb + b1) * nkb;
+            bg_decode_tile(tiles, tile, kBgRows, g, cb, row0, nvalid);
             f32x2 acc[2][32];  // [half][column pair]
 #pragma unroll
             for (int j = 0; j < 32; ++j) acc[0][j] = acc[1][j] = 0ull;
-            float x_next = __ldg(sx), w0_next = __ldg(sw0), w1_next = __ldg(sw1);
+            BgScales sc;
+            sc.start<EPI>(args, g, cb, row0 + min(w.row, nvalid - 1), nkb);
             for (int kb = 0; kb < nkb; ++kb, ++it) {
-                const float s0 = __fmul_rn(x_next, w0_next), s1 = __fmul_rn(x_next, w1_next);
-                const f32x2 sc[2] = {pack2(s0, s0), pack2(s1, s1)};
-                if (kb + 1 < nkb) {
-                    x_next = __ldg(sx + kb + 1);
-                    w0_next = __ldg(sw0 + kb + 1);
-                    w1_next = __ldg(sw1 + kb + 1);
-                }
+                float s0, s1;
+                sc.next(kb, nkb, s0, s1);
                 const uint32_t d = it & 1u;
                 if (!warp_wait(&acc_full[d], (it >> 1) & 1u, ctl)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t a = col_addr + d * kBgCols;
-                uint32_t v[2][16];  // the next 16 columns load while these are summed
-                tmem_ld_16(a, v[0]);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    bg_wait_ld(v[c & 1]);
-                    if (c < 7) tmem_ld_16(a + ((c + 1) >> 2) * kBlk + ((c + 1) & 3) * 16, v[(c + 1) & 1]);
-                    if (c == 7) {  // every column is in registers: release the buffer
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&acc_empty[d]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        fma2(acc[c >> 2][(c & 3) * 8 + j],
-                             pack2(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])), sc[c >> 2]);
-                }
+                bg_add_block(acc, w.addr(tmem + d * kBgCols), s0, s1, [&] {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&acc_empty[d]);
+                });
             }
-            if (!ok) break;
-            if (EPI == (int)BlockEpi::GateUp) {
-                float amax = 0.f;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    float g0, g1, u0, u1;
-                    unpack2(acc[0][j], g0, g1);
-                    unpack2(acc[1][j], u0, u1);
-                    g0 = silu_mul(g0, u0);
-                    g1 = silu_mul(g1, u1);
-                    amax = amax_nan(amax_nan(amax, g0), g1);
-                    acc[0][j] = pack2(g0, g1);
-                }
-                // the row's other 64 columns are the partner warp's
-                float* mine = xch + (tl & 1u) * 2 * kBgRows;
-                mine[w2 * kBgRows + row] = amax;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&pair_bar[q]);
-                if (!warp_wait(&pair_bar[q], tl & 1u, ctl)) break;
-                amax = amax_nan(amax, mine[(w2 ^ 1) * kBgRows + row]);
-                const float s = block_scale(amax);
-                // the quotient as a product with 1 / s: h is rounded already,
-                // see silu_mul
-                const float inv = s == 0.f ? 0.f : __fdiv_rn(1.0f, s);
-                if (row < nvalid) {
-                    const int n_ch = args.up_offset;
-                    uint4* out = reinterpret_cast<uint4*>(args.q_out + (size_t)r * n_ch + cb * kBlk + w2 * 64);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t c4[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float h0, h1, h2, h3;
-                            unpack2(acc[0][i * 8 + j * 2], h0, h1);
-                            unpack2(acc[0][i * 8 + j * 2 + 1], h2, h3);
-                            c4[j] = e4m3_pair(h0 * inv, h1 * inv) | (e4m3_pair(h2 * inv, h3 * inv) << 16);
-                        }
-                        out[i] = make_uint4(c4[0], c4[1], c4[2], c4[3]);
-                    }
-                    if (w2 == 0) args.s_out[(size_t)r * (n_ch / kBlk) + cb] = s;
-                }
-            } else if (row < nvalid) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int col = cb * kBgCols + half * kBlk + w2 * 64;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {  // 8 columns a step; w_rows is a multiple of 16
-                        if (col + i * 8 < args.w_rows) {
-                            float f[8];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) unpack2(acc[half][i * 4 + j], f[2 * j], f[2 * j + 1]);
-                            const size_t at = (size_t)r * args.w_rows + col + i * 8;
-                            if (EPI == (int)BlockEpi::F32) {
-                                float4* out = reinterpret_cast<float4*>(static_cast<float*>(args.out) + at);
-                                out[0] = make_float4(f[0], f[1], f[2], f[3]);
-                                out[1] = make_float4(f[4], f[5], f[6], f[7]);
-                            } else {
-                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.out) + at) =
-                                    make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]),
-                                               bf16_pair(f[6], f[7]));
-                            }
-                        }
-                    }
-                }
-            }
+            ok = ok && bg_output<EPI>(args, acc, w, row0, nvalid, cb, xch, pair_bar, tl, staging, ctl);
         }
     }
 
@@ -392,8 +510,8 @@ cudaError_t launch_block_impl(const BlockGemmArgs& args, cudaStream_t st, bool p
         if (!make_tensor_map_2d(&ta[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, args.act, args.K, (uint64_t)args.total_rows,
                                 kBlk, bg_box_rows(i), CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
-    const int n_cb = EPI == (int)BlockEpi::GateUp ? args.up_offset / kBlk : (args.w_rows + kBgCols - 1) / kBgCols;
-    const long max_tiles = ((long)(args.total_rows + kBgRows - 1) / kBgRows + args.n_groups - 1) * n_cb;
+    const long max_tiles =
+        ((long)(args.total_rows + kBgRows - 1) / kBgRows + args.n_groups - 1) * bg_col_blocks<EPI>(args);
     long grid = num_sms();
     if (max_tiles < grid) grid = max_tiles;
     if (grid < 1) grid = 1;
@@ -407,7 +525,7 @@ cudaError_t launch_block_gemm(BlockEpi epi, const BlockGemmArgs& args, cudaStrea
     if (args.total_rows == 0) return cudaSuccess;
     switch (epi) {
         case BlockEpi::GateUp: return launch_block_impl<0>(args, st, pdl);
-        case BlockEpi::F32: return launch_block_impl<1>(args, st, pdl);
+        case BlockEpi::Half: return launch_block_impl<1>(args, st, pdl);
         case BlockEpi::BF16: return launch_block_impl<2>(args, st, pdl);
     }
     return cudaErrorInvalidValue;
