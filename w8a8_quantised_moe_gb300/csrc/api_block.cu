@@ -183,7 +183,10 @@ moe_status_t moe_w8a8_fp8_block_forward(const uint16_t* x, const float* router_w
     g.error = err;
     g.timeout_ns = timeout;
     g.stall = injected(kInjectStall) ? 1 : 0;
-    if ((e = launch_block_gemm(BlockEpi::GateUp, g, st, pdl)) != cudaSuccess) return from_cuda(e);
+    auto product = [&](BlockEpi epi) {
+        return block_gemm_few_wanted(g) ? launch_block_gemm_few(epi, g, st, pdl) : launch_block_gemm(epi, g, st, pdl);
+    };
+    if ((e = product(BlockEpi::GateUp)) != cudaSuccess) return from_cuda(e);
 
     g.act = at<uint8_t>(workspace, L.q_h);
     g.act_scale = at<float>(workspace, L.s_h);
@@ -194,7 +197,7 @@ moe_status_t moe_w8a8_fp8_block_forward(const uint16_t* x, const float* router_w
     g.up_offset = 0;
     g.out = at<uint16_t>(workspace, L.o);
     g.s_out = at<float>(workspace, L.s_o);
-    if ((e = launch_block_gemm(BlockEpi::Half, g, st, pdl)) != cudaSuccess) return from_cuda(e);
+    if ((e = product(BlockEpi::Half)) != cudaSuccess) return from_cuda(e);
     return from_cuda(launch_combine_half(at<uint16_t>(workspace, L.o), at<float>(workspace, L.s_o),
                                          at<int32_t>(workspace, L.slot_of), at<float>(workspace, L.topk_w), (int)T,
                                          (int)H, (int)top_k, y, err, st, pdl));

@@ -39,8 +39,13 @@ struct BlockGemmArgs {
     int stall;               // test hook (MOE_INJECT=stall)
 };
 
-// Tensor-core product (gemm_block.cu).
+// Tensor-core product, groups of many rows (gemm_block.cu).
 cudaError_t launch_block_gemm(BlockEpi epi, const BlockGemmArgs& args, cudaStream_t st, bool pdl);
+// The same for groups of a few rows (gemm_block_few.cu), GateUp and Half; reads
+// the offsets before its wait for the previous kernel, which must have waited
+// for the kernel that wrote them.
+bool block_gemm_few_wanted(const BlockGemmArgs& args);
+cudaError_t launch_block_gemm_few(BlockEpi epi, const BlockGemmArgs& args, cudaStream_t st, bool pdl);
 
 // The linear layer for few rows (linear_block_few.cu): g as for
 // launch_block_gemm with BlockEpi::BF16 and one group.  Where

@@ -35,8 +35,7 @@
 #include <mutex>
 
 #include "block.h"
-#include "block_dev.cuh"
-#include "gemm_common.cuh"
+#include "block_tiles.cuh"
 
 namespace moe {
 namespace {
@@ -239,58 +238,6 @@ __device__ __forceinline__ bool bg_output(const BlockGemmArgs& args, f32x2 (&acc
     return true;
 }
 
-// Tile table of a launch, by one warp: group g has ceil(rows_g / rows_tile) *
-// n_cb tiles.
-__device__ __forceinline__ void bg_tile_table(const BlockGemmArgs& args, int rows_tile, int n_cb, int* tile_start,
-                                              int* row_start, int lane) {
-    const int n = args.n_groups;
-    int carry = 0;
-    bool bad = false;  // checked build: an offset out of order or range
-    for (int base = 0; base < n; base += 32) {
-        const int g = base + lane;
-        int r0 = 0, r1 = 0;
-        if (g < n) {
-            r0 = args.offsets ? args.offsets[g] : 0;
-            r1 = args.offsets ? args.offsets[g + 1] : args.total_rows;
-            if (!group_rows_ok(r0, r1, args.total_rows, args.error)) {
-                bad = true;
-                r0 = r1 = 0;
-            }
-            row_start[g] = r0;
-            if (g == n - 1) row_start[n] = r1;
-        }
-        const int v = (g < n) ? ((r1 - r0 + rows_tile - 1) / rows_tile) * n_cb : 0;
-        int incl = v;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += o;
-        }
-        if (g < n) tile_start[g] = carry + incl - v;
-        carry += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) tile_start[n] = carry;
-    if (kChecked && __any_sync(0xffffffffu, bad)) {  // an empty, consistent table: no tile runs
-        for (int g = lane; g <= n; g += 32) {
-            row_start[g] = 0;
-            tile_start[g] = 0;
-        }
-    }
-}
-
-// Tile -> group, column block, first row, valid rows (row blocks fastest, so
-// that a group's row blocks run together and share weight tiles in L2).
-__device__ __forceinline__ void bg_decode_tile(const Tiles& t, int tile, int rows_tile, int& g, int& cb, int& row0,
-                                               int& nvalid) {
-    g = last_le(t.tile_start, t.n_groups, tile);
-    const int local = tile - t.tile_start[g];
-    const int rows = t.row_start[g + 1] - t.row_start[g];
-    const int ntb = (rows + rows_tile - 1) / rows_tile;
-    cb = local / ntb;
-    row0 = t.row_start[g] + (local - cb * ntb) * rows_tile;
-    nvalid = min(rows_tile, t.row_start[g + 1] - row0);
-}
-
 template <int EPI>
 __host__ __device__ inline int bg_col_blocks(const BlockGemmArgs& a) {
     return EPI == (int)BlockEpi::GateUp ? a.up_offset / kBlk : (a.w_rows + kBgCols - 1) / kBgCols;
@@ -366,7 +313,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     }
     pdl_wait();  // the previous kernel's outputs (offsets, codes, scales) are visible from here
     pdl_trigger();
-    if (warp == 2) bg_tile_table(args, kBgRows, bg_col_blocks<EPI>(args), tile_start, row_start, lane);
+    if (warp == 2) block_tile_table(args, kBgRows, bg_col_blocks<EPI>(args), tile_start, row_start, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -392,7 +339,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
                 ok = __shfl_sync(0x7u, ok, 0);
                 for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
                     int g, cb, row0, nvalid;
-                    bg_decode_tile(tiles, tile, kBgRows, g, cb, row0, nvalid);
+                    block_decode_tile(tiles, tile, kBgRows, g, cb, row0, nvalid);
                     const int halves = halves_of(cb);
                     const int bi = bg_box_index(nvalid);
                     const CUtensorMap* ma = bi == 0 ? &tmap_a0 : bi == 1 ? &tmap_a1 : &tmap_a2;
@@ -426,7 +373,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
                 bool ok = true;
                 for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
                     int g, cb, row0, nvalid;
-                    bg_decode_tile(tiles, tile, kBgRows, g, cb, row0, nvalid);
+                    block_decode_tile(tiles, tile, kBgRows, g, cb, row0, nvalid);
                     const uint32_t idesc = idesc_e4m3(kBgRows, (uint32_t)(halves_of(cb) * kBlk));
                     for (int kb = 0; kb < nkb; ++kb, ++it) {
                         const uint32_t s = it % kBgNS, d = it & 1u;
@@ -459,7 +406,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
         bool ok = true;
         for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x, ++tl) {
             int g, cb, row0, nvalid;
-            bg_decode_tile(tiles, tile, kBgRows, g, cb, row0, nvalid);
+            block_decode_tile(tiles, tile, kBgRows, g, cb, row0, nvalid);
             f32x2 acc[2][32];  // [half][column pair]
 #pragma unroll
             for (int j = 0; j < 32; ++j) acc[0][j] = acc[1][j] = 0ull;

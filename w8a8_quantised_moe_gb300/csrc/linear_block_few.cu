@@ -25,11 +25,7 @@
 //   warp 8     TMEM allocator, MMA issuer
 //   warp 9     TMA producer
 // Every wait is bounded; the cluster barriers are reached on every path.
-#include <mutex>
-
-#include "block.h"
-#include "block_dev.cuh"
-#include "gemm_common.cuh"
+#include "block_tiles.cuh"
 
 namespace moe {
 namespace {
@@ -90,15 +86,6 @@ __device__ __forceinline__ void lf_wait_ld(uint32_t (&r)[C]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < C; ++i) asm volatile("" : "+r"(r[i]));
-}
-
-__device__ __forceinline__ float4 ld_dsmem(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
 }
 
 template <int NTOK, bool FUSED>
@@ -309,29 +296,42 @@ __global__ void __launch_bounds__(kLfThreads, NTOK <= 64 ? 2 : 1)
 
 int lf_ntok(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
-// CTAs of a cluster: as many parts of K (at most 8) as still run at once, two
-// CTAs an SM where their shared memory allows; 0 where no split fits.
-int lf_cluster(int ntok, bool fused, int N, int nkb) {
-    const int tiles = blocks_of(N);
+template <int NTOK, bool FUSED>
+cudaError_t lf_smem_limit() {
+    static const cudaError_t e = cudaFuncSetAttribute(block_linear_few_kernel<NTOK, FUSED>,
+                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kLfMaxSmem);
+    return e;
+}
+
+// CTAs of a cluster: as many parts of K as still run at once, two CTAs an SM where
+// their shared memory allows; 0 where no split fits (FUSED keeps all its part's
+// codes).
+template <int NTOK, bool FUSED>
+int lf_cluster(int N, int nkb) {
+    if (lf_smem_limit<NTOK, FUSED>() != cudaSuccess) return 0;
+    const void* kern = reinterpret_cast<const void*>(block_linear_few_kernel<NTOK, FUSED>);
+    static const ClusterCounts two(kern, kLfThreads, kLfMaxSmem / 2 - 1024), one(kern, kLfThreads, kLfMaxSmem);
+    const int tiles = blocks_of(N), most = nkb < 8 ? nkb : 8;
     int best = 0;
-    for (int cs = 1; cs <= 8 && cs <= nkb; cs *= 2) {
-        const int smem = lf_layout(ntok, fused, (nkb + cs - 1) / cs).total;
+    for (int cs = 1; cs <= most; ++cs) {
+        const int smem = lf_layout(NTOK, FUSED, (nkb + cs - 1) / cs).total;
         if (smem > kLfMaxSmem) continue;
-        const int per_sm = ntok <= 64 && smem <= kLfMaxSmem / 2 ? 2 : 1;
-        if (best == 0 || tiles * cs <= per_sm * num_sms()) best = cs;
+        const int at_once = (smem <= kLfMaxSmem / 2 - 1024 ? two : one).of[cs];
+        if (best == 0 || tiles <= at_once) best = cs;
     }
     return best;
+}
+int lf_cluster(int ntok, bool fused, int N, int nkb) {
+    if (fused) return lf_cluster<16, true>(N, nkb);
+    return ntok == 16   ? lf_cluster<16, false>(N, nkb)
+           : ntok == 32 ? lf_cluster<32, false>(N, nkb)
+           : ntok == 64 ? lf_cluster<64, false>(N, nkb)
+                        : lf_cluster<128, false>(N, nkb);
 }
 
 template <int NTOK, bool FUSED>
 cudaError_t launch_lf(const CUtensorMap& tw, const CUtensorMap& tx, const LinFewArgs& a, cudaStream_t st, bool pdl) {
     auto kern = block_linear_few_kernel<NTOK, FUSED>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLfMaxSmem);
-    });
-    if (attr_err != cudaSuccess) return attr_err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(blocks_of(a.N) * a.cs));
     cfg.blockDim = dim3(kLfThreads);
