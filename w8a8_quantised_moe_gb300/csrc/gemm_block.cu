@@ -10,28 +10,29 @@
 //
 // Tile: 128 activation rows (the MMA's M, one TMEM lane each) x 256 weight rows
 // (N) in two halves of 128.  With rows on the lanes a thread's scale is one value
-// per half and block: sx of its row times sw of the half.  GateUp's halves are
-// 128 gate rows and the 128 up rows of the same channels, so the tile holds
-// whole scale blocks of h: each thread applies silu(gate) * up to its 64 + 64
-// columns and h leaves the kernel as E4M3 codes with their scale, never as
-// binary32.
-//   warp 0      TMA producer (ring of kBgNS stages: activation rows and both
-//               halves' weight rows, 128 bytes of K each)
-//   warp 1      TMEM allocator and MMA issuer: four K = 32 MMAs a block into one
-//               of two 256-column TMEM buffers
-//   warps 4-11  scale and sum the blocks, then the epilogue
+// per half and block: sx of its row times sw of the half.  GateUp's halves are 64
+// gate rows and the 64 up rows of the same channels, so the tile holds whole
+// scale blocks of h: each thread applies silu(gate) * up to its 64 + 64 columns
+// and h leaves the kernel as E4M3 codes with their scale, never as binary32.
+//   warp 0      TMA producer (ring of kBgNS stages: activation rows and four
+//               quarters of the weight rows, 128 bytes of K each)
+//   warps 1, 2  MMA issuers, one a half (warp 1 also the TMEM allocator): four
+//               K = 32 MMAs a block into one of the half's two 128-column buffers
+//   warps 4-11  scale and sum the blocks, then the epilogue: four warps a half
 // Persistent grid, tiles dealt round-robin.  Every wait is bounded (ptx.cuh).
 //
-// What bounds it: 8192^3 takes 489 us beside its quantiser, 1040 clocks a block
-// of a tile, of which the MMAs are 512.  With the sums cut to a quarter of the
-// columns a block took 780, without the operands' loads as well 670.  The sums
-// are a chain for each warp (wait for the MMAs 180 clocks, eight tensor-memory
-// loads of 16 columns 650, and their multiply-adds, 80 to 100 a clock and SM,
-// partly behind them) on two buffers, all that tensor memory holds.  Tried and
-// slower: CTA pairs that share the weights (less to load, the same chain: 562),
-// two MMA-issuing threads (525), sixteen epilogue warps (639), loads of 32
-// columns (522 to 697 with the registers the compiler then lacks), scalar
-// multiply-adds (642 against 611).
+// What bounds it: 8192^3 takes 471 us beside its quantiser, about 980 clocks a
+// block of a tile, of which the MMAs are 512 and the operands' loads, at the rate
+// an SM takes in, 830.  With the sums cut to a quarter of the columns a block took
+// 780, without the loads as well 670.  The sums are a chain for each warp: a wait
+// for the MMAs (170 clocks even when satisfied), eight tensor-memory loads of 16
+// columns (500) and their multiply-adds (80 to 100 a clock and SM), behind two
+// buffers, all that tensor memory holds.  With one commit for both halves, so
+// that all eight warps load and then all add, 8192^3 took 522 us against 506.
+// Tried and slower: CTA pairs that share the weights (less to load, the same
+// chain: 562 against 522), two MMA-issuing threads on alternate blocks (525),
+// sixteen epilogue warps (639), scalar multiply-adds (642 against 611), the next
+// block's first load before the last sums of a block (560 against 506).
 #include <mutex>
 
 #include "block.h"
@@ -42,7 +43,7 @@ namespace {
 
 constexpr int kBgRows = 128;     // activation rows of a CTA
 constexpr int kBgCols = 256;     // weight rows of a tile
-constexpr int kBgThreads = 384;  // producer, MMA issuer, two idle and 8 epilogue warps
+constexpr int kBgThreads = 384;  // producer, two MMA issuers, an idle and 8 epilogue warps
 constexpr int kBgEpi0 = 4;       // first epilogue warp
 constexpr int kBgEpiWarps = 8;
 constexpr int kBgHalf = kBlk * kBlk;         // bytes of 128 rows x 128 channels
@@ -64,20 +65,21 @@ __device__ __forceinline__ void bg_wait_ld(uint32_t (&r)[16]) {
                    "+r"(r[15])::"memory");
 }
 
-// An epilogue warp: 32 lanes' rows x columns 64 w2 .. of each half.
+// An epilogue warp: 32 lanes' rows x the 128 columns of half w2.
 struct BgWarp {
-    int q, w2, row, lane;  // lane quarter, column half, row of the CTA's 128
+    int q, w2, row, lane;  // lane quarter, half of the columns, row of the CTA's 128
     __device__ __forceinline__ BgWarp(int warp, int ln) : q(warp & 3), w2((warp - kBgEpi0) >> 2), lane(ln) {
         row = q * 32 + lane;
     }
     // its columns of a 256-column buffer at `tmem`
     __device__ __forceinline__ uint32_t addr(uint32_t tmem) const {
-        return tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(w2 * 64);
+        return tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(w2 * kBlk);
     }
 };
 
-// Adds the block's sums at `a` (this warp's columns), times the halves' scales,
-// to acc[half][column pair]; the next 16 columns load while 16 are summed.
+// Adds the block's sums at `a` (this warp's 128 columns), times the scales of the
+// first and last 64, to acc[part][column pair]; the next 16 columns load while 16
+// are summed.
 // `release` runs once every column is in registers.
 template <class Release>
 __device__ __forceinline__ void bg_add_block(f32x2 (&acc)[2][32], uint32_t a, float s0, float s1, Release release) {
@@ -87,7 +89,7 @@ __device__ __forceinline__ void bg_add_block(f32x2 (&acc)[2][32], uint32_t a, fl
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
         bg_wait_ld(v[c & 1]);
-        if (c < 7) tmem_ld_16(a + ((c + 1) >> 2) * kBlk + ((c + 1) & 3) * 16, v[(c + 1) & 1]);
+        if (c < 7) tmem_ld_16(a + (c + 1) * 16, v[(c + 1) & 1]);
         if (c == 7) release();
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -105,10 +107,10 @@ struct BgScales {
     const float *sx, *sw0, *sw1;
     float x, w0, w1;
     template <int EPI>
-    __device__ __forceinline__ void start(const BlockGemmArgs& a, int g, int cb, int r, int nkb) {
+    __device__ __forceinline__ void start(const BlockGemmArgs& a, int g, int cb, int w2, int r, int nkb) {
         const int nb = blocks_of(a.w_rows);
-        const int b0 = EPI == (int)BlockEpi::GateUp ? cb : 2 * cb;
-        const int b1 = EPI == (int)BlockEpi::GateUp ? cb + a.up_offset / kBlk : min(2 * cb + 1, nb - 1);
+        const int b0 = EPI == (int)BlockEpi::GateUp ? cb : min(2 * cb + w2, nb - 1);
+        const int b1 = EPI == (int)BlockEpi::GateUp ? cb + a.up_offset / kBlk : b0;
         sx = a.act_scale + (size_t)r * nkb;
         sw0 = a.w_scale + ((size_t)g * nb + b0) * nkb;
         sw1 = a.w_scale + ((size_t)g * nb + b1) * nkb;
@@ -195,7 +197,7 @@ __device__ __forceinline__ bool bg_output(const BlockGemmArgs& args, f32x2 (&acc
     } else {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int col = cb * kBgCols + half * kBlk + w.w2 * 64;
+            const int col = cb * kBgCols + w.w2 * kBlk + half * 64;
 #pragma unroll
             for (int p = 0; p < 2; ++p) {  // 32 columns: 64 bytes
                 const int c0 = col + p * 32;
@@ -243,17 +245,18 @@ __host__ __device__ inline int bg_col_blocks(const BlockGemmArgs& a) {
     return EPI == (int)BlockEpi::GateUp ? a.up_offset / kBlk : (a.w_rows + kBgCols - 1) / kBgCols;
 }
 
-// First weight row of a tile's halves.
+// First weight row of a tile's quarters of 64: GateUp's halves are 64 gate rows,
+// then the same channels' up rows.
 template <int EPI>
-__device__ __forceinline__ int bg_weight_row(const BlockGemmArgs& a, int g, int cb, int half) {
-    return EPI == (int)BlockEpi::GateUp ? g * a.w_rows + half * a.up_offset + cb * kBlk
-                                        : g * a.w_rows + cb * kBgCols + half * kBlk;
+__device__ __forceinline__ int bg_weight_row(const BlockGemmArgs& a, int g, int cb, int i) {
+    return EPI == (int)BlockEpi::GateUp ? g * a.w_rows + (i & 1) * a.up_offset + cb * kBlk + (i >> 1) * 64
+                                        : g * a.w_rows + cb * kBgCols + i * 64;
 }
 
 constexpr int kBgNS = 4;  // stages
 constexpr int kBgStage = 3 * kBgHalf;
 constexpr int kBgOffBars = kBgNS * kBgStage;
-constexpr int kBgNumBars = 2 * kBgNS + 4 + 2 + 4;  // full, empty, acc_full/empty[2], teardown, stall, pair[4]
+constexpr int kBgNumBars = 2 * kBgNS + 8 + 2 + 4;  // full, empty, acc_full/empty[4], teardown, stall, pair[4]
 constexpr int kBgOffTiles = kBgOffBars + kBgNumBars * 8;
 constexpr int kBgOffXch = (kBgOffTiles + (kMaxExperts + 1) * 4 * 2 + 15) / 16 * 16;
 constexpr int kBgOffStaging = kBgOffXch + kBgXch;
@@ -276,9 +279,9 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBgOffBars);
     uint64_t* full = bars;              // [NS] the stage landed
     uint64_t* empty = full + kBgNS;     // [NS] the MMAs of the stage completed
-    uint64_t* acc_full = empty + kBgNS; // [2] a block's partial sums are in tensor memory
-    uint64_t* acc_empty = acc_full + 2; // [2] the epilogue warps have read them
-    uint64_t* teardown = acc_empty + 2;
+    uint64_t* acc_full = empty + kBgNS; // [2 buffers][2 halves] a block's partial sums are in tensor memory
+    uint64_t* acc_empty = acc_full + 4; // [2][2] the half's epilogue warps have read them
+    uint64_t* teardown = acc_empty + 4;
     uint64_t* stall_bar = teardown + 1; // test hook: nothing arrives on it
     uint64_t* pair_bar = stall_bar + 1; // [4] the two warps of a lane quarter
     int* tile_start = reinterpret_cast<int*>(smem + kBgOffTiles);
@@ -293,13 +296,13 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kBgNS; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], 2);
         }
-        for (int d = 0; d < 2; ++d) {
+        for (int d = 0; d < 4; ++d) {
             mbar_init(&acc_full[d], 1);
-            mbar_init(&acc_empty[d], kBgEpiWarps);
+            mbar_init(&acc_empty[d], kBgEpiWarps / 2);
         }
-        mbar_init(teardown, 1);
+        mbar_init(teardown, 2);
         mbar_init(stall_bar, 1);
         for (int i = 0; i < 4; ++i) mbar_init(&pair_bar[i], 2);
         *abort_flag = 0;
@@ -330,13 +333,13 @@ __global__ void __launch_bounds__(kBgThreads, 1)
         bg_regs_few();
         if (warp == 0) {
             // ---------------------------------------------------------- producer
-            // lanes 0-2 issue one box each (both halves' weight rows, activation
+            // lanes 0-4 issue one box each (64 weight rows each, the activation
             // rows) in the same warp instruction; lane 0 owns the waits
-            if (lane < 3) {
+            if (lane < 5) {
                 uint32_t it = 0;
                 int ok = 1;
                 if (lane == 0) ok = !args.stall || mbar_wait(stall_bar, 0, ctl);  // the test hook's wait runs out
-                ok = __shfl_sync(0x7u, ok, 0);
+                ok = __shfl_sync(0x1fu, ok, 0);
                 for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
                     int g, cb, row0, nvalid;
                     block_decode_tile(tiles, tile, kBgRows, g, cb, row0, nvalid);
@@ -344,18 +347,18 @@ __global__ void __launch_bounds__(kBgThreads, 1)
                     const int bi = bg_box_index(nvalid);
                     const CUtensorMap* ma = bi == 0 ? &tmap_a0 : bi == 1 ? &tmap_a1 : &tmap_a2;
                     const uint32_t bytes = (uint32_t)((bg_box_rows(bi) + halves * kBlk) * kBlk);
-                    const CUtensorMap* map = lane == 2 ? ma : &tmap_w;
-                    const int row = lane == 2 ? row0 : bg_weight_row<EPI>(args, g, cb, lane);
-                    const int off = lane == 2 ? 0 : (1 + lane) * kBgHalf;
+                    const CUtensorMap* map = lane == 4 ? ma : &tmap_w;
+                    const int row = lane == 4 ? row0 : bg_weight_row<EPI>(args, g, cb, lane);
+                    const int off = lane == 4 ? 0 : kBgHalf + lane * (kBgHalf / 2);
                     for (int kb = 0; kb < nkb; ++kb, ++it) {
                         const uint32_t s = it % kBgNS, ph = (it / kBgNS) & 1u;
                         if (lane == 0) {
                             ok = mbar_wait(&empty[s], ph ^ 1u, ctl);
                             if (ok) mbar_arrive_expect_tx(&full[s], bytes);
                         }
-                        ok = __shfl_sync(0x7u, ok, 0);
+                        ok = __shfl_sync(0x1fu, ok, 0);
                         if (!ok) break;
-                        if (lane != 1 || halves == 2)
+                        if (lane < 2 * halves || lane == 4)
                             tma_load_2d(smem + s * kBgStage + off, map, &full[s], kb * kBlk, row);
                     }
                 }
@@ -366,33 +369,33 @@ __global__ void __launch_bounds__(kBgThreads, 1)
                         mbar_wait_drain(&full[s], (last / kBgNS) & 1u);
                     }
             }
-        } else if (warp == 1) {
-            // ------------------------------------------------------ MMA issuer
+        } else if (warp < 3) {
+            // ----------------------------------------------------- MMA issuers
+            // warp 1 the first half's, warp 2 the second's
             if (lane == 0) {
+                constexpr uint32_t idesc = idesc_e4m3(kBgRows, kBlk);
+                const int h = warp - 1;
                 uint32_t it = 0;
                 bool ok = true;
-                for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
-                    int g, cb, row0, nvalid;
-                    block_decode_tile(tiles, tile, kBgRows, g, cb, row0, nvalid);
-                    const uint32_t idesc = idesc_e4m3(kBgRows, (uint32_t)(halves_of(cb) * kBlk));
+                for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x)
                     for (int kb = 0; kb < nkb; ++kb, ++it) {
                         const uint32_t s = it % kBgNS, d = it & 1u;
-                        if (!mbar_wait(&acc_empty[d], ((it >> 1) & 1u) ^ 1u, ctl) ||
+                        if (!mbar_wait(&acc_empty[d * 2 + h], ((it >> 1) & 1u) ^ 1u, ctl) ||
                             !mbar_wait(&full[s], (it / kBgNS) & 1u, ctl)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         const uint32_t a_base = smem_u32(smem + s * kBgStage);
-                        const uint64_t a_desc = smem_desc_sw128(a_base), b_desc = smem_desc_sw128(a_base + kBgHalf);
+                        const uint64_t a_desc = smem_desc_sw128(a_base),
+                                       b_desc = smem_desc_sw128(a_base + (1 + h) * kBgHalf);
 #pragma unroll
                         for (int ks = 0; ks < kBlk / 32; ++ks)  // 32 bytes of K per MMA
-                            mma_e4m3(tmem + d * kBgCols, a_desc + (uint64_t)(ks * 2), b_desc + (uint64_t)(ks * 2), idesc,
-                                     ks != 0 ? 1u : 0u);
+                            mma_e4m3(tmem + d * kBgCols + h * kBlk, a_desc + (uint64_t)(ks * 2),
+                                     b_desc + (uint64_t)(ks * 2), idesc, ks != 0 ? 1u : 0u);
+                        mma_commit(&acc_full[d * 2 + h]);
                         mma_commit(&empty[s]);
-                        mma_commit(&acc_full[d]);
                     }
-                }
                 mma_commit(teardown);
                 mbar_wait_drain(teardown, 0);
             }
@@ -407,16 +410,16 @@ __global__ void __launch_bounds__(kBgThreads, 1)
         for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x, ++tl) {
             int g, cb, row0, nvalid;
             block_decode_tile(tiles, tile, kBgRows, g, cb, row0, nvalid);
-            f32x2 acc[2][32];  // [half][column pair]
+            f32x2 acc[2][32];  // [64 columns][column pair]
 #pragma unroll
             for (int j = 0; j < 32; ++j) acc[0][j] = acc[1][j] = 0ull;
             BgScales sc;
-            sc.start<EPI>(args, g, cb, row0 + min(w.row, nvalid - 1), nkb);
+            sc.start<EPI>(args, g, cb, w.w2, row0 + min(w.row, nvalid - 1), nkb);
             for (int kb = 0; kb < nkb; ++kb, ++it) {
                 float s0, s1;
                 sc.next(kb, nkb, s0, s1);
                 const uint32_t d = it & 1u;
-                if (!warp_wait(&acc_full[d], (it >> 1) & 1u, ctl)) {
+                if (!warp_wait(&acc_full[d * 2 + w.w2], (it >> 1) & 1u, ctl)) {
                     ok = false;
                     break;
                 }
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
                 bg_add_block(acc, w.addr(tmem + d * kBgCols), s0, s1, [&] {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&acc_empty[d]);
+                    if (lane == 0) mbar_arrive(&acc_empty[d * 2 + w.w2]);
                 });
             }
             ok = ok && bg_output<EPI>(args, acc, w, row0, nvalid, cb, xch, pair_bar, tl, staging, ctl);
@@ -451,7 +454,7 @@ cudaError_t launch_block_impl(const BlockGemmArgs& args, cudaStream_t st, bool p
     if (attr_err != cudaSuccess) return attr_err;
     CUtensorMap tw, ta[3];
     if (!make_tensor_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, args.w, args.K,
-                            (uint64_t)args.n_groups * args.w_rows, kBlk, kBlk, CU_TENSOR_MAP_SWIZZLE_128B))
+                            (uint64_t)args.n_groups * args.w_rows, kBlk, 64, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     for (int i = 0; i < 3; ++i)
         if (!make_tensor_map_2d(&ta[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, args.act, args.K, (uint64_t)args.total_rows,
