@@ -205,6 +205,10 @@ LAYERS = [
     (16, 256, 512, 8, 2, None), (33, 640, 256, 5, 1, None), (64, 1024, 512, 64, 2, None), (128, 384, 256, 4, 4, None),
     (129, 384, 256, 4, 4, None), (333, 1408, 640, 7, 3, 1.0), (700, 512, 1024, 3, 2, None),
     (1500, 256, 256, 40, 6, 0.7),
+    # few tokens: up to 32 (token, choice) pairs, few and many tiles, shared experts
+    (1, 4096, 256, 64, 8, None), (2, 512, 1408, 256, 8, None), (4, 1024, 384, 64, 8, 0.5), (8, 640, 256, 33, 4, None),
+    (8, 2048, 1024, 6, 2, 1.0), (7, 16384, 128, 3, 3, None), (5, 128, 2048, 20, 1, None), (8, 256, 128, 64, 4, None),
+    (9, 256, 128, 64, 3, None), (8, 256, 128, 40, 5, None),
 ]
 
 

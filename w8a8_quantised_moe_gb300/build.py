@@ -21,7 +21,8 @@ BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libmoe_w8a8_checked.so")
 SOURCES = ["api.cu", "route.cu", "router.cu", "pointwise.cu", "gemm.cu", "gemm_pair.cu", "gemm_skinny.cu",
            "static_linear.cu", "fp8.cu", "gemm_fp8_pair.cu", "fused.cu", "api_block.cu", "block.cu", "gemm_block.cu",
-           "gemm_block_few.cu", "linear_block_few.cu", "norm.cu"]
+           "gemm_block_few.cu", "linear_block_few.cu", "block_route.cu",
+           "norm.cu"]
 HEADERS = ["internal.h", "ptx.cuh", "gemm_common.cuh", "gemm_skinny.cuh", "router_small.cuh", "api_common.h",
            "block.h", "block_dev.cuh", "block_tiles.cuh"]
 

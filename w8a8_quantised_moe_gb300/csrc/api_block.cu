@@ -32,7 +32,7 @@ bool lin_shape_ok(int64_t M, int64_t N, int64_t K) {
 // one byte, a scale per slot and 128 channels.
 struct BlockFwdLayout {
     size_t err, counts, wsplit, logits, topk_ids, topk_w, rank, hist, offsets, slot_of, slot_token, q_x, s_x, q_h,
-        s_h, o, s_o, total;
+        s_h, o, s_o, done, total;
 };
 BlockFwdLayout block_fwd_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
     BlockFwdLayout L{};
@@ -47,7 +47,9 @@ BlockFwdLayout block_fwd_layout(int64_t T, int64_t H, int64_t I, int64_t E, int6
     L.err = take(256);
     L.counts = take(2 * 4);
     L.wsplit = take((size_t)3 * rp.E_pad * H * 2);
-    L.logits = take((size_t)rp.KS * T * rp.E_pad * 4);
+    const size_t few = block_few_tokens(T, E, k) ? block_route_scratch(T, H) : 0;
+    const size_t logits = (size_t)rp.KS * T * rp.E_pad * 4;
+    L.logits = take(logits > few ? logits : few);
     L.topk_ids = take(S * 4);
     L.topk_w = take(S * 4);
     L.rank = take(S * 4);
@@ -61,6 +63,7 @@ BlockFwdLayout block_fwd_layout(int64_t T, int64_t H, int64_t I, int64_t E, int6
     L.s_h = take(S * (I / kBlk) * 4);
     L.o = take(S * H * 2);
     L.s_o = take(S * (H / 32) * 4);
+    L.done = take((H + 255) / 256 * 4);
     L.total = off;
     return L;
 }
@@ -153,7 +156,67 @@ moe_status_t moe_w8a8_fp8_block_forward(const uint16_t* x, const float* router_w
     int32_t* counts = at<int32_t>(workspace, L.counts);
     const uint64_t timeout = current_timeout_ns();
 
-    cudaError_t e = launch_router(x, router_w, router_bias, (int)T, (int)H, (int)E, (int)top_k,
+    BlockGemmArgs g{};
+    g.n_groups = (int)E;
+    g.error = err;
+    g.timeout_ns = timeout;
+    g.stall = injected(kInjectStall) ? 1 : 0;
+    auto first_product = [&](int rows) {
+        g.act = at<uint8_t>(workspace, L.q_x);
+        g.act_scale = at<float>(workspace, L.s_x);
+        g.w = w13_q;
+        g.w_scale = w13_scale;
+        g.K = (int)H;
+        g.w_rows = (int)(2 * I);
+        g.up_offset = (int)I;
+        g.total_rows = rows;
+        g.q_out = at<uint8_t>(workspace, L.q_h);
+        g.s_out = at<float>(workspace, L.s_h);
+    };
+    auto second_product = [&] {
+        g.act = at<uint8_t>(workspace, L.q_h);
+        g.act_scale = at<float>(workspace, L.s_h);
+        g.w = w2_q;
+        g.w_scale = w2_scale;
+        g.K = (int)I;
+        g.w_rows = (int)H;
+        g.up_offset = 0;
+        g.total_rows = S;
+        g.out = at<uint16_t>(workspace, L.o);
+        g.s_out = at<float>(workspace, L.s_o);
+    };
+    cudaError_t e;
+    if (block_few_tokens(T, E, top_k)) {  // three launches
+        BlockRouteArgs r{};
+        r.x = x;
+        r.Wr = router_w;
+        r.bias = router_bias;
+        r.T = (int)T;
+        r.H = (int)H;
+        r.E = (int)E;
+        r.k = (int)top_k;
+        r.P = at<float>(workspace, L.logits);
+        r.q = at<uint8_t>(workspace, L.q_x);
+        r.s = at<float>(workspace, L.s_x);
+        r.topk_ids = at<int32_t>(workspace, L.topk_ids);
+        r.topk_w = at<float>(workspace, L.topk_w);
+        r.done = at<unsigned int>(workspace, L.done);
+        r.n_done = (int)((H + 255) / 256);
+        r.ticket = at<unsigned int>(workspace, L.err + kTicketOffset);
+        r.error = err;
+        if ((e = launch_block_route_few(r, st, pdl)) != cudaSuccess) return from_cuda(e);
+        g.ids = r.topk_ids;
+        g.topk_w = r.topk_w;
+        g.T = (int)T;
+        g.k = (int)top_k;
+        g.done = r.done;
+        g.y = y;
+        first_product((int)T);
+        if ((e = launch_block_gemm_few(BlockEpi::GateUp, g, st, pdl)) != cudaSuccess) return from_cuda(e);
+        second_product();
+        return from_cuda(launch_block_gemm_few(BlockEpi::Half, g, st, pdl));
+    }
+    e = launch_router(x, router_w, router_bias, (int)T, (int)H, (int)E, (int)top_k,
                                   at<uint16_t>(workspace, L.wsplit), at<float>(workspace, L.logits),
                                   at<int32_t>(workspace, L.topk_ids), at<float>(workspace, L.topk_w),
                                   at<int32_t>(workspace, L.rank), hist, offsets, counts,
@@ -167,36 +230,14 @@ moe_status_t moe_w8a8_fp8_block_forward(const uint16_t* x, const float* router_w
                                    at<float>(workspace, L.s_x), err, st, pdl);
     if (e != cudaSuccess) return from_cuda(e);
 
-    BlockGemmArgs g{};
-    g.act = at<uint8_t>(workspace, L.q_x);
-    g.act_scale = at<float>(workspace, L.s_x);
-    g.w = w13_q;
-    g.w_scale = w13_scale;
-    g.K = (int)H;
-    g.w_rows = (int)(2 * I);
-    g.up_offset = (int)I;
-    g.n_groups = (int)E;
-    g.total_rows = S;
     g.offsets = offsets;
-    g.q_out = at<uint8_t>(workspace, L.q_h);
-    g.s_out = at<float>(workspace, L.s_h);
-    g.error = err;
-    g.timeout_ns = timeout;
-    g.stall = injected(kInjectStall) ? 1 : 0;
+    first_product(S);
     auto product = [&](BlockEpi epi) {
         return block_gemm_few_wanted(g) ? launch_block_gemm_few(epi, g, st, pdl) : launch_block_gemm(epi, g, st, pdl);
     };
     if ((e = product(BlockEpi::GateUp)) != cudaSuccess) return from_cuda(e);
 
-    g.act = at<uint8_t>(workspace, L.q_h);
-    g.act_scale = at<float>(workspace, L.s_h);
-    g.w = w2_q;
-    g.w_scale = w2_scale;
-    g.K = (int)I;
-    g.w_rows = (int)H;
-    g.up_offset = 0;
-    g.out = at<uint16_t>(workspace, L.o);
-    g.s_out = at<float>(workspace, L.s_o);
+    second_product();
     if ((e = product(BlockEpi::Half)) != cudaSuccess) return from_cuda(e);
     return from_cuda(launch_combine_half(at<uint16_t>(workspace, L.o), at<float>(workspace, L.s_o),
                                          at<int32_t>(workspace, L.slot_of), at<float>(workspace, L.topk_w), (int)T,

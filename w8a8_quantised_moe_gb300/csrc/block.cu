@@ -6,7 +6,6 @@
 // zeros has s = 0 and codes 0.
 // Activations: a block is 128 channels of one row, so a row needs no
 // reduction across its blocks.  Weights: a block is 128 x 128.
-#include <cuda_fp16.h>
 
 #include "block.h"
 #include "block_dev.cuh"
@@ -135,15 +134,7 @@ __global__ void __launch_bounds__(256) combine_half_kernel(const uint16_t* __res
     }
     float a[8] = {};
 #pragma unroll
-    for (int j = 0; j < KMAX; ++j) {
-        const __half2* h = reinterpret_cast<const __half2*>(&v[j]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(h[i]);
-            a[2 * i] = fmaf(w[j], f.x, a[2 * i]);
-            a[2 * i + 1] = fmaf(w[j], f.y, a[2 * i + 1]);
-        }
-    }
+    for (int j = 0; j < KMAX; ++j) add_half8(a, v[j], w[j]);
     *reinterpret_cast<uint4*>(y + (size_t)t * H + col) =
         make_uint4(bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3]), bf16_pair(a[4], a[5]), bf16_pair(a[6], a[7]));
 }

@@ -37,6 +37,13 @@ struct BlockGemmArgs {
     int* error;              // sticky device error word
     uint64_t timeout_ns;
     int stall;               // test hook (MOE_INJECT=stall)
+    // few tokens only (ids != nullptr; offsets unused): total_rows activation
+    // rows, all of them in every tile
+    const int32_t* ids;      // [T][k] experts
+    const float* topk_w;     // [T][k] (Half)
+    int T, k;
+    unsigned int* done;      // [column blocks] finished experts, zero before the launch (Half)
+    uint16_t* y;             // bf16 [T][w_rows] (Half): the combine
 };
 
 // Tensor-core product, groups of many rows (gemm_block.cu).
@@ -53,6 +60,31 @@ cudaError_t launch_block_gemm_few(BlockEpi epi, const BlockGemmArgs& args, cudaS
 bool block_linear_few_fused(int M);
 bool block_linear_few_supported(int M, int N, int K);
 cudaError_t launch_block_linear_few(const BlockGemmArgs& g, const uint16_t* x, cudaStream_t st, bool pdl);
+
+// Few tokens (block_route.cu): the layer in three launches, without a
+// permutation.  Rows of q_out, out and the scales that go with them are then
+// slots t k + j, and every tile's columns are all tokens (first product) or all
+// slots (second).
+constexpr int kFewTokens = 8, kFewSlots = 32;
+constexpr int kRouterMaxSlicesFew = 128;   // slices of the router's rows, at most
+constexpr int kRouterMaxSliceRows = 128;   // rows of one (H <= 16384)
+bool block_few_tokens(int64_t T, int64_t E, int64_t k);
+size_t block_route_scratch(int64_t T, int64_t H);  // bytes of P
+struct BlockRouteArgs {
+    const uint16_t* x;       // bf16 [T][H]
+    const float *Wr, *bias;  // fp32 [H][E]; [E] or nullptr
+    int T, H, E, k, hs;      // hs: set by the launch
+    float* P;                // sums of the clusters [n][T][E rounded up to 32, 64, 128 or 256]
+    uint8_t* q;              // codes [T][H]
+    float* s;                // scales [T][H / 128]
+    int32_t* topk_ids;       // [T][k]
+    float* topk_w;           // [T][k]
+    unsigned int* done;      // [n_done], cleared for the second product
+    int n_done;
+    unsigned int* ticket;    // zero between calls
+    int* error;
+};
+cudaError_t launch_block_route_few(BlockRouteArgs a, cudaStream_t st, bool pdl);
 
 // Weights fp32 [groups][rows][K] to E4M3 codes and scales per 128 x 128 block.
 cudaError_t launch_quantize_weights_block(const float* w, int64_t groups, int rows, int K, uint8_t* q, float* s,

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda_fp16.h>
 
 #include "block.h"
 
@@ -95,6 +96,17 @@ __device__ __forceinline__ void half_scale(float amax, float& s, float& inv) {
     const bool finite = amax < INFINITY;
     s = finite ? __uint_as_float((e - 14) << 23) : 1.f;
     inv = finite ? __uint_as_float((268 - e) << 23) : 1.f;
+}
+
+// a += w * eight fp16 values.
+__device__ __forceinline__ void add_half8(float (&a)[8], const uint4& v, float w) {
+    const __half2* h = reinterpret_cast<const __half2*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(h[i]);
+        a[2 * i] = fmaf(w, f.x, a[2 * i]);
+        a[2 * i + 1] = fmaf(w, f.y, a[2 * i + 1]);
+    }
 }
 
 // h = g / (1 + exp(-g)) * u.  The exponential and the quotient are the fast

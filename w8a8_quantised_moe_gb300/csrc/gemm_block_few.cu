@@ -135,7 +135,46 @@ __device__ __forceinline__ void few_output(const BlockGemmArgs& args, int r, int
     }
 }
 
-template <int EPI, int NTOK, bool SPLIT>
+// TOK: the experts' ids to out[0 .. T k), the distinct ones among them, in the
+// order of their first slots, from out[kFewSlots], their number to out[2 kFewSlots].
+__device__ __forceinline__ void few_distinct(const BlockGemmArgs& args, int* out, int lane) {
+    const int n = args.T * args.k;  // <= kFewSlots = 32
+    int id = lane < n ? __ldcg(args.ids + lane) : -1;
+    if (lane < n && !in_range(id, 0, args.n_groups, args.error)) id = 0;  // checked build
+    const unsigned same = __match_any_sync(0xffffffffu, id);
+    const bool first = lane < n && (same & ((1u << lane) - 1u)) == 0u;
+    const unsigned firsts = __ballot_sync(0xffffffffu, first);
+    out[lane] = id;
+    if (first) out[kFewSlots + __popc(firsts & ((1u << lane) - 1u))] = id;
+    if (lane == 0) out[2 * kFewSlots] = __popc(firsts);
+}
+
+// Whether this was the last of n experts to write its rows' columns of block cb.
+// The rows were written before a barrier that the calling thread has passed.
+__device__ __forceinline__ int few_last(const BlockGemmArgs& args, int cb, int n) {
+    __threadfence();
+    const bool last = atomicAdd(args.done + cb, 1u) == (unsigned)n - 1u;
+    __threadfence();
+    return last;
+}
+
+// y of every token over the 256 columns of block cb, in top-k order, by n threads.
+__device__ __forceinline__ void few_combine(const BlockGemmArgs& args, int cb, int i0, int n) {
+    const int H = args.w_rows, per = min(2 * kBlk, H - cb * 2 * kBlk) / 8;  // 8 columns a thread
+    for (int i = i0; i < args.T * per; i += n) {
+        const int t = i / per, col = cb * 2 * kBlk + (i - t * per) * 8;
+        float a[8] = {};
+        for (int j = 0; j < args.k; ++j) {
+            const size_t slot = (size_t)t * args.k + j;
+            const uint4 v = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.out) + slot * H + col));
+            add_half8(a, v, __ldg(args.topk_w + slot) * __ldcg(args.s_out + slot * (H / 32) + col / 32));
+        }
+        *reinterpret_cast<uint4*>(args.y + (size_t)t * H + col) =
+            make_uint4(bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3]), bf16_pair(a[4], a[5]), bf16_pair(a[6], a[7]));
+    }
+}
+
+template <int EPI, int NTOK, bool SPLIT, bool TOK>
 __global__ void __launch_bounds__(kGfThreads, 1)
     block_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a,
                      const BlockGemmArgs args, int cs) {
@@ -158,11 +197,13 @@ __global__ void __launch_bounds__(kGfThreads, 1)
     uint64_t* epi_bar = stall_bar + 1;      // the epilogue warps
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* last_flag = abort_flag + 1;  // TOK, Half: this tile was its columns' last
     int* tile_start = reinterpret_cast<int*>(smem + L.tiles);
     int* row_start = tile_start + (kMaxExperts + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = SPLIT ? (int)cluster_ctarank() : 0;
     const int kb0 = SPLIT ? nkb * rank / cs : 0, kb1 = SPLIT ? nkb * (rank + 1) / cs : nkb;
+    int* ids_s = tile_start;  // TOK, instead of the tables: [T k] experts, then the distinct ones
     const int tile0 = SPLIT ? (int)blockIdx.x / cs : (int)blockIdx.x;
     const int tile_step = SPLIT ? 1 << 30 : (int)gridDim.x;
 
@@ -190,13 +231,38 @@ __global__ void __launch_bounds__(kGfThreads, 1)
     // The expert offsets were complete before the kernel before this one passed
     // its own wait, and no kernel of the layer writes weights: the table and the
     // first stages' weights need not wait for it.
-    if (warp == 2) block_tile_table(args, NTOK, few_col_blocks<EPI>(args), tile_start, row_start, lane);
+    // (TOK: the first product follows the router itself and waits; to the second
+    // the same holds for the experts' ids.)
+    if (TOK && EPI == (int)BlockEpi::GateUp) pdl_wait();
+    if (warp == 2) {
+        if (TOK) few_distinct(args, ids_s, lane);
+        else block_tile_table(args, NTOK, few_col_blocks<EPI>(args), tile_start, row_start, lane);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int total_tiles = tile_start[args.n_groups];
+    const int n_cb = few_col_blocks<EPI>(args);
+    const int total_tiles = TOK ? ids_s[2 * kFewSlots] * n_cb : tile_start[args.n_groups];
     const Tiles tiles{tile_start, row_start, args.n_groups};
+    auto decode = [&](int tile, int& g, int& cb, int& row0, int& nvalid) {
+        if (TOK) {
+            g = ids_s[kFewSlots + tile / n_cb];
+            cb = tile % n_cb;
+            row0 = 0;
+            nvalid = args.total_rows;
+        } else {
+            block_decode_tile(tiles, tile, NTOK, g, cb, row0, nvalid);
+        }
+    };
+    // TOK: the slot that column m of expert g's tile is written to, or -1
+    auto slot_of = [&](int g, int m) {
+        if (EPI != (int)BlockEpi::GateUp) return ids_s[m] == g ? m : -1;
+        int slot = -1;
+        for (int j = 0; j < args.k; ++j)
+            if (ids_s[m * args.k + j] == g) slot = m * args.k + j;
+        return slot;
+    };
     const WaitCtl ctl{abort_flag, args.error, args.timeout_ns, 0u};
 
     if (warp == 0) {
@@ -211,7 +277,7 @@ __global__ void __launch_bounds__(kGfThreads, 1)
             ok = __shfl_sync(0x7u, ok, 0);
             for (int tile = tile0; ok && tile < total_tiles; tile += tile_step) {
                 int g, cb, row0, nvalid;
-                block_decode_tile(tiles, tile, NTOK, g, cb, row0, nvalid);
+                decode(tile, g, cb, row0, nvalid);
                 const bool two = EPI == (int)BlockEpi::GateUp || args.w_rows - cb * 2 * kBlk > kBlk;
                 const uint32_t bytes = (uint32_t)(((two ? 2 : 1) * kBlk + NTOK) * kBlk);
                 const int row = lane == 2 ? row0 : few_weight_row<EPI>(args, g, cb, lane);
@@ -292,7 +358,7 @@ __global__ void __launch_bounds__(kGfThreads, 1)
         auto stage_scales = [&](int tile, uint32_t tl) {
             if (tile < total_tiles) {
                 int g, cb, row0, nvalid;
-                block_decode_tile(tiles, tile, NTOK, g, cb, row0, nvalid);
+                decode(tile, g, cb, row0, nvalid);
                 float* d = scales + (tl & 1u) * nkb * NTOK;
                 for (int i = kb0 * NTOK + et; i < kb1 * NTOK; i += kGfEpiWarps * 32)
                     cp_async4(d + i, args.act_scale + (size_t)(row0 + min(i % NTOK, nvalid - 1)) * nkb + i / NTOK);
@@ -305,7 +371,7 @@ __global__ void __launch_bounds__(kGfThreads, 1)
         bool ok = true;
         for (int tile = tile0; ok && tile < total_tiles; tile += tile_step, ++tl) {
             int g, cb, row0, nvalid;
-            block_decode_tile(tiles, tile, NTOK, g, cb, row0, nvalid);
+            decode(tile, g, cb, row0, nvalid);
             const int nb = blocks_of(args.w_rows);
             const float* sw = args.w_scale + ((size_t)g * nb + few_scale_block<EPI>(args, cb, h, nb)) * nkb;
             float sw_next = __ldg(sw + kb0);
@@ -348,9 +414,17 @@ __global__ void __launch_bounds__(kGfThreads, 1)
             if (SPLIT) break;  // the cluster adds up below
             if (!(ok = epi_sync(epi_bar, sync, ctl))) break;
             for (int m = warp - kGfEpi0; m < nvalid; m += kGfEpiWarps) {
+                const int r = TOK ? slot_of(g, m) : row0 + m;
+                if (r < 0) continue;
                 const float4 a = *reinterpret_cast<const float4*>(part + m * kBlk + lane * 4);
                 const float4 b = *reinterpret_cast<const float4*>(part + (NTOK + m) * kBlk + lane * 4);
-                few_output<EPI>(args, row0 + m, cb, lane, a, b);
+                few_output<EPI>(args, r, cb, lane, a, b);
+            }
+            if (TOK && EPI == (int)BlockEpi::Half) {  // this expert's rows are written: the combine of the last
+                if (!(ok = epi_sync(epi_bar, sync, ctl))) break;
+                if (et == 0) *last_flag = few_last(args, cb, ids_s[2 * kFewSlots]);
+                if (!(ok = epi_sync(epi_bar, sync, ctl))) break;
+                if (*last_flag) few_combine(args, cb, et, kGfEpiWarps * 32);
             }
         }
     }
@@ -361,8 +435,10 @@ __global__ void __launch_bounds__(kGfThreads, 1)
         cluster_sync_all();
         if (tile0 < total_tiles) {
             int g, cb, row0, nvalid;
-            block_decode_tile(tiles, tile0, NTOK, g, cb, row0, nvalid);
+            decode(tile0, g, cb, row0, nvalid);
             for (int m = rank + cs * warp; m < nvalid; m += cs * (kGfThreads / 32)) {  // a warp per row
+                const int r_out = TOK ? slot_of(g, m) : row0 + m;
+                if (r_out < 0) continue;
                 float4 a[8], b[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r)
@@ -376,10 +452,17 @@ __global__ void __launch_bounds__(kGfThreads, 1)
                         a[0] = gf_add(a[0], a[r]);
                         b[0] = gf_add(b[0], b[r]);
                     }
-                few_output<EPI>(args, row0 + m, cb, lane, a[0], b[0]);
+                few_output<EPI>(args, r_out, cb, lane, a[0], b[0]);
             }
         }
         cluster_sync_all();  // no CTA leaves while another reads its part
+        if (TOK && EPI == (int)BlockEpi::Half && rank == 0 && tile0 < total_tiles) {
+            // this expert's rows are written (by the cluster): the combine of the last
+            const int cb = tile0 % n_cb;
+            if (threadIdx.x == 0) *last_flag = few_last(args, cb, ids_s[2 * kFewSlots]);
+            __syncthreads();
+            if (*last_flag) few_combine(args, cb, threadIdx.x, kGfThreads);
+        }
     }
     if (warp == 1) {
         __syncwarp();
@@ -388,26 +471,26 @@ __global__ void __launch_bounds__(kGfThreads, 1)
     }
 }
 
-template <int EPI, int NTOK, bool SPLIT>
+template <int EPI, int NTOK, bool SPLIT, bool TOK>
 cudaError_t few_smem_limit() {
-    static const cudaError_t e = cudaFuncSetAttribute(block_few_kernel<EPI, NTOK, SPLIT>,
+    static const cudaError_t e = cudaFuncSetAttribute(block_few_kernel<EPI, NTOK, SPLIT, TOK>,
                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kGfMaxSmem);
     return e;
 }
 
 // CTAs of a cluster that splits one of `tiles` tiles: 1 where they do not all run at once.
-template <int EPI, int NTOK>
+template <int EPI, int NTOK, bool TOK>
 int few_cluster(long tiles, int nkb) {
-    if (few_smem_limit<EPI, NTOK, true>() != cudaSuccess) return 1;
-    static const ClusterCounts counts(reinterpret_cast<const void*>(block_few_kernel<EPI, NTOK, true>), kGfThreads,
+    if (few_smem_limit<EPI, NTOK, true, TOK>() != cudaSuccess) return 1;
+    static const ClusterCounts counts(reinterpret_cast<const void*>(block_few_kernel<EPI, NTOK, true, TOK>), kGfThreads,
                                       kGfMaxSmem);
     return counts.largest(tiles, nkb);
 }
 
-template <int EPI, int NTOK, bool SPLIT>
+template <int EPI, int NTOK, bool SPLIT, bool TOK>
 cudaError_t launch_few_impl(const BlockGemmArgs& args, long tiles, int cs, cudaStream_t st, bool pdl) {
-    auto kern = block_few_kernel<EPI, NTOK, SPLIT>;
-    const cudaError_t attr_err = few_smem_limit<EPI, NTOK, SPLIT>();
+    auto kern = block_few_kernel<EPI, NTOK, SPLIT, TOK>;
+    const cudaError_t attr_err = few_smem_limit<EPI, NTOK, SPLIT, TOK>();
     if (attr_err != cudaSuccess) return attr_err;
     CUtensorMap tw, ta;
     if (!make_tensor_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, args.w, args.K,
@@ -441,21 +524,28 @@ cudaError_t launch_few_impl(const BlockGemmArgs& args, long tiles, int cs, cudaS
     return e;
 }
 
+template <int EPI, int NTOK, bool TOK>
+cudaError_t launch_few_ntok(const BlockGemmArgs& args, long tiles, cudaStream_t st, bool pdl) {
+    const int cs = few_cluster<EPI, NTOK, TOK>(tiles, blocks_of(args.K));
+    return cs > 1 ? launch_few_impl<EPI, NTOK, true, TOK>(args, tiles, cs, st, pdl)
+                  : launch_few_impl<EPI, NTOK, false, TOK>(args, tiles, 1, st, pdl);
+}
+
 template <int EPI>
 cudaError_t launch_few(const BlockGemmArgs& args, cudaStream_t st, bool pdl) {
-    const int ntok = args.total_rows <= kFewRows16 * (long)args.n_groups || args.total_rows <= 16 ? 16 : 32;
-    // at most this many groups have rows, and so many more tiles than whole ones
-    const long groups = args.total_rows < args.n_groups ? args.total_rows : args.n_groups;
-    const long tiles = (args.total_rows <= ntok ? groups : args.total_rows / ntok + groups) * few_col_blocks<EPI>(args);
-    const int nkb = blocks_of(args.K);
-    if (ntok == 16) {
-        const int cs = few_cluster<EPI, 16>(tiles, nkb);
-        return cs > 1 ? launch_few_impl<EPI, 16, true>(args, tiles, cs, st, pdl)
-                      : launch_few_impl<EPI, 16, false>(args, tiles, 1, st, pdl);
+    const long rows = args.total_rows;
+    if (args.ids != nullptr) {
+        const long slots = (long)args.T * args.k;
+        const long tiles = (slots < args.n_groups ? slots : args.n_groups) * few_col_blocks<EPI>(args);
+        return rows <= 16 ? launch_few_ntok<EPI, 16, true>(args, tiles, st, pdl)
+                          : launch_few_ntok<EPI, 32, true>(args, tiles, st, pdl);
     }
-    const int cs = few_cluster<EPI, 32>(tiles, nkb);
-    return cs > 1 ? launch_few_impl<EPI, 32, true>(args, tiles, cs, st, pdl)
-                  : launch_few_impl<EPI, 32, false>(args, tiles, 1, st, pdl);
+    const int ntok = rows <= kFewRows16 * (long)args.n_groups || rows <= 16 ? 16 : 32;
+    // at most this many groups have rows, and so many more tiles than whole ones
+    const long groups = rows < args.n_groups ? rows : args.n_groups;
+    const long tiles = (rows <= ntok ? groups : rows / ntok + groups) * few_col_blocks<EPI>(args);
+    return ntok == 16 ? launch_few_ntok<EPI, 16, false>(args, tiles, st, pdl)
+                      : launch_few_ntok<EPI, 32, false>(args, tiles, st, pdl);
 }
 
 }  // namespace
