@@ -421,13 +421,24 @@ def fp8_forward_host(x_host, router_w, router_bias, w13_q, w13_scale, w2_q, w2_s
 
 # ---- block-scaled FP8 (E4M3, a scale per 128 channels) ---------------------
 # A decode step calls these with a few microseconds of GPU work each, so their
-# argument handling is kept short.
+# argument handling is kept short: _fits is the check, _need words its refusal.
 
 BLOCK = 128  # input channels, and output channels of a weight, that share a scale
 
 
 def _blocks(n):
     return -(-n // BLOCK)
+
+
+def _fits(t, dtype, shape):
+    return t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
+
+
+def _check_all(*wanted):
+    """Refuses the first of (name, tensor, dtype, shape) that does not fit."""
+    for name, t, dtype, shape in wanted:
+        if t is not None:
+            _need(t, dtype, shape, name)
 
 
 def _raw_stream(stream, t):
@@ -463,20 +474,23 @@ def fp8_block_linear(x, w_q, w_scale, workspace=None, out=None, stream=None):
     """Block-scaled FP8 linear layer: bf16 x [M, K], E4M3 w_q [N, K] (uint8), fp32
     w_scale [ceil(N / 128), ceil(K / 128)] -> bf16 [M, N]."""
     torch = _torch()
+    bf16 = torch.bfloat16
     M, K = x.shape
     N = w_q.shape[0]
-    _need(x, torch.bfloat16, (M, K), "x")
-    _need(w_q, torch.uint8, (N, K), "w_q")
-    _need(w_scale, torch.float32, (_blocks(N), _blocks(K)), "w_scale")
+    if not (_fits(x, bf16, (M, K)) and _fits(w_q, torch.uint8, (N, K))
+            and _fits(w_scale, torch.float32, (_blocks(N), _blocks(K)))
+            and (out is None or _fits(out, bf16, (M, N)))):
+        _check_all(("x", x, bf16, (M, K)), ("w_q", w_q, torch.uint8, (N, K)),
+                   ("w_scale", w_scale, torch.float32, (_blocks(N), _blocks(K))), ("out", out, bf16, (M, N)))
     if workspace is None:
         workspace = new_workspace(fp8_block_linear_workspace_size(M, N, K), x.device)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    else:
-        _need(out, torch.bfloat16, (M, N), "out")
-    _lib.check(_lib.load().moe_w8a8_fp8_block_linear(
+        out = torch.empty((M, N), dtype=bf16, device=x.device)
+    status = _lib.load().moe_w8a8_fp8_block_linear(
         x.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), M, N, K, out.data_ptr(), workspace.data_ptr(),
-        workspace.nbytes, _raw_stream(stream, x)), "moe_w8a8_fp8_block_linear")
+        workspace.nbytes, _raw_stream(stream, x))
+    if status:
+        raise MoeError(status, "moe_w8a8_fp8_block_linear")
     return out
 
 
@@ -493,27 +507,29 @@ def fp8_block_forward(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale
     w13_q [E, 2I, H] and w2_q [E, H, I] E4M3 (uint8) with fp32 scales
     [E, 2I / 128, H / 128] and [E, H / 128, I / 128]."""
     torch = _torch()
-    T, H = x.shape
+    bf16, fp32, u8 = torch.bfloat16, torch.float32, torch.uint8
+    T, H = shape = x.shape
     E = router_w.shape[1]
     I = w2_q.shape[2] if w2_q.dim() == 3 else 0
-    _need(x, torch.bfloat16, (T, H), "x")
-    _need(router_w, torch.float32, (H, E), "router_w")
-    if router_bias is not None:
-        _need(router_bias, torch.float32, (E,), "router_bias")
-    _need(w13_q, torch.uint8, (E, 2 * I, H), "w13_q")
-    _need(w13_scale, torch.float32, (E, 2 * I // BLOCK, H // BLOCK), "w13_scale")
-    _need(w2_q, torch.uint8, (E, H, I), "w2_q")
-    _need(w2_scale, torch.float32, (E, H // BLOCK, I // BLOCK), "w2_scale")
+    hb, ib = H // BLOCK, I // BLOCK
+    if not (_fits(x, bf16, shape) and _fits(router_w, fp32, (H, E)) and _fits(w13_q, u8, (E, 2 * I, H))
+            and _fits(w13_scale, fp32, (E, 2 * ib, hb)) and _fits(w2_q, u8, (E, H, I))
+            and _fits(w2_scale, fp32, (E, hb, ib)) and (router_bias is None or _fits(router_bias, fp32, (E,)))
+            and (out is None or _fits(out, bf16, shape))):
+        _check_all(("x", x, bf16, shape), ("router_w", router_w, fp32, (H, E)),
+                   ("router_bias", router_bias, fp32, (E,)), ("w13_q", w13_q, u8, (E, 2 * I, H)),
+                   ("w13_scale", w13_scale, fp32, (E, 2 * ib, hb)), ("w2_q", w2_q, u8, (E, H, I)),
+                   ("w2_scale", w2_scale, fp32, (E, hb, ib)), ("out", out, bf16, shape))
     if workspace is None:
         workspace = new_workspace(fp8_block_workspace_size(T, H, I, E, top_k), x.device)
     if out is None:
         out = torch.empty_like(x)
-    else:
-        _need(out, torch.bfloat16, (T, H), "out")
-    _lib.check(_lib.load().moe_w8a8_fp8_block_forward(
+    status = _lib.load().moe_w8a8_fp8_block_forward(
         x.data_ptr(), router_w.data_ptr(), _ptr(router_bias), w13_q.data_ptr(), w13_scale.data_ptr(), w2_q.data_ptr(),
         w2_scale.data_ptr(), T, H, I, E, top_k, out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-        _raw_stream(stream, x)), "moe_w8a8_fp8_block_forward")
+        _raw_stream(stream, x))
+    if status:
+        raise MoeError(status, "moe_w8a8_fp8_block_forward")
     return out
 
 
@@ -534,28 +550,22 @@ def norm_residual(x, branch=None, post_w=None, gate=None, scale=1.0, pre_w=None,
     bf16 = torch.bfloat16
     fp32 = x.dtype is torch.float32
     T, H = shape = x.shape
-    _need(x, torch.float32 if fp32 else bf16, shape, "x")
-    form, r, n = 0, x, None
-    if branch is not None:
-        _need(branch, bf16, shape, "branch")
-        if x_out is None:
-            r = torch.empty_like(x)
-        else:
-            r = x_out
-            _need(r, x.dtype, shape, "x_out")
-    if post_w is not None:
-        _need(post_w, bf16, (H,), "post_w")
-    if gate is not None:
-        form = 1 if gate.dim() == 1 else 2 if gate.dim() == 2 and gate.shape[1] == 1 else 3
-        _need(gate, bf16, ((H,), (T, 1), shape)[form - 1], "gate")
-    if pre_w is not None:
-        _need(pre_w, bf16, (H,), "pre_w")
-        if n_out is None:
-            n = torch.empty_like(x, dtype=bf16)
-        else:
-            n = n_out
-            _need(n, bf16, shape, "n_out")
-    _lib.check(_lib.load().moe_w8a8_norm_residual(
+    row = (H,)
+    form = 0 if gate is None else 1 if gate.dim() == 1 else 2 if gate.dim() == 2 and gate.shape[1] == 1 else 3
+    if not ((fp32 or x.dtype is bf16) and x.is_cuda and x.is_contiguous()
+            and (branch is None or _fits(branch, bf16, shape)) and (post_w is None or _fits(post_w, bf16, row))
+            and (pre_w is None or _fits(pre_w, bf16, row))
+            and (gate is None or _fits(gate, bf16, (row, (T, 1), shape)[form - 1]))
+            and (x_out is None or _fits(x_out, x.dtype, shape)) and (n_out is None or _fits(n_out, bf16, shape))):
+        _check_all(("x", x, torch.float32 if fp32 else bf16, shape), ("branch", branch, bf16, shape),
+                   ("post_w", post_w, bf16, row), ("pre_w", pre_w, bf16, row),
+                   ("gate", gate, bf16, (row, (T, 1), shape)[form - 1]), ("x_out", x_out, x.dtype, shape),
+                   ("n_out", n_out, bf16, shape))
+    r = x if branch is None else torch.empty_like(x) if x_out is None else x_out
+    n = None if pre_w is None else torch.empty_like(x, dtype=bf16) if n_out is None else n_out
+    status = _lib.load().moe_w8a8_norm_residual(
         x.data_ptr(), fp32, _ptr(branch), _ptr(post_w), _ptr(gate), form, scale, _ptr(pre_w), eps, T, H,
-        r.data_ptr(), _ptr(n), _raw_stream(stream, x)), "moe_w8a8_norm_residual")
+        r.data_ptr(), _ptr(n), _raw_stream(stream, x))
+    if status:
+        raise MoeError(status, "moe_w8a8_norm_residual")
     return r, n

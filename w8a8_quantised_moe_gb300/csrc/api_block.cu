@@ -1,6 +1,8 @@
 // api_block.cu -- the C entry points of the block-scaled FP8 operators and of
 // the norms around a block (include/moe_w8a8.h): argument checks, workspace
 // layout and launch sequences.
+#include <initializer_list>
+
 #include "api_common.h"
 #include "block.h"
 
@@ -62,14 +64,19 @@ BlockFwdLayout block_fwd_layout(int64_t T, int64_t H, int64_t I, int64_t E, int6
     L.q_h = take(S * I);
     L.s_h = take(S * (I / kBlk) * 4);
     L.o = take(S * H * 2);
-    L.s_o = take(S * (H / 32) * 4);
+    L.s_o = take(S * (H / kBlk) * 4);
     L.done = take((H + 255) / 256 * 4);
     L.total = off;
     return L;
 }
 
-// Null or misaligned (or faked so by the test hook).
-bool bad_ptr(const void* p) { return p == nullptr || !aligned16(p) || injected(kInjectBadPtr); }
+// One of them null or misaligned (or faked so by the test hook).
+bool bad_ptrs(std::initializer_list<const void*> ptrs) {
+    for (const void* p : ptrs)
+        if (p == nullptr || !aligned16(p)) return true;
+    return injected(kInjectBadPtr);
+}
+bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 
 }  // namespace
 
@@ -81,7 +88,7 @@ moe_status_t moe_w8a8_fp8_block_quantize_weights(const float* w, int64_t groups,
         K > kMaxLinDim || K % 16)
         return MOE_ERR_UNSUPPORTED_SHAPE;
     if (groups == 0) return MOE_OK;
-    if (bad_ptr(w) || bad_ptr(w_q) || bad_ptr(w_scale)) return MOE_ERR_INVALID_ARG;
+    if (bad_ptrs({w, w_q, w_scale})) return MOE_ERR_INVALID_ARG;
     return from_cuda(launch_quantize_weights_block(w, groups, (int)rows, (int)K, w_q, w_scale,
                                                    static_cast<cudaStream_t>(stream)));
 }
@@ -95,9 +102,7 @@ moe_status_t moe_w8a8_fp8_block_linear(const uint16_t* x, const uint8_t* w_q, co
                                        void* stream) {
     if (!lin_shape_ok(M, N, K)) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (M == 0) return MOE_OK;
-    if (bad_ptr(x) || bad_ptr(w_q) || bad_ptr(w_scale) || bad_ptr(y) || bad_ptr(workspace) ||
-        (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-        return MOE_ERR_INVALID_ARG;
+    if (bad_ptrs({x, w_q, w_scale, y, workspace}) || !aligned256(workspace)) return MOE_ERR_INVALID_ARG;
     const BlockLinLayout L = block_lin_layout(M, K);
     if (workspace_bytes < L.total || injected(kInjectWsShort)) return MOE_ERR_WORKSPACE_TOO_SMALL;
     if (gemm_path_forced()) return MOE_ERR_NOT_IMPLEMENTED;
@@ -137,12 +142,9 @@ moe_status_t moe_w8a8_fp8_block_forward(const uint16_t* x, const float* router_w
                                         void* stream) {
     if (!moe_shape_ok(T, H, I, E, top_k)) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return MOE_OK;
-    for (const void* p : {static_cast<const void*>(x), static_cast<const void*>(router_w),
-                          static_cast<const void*>(w13_q), static_cast<const void*>(w13_scale),
-                          static_cast<const void*>(w2_q), static_cast<const void*>(w2_scale),
-                          static_cast<const void*>(y), static_cast<const void*>(workspace)})
-        if (bad_ptr(p)) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(router_bias) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MOE_ERR_INVALID_ARG;
+    if (bad_ptrs({x, router_w, w13_q, w13_scale, w2_q, w2_scale, y, workspace}) || !aligned16(router_bias) ||
+        !aligned256(workspace))
+        return MOE_ERR_INVALID_ARG;
     const BlockFwdLayout L = block_fwd_layout(T, H, I, E, top_k);
     if (workspace_bytes < L.total || injected(kInjectWsShort)) return MOE_ERR_WORKSPACE_TOO_SMALL;
     if (gemm_path_forced()) return MOE_ERR_NOT_IMPLEMENTED;
@@ -252,10 +254,9 @@ moe_status_t moe_w8a8_norm_residual(const void* x, int x_fp32, const uint16_t* b
         (branch == nullptr && (post_w != nullptr || gate_form != 0)) || !(eps >= 0.f))
         return MOE_ERR_INVALID_ARG;
     if (T == 0) return MOE_OK;
-    if (bad_ptr(x) || (branch != nullptr && bad_ptr(x_out)) || (pre_w != nullptr && bad_ptr(n_out)) ||
-        (gate_form != 0 && gate == nullptr))
+    if (bad_ptrs({x, branch != nullptr ? x_out : x, pre_w != nullptr ? n_out : x, gate_form != 0 ? gate : x}) ||
+        !aligned16(branch) || !aligned16(post_w) || !aligned16(gate) || !aligned16(pre_w))
         return MOE_ERR_INVALID_ARG;
-    if (!aligned16(branch) || !aligned16(post_w) || !aligned16(gate) || !aligned16(pre_w)) return MOE_ERR_INVALID_ARG;
     NormArgs a{};
     a.x = x;
     a.branch = branch;

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(256) combine_half_kernel(const uint16_t* __res
         const int slot = slot_of[(size_t)t * k + j];
         if (!in_range(slot, 0, (long long)T * k, error)) continue;  // checked build: contributes nothing
         v[j] = *reinterpret_cast<const uint4*>(o + (size_t)slot * H + col);
-        w[j] = topk_w[(size_t)t * k + j] * o_scale[(size_t)slot * (H / 32) + col / 32];
+        w[j] = topk_w[(size_t)t * k + j] * o_scale[(size_t)slot * (H / kBlk) + col / kBlk];
     }
     float a[8] = {};
 #pragma unroll

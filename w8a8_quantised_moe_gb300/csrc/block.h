@@ -16,7 +16,7 @@ __host__ __device__ constexpr int blocks_of(int n) { return (n + kBlk - 1) / kBl
 // What a block-scaled product writes.
 enum class BlockEpi : int {
     GateUp = 0,  // h = silu(gate) * up, requantised: E4M3 codes and a scale per row and 128 channels
-    Half = 1,    // fp16 rows with a power-of-two scale per 32 columns (second expert product)
+    Half = 1,    // fp16 rows with a power-of-two scale per 128 columns (second expert product)
     BF16 = 2     // bf16 rows (linear layer)
 };
 
@@ -33,7 +33,7 @@ struct BlockGemmArgs {
     const int32_t* offsets;  // [n_groups + 1] first row of each group, or nullptr: one group
     void* out;               // Half / BF16: [total_rows][w_rows]
     uint8_t* q_out;          // GateUp: codes [total_rows][up_offset]
-    float* s_out;            // GateUp: scales [total_rows][up_offset / 128]; Half: [total_rows][w_rows / 32]
+    float* s_out;            // GateUp: scales [total_rows][up_offset / 128]; Half: [total_rows][w_rows / 128]
     int* error;              // sticky device error word
     uint64_t timeout_ns;
     int stall;               // test hook (MOE_INJECT=stall)
@@ -99,7 +99,7 @@ cudaError_t launch_permute_quant_block(const uint16_t* x, const int32_t* topk_id
                                        bool pdl);
 
 // y[t] = bf16(sum_j w[t][j] * o[slot(t, j)]) over the scaled fp16 rows of
-// BlockEpi::Half (o [S][H], o_scale [S][H / 32]).
+// BlockEpi::Half (o [S][H], o_scale [S][H / 128]).
 cudaError_t launch_combine_half(const uint16_t* o, const float* o_scale, const int32_t* slot_of, const float* topk_w,
                                 int T, int H, int k, uint16_t* y, int* error, cudaStream_t st, bool pdl);
 

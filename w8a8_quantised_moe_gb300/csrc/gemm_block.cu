@@ -195,25 +195,26 @@ __device__ __forceinline__ bool bg_output(const BlockGemmArgs& args, f32x2 (&acc
         bg_store_rows(staging, v, w.lane, args.q_out + r0 * n_ch + cb * kBlk + w.w2 * 64, n_ch, rows);
         if (w.w2 == 0 && w.lane < rows) args.s_out[(r0 + w.lane) * (n_ch / kBlk) + cb] = s;
     } else {
+        const int col0 = cb * kBgCols + w.w2 * kBlk;  // this warp's 128 columns
+        float inv = 1.f;
+        if (EPI == (int)BlockEpi::Half) {
+            float amax = 0.f, s;
+#pragma unroll
+            for (int j = 0; j < 64; ++j) {
+                float a, b;
+                unpack2(acc[j >> 5][j & 31], a, b);
+                amax = amax_nan(amax_nan(amax, a), b);
+            }
+            half_scale(amax, s, inv);
+            if (w.lane < rows && col0 < args.w_rows) args.s_out[(r0 + w.lane) * (args.w_rows / kBlk) + col0 / kBlk] = s;
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int col = cb * kBgCols + w.w2 * kBlk + half * 64;
+            const int col = col0 + half * 64;
 #pragma unroll
             for (int p = 0; p < 2; ++p) {  // 32 columns: 64 bytes
                 const int c0 = col + p * 32;
                 if (c0 >= args.w_rows) continue;
-                float inv = 1.f;
-                if (EPI == (int)BlockEpi::Half) {
-                    float amax = 0.f, s;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float a, b;
-                        unpack2(acc[half][p * 16 + j], a, b);
-                        amax = amax_nan(amax_nan(amax, a), b);
-                    }
-                    half_scale(amax, s, inv);
-                    if (w.lane < rows) args.s_out[(r0 + w.lane) * (args.w_rows / 32) + c0 / 32] = s;
-                }
                 uint4 v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -424,11 +425,15 @@ __global__ void __launch_bounds__(kBgThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                bg_add_block(acc, w.addr(tmem + d * kBgCols), s0, s1, [&] {
+                auto release = [&] {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&acc_empty[d * 2 + w.w2]);
-                });
+                };
+                if (EPI == (int)BlockEpi::BF16 || nvalid > w.q * 32)  // else none of this warp's rows
+                    bg_add_block(acc, w.addr(tmem + d * kBgCols), s0, s1, release);
+                else
+                    release();
             }
             ok = ok && bg_output<EPI>(args, acc, w, row0, nvalid, cb, xch, pair_bar, tl, staging, ctl);
         }

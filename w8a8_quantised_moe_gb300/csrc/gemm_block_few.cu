@@ -124,13 +124,13 @@ __device__ __forceinline__ void few_output(const BlockGemmArgs& args, int r, int
             const int col = (2 * cb + half) * kBlk + lane * 4;
             float amax = amax_nan(amax_nan(amax_nan(amax_nan(0.f, f.x), f.y), f.z), f.w);
 #pragma unroll
-            for (int off = 4; off > 0; off >>= 1) amax = amax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+            for (int off = 16; off > 0; off >>= 1) amax = amax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
             float s, inv;
             half_scale(amax, s, inv);
             if (col >= args.w_rows) continue;  // the same for the whole warp: w_rows is a multiple of 128
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(args.out) + (size_t)r * args.w_rows + col) =
                 make_uint2(half_pair(f.x * inv, f.y * inv), half_pair(f.z * inv, f.w * inv));
-            if ((lane & 7) == 0) args.s_out[(size_t)r * (args.w_rows / 32) + col / 32] = s;
+            if (lane == 0) args.s_out[(size_t)r * (args.w_rows / kBlk) + 2 * cb + half] = s;
         }
     }
 }
@@ -167,7 +167,7 @@ __device__ __forceinline__ void few_combine(const BlockGemmArgs& args, int cb, i
         for (int j = 0; j < args.k; ++j) {
             const size_t slot = (size_t)t * args.k + j;
             const uint4 v = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.out) + slot * H + col));
-            add_half8(a, v, __ldg(args.topk_w + slot) * __ldcg(args.s_out + slot * (H / 32) + col / 32));
+            add_half8(a, v, __ldg(args.topk_w + slot) * __ldcg(args.s_out + slot * (H / kBlk) + col / kBlk));
         }
         *reinterpret_cast<uint4*>(args.y + (size_t)t * H + col) =
             make_uint4(bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3]), bf16_pair(a[4], a[5]), bf16_pair(a[6], a[7]));

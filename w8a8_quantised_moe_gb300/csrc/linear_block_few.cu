@@ -9,7 +9,7 @@
 // from the start.
 //
 //   A  128 weight rows (the MMA's M) x 128 channels, by TMA
-//   B  NTOK >= M quantised rows of x (N) x 128 channels: up to 8 rows are
+//   B  NTOK >= M quantised rows of x (N) x 128 channels: up to 16 rows are
 //      quantised here while the weights fly (FUSED: each CTA its part of K, written
 //      in the 128-byte swizzle); more come by TMA from the quantiser's launch
 //      before, which the weights' loads overlap.  (Measured at 64 x 4096 x 4096:
@@ -33,7 +33,7 @@ namespace {
 constexpr int kLfThreads = 320;
 constexpr int kLfNS = 4;                  // weight stages, and tensor-memory buffers
 constexpr int kLfStageA = kBlk * kBlk;    // 128 weight rows x 128 channels
-constexpr int kLfFusedRows = 8;           // up to this many rows are quantised here
+constexpr int kLfFusedRows = 16;          // up to this many rows are quantised here
 constexpr int kLfMaxSmem = 232448;
 
 struct LinFewArgs {
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kLfThreads, NTOK <= 64 ? 2 : 1)
     } else if (warp < 8) {
         // this part of x to codes, 16 lanes a block, 8 channels a lane.  Rows
         // from M on hold whatever is there: they reach their own columns of D only.
-        constexpr int kBatch = 2;  // loads in flight per lane
+        constexpr int kBatch = 4;  // loads in flight per lane
         const int l16 = threadIdx.x & 15, items = a.M * len;
         for (int i0 = threadIdx.x >> 4; i0 - (int)(threadIdx.x >> 4 & 1) < items; i0 += 16 * kBatch) {
             uint4 v[kBatch];
