@@ -47,8 +47,9 @@ constexpr int kBgThreads = 384;  // producer, two MMA issuers, an idle and 8 epi
 constexpr int kBgEpi0 = 4;       // first epilogue warp
 constexpr int kBgEpiWarps = 8;
 constexpr int kBgHalf = kBlk * kBlk;         // bytes of 128 rows x 128 channels
-constexpr int kBgStaging = 32 * 64;          // per epilogue warp: 32 rows x 64 bytes
-constexpr int kBgXch = 2 * 2 * kBgRows * 4;  // row maxima [2 tiles][2 warps][rows]
+// per epilogue warp: 32 rows x 64 codes, or x 64 columns of two bytes
+__host__ __device__ constexpr int bg_staging(int epi) { return epi == (int)BlockEpi::GateUp ? 32 * 64 : 32 * 128; }
+constexpr int kBgXch = 2 * 2 * kBgRows * 4;  // GateUp: row maxima [2 tiles][2 warps][rows]
 
 // The launch gives every thread 168 registers; the epilogue warps hold 128 sums
 // and their next columns each, so the first four warps pass them theirs: 128 x
@@ -129,22 +130,23 @@ struct BgScales {
     }
 };
 
-// The warp's 32 rows x 64 bytes (v: this lane's row) to memory through shared
-// memory, so that an instruction writes whole 64-byte pieces of 8 rows instead
-// of 16 bytes of 32.  dst: row 0's piece; rows from `rows` on are not written.
-__device__ __forceinline__ void bg_store_rows(uint8_t* staging, const uint4 (&v)[4], int lane, uint8_t* dst,
+// The warp's 32 rows x 16 N bytes (v: this lane's row; N 4 or 8) to memory through
+// shared memory, so that an instruction writes whole pieces of 32 / N rows
+// instead of 16 bytes of 32.  dst: row 0's piece; rows from `rows` on are not written.
+template <int N>
+__device__ __forceinline__ void bg_store_rows(uint8_t* staging, const uint4 (&v)[N], int lane, uint8_t* dst,
                                               size_t stride, int rows) {
+    auto place = [&](int r, int c) {
+        return reinterpret_cast<uint4*>(staging + r * 16 * N + ((c ^ (N == 8 ? r & 7 : r >> 1 & 3)) << 4));
+    };
     __syncwarp();  // the previous piece has been read
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-        *reinterpret_cast<uint4*>(staging + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)) = v[c];
+    for (int c = 0; c < N; ++c) *place(lane, c) = v[c];
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + (lane >> 2), c = lane & 3;
-        if (r < rows)
-            *reinterpret_cast<uint4*>(dst + (size_t)r * stride + c * 16) =
-                *reinterpret_cast<const uint4*>(staging + r * 64 + ((c ^ (r >> 1 & 3)) << 4));
+    for (int i = 0; i < N; ++i) {
+        const int r = i * (32 / N) + lane / N, c = lane % N;
+        if (r < rows) *reinterpret_cast<uint4*>(dst + (size_t)r * stride + c * 16) = *place(r, c);
     }
 }
 
@@ -211,30 +213,27 @@ __device__ __forceinline__ bool bg_output(const BlockGemmArgs& args, f32x2 (&acc
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int col = col0 + half * 64;
+            if (col >= args.w_rows) continue;
+            uint4 v[8];  // 64 columns: 128 bytes
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {  // 32 columns: 64 bytes
-                const int c0 = col + p * 32;
-                if (c0 >= args.w_rows) continue;
-                uint4 v[4];
+            for (int i = 0; i < 8; ++i) {
+                uint32_t c4[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t c4[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float a, b;
-                        unpack2(acc[half][p * 16 + i * 4 + j], a, b);
-                        c4[j] = EPI == (int)BlockEpi::Half ? half_pair(a * inv, b * inv) : bf16_pair(a, b);
-                    }
-                    v[i] = make_uint4(c4[0], c4[1], c4[2], c4[3]);
+                for (int j = 0; j < 4; ++j) {
+                    float a, b;
+                    unpack2(acc[half][i * 4 + j], a, b);
+                    c4[j] = EPI == (int)BlockEpi::Half ? half_pair(a * inv, b * inv) : bf16_pair(a, b);
                 }
-                uint8_t* dst = static_cast<uint8_t*>(args.out) + (r0 * args.w_rows + c0) * 2;
-                if (c0 + 32 <= args.w_rows) {
-                    bg_store_rows(staging, v, w.lane, dst, (size_t)args.w_rows * 2, rows);
-                } else if (w.lane < rows) {  // the last 16 columns of a matrix
-                    uint4* d = reinterpret_cast<uint4*>(dst + (size_t)w.lane * args.w_rows * 2);
-                    d[0] = v[0];
-                    d[1] = v[1];
-                }
+                v[i] = make_uint4(c4[0], c4[1], c4[2], c4[3]);
+            }
+            uint8_t* dst = static_cast<uint8_t*>(args.out) + (r0 * args.w_rows + col) * 2;
+            if (col + 64 <= args.w_rows) {
+                bg_store_rows(staging, v, w.lane, dst, (size_t)args.w_rows * 2, rows);
+            } else if (w.lane < rows) {  // the last 16 to 48 columns of a matrix
+#pragma unroll
+                for (int i = 0; i < 6; ++i)
+                    if (col + i * 8 < args.w_rows)
+                        reinterpret_cast<uint4*>(dst + (size_t)w.lane * args.w_rows * 2)[i] = v[i];
             }
         }
     }
@@ -259,12 +258,14 @@ constexpr int kBgStage = 3 * kBgHalf;
 constexpr int kBgOffBars = kBgNS * kBgStage;
 constexpr int kBgNumBars = 2 * kBgNS + 8 + 2 + 4;  // full, empty, acc_full/empty[4], teardown, stall, pair[4]
 constexpr int kBgOffTiles = kBgOffBars + kBgNumBars * 8;
-constexpr int kBgOffXch = (kBgOffTiles + (kMaxExperts + 1) * 4 * 2 + 15) / 16 * 16;
-constexpr int kBgOffStaging = kBgOffXch + kBgXch;
-constexpr int kBgOffMisc = kBgOffStaging + kBgEpiWarps * kBgStaging;
-constexpr int kBgSmem = kBgOffMisc + 64 + 1024;  // + alignment slack
-static_assert(kBgOffTiles % 8 == 0, "alignment");
-static_assert(kBgSmem <= 232448, "shared memory budget");
+constexpr int kBgOffMisc = (kBgOffTiles + (kMaxExperts + 1) * 4 * 2 + 15) / 16 * 16;
+constexpr int kBgOffStaging = kBgOffMisc + 64;  // then GateUp's row maxima
+__host__ __device__ constexpr int bg_off_xch(int epi) { return kBgOffStaging + kBgEpiWarps * bg_staging(epi); }
+__host__ __device__ constexpr int bg_smem(int epi) {
+    return bg_off_xch(epi) + (epi == (int)BlockEpi::GateUp ? kBgXch : 0);
+}
+static_assert(kBgOffTiles % 8 == 0 && kBgOffStaging % 16 == 0, "alignment");
+static_assert(bg_smem(0) <= 232448 && bg_smem(1) <= 232448, "shared memory budget");
 
 // Box heights of the activation maps: the smallest that covers a tile's rows.
 __host__ __device__ constexpr int bg_box_rows(int i) { return i == 0 ? 32 : i == 1 ? 64 : kBgRows; }
@@ -275,8 +276,13 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a0,
                       const __grid_constant__ CUtensorMap tmap_a1, const __grid_constant__ CUtensorMap tmap_a2,
                       const BlockGemmArgs args) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // The budget leaves no room to round the base up to the swizzle's 1024 bytes;
+    // dynamic shared memory starts there.
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if ((smem_u32(smem) & 1023u) != 0u) {
+        if (threadIdx.x == 0) atomicOr(args.error, kErrDevice);
+        return;
+    }
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBgOffBars);
     uint64_t* full = bars;              // [NS] the stage landed
     uint64_t* empty = full + kBgNS;     // [NS] the MMAs of the stage completed
@@ -287,7 +293,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     uint64_t* pair_bar = stall_bar + 1; // [4] the two warps of a lane quarter
     int* tile_start = reinterpret_cast<int*>(smem + kBgOffTiles);
     int* row_start = tile_start + (kMaxExperts + 1);
-    float* xch = reinterpret_cast<float*>(smem + kBgOffXch);
+    float* xch = reinterpret_cast<float*>(smem + bg_off_xch(EPI));
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBgOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kBgOffMisc + 8);
 
@@ -405,7 +411,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
         bg_regs_many();
         // ------------------------------------- block sums and the epilogue
         const BgWarp w(warp, lane);
-        uint8_t* staging = smem + kBgOffStaging + (warp - kBgEpi0) * kBgStaging;
+        uint8_t* staging = smem + kBgOffStaging + (warp - kBgEpi0) * bg_staging(EPI);
         uint32_t it = 0, tl = 0;  // blocks, tiles
         bool ok = true;
         for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x, ++tl) {
@@ -454,7 +460,7 @@ cudaError_t launch_block_impl(const BlockGemmArgs& args, cudaStream_t st, bool p
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBgSmem);
+        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bg_smem(EPI));
     });
     if (attr_err != cudaSuccess) return attr_err;
     CUtensorMap tw, ta[3];
@@ -470,7 +476,7 @@ cudaError_t launch_block_impl(const BlockGemmArgs& args, cudaStream_t st, bool p
     long grid = num_sms();
     if (max_tiles < grid) grid = max_tiles;
     if (grid < 1) grid = 1;
-    return launch_kernel(kern, dim3((unsigned)grid), dim3(kBgThreads), kBgSmem, st, pdl, tw, ta[0], ta[1], ta[2],
+    return launch_kernel(kern, dim3((unsigned)grid), dim3(kBgThreads), bg_smem(EPI), st, pdl, tw, ta[0], ta[1], ta[2],
                          args);
 }
 
