@@ -28,15 +28,14 @@
 namespace moe {
 namespace {
 
-// Rows a group on average up to which this kernel is taken, and up to which its
-// tile holds 16 of them.
-#ifndef FEWMAX
-#define FEWMAX 8
-#endif
-#ifndef FEW16
-#define FEW16 4
-#endif
-constexpr long kFewRowsMax = FEWMAX, kFewRows16 = FEW16;
+// Rows a group on average up to which this kernel is taken.  (Layer of 64 experts,
+// H 4096, I 1536, top-2, cold, this kernel against gemm_block.cu, us: 16 tokens 108
+// and 112; 64 tokens, 2 rows a group, 200 and 200; 128 tokens 216 and 222; 256
+// tokens, 8 rows a group, 247 and 245; 512 tokens 290 and 247.)
+constexpr long kFewRowsMax = 4;
+// Activation rows of a tile then.  (32 of them leave room for a stage less: 64
+// tokens 206, 256 tokens 249.)
+constexpr int kFewTile = 16;
 
 constexpr int kGfThreads = 320;
 constexpr int kGfEpi0 = 2;
@@ -540,18 +539,16 @@ cudaError_t launch_few(const BlockGemmArgs& args, cudaStream_t st, bool pdl) {
         return rows <= 16 ? launch_few_ntok<EPI, 16, true>(args, tiles, st, pdl)
                           : launch_few_ntok<EPI, 32, true>(args, tiles, st, pdl);
     }
-    const int ntok = rows <= kFewRows16 * (long)args.n_groups || rows <= 16 ? 16 : 32;
     // at most this many groups have rows, and so many more tiles than whole ones
     const long groups = rows < args.n_groups ? rows : args.n_groups;
-    const long tiles = (rows <= ntok ? groups : rows / ntok + groups) * few_col_blocks<EPI>(args);
-    return ntok == 16 ? launch_few_ntok<EPI, 16, false>(args, tiles, st, pdl)
-                      : launch_few_ntok<EPI, 32, false>(args, tiles, st, pdl);
+    const long tiles = (rows <= kFewTile ? groups : rows / kFewTile + groups) * few_col_blocks<EPI>(args);
+    return launch_few_ntok<EPI, kFewTile, false>(args, tiles, st, pdl);
 }
 
 }  // namespace
 
 bool block_gemm_few_wanted(const BlockGemmArgs& args) {
-    return args.total_rows <= kFewRowsMax * (long)args.n_groups && gf_layout(32, blocks_of(args.K)).ns >= 3;
+    return args.total_rows <= kFewRowsMax * (long)args.n_groups;
 }
 
 cudaError_t launch_block_gemm_few(BlockEpi epi, const BlockGemmArgs& args, cudaStream_t st, bool pdl) {
