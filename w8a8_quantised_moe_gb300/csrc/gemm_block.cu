@@ -16,24 +16,34 @@
 // and h leaves the kernel as E4M3 codes with their scale, never as binary32.
 //   warp 0      TMA producer (ring of kBgNS stages: activation rows and four
 //               quarters of the weight rows, 128 bytes of K each)
-//   warps 1, 2  MMA issuers, one a half (warp 1 also the TMEM allocator): four
-//               K = 32 MMAs a block into one of the half's two 128-column buffers
+//   warp 1      MMA issuer (and TMEM allocator): four K = 32 MMAs a block into one
+//               of two 256-column buffers
 //   warps 4-11  scale and sum the blocks, then the epilogue: four warps a half
 // Persistent grid, tiles dealt round-robin.  Every wait is bounded (ptx.cuh).
 //
-// What bounds it: 8192^3 takes 471 us beside its quantiser, about 980 clocks a
-// block of a tile, of which the MMAs are 512 and the operands' loads, at the rate
-// an SM takes in, 830.  With the sums cut to a quarter of the columns a block took
-// 780, without the loads as well 670.  The sums are a chain for each warp: a wait
-// for the MMAs (170 clocks even when satisfied), eight tensor-memory loads of 16
-// columns (500) and their multiply-adds (80 to 100 a clock and SM), behind two
-// buffers, all that tensor memory holds.  With one commit for both halves, so
-// that all eight warps load and then all add, 8192^3 took 522 us against 506.
-// Tried and slower: CTA pairs that share the weights (less to load, the same
-// chain: 562 against 522), two MMA-issuing threads on alternate blocks (525),
-// sixteen epilogue warps of 64 columns (624 against 492), scalar multiply-adds
-// (642 against 611), the next block's first load before the last sums of a block
-// (560 against 506).
+// What bounds it: a block of a tile takes about 845 clocks (4864 x 4864, K 4096 to
+// 12288, 2070 MHz), of which the MMAs are 512.  Two chains of about that length
+// meet there.  Shared memory: the MMAs read 48 KB and the copies write 48 KB, 750
+// clocks at 128 B.  Tensor memory, full with two buffers: given back, a buffer is
+// summed again after a wait, 512 clocks of MMAs and another wait, while the
+// other's 128 columns a warp take four loads and their multiply-adds; without the
+// sums a block still took 795 to 836.  What counts on both sides are a lone warp's
+// instructions: 65 more per block and scheduler cost 115 clocks, 115 more (scalar
+// multiply-adds) 180.  At 8192^3 (440 us beside its quantiser) the card's power
+// limit sets the clock besides: 1370 W, about 1.75 GHz.
+//
+// Measured on the way, the layer of the quantiser and this kernel at 8192^3, us:
+// issued by one thread whose addresses did not stay uniform, with an issuer a half
+// (the activation rows read twice), 16 columns a load: 490; the issuer as below
+// 484; one 256-column MMA for both halves and 32 columns a load 469.  One barrier
+// for both halves' sums instead of one each 474.  Tried and slower before that:
+// two issuers on alternate blocks, sixteen epilogue warps (624), scalar
+// multiply-adds (540), tests of the next block's barriers ahead of time (504), row
+// scales read four blocks at a time (520) or stored block by block (617).  CTA
+// pairs (cta_group::2, 32 KB a CTA and block) came to 447 here, by drawing less
+// power, and to the same time at 4096^3, but a group's odd tile of 128 rows leaves a
+// CTA idle: 16 experts of 2048 rows took 992 against 837.  Weights multicast to two
+// CTAs: 483 against 490.
 #include <mutex>
 
 #include "block.h"
@@ -44,7 +54,7 @@ namespace {
 
 constexpr int kBgRows = 128;     // activation rows of a CTA
 constexpr int kBgCols = 256;     // weight rows of a tile
-constexpr int kBgThreads = 384;  // producer, two MMA issuers, an idle and 8 epilogue warps
+constexpr int kBgThreads = 384;  // producer, MMA issuer, tile table, idle and 8 epilogue warps
 constexpr int kBgEpi0 = 4;       // first epilogue warp
 constexpr int kBgEpiWarps = 8;
 constexpr int kBgHalf = kBlk * kBlk;         // bytes of 128 rows x 128 channels
@@ -58,13 +68,36 @@ constexpr int kBgXch = 2 * 2 * kBgRows * 4;  // GateUp: row maxima [2 tiles][2 w
 __device__ __forceinline__ void bg_regs_few() { asm volatile("setmaxnreg.dec.sync.aligned.u32 40;"); }
 __device__ __forceinline__ void bg_regs_many() { asm volatile("setmaxnreg.inc.sync.aligned.u32 232;"); }
 
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+
+// This lane's 32 columns from OFF on, of the tensor memory at `a`.
+template <int OFF>
+__device__ __forceinline__ void bg_ld_32(uint32_t a, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32 + %33];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+          "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+          "=r"(r[30]), "=r"(r[31])
+        : "r"(a), "n"(OFF));
+}
+
 // Waits for this warp's tensor-memory loads; the registers pass through, so
 // that no use of them moves above the wait.
-__device__ __forceinline__ void bg_wait_ld(uint32_t (&r)[16]) {
+__device__ __forceinline__ void bg_wait_ld(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15])::"memory");
+                   "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                   "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
 // An epilogue warp: 32 lanes' rows x the 128 columns of half w2.
@@ -80,31 +113,35 @@ struct BgWarp {
 };
 
 // Adds the block's sums at `a` (this warp's 128 columns), times the scales of the
-// first and last 64, to acc[part][column pair]; the next 16 columns load while 16
-// are summed.
-// `release` runs once every column is in registers.
+// first and last 64, to acc[part][column pair].  `release` runs once every column
+// is in registers.  (Offsets within the instruction and 32 columns a load: each
+// instruction less an epilogue warp spends on a block counted, see above.)
 template <class Release>
 __device__ __forceinline__ void bg_add_block(f32x2 (&acc)[2][32], uint32_t a, float s0, float s1, Release release) {
     const f32x2 sc[2] = {pack2(s0, s0), pack2(s1, s1)};
-    uint32_t v[2][16];
-    tmem_ld_16(a, v[0]);
+    auto step = [&](auto part) {
+        constexpr int c = decltype(part)::value;
+        uint32_t v[32];
+        bg_ld_32<c * 32>(a, v);
+        bg_wait_ld(v);
+        if constexpr (c == 3) release();
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        bg_wait_ld(v[c & 1]);
-        if (c < 7) tmem_ld_16(a + (c + 1) * 16, v[(c + 1) & 1]);
-        if (c == 7) release();
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            fma2(acc[c >> 2][(c & 3) * 8 + j],
-                 pack2(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])), sc[c >> 2]);
-    }
+        for (int j = 0; j < 16; ++j)
+            fma2(acc[c >> 1][(c & 1) * 16 + j],
+                 pack2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), sc[c >> 1]);
+    };
+    step(Int<0>{});
+    step(Int<1>{});
+    step(Int<2>{});
+    step(Int<3>{});
 }
 
 // The scales that an epilogue thread applies, read one block ahead: its row's
 // (blocks of a row are next to each other: seven of eight reads hit L1) and the
-// weights' two.  Measured at 8192^3, us: this 522; the rows' scales stored block
-// by block, one line a warp and block, 617; staged in shared memory by a fourth
-// warp or by the producer's copies, behind barriers of their own, 608 and 728.
+// weights' two, one where both halves' parts share it.  Measured at 8192^3 on the
+// first forms of this kernel, us: this 522; the rows' scales stored block by block,
+// one line a warp and block, 617; staged in shared memory by a fourth warp or by
+// the producer's copies, behind barriers of their own, 608 and 728.
 struct BgScales {
     const float *sx, *sw0, *sw1;
     float x, w0, w1;
@@ -118,15 +155,16 @@ struct BgScales {
         sw1 = a.w_scale + ((size_t)g * nb + b1) * nkb;
         x = __ldg(sx);
         w0 = __ldg(sw0);
-        w1 = __ldg(sw1);
+        w1 = EPI == (int)BlockEpi::GateUp ? __ldg(sw1) : w0;
     }
+    template <int EPI>
     __device__ __forceinline__ void next(int kb, int nkb, float& s0, float& s1) {
         s0 = __fmul_rn(x, w0);
-        s1 = __fmul_rn(x, w1);
+        s1 = EPI == (int)BlockEpi::GateUp ? __fmul_rn(x, w1) : s0;
         if (kb + 1 < nkb) {
             x = __ldg(sx + kb + 1);
             w0 = __ldg(sw0 + kb + 1);
-            w1 = __ldg(sw1 + kb + 1);
+            if (EPI == (int)BlockEpi::GateUp) w1 = __ldg(sw1 + kb + 1);
         }
     }
 };
@@ -304,13 +342,13 @@ __global__ void __launch_bounds__(kBgThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kBgNS; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 2);
+            mbar_init(&empty[s], 1);
         }
         for (int d = 0; d < 4; ++d) {
             mbar_init(&acc_full[d], 1);
             mbar_init(&acc_empty[d], kBgEpiWarps / 2);
         }
-        mbar_init(teardown, 2);
+        mbar_init(teardown, 1);
         mbar_init(stall_bar, 1);
         for (int i = 0; i < 4; ++i) mbar_init(&pair_bar[i], 2);
         *abort_flag = 0;
@@ -377,33 +415,43 @@ __global__ void __launch_bounds__(kBgThreads, 1)
                         mbar_wait_drain(&full[s], (last / kBgNS) & 1u);
                     }
             }
-        } else if (warp < 3) {
-            // ----------------------------------------------------- MMA issuers
-            // warp 1 the first half's, warp 2 the second's
-            if (lane == 0) {
-                constexpr uint32_t idesc = idesc_e4m3(kBgRows, kBlk);
-                const int h = warp - 1;
-                uint32_t it = 0;
-                bool ok = true;
-                for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x)
-                    for (int kb = 0; kb < nkb; ++kb, ++it) {
-                        const uint32_t s = it % kBgNS, d = it & 1u;
-                        if (!mbar_wait(&acc_empty[d * 2 + h], ((it >> 1) & 1u) ^ 1u, ctl) ||
-                            !mbar_wait(&full[s], (it / kBgNS) & 1u, ctl)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t a_base = smem_u32(smem + s * kBgStage);
-                        const uint64_t a_desc = smem_desc_sw128(a_base),
-                                       b_desc = smem_desc_sw128(a_base + (1 + h) * kBgHalf);
+        } else if (warp == 1) {
+            // ------------------------------------------------------ MMA issuer
+            // The whole warp runs the loop, so that what the MMAs take stays uniform, and
+            // asks every barrier before it uses an answer; lane 0 issues.
+            constexpr uint32_t idesc = idesc_e4m3(kBgRows, kBgCols);
+            const uint64_t a0 = smem_desc_sw128(smem_u32(smem)), b0 = smem_desc_sw128(smem_u32(smem) + kBgHalf);
+            const int cta = blockIdx.x, ctas = gridDim.x;
+            const int my_tiles = cta < total_tiles ? (total_tiles - 1 - cta) / ctas + 1 : 0;
+            uint32_t s = 0, ph = 0, d = 0, dph = 1;  // stage, its phase, buffer, its phase
+            for (int n = my_tiles * nkb; n > 0; --n) {
+                const bool free0 = mbar_try_wait(&acc_empty[d * 2], dph),
+                           free1 = mbar_try_wait(&acc_empty[d * 2 + 1], dph),
+                           landed = mbar_try_wait(&full[s], ph);
+                if (!__all_sync(0xffffffffu, free0 && free1 && landed) &&
+                    (!warp_wait(&acc_empty[d * 2], dph, ctl) || !warp_wait(&acc_empty[d * 2 + 1], dph, ctl) ||
+                     !warp_wait(&full[s], ph, ctl)))
+                    break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t a = a0 + (uint64_t)(s * (kBgStage >> 4)), b = b0 + (uint64_t)(s * (kBgStage >> 4));
 #pragma unroll
-                        for (int ks = 0; ks < kBlk / 32; ++ks)  // 32 bytes of K per MMA
-                            mma_e4m3(tmem + d * kBgCols + h * kBlk, a_desc + (uint64_t)(ks * 2),
-                                     b_desc + (uint64_t)(ks * 2), idesc, ks != 0 ? 1u : 0u);
-                        mma_commit(&acc_full[d * 2 + h]);
-                        mma_commit(&empty[s]);
-                    }
+                    for (int ks = 0; ks < kBlk / 32; ++ks)  // 32 bytes of K per MMA
+                        mma_e4m3(tmem + d * kBgCols, a + (uint64_t)(ks * 2), b + (uint64_t)(ks * 2), idesc,
+                                 ks != 0 ? 1u : 0u);
+                    mma_commit(&acc_full[d * 2]);
+                    mma_commit(&acc_full[d * 2 + 1]);
+                    mma_commit(&empty[s]);
+                }
+                __syncwarp();
+                if (++s == kBgNS) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+                d ^= 1u;
+                dph ^= d ^ 1u;
+            }
+            if (lane == 0) {
                 mma_commit(teardown);
                 mbar_wait_drain(teardown, 0);
             }
@@ -413,7 +461,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
         // ------------------------------------- block sums and the epilogue
         const BgWarp w(warp, lane);
         uint8_t* staging = smem + kBgOffStaging + (warp - kBgEpi0) * bg_staging(EPI);
-        uint32_t it = 0, tl = 0;  // blocks, tiles
+        uint32_t d = 0, ph = 0, tl = 0;  // buffer, its phase, tiles
         bool ok = true;
         for (int tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x, ++tl) {
             int g, cb, row0, nvalid;
@@ -423,11 +471,10 @@ __global__ void __launch_bounds__(kBgThreads, 1)
             for (int j = 0; j < 32; ++j) acc[0][j] = acc[1][j] = 0ull;
             BgScales sc;
             sc.start<EPI>(args, g, cb, w.w2, row0 + min(w.row, nvalid - 1), nkb);
-            for (int kb = 0; kb < nkb; ++kb, ++it) {
+            for (int kb = 0; kb < nkb; ++kb) {
                 float s0, s1;
-                sc.next(kb, nkb, s0, s1);
-                const uint32_t d = it & 1u;
-                if (!warp_wait(&acc_full[d * 2 + w.w2], (it >> 1) & 1u, ctl)) {
+                sc.next<EPI>(kb, nkb, s0, s1);
+                if (!warp_wait(&acc_full[d * 2 + w.w2], ph, ctl)) {
                     ok = false;
                     break;
                 }
@@ -441,6 +488,8 @@ __global__ void __launch_bounds__(kBgThreads, 1)
                     bg_add_block(acc, w.addr(tmem + d * kBgCols), s0, s1, release);
                 else
                     release();
+                d ^= 1u;
+                ph ^= d ^ 1u;
             }
             ok = ok && bg_output<EPI>(args, acc, w, row0, nvalid, cb, xch, pair_bar, tl, staging, ctl);
         }
