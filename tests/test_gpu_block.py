@@ -269,7 +269,7 @@ def test_layer_on_a_side_stream_with_no_tokens_between():
     assert torch.equal(out, want)
 
 
-@pytest.mark.parametrize("M", [20, 400])
+@pytest.mark.parametrize("M", [4, 20, 400])
 def test_a_wait_that_runs_out_is_reported(monkeypatch, M):
     """The test hook makes the tensor-core product's producer wait for nothing."""
     g = gen(11)
@@ -285,6 +285,25 @@ def test_a_wait_that_runs_out_is_reported(monkeypatch, M):
         monkeypatch.delenv("MOE_INJECT")
         moe.set_wait_timeout_ns(prev)
     assert torch.equal(moe.fp8_block_linear(x, w_q, w_s, workspace=ws), want)
+    assert moe.device_error(ws) == 0
+
+
+# one launch's tiles split over clusters, whole tiles, grouped few rows, many rows
+@pytest.mark.parametrize("shape", [(3, 512, 256, 8, 2), (8, 2048, 1024, 64, 4), (40, 512, 256, 64, 2),
+                                   (300, 512, 256, 8, 2)])
+def test_a_wait_of_the_layer_that_runs_out_is_reported(monkeypatch, shape):
+    layer = Layer(*shape, seed=13)
+    ws = moe.new_workspace(moe.fp8_block_workspace_size(*shape))
+    want = moe.fp8_block_forward(*layer.args(), workspace=ws)
+    prev = moe.set_wait_timeout_ns(2_000_000)
+    try:
+        monkeypatch.setenv("MOE_INJECT", "stall")
+        moe.fp8_block_forward(*layer.args(), workspace=ws)
+        assert moe.device_error(ws) == -5
+    finally:
+        monkeypatch.delenv("MOE_INJECT")
+        moe.set_wait_timeout_ns(prev)
+    assert torch.equal(moe.fp8_block_forward(*layer.args(), workspace=ws), want)
     assert moe.device_error(ws) == 0
 
 
