@@ -1,0 +1,101 @@
+"""The block-scaled layer on inputs whose every intermediate is exact up to the codes
+of h, so that y shows each code: one nonzero product a sum in the second product, a
+weight of one per token, and gates where silu is exact in binary32."""
+import pytest
+import torch
+
+import block_reference as ref
+import w8a8_quantised_moe_gb300 as moe
+
+pytestmark = pytest.mark.gpu
+
+H, I = 256, 256
+ONE = 0x38  # E4M3 code of 1.0
+UP = 2.0**60  # scale of the second product's unit weights: small h become normal numbers of y
+
+
+class ExactLayer:
+    """h[t][n] = silu(gate_t * |c|) * p_t * u for values[expert of t][n] = c * u, exactly.
+
+    values: integers, products of a c of 1..15 (a weight of the gate row) and a u of
+    -255..255 (16 hi + lo in two weights of the up row).  p_t: a power of two, at least 1
+    with a gate of 32 p_t (1 + exp(-32) rounds to 1, so silu(g) = g), or below 2^-30
+    with a gate of p_t (1 + exp(-g) rounds to 2, so silu(g) = g / 2)."""
+
+    def __init__(self, values, p):
+        E, T = len(values), len(p)
+        v = torch.tensor(values)
+        c = torch.ones_like(v)
+        for d in range(2, 16):
+            c = torch.where((v.abs() > 255 * c) & (v % d == 0), d, c)
+        u = v // c
+        assert v.shape == (E, I) and u.abs().max() <= 255
+        codes = ref.e4m3_codes(torch.arange(16).float()).int()
+        sign = 128 * (u < 0)
+        w13 = torch.zeros(E, 2 * I, H, dtype=torch.uint8)
+        w13[:, :I, 2] = codes[c].to(torch.uint8)
+        w13[:, I:, 0] = (codes[u.abs() // 16] + sign * (u.abs() >= 16)).to(torch.uint8)
+        w13[:, I:, 1] = (codes[u.abs() % 16] + sign * (u.abs() % 16 > 0)).to(torch.uint8)
+        w2 = torch.zeros(E, H, I, dtype=torch.uint8)
+        w2[:, torch.arange(H), torch.arange(H)] = ONE
+        p = torch.tensor(p, dtype=torch.float64)
+        assert ((p >= 1) | (p < 2.0**-30)).all()
+        gate = torch.where(p >= 1, 32 * p, p)
+        self.e = torch.arange(T) % E
+        x = torch.zeros(T, H, dtype=torch.float64)
+        x[:, 0], x[:, 1], x[:, 2], x[:, 3] = 16 * p, p, gate, 448 * p  # the scale of this block is p
+        x[torch.arange(T), 128 + self.e] = p  # the router's choice
+        router_w = torch.zeros(H, E)
+        router_w[128 + torch.arange(E), torch.arange(E)] = 1
+        self.h = (torch.where(p >= 1, gate, gate / 2) * p)[:, None] * v[self.e].double()
+        assert torch.equal(self.h.float().double(), self.h)
+        self.args = tuple(t.cuda() if t is not None else None for t in (
+            x.bfloat16(), router_w, None, w13, torch.ones(E, 2 * I // 128, H // 128), w2,
+            torch.full((E, H // 128, I // 128), UP))) + (1,)
+        assert torch.equal(x.bfloat16().double(), x)
+
+    def codes(self):
+        """Codes [T, I] of h and the value that each stands for in y."""
+        code, s = ref.quantize_rows(self.h.float())
+        return code, ref.e4m3_values()[code.long()] * s.double().repeat_interleave(128, 1) * UP
+
+    def check(self):
+        y = moe.fp8_block_forward(*self.args).double().cpu()
+        _, want = self.codes()
+        # neighbouring codes are at least 2^-4 of each other apart; y is rounded to bf16's 2^-8
+        bad = (y - want).abs() > 2.0**-7 * want.abs()
+        bad |= ~y.isfinite()
+        assert not bad.any(), (bad.sum().item(), y[bad][:4], want[bad][:4])
+
+
+# tokens, experts: the form for a few tokens, few rows an expert, many rows
+FORMS = [(7, 2), (40, 16), (300, 2)]
+
+
+def random_values(E, seed):
+    g = torch.Generator().manual_seed(seed)
+    v = torch.randint(-255, 256, (E, I), generator=g)
+    v[:, ::5] = 0  # channels that are exactly zero
+    v[:, 128:] = v[:, 128:] // 16  # a block of smaller values
+    return v.tolist()
+
+
+@pytest.mark.parametrize("T,E", FORMS)
+def test_codes_of_h_over_the_range_of_binary32(T, E):
+    """Rows whose h reaches from binary32's smallest subnormal to 2^22."""
+    powers = [2.0**e for e in (-74, -72, -70, -67, -66, -65, -64, -63, -62, -60, -58, -50, -32, 0, 4)]
+    ExactLayer(random_values(E, T), [powers[(4 * t) % len(powers)] for t in range(T)]).check()
+
+
+@pytest.mark.parametrize("T,E", FORMS)
+def test_codes_of_h_next_to_midpoints(T, E):
+    """Quotients so near the midpoint of two codes that a product with the rounded
+    reciprocal of the scale lands on its other side: block maximum, and values under it."""
+    near = [(868, [837]), (1148, [1107]), (1540, [1045, 1265, 1485]), (1736, [837, 1674]), (2296, [1107, 2214]),
+            (2324, [2241]), (3080, [1045, 1265, 1485, 2090, 2530, 2970]), (3388, [2299]), (3472, [837, 1674])]
+    blocks = [[top, *v, *(-i for i in v)] + [0] * (127 - 2 * len(v)) for top, v in near]
+    layer = ExactLayer([blocks[2 * e % 9] + blocks[(2 * e + 1) % 9] for e in range(E)], [1.0] * T)
+    h = layer.h.float().reshape(T, 2, 128)
+    product = h * (1 / (h.abs().amax(2) * ref.RECIPROCAL))[:, :, None]
+    assert (ref.e4m3_codes(product.reshape(T, I).clamp(-448, 448)) != layer.codes()[0]).sum() >= 2 * T
+    layer.check()

@@ -217,20 +217,16 @@ __device__ __forceinline__ bool bg_output(const BlockGemmArgs& args, f32x2 (&acc
         if (!warp_wait(&pair_bar[w.q], tl & 1u, ctl)) return false;
         amax = amax_nan(amax, mine[(w.w2 ^ 1) * kBgRows + w.row]);
         const float s = block_scale(amax);
-        // the quotient as a product with 1 / s: h is rounded already, see silu_mul
-        const float inv = s == 0.f ? 0.f : __fdiv_rn(1.0f, s);
+        const BlockQuot quot(s);
         const int n_ch = args.up_offset;
         uint4 v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+            float h[16];
             uint32_t c4[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float h0, h1, h2, h3;
-                unpack2(acc[0][i * 8 + j * 2], h0, h1);
-                unpack2(acc[0][i * 8 + j * 2 + 1], h2, h3);
-                c4[j] = e4m3_pair(h0 * inv, h1 * inv) | (e4m3_pair(h2 * inv, h3 * inv) << 16);
-            }
+            for (int j = 0; j < 8; ++j) unpack2(acc[0][i * 8 + j], h[2 * j], h[2 * j + 1]);
+            quot.codes(h, c4);
             v[i] = make_uint4(c4[0], c4[1], c4[2], c4[3]);
         }
         bg_store_rows(staging, v, w.lane, args.q_out + r0 * n_ch + cb * kBlk + w.w2 * 64, n_ch, rows);

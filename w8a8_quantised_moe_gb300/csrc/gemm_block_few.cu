@@ -117,10 +117,10 @@ __device__ __forceinline__ void few_output(const BlockGemmArgs& args, int r, int
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) amax = amax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
         const float s = block_scale(amax);
-        const float inv = s == 0.f ? 0.f : __fdiv_rn(1.0f, s);  // h is rounded already, see silu_mul
+        uint32_t code[1];
+        BlockQuot(s).codes(h, code);
         const size_t n_ch = (size_t)args.up_offset;
-        *reinterpret_cast<uint32_t*>(args.q_out + (size_t)r * n_ch + cb * kBlk + lane * 4) =
-            e4m3_pair(h[0] * inv, h[1] * inv) | (e4m3_pair(h[2] * inv, h[3] * inv) << 16);
+        *reinterpret_cast<uint32_t*>(args.q_out + (size_t)r * n_ch + cb * kBlk + lane * 4) = code[0];
         if (lane == 0) args.s_out[(size_t)r * (n_ch / kBlk) + cb] = s;
     } else {
 #pragma unroll
