@@ -99,3 +99,40 @@ def test_codes_of_h_next_to_midpoints(T, E):
     product = h * (1 / (h.abs().amax(2) * ref.RECIPROCAL))[:, :, None]
     assert (ref.e4m3_codes(product.reshape(T, I).clamp(-448, 448)) != layer.codes()[0]).sum() >= 2 * T
     layer.check()
+
+
+# ---------------------------------------------------------------- rows between the product and the combine
+
+
+def set_rows(layer, rows, scale):
+    """Rows of the second product's weights {column: {channel: weight}}, each an E4M3 value."""
+    w2 = torch.zeros(H, I, dtype=torch.uint8)
+    for c, row in rows.items():
+        for n, w in row.items():
+            w2[c, n] = ref.e4m3_codes(torch.tensor(w))
+    layer.args[5][:] = w2.cuda()
+    layer.args[6][:] = scale
+
+
+@pytest.mark.parametrize("T,E", FORMS)
+def test_rows_are_rounded_once(T, E):
+    """257 + 2^-6 lies above the midpoint of bf16's 256 and 258, 259 - 2^-6 below that of 258
+    and 260; 11 bits in between would take each to the midpoint and then to the other neighbour."""
+    layer = ExactLayer([[448, 256, 1, -1] + [0] * (I - 4)] * E, [1.0] * T)
+    up, down = {1: 1.0, 2: 1.0, 3: -(2.0**-6)}, {1: 1.0, 2: 3.0, 3: 2.0**-6}
+    set_rows(layer, {c: (up, down)[c % 2] for c in range(H)}, 1.0 / 32)  # h = 32 * values
+    y = moe.fp8_block_forward(*layer.args).float().cpu()
+    assert (y[:, ::2] == 258).all() and (y[:, 1::2] == 258).all()
+
+
+@pytest.mark.parametrize("T,E", FORMS)
+def test_an_infinite_sum_leaves_its_neighbours(T, E):
+    """One column's sum passes binary32's range; the others of its 128 stay what they are."""
+    layer = ExactLayer([[448, 1, 7] + [0] * (I - 3)] * E, [1.0] * T)
+    rows = {c: {1: 1.0} if c % 3 else {2: 1.0} for c in range(H)}
+    rows[5] = {0: 448.0, 1: 448.0, 2: 448.0}
+    set_rows(layer, rows, 2.0**112 / 32)
+    y = moe.fp8_block_forward(*layer.args).double().cpu()
+    want = torch.where(torch.arange(H) % 3 == 0, 7.0, 1.0).double() * 2.0**112
+    want[5] = float("inf")
+    assert torch.equal(y, want.expand(T, H))

@@ -34,7 +34,7 @@ bool lin_shape_ok(int64_t M, int64_t N, int64_t K) {
 // one byte, a scale per slot and 128 channels.
 struct BlockFwdLayout {
     size_t err, counts, wsplit, logits, topk_ids, topk_w, rank, hist, offsets, slot_of, slot_token, q_x, s_x, q_h,
-        s_h, o, s_o, done, total;
+        s_h, o, done, total;
 };
 BlockFwdLayout block_fwd_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
     BlockFwdLayout L{};
@@ -63,8 +63,7 @@ BlockFwdLayout block_fwd_layout(int64_t T, int64_t H, int64_t I, int64_t E, int6
     L.s_x = take(S * (H / kBlk) * 4);
     L.q_h = take(S * I);
     L.s_h = take(S * (I / kBlk) * 4);
-    L.o = take(S * H * 2);
-    L.s_o = take(S * (H / kBlk) * 4);
+    L.o = take(S * H * 4);
     L.done = take((H + 255) / 256 * 4);
     L.total = off;
     return L;
@@ -184,8 +183,7 @@ moe_status_t moe_w8a8_fp8_block_forward(const uint16_t* x, const float* router_w
         g.w_rows = (int)H;
         g.up_offset = 0;
         g.total_rows = S;
-        g.out = at<uint16_t>(workspace, L.o);
-        g.s_out = at<float>(workspace, L.s_o);
+        g.out = at<float>(workspace, L.o);
     };
     cudaError_t e;
     if (block_few_tokens(T, E, top_k)) {  // three launches
@@ -216,7 +214,7 @@ moe_status_t moe_w8a8_fp8_block_forward(const uint16_t* x, const float* router_w
         first_product((int)T);
         if ((e = launch_block_gemm_few(BlockEpi::GateUp, g, st, pdl)) != cudaSuccess) return from_cuda(e);
         second_product();
-        return from_cuda(launch_block_gemm_few(BlockEpi::Half, g, st, pdl));
+        return from_cuda(launch_block_gemm_few(BlockEpi::F32, g, st, pdl));
     }
     e = launch_router(x, router_w, router_bias, (int)T, (int)H, (int)E, (int)top_k,
                                   at<uint16_t>(workspace, L.wsplit), at<float>(workspace, L.logits),
@@ -240,10 +238,9 @@ moe_status_t moe_w8a8_fp8_block_forward(const uint16_t* x, const float* router_w
     if ((e = product(BlockEpi::GateUp)) != cudaSuccess) return from_cuda(e);
 
     second_product();
-    if ((e = product(BlockEpi::Half)) != cudaSuccess) return from_cuda(e);
-    return from_cuda(launch_combine_half(at<uint16_t>(workspace, L.o), at<float>(workspace, L.s_o),
-                                         at<int32_t>(workspace, L.slot_of), at<float>(workspace, L.topk_w), (int)T,
-                                         (int)H, (int)top_k, y, err, st, pdl));
+    if ((e = product(BlockEpi::F32)) != cudaSuccess) return from_cuda(e);
+    return from_cuda(launch_combine(at<float>(workspace, L.o), at<int32_t>(workspace, L.slot_of),
+                                    at<float>(workspace, L.topk_w), (int)T, (int)H, (int)top_k, y, err, st, pdl));
 }
 
 moe_status_t moe_w8a8_norm_residual(const void* x, int x_fp32, const uint16_t* branch, const uint16_t* post_w,

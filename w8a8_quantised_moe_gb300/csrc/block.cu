@@ -1,4 +1,4 @@
-// block.cu -- quantisers and the combine of the block-scaled FP8 operators.
+// block.cu -- quantisers of the block-scaled FP8 operators.
 //
 // A block's scale is s = amax * (1/448) (one binary32 product with the rounded
 // reciprocal) and its codes are the E4M3 values nearest to the binary32
@@ -105,40 +105,6 @@ __global__ void __launch_bounds__(256) quantize_rows_block_kernel(
     }
 }
 
-// A warp per (token, 256 columns): the token's k rows are all in flight before
-// the sum, which runs in top-k order.
-template <int KMAX>
-__global__ void __launch_bounds__(256) combine_half_kernel(const uint16_t* __restrict__ o,
-                                                           const float* __restrict__ o_scale,
-                                                           const int32_t* __restrict__ slot_of,
-                                                           const float* __restrict__ topk_w, int T, int H, int k,
-                                                           uint16_t* __restrict__ y, int* __restrict__ error) {
-    const int lane = threadIdx.x & 31;
-    const int parts = (H + 255) / 256;
-    const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int t = (int)(item / parts), col = (int)(item - (int64_t)t * parts) * 256 + lane * 8;
-    pdl_wait();
-    pdl_trigger();
-    if (t >= T || col >= H) return;
-    uint4 v[KMAX];
-    float w[KMAX];
-#pragma unroll
-    for (int j = 0; j < KMAX; ++j) {
-        v[j] = make_uint4(0u, 0u, 0u, 0u);
-        w[j] = 0.f;
-        if (j >= k) continue;
-        const int slot = slot_of[(size_t)t * k + j];
-        if (!in_range(slot, 0, (long long)T * k, error)) continue;  // checked build: contributes nothing
-        v[j] = *reinterpret_cast<const uint4*>(o + (size_t)slot * H + col);
-        w[j] = topk_w[(size_t)t * k + j] * o_scale[(size_t)slot * (H / kBlk) + col / kBlk];
-    }
-    float a[8] = {};
-#pragma unroll
-    for (int j = 0; j < KMAX; ++j) add_half8(a, v[j], w[j]);
-    *reinterpret_cast<uint4*>(y + (size_t)t * H + col) =
-        make_uint4(bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3]), bf16_pair(a[4], a[5]), bf16_pair(a[6], a[7]));
-}
-
 // Four vectors a lane where that still leaves work for every SM, else one.
 template <bool SLOTS, typename... Args>
 cudaError_t launch_quantize_rows(cudaStream_t st, bool pdl, const uint16_t* x, int M, int K, Args... args) {
@@ -173,21 +139,6 @@ cudaError_t launch_permute_quant_block(const uint16_t* x, const int32_t* topk_id
                                        bool pdl) {
     if (T == 0) return cudaSuccess;
     return launch_quantize_rows<true>(st, pdl, x, T, H, q, s, topk_ids, rank, base, E, k, slot_of, slot_token, error);
-}
-
-cudaError_t launch_combine_half(const uint16_t* o, const float* o_scale, const int32_t* slot_of, const float* topk_w,
-                                int T, int H, int k, uint16_t* y, int* error, cudaStream_t st, bool pdl) {
-    if (T == 0) return cudaSuccess;
-    const int64_t items = (int64_t)T * ((H + 255) / 256);
-    const dim3 grid((unsigned)((items + 7) / 8)), block(256);
-    if (k <= 2)
-        return launch_kernel(combine_half_kernel<2>, grid, block, 0, st, pdl, o, o_scale, slot_of, topk_w, T, H, k, y,
-                             error);
-    if (k <= 4)
-        return launch_kernel(combine_half_kernel<4>, grid, block, 0, st, pdl, o, o_scale, slot_of, topk_w, T, H, k, y,
-                             error);
-    return launch_kernel(combine_half_kernel<8>, grid, block, 0, st, pdl, o, o_scale, slot_of, topk_w, T, H, k, y,
-                         error);
 }
 
 }  // namespace moe

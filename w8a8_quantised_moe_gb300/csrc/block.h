@@ -16,7 +16,7 @@ __host__ __device__ constexpr int blocks_of(int n) { return (n + kBlk - 1) / kBl
 // What a block-scaled product writes.
 enum class BlockEpi : int {
     GateUp = 0,  // h = silu(gate) * up, requantised: E4M3 codes and a scale per row and 128 channels
-    Half = 1,    // fp16 rows with a power-of-two scale per 128 columns (second expert product)
+    F32 = 1,     // binary32 rows (second expert product)
     BF16 = 2     // bf16 rows (linear layer)
 };
 
@@ -31,24 +31,24 @@ struct BlockGemmArgs {
     int n_groups;
     int total_rows;          // activation rows
     const int32_t* offsets;  // [n_groups + 1] first row of each group, or nullptr: one group
-    void* out;               // Half / BF16: [total_rows][w_rows]
+    void* out;               // F32 / BF16: [total_rows][w_rows]
     uint8_t* q_out;          // GateUp: codes [total_rows][up_offset]
-    float* s_out;            // GateUp: scales [total_rows][up_offset / 128]; Half: [total_rows][w_rows / 128]
+    float* s_out;            // GateUp: scales [total_rows][up_offset / 128]
     int* error;              // sticky device error word
     uint64_t timeout_ns;
     int stall;               // test hook (MOE_INJECT=stall)
     // few tokens only (ids != nullptr; offsets unused): total_rows activation
     // rows, all of them in every tile
     const int32_t* ids;      // [T][k] experts
-    const float* topk_w;     // [T][k] (Half)
+    const float* topk_w;     // [T][k] (F32)
     int T, k;
-    unsigned int* done;      // [column blocks] finished experts, zero before the launch (Half)
-    uint16_t* y;             // bf16 [T][w_rows] (Half): the combine
+    unsigned int* done;      // [column blocks] finished experts, zero before the launch (F32)
+    uint16_t* y;             // bf16 [T][w_rows] (F32): the combine
 };
 
 // Tensor-core product, groups of many rows (gemm_block.cu).
 cudaError_t launch_block_gemm(BlockEpi epi, const BlockGemmArgs& args, cudaStream_t st, bool pdl);
-// The same for groups of a few rows (gemm_block_few.cu), GateUp and Half; reads
+// The same for groups of a few rows (gemm_block_few.cu), GateUp and F32; reads
 // the offsets before its wait for the previous kernel, which must have waited
 // for the kernel that wrote them.
 bool block_gemm_few_wanted(const BlockGemmArgs& args);
@@ -97,11 +97,6 @@ cudaError_t launch_permute_quant_block(const uint16_t* x, const int32_t* topk_id
                                        const int32_t* base, int T, int H, int E, int k, int32_t* slot_of,
                                        int32_t* slot_token, uint8_t* q, float* s, int* error, cudaStream_t st,
                                        bool pdl);
-
-// y[t] = bf16(sum_j w[t][j] * o[slot(t, j)]) over the scaled fp16 rows of
-// BlockEpi::Half (o [S][H], o_scale [S][H / 128]).
-cudaError_t launch_combine_half(const uint16_t* o, const float* o_scale, const int32_t* slot_of, const float* topk_w,
-                                int T, int H, int k, uint16_t* y, int* error, cudaStream_t st, bool pdl);
 
 // Shape of the gate of norm_residual.
 enum class GateForm : int { None = 0, Channel = 1, Token = 2, Element = 3 };

@@ -2,7 +2,6 @@
 #pragma once
 
 #include <cstdint>
-#include <cuda_fp16.h>
 
 #include "block.h"
 
@@ -94,34 +93,6 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
-}
-
-// Two fp16 (lo in the low half), each rounded to nearest even.
-__device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-// Scale s = 2^(e - 14), amax in [2^e, 2^(e + 1)), and inv = 1 / s: v * inv is
-// below 2^15, so it fits fp16, and what lies 2^-28 below the largest still has
-// fp16's full 11 bits: an eighth of bf16's rounding error for the same bytes.  A
-// NaN or an infinity keeps the scale 1 and stays what it is.
-__device__ __forceinline__ void half_scale(float amax, float& s, float& inv) {
-    const uint32_t e = min(max(__float_as_uint(amax) >> 23, 16u), 254u);
-    const bool finite = amax < INFINITY;
-    s = finite ? __uint_as_float((e - 14) << 23) : 1.f;
-    inv = finite ? __uint_as_float((268 - e) << 23) : 1.f;
-}
-
-// a += w * eight fp16 values.
-__device__ __forceinline__ void add_half8(float (&a)[8], const uint4& v, float w) {
-    const __half2* h = reinterpret_cast<const __half2*>(&v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(h[i]);
-        a[2 * i] = fmaf(w, f.x, a[2 * i]);
-        a[2 * i + 1] = fmaf(w, f.y, a[2 * i + 1]);
-    }
 }
 
 // h = g / (1 + exp(-g)) * u.  The exponential and the quotient are the fast

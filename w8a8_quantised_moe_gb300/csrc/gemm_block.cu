@@ -58,7 +58,7 @@ constexpr int kBgThreads = 384;  // producer, MMA issuer, tile table, idle and 8
 constexpr int kBgEpi0 = 4;       // first epilogue warp
 constexpr int kBgEpiWarps = 8;
 constexpr int kBgHalf = kBlk * kBlk;         // bytes of 128 rows x 128 channels
-// per epilogue warp: 32 rows x 64 codes, or x 64 columns of two bytes
+// per epilogue warp: 32 rows x 64 codes, or x 128 bytes of columns
 __host__ __device__ constexpr int bg_staging(int epi) { return epi == (int)BlockEpi::GateUp ? 32 * 64 : 32 * 128; }
 constexpr int kBgXch = 2 * 2 * kBgRows * 4;  // GateUp: row maxima [2 tiles][2 warps][rows]
 
@@ -233,37 +233,27 @@ __device__ __forceinline__ bool bg_output(const BlockGemmArgs& args, f32x2 (&acc
         if (w.w2 == 0 && w.lane < rows) args.s_out[(r0 + w.lane) * (n_ch / kBlk) + cb] = s;
     } else {
         const int col0 = cb * kBgCols + w.w2 * kBlk;  // this warp's 128 columns
-        float inv = 1.f;
-        if (EPI == (int)BlockEpi::Half) {
-            float amax = 0.f, s;
+        constexpr int kElem = EPI == (int)BlockEpi::F32 ? 4 : 2, kCols = 128 / kElem;  // columns of a piece
 #pragma unroll
-            for (int j = 0; j < 64; ++j) {
-                float a, b;
-                unpack2(acc[j >> 5][j & 31], a, b);
-                amax = amax_nan(amax_nan(amax, a), b);
-            }
-            half_scale(amax, s, inv);
-            if (w.lane < rows && col0 < args.w_rows) args.s_out[(r0 + w.lane) * (args.w_rows / kBlk) + col0 / kBlk] = s;
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int col = col0 + half * 64;
+        for (int piece = 0; piece < kBlk / kCols; ++piece) {
+            const int col = col0 + piece * kCols;
             if (col >= args.w_rows) continue;
-            uint4 v[8];  // 64 columns: 128 bytes
+            uint4 v[8];  // this lane's 128 bytes
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 uint32_t c4[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
+                    const int p = piece * kCols / 2 + (i * 4 + j) * kCols / 64;  // column pair
                     float a, b;
-                    unpack2(acc[half][i * 4 + j], a, b);
-                    c4[j] = EPI == (int)BlockEpi::Half ? half_pair(a * inv, b * inv) : bf16_pair(a, b);
+                    unpack2(acc[p >> 5][p & 31], a, b);
+                    c4[j] = EPI != (int)BlockEpi::F32 ? bf16_pair(a, b) : __float_as_uint(j & 1 ? b : a);
                 }
                 v[i] = make_uint4(c4[0], c4[1], c4[2], c4[3]);
             }
-            uint8_t* dst = static_cast<uint8_t*>(args.out) + (r0 * args.w_rows + col) * 2;
-            if (col + 64 <= args.w_rows) {
-                bg_store_rows(staging, v, w.lane, dst, (size_t)args.w_rows * 2, rows);
+            uint8_t* dst = static_cast<uint8_t*>(args.out) + (r0 * args.w_rows + col) * kElem;
+            if (EPI == (int)BlockEpi::F32 || col + kCols <= args.w_rows) {  // F32: w_rows is a multiple of 128
+                bg_store_rows(staging, v, w.lane, dst, (size_t)args.w_rows * kElem, rows);
             } else if (w.lane < rows) {  // the last 16 to 48 columns of a matrix
 #pragma unroll
                 for (int i = 0; i < 6; ++i)
@@ -532,7 +522,7 @@ cudaError_t launch_block_gemm(BlockEpi epi, const BlockGemmArgs& args, cudaStrea
     if (args.total_rows == 0) return cudaSuccess;
     switch (epi) {
         case BlockEpi::GateUp: return launch_block_impl<0>(args, st, pdl);
-        case BlockEpi::Half: return launch_block_impl<1>(args, st, pdl);
+        case BlockEpi::F32: return launch_block_impl<1>(args, st, pdl);
         case BlockEpi::BF16: return launch_block_impl<2>(args, st, pdl);
     }
     return cudaErrorInvalidValue;

@@ -13,7 +13,7 @@
 //
 // At the tile's end the sums go through shared memory and a warp takes an
 // activation row: GateUp forms h of 128 channels, a whole scale block, and writes
-// its codes and scale; Half and BF16 write 256 columns.
+// its codes and scale; F32 writes 256 columns.
 //
 // SPLIT: where the tiles leave SMs without one (one token through two experts: 24
 // tiles) a cluster of CTAs splits each tile's K, one tile a cluster, as long as
@@ -127,15 +127,8 @@ __device__ __forceinline__ void few_output(const BlockGemmArgs& args, int r, int
         for (int half = 0; half < 2; ++half) {
             const float4& f = half ? b : a;
             const int col = (2 * cb + half) * kBlk + lane * 4;
-            float amax = amax_nan(amax_nan(amax_nan(amax_nan(0.f, f.x), f.y), f.z), f.w);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) amax = amax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-            float s, inv;
-            half_scale(amax, s, inv);
             if (col >= args.w_rows) continue;  // the same for the whole warp: w_rows is a multiple of 128
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(args.out) + (size_t)r * args.w_rows + col) =
-                make_uint2(half_pair(f.x * inv, f.y * inv), half_pair(f.z * inv, f.w * inv));
-            if (lane == 0) args.s_out[(size_t)r * (args.w_rows / kBlk) + 2 * cb + half] = s;
+            *reinterpret_cast<float4*>(static_cast<float*>(args.out) + (size_t)r * args.w_rows + col) = f;
         }
     }
 }
@@ -171,8 +164,11 @@ __device__ __forceinline__ void few_combine(const BlockGemmArgs& args, int cb, i
         float a[8] = {};
         for (int j = 0; j < args.k; ++j) {
             const size_t slot = (size_t)t * args.k + j;
-            const uint4 v = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.out) + slot * H + col));
-            add_half8(a, v, __ldg(args.topk_w + slot) * __ldcg(args.s_out + slot * (H / kBlk) + col / kBlk));
+            const float4* o = reinterpret_cast<const float4*>(static_cast<const float*>(args.out) + slot * H + col);
+            const float4 lo = __ldcg(o), hi = __ldcg(o + 1);
+            const float w = __ldg(args.topk_w + slot), v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+            for (int c = 0; c < 8; ++c) a[c] = __fadd_rn(a[c], __fmul_rn(w, v[c]));
         }
         *reinterpret_cast<uint4*>(args.y + (size_t)t * H + col) =
             make_uint4(bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3]), bf16_pair(a[4], a[5]), bf16_pair(a[6], a[7]));
@@ -202,7 +198,7 @@ __global__ void __launch_bounds__(kGfThreads, 1)
     uint64_t* epi_bar = stall_bar + 1;      // the epilogue warps
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    volatile int* last_flag = abort_flag + 1;  // TOK, Half: this tile was its columns' last
+    volatile int* last_flag = abort_flag + 1;  // TOK, F32: this tile was its columns' last
     int* tile_start = reinterpret_cast<int*>(smem + L.tiles);
     int* row_start = tile_start + (kMaxExperts + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -425,7 +421,7 @@ __global__ void __launch_bounds__(kGfThreads, 1)
                 const float4 b = *reinterpret_cast<const float4*>(part + (NTOK + m) * kBlk + lane * 4);
                 few_output<EPI>(args, r, cb, lane, a, b);
             }
-            if (TOK && EPI == (int)BlockEpi::Half) {  // this expert's rows are written: the combine of the last
+            if (TOK && EPI == (int)BlockEpi::F32) {  // this expert's rows are written: the combine of the last
                 if (!(ok = epi_sync(epi_bar, sync, ctl))) break;
                 if (et == 0) *last_flag = few_last(args, cb, ids_s[2 * kFewSlots]);
                 if (!(ok = epi_sync(epi_bar, sync, ctl))) break;
@@ -461,7 +457,7 @@ __global__ void __launch_bounds__(kGfThreads, 1)
             }
         }
         cluster_sync_all();  // no CTA leaves while another reads its part
-        if (TOK && EPI == (int)BlockEpi::Half && rank == 0 && tile0 < total_tiles) {
+        if (TOK && EPI == (int)BlockEpi::F32 && rank == 0 && tile0 < total_tiles) {
             // this expert's rows are written (by the cluster): the combine of the last
             const int cb = tile0 % n_cb;
             if (threadIdx.x == 0) *last_flag = few_last(args, cb, ids_s[2 * kFewSlots]);
@@ -561,7 +557,7 @@ cudaError_t launch_block_gemm_few(BlockEpi epi, const BlockGemmArgs& args, cudaS
     if (args.total_rows == 0) return cudaSuccess;
     switch (epi) {
         case BlockEpi::GateUp: return launch_few<0>(args, st, pdl);
-        case BlockEpi::Half: return launch_few<1>(args, st, pdl);
+        case BlockEpi::F32: return launch_few<1>(args, st, pdl);
         default: return cudaErrorInvalidValue;
     }
 }
