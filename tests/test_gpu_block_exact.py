@@ -136,3 +136,55 @@ def test_an_infinite_sum_leaves_its_neighbours(T, E):
     want = torch.where(torch.arange(H) % 3 == 0, 7.0, 1.0).double() * 2.0**112
     want[5] = float("inf")
     assert torch.equal(y, want.expand(T, H))
+
+
+# ---------------------------------------------------------------- far negative gates
+
+
+def gate_blocks(n_blocks, seed):
+    """Blocks of (gate in quarters, up) for 128 channels, the first the largest h, whose quotients lie
+    2^-19 to 2^-17.5 from a midpoint of two codes (relatively), far enough for the error below."""
+    g = torch.Generator().manual_seed(seed)
+    quarters, ups = torch.arange(200, 241).double(), torch.arange(1, 256).double()
+    h = (quarters / -4 / (1 + torch.exp(quarters / 4)))[:, None] * ups
+    v = ref.e4m3_values()[:127]
+    mids = ((v[:-1] + v[1:]) / 2)[16:]
+    blocks = []
+    while len(blocks) < n_blocks:
+        i, j = (torch.randint(0, n, (1,), generator=g).item() for n in h.shape)
+        s = h[i, j].abs().float() * ref.RECIPROCAL
+        q = h.abs() / s.double()
+        at = torch.searchsorted(mids, q.contiguous()).clamp(1, len(mids) - 1)
+        off = torch.minimum((q / mids[at] - 1).abs(), (q / mids[at - 1] - 1).abs())
+        near = ((h.abs() < h[i, j].abs()) & (off > 2.0**-19) & (off < 2.0**-17.5)).nonzero()
+        if len(near) >= 3:
+            picked = [(i, j)] + [tuple(r) for r in near[:127].tolist()]
+            blocks.append([(int(quarters[a]), int(ups[b])) for a, b in picked])
+    return blocks
+
+
+@pytest.mark.parametrize("T,E", FORMS)
+def test_codes_of_h_for_far_negative_gates(T, E):
+    """Gates of -50 to -60.  h is within 5 * 2^-23 of its value: expf within 2 units in the last
+    place, the sum half a unit, the quotient 2 and the product half; its block's maximum
+    likewise, the scale and the quotient by it half a unit each: under 2^-19 together."""
+    layer = ExactLayer([[0] * I] * E, [1.0] * T)
+    w13, x = layer.args[3], layer.args[0]
+    codes = ref.e4m3_codes(torch.arange(16).float())
+    blocks = gate_blocks(2 * E, T)
+    gate, up = torch.zeros(E, I, dtype=torch.long), torch.zeros(E, I, dtype=torch.long)
+    for i, block in enumerate(blocks):
+        at = slice(i % 2 * 128, i % 2 * 128 + len(block))
+        gate[i // 2, at], up[i // 2, at] = torch.tensor(block).T
+    x[:, 2], x[:, 4] = -4, -0.25
+    w13[:, :I, 2], w13[:, :I, 4] = codes[gate // 16].cuda(), codes[gate % 16].cuda()
+    w13[:, I:, 0], w13[:, I:, 1] = codes[up // 16].cuda(), codes[up % 16].cuda()
+    layer.args[6][:] = 2.0**100
+    g = gate.double() / -4
+    layer.h = (g / (1 + torch.exp(-g)) * up.double())[layer.e]
+    code, _ = layer.codes()
+    y = moe.fp8_block_forward(*layer.args).double().cpu()
+    s = layer.h.float().reshape(T, 2, 128).abs().amax(2) * ref.RECIPROCAL
+    want = ref.e4m3_values()[code.long()] * s.double().repeat_interleave(128, 1) * 2.0**100
+    assert (up > 0).sum() >= 8 * E
+    assert ((y - want).abs() <= 2.0**-7 * want.abs()).all()

@@ -95,11 +95,13 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return r;
 }
 
-// h = g / (1 + exp(-g)) * u.  The exponential and the quotient are the fast
-// forms (about 2 ulp each): h is rounded to a 4-bit significand next, and a
-// code that such an error moves lies as close to its neighbour as to h.
+// h = g / (1 + exp(-g)) * u within 5 * 2^-23: expf to 2 ulp over its whole range,
+// the fast quotient to 2 ulp (it gives 0 for 1 + exp(-g) above 2^126, g below -87.3).
+// The fast exponential's error grows with its argument (2 + 1.17 |g| ulp) and so
+// moved codes of h for far negative gates; in its place, layer of 8192 tokens: 547
+// and 546 us.  A rounded quotient as well (the other layers' form): 636.
 __device__ __forceinline__ float silu_mul(float g, float u) {
-    return __fdividef(g, 1.0f + __expf(-g)) * u;
+    return __fdividef(g, 1.0f + expf(-g)) * u;
 }
 
 // Two binary32 values in one 64-bit register, and the packed multiply-add on
