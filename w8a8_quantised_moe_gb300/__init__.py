@@ -10,9 +10,14 @@ PyTorch fallback: without the library every call raises.
     w2_q, w2_s = moe.quantize_weights(w2_fp32.view(-1, I))
     y = moe.forward(x, router_w, None, w13_q.view(E, 2 * I, H), w13_s.view(E, 2 * I),
                     w2_q.view(E, H, I), w2_s.view(E, H), top_k=2)
+
+A call runs on ``stream`` (default: the current one) and allocates what it is
+not given there: a result is that stream's tensor, as if the call stood under
+``torch.cuda.stream(stream)``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 from . import _lib
@@ -42,6 +47,11 @@ def _stream(stream):
     torch = _torch()
     s = torch.cuda.current_stream() if stream is None else stream
     return s.cuda_stream
+
+
+def _on(stream):
+    """Context of a call's allocations: the stream that uses them."""
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
 
 
 def _need(t, dtype, shape, name):
@@ -81,8 +91,9 @@ def quantize_weights(w, stream=None):
     torch = _torch()
     rows, K = w.shape
     _need(w, torch.float32, (rows, K), "w")
-    q = torch.empty((rows, K), dtype=torch.int8, device=w.device)
-    s = torch.empty((rows,), dtype=torch.float32, device=w.device)
+    with _on(stream):
+        q = torch.empty((rows, K), dtype=torch.int8, device=w.device)
+        s = torch.empty((rows,), dtype=torch.float32, device=w.device)
     _lib.check(_lib.load().moe_w8a8_quantize_weights(_ptr(w), rows, K, _ptr(q), _ptr(s), _stream(stream)),
                "moe_w8a8_quantize_weights")
     return q, s
@@ -124,9 +135,10 @@ def forward(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, top_k, w
     torch = _torch()
     T, H, I, E = _forward_args(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, top_k)
     need = workspace_size(T, H, I, E, top_k)
-    if workspace is None:
-        workspace = new_workspace(need, x.device)
-    y = out if out is not None else torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    with _on(stream):
+        if workspace is None:
+            workspace = new_workspace(need, x.device)
+        y = out if out is not None else torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
     _need(y, torch.bfloat16, (T, H), "out")
     _lib.check(_lib.load().moe_w8a8_forward(
         _ptr(x), _ptr(router_w), _ptr(router_bias), _ptr(w13_q), _ptr(w13_scale), _ptr(w2_q), _ptr(w2_scale),
@@ -168,14 +180,15 @@ def _forward_host(fn, name, code_dtype, x_host, router_w, router_bias, w13_q, w1
     if y_host is None:
         y_host = torch.empty((T, H), dtype=torch.bfloat16).pin_memory()
     _need_host(y_host, torch.bfloat16, (T, H), "y_host")
-    if x_dev is None:
-        x_dev = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    if y_dev is None:
-        y_dev = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    with _on(stream):
+        if x_dev is None:
+            x_dev = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        if y_dev is None:
+            y_dev = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        if workspace is None:
+            workspace = new_workspace(workspace_size(T, H, I, E, top_k), dev)
     _need(x_dev, torch.bfloat16, (T, H), "x_dev")
     _need(y_dev, torch.bfloat16, (T, H), "y_dev")
-    if workspace is None:
-        workspace = new_workspace(workspace_size(T, H, I, E, top_k), dev)
     cs = None if copy_stream is None else copy_stream.cuda_stream
     _lib.check(fn(
         _ptr(x_host), _ptr(router_w), _ptr(router_bias), _ptr(w13_q), _ptr(w13_scale), _ptr(w2_q), _ptr(w2_scale),
@@ -222,17 +235,18 @@ def forward_debug(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, to
     torch = _torch()
     T, H, I, E = _forward_args(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, top_k)
     need = workspace_size(T, H, I, E, top_k)
-    if workspace is None:
-        workspace = new_workspace(need, x.device)
     fields = tuple(_DEBUG_FIELDS) if fields is None else tuple(fields)
     bufs = _lib.DebugBuffers()
     out = {}
-    for name in fields:
-        dt, shape = _DEBUG_FIELDS[name]
-        t = torch.zeros(shape(T, H, I, E, top_k), dtype=getattr(torch, dt), device=x.device)
-        out[name] = t
-        setattr(bufs, name, t.data_ptr())
-    y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    with _on(stream):
+        if workspace is None:
+            workspace = new_workspace(need, x.device)
+        for name in fields:
+            dt, shape = _DEBUG_FIELDS[name]
+            t = torch.zeros(shape(T, H, I, E, top_k), dtype=getattr(torch, dt), device=x.device)
+            out[name] = t
+            setattr(bufs, name, t.data_ptr())
+        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
     _lib.check(_lib.load().moe_w8a8_forward_debug(
         _ptr(x), _ptr(router_w), _ptr(router_bias), _ptr(w13_q), _ptr(w13_scale), _ptr(w2_q), _ptr(w2_scale),
         T, H, I, E, top_k, _ptr(y), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -254,9 +268,10 @@ def forward_fused(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, to
     is given (None: all)."""
     torch = _torch()
     T, H, I, E = _forward_args(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, top_k)
-    if workspace is None:
-        workspace = new_workspace(workspace_size(T, H, I, E, top_k), x.device)
-    y = out if out is not None else torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    with _on(stream):
+        if workspace is None:
+            workspace = new_workspace(workspace_size(T, H, I, E, top_k), x.device)
+        y = out if out is not None else torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
     _need(y, torch.bfloat16, (T, H), "out")
     fields = tuple(_DEBUG_FIELDS) if fields is None else tuple(fields)
     bufs, dumps = None, {}
@@ -264,7 +279,8 @@ def forward_fused(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, to
         bufs = _lib.DebugBuffers()
         for name in fields:
             dt, shape = _DEBUG_FIELDS[name]
-            t = torch.zeros(shape(T, H, I, E, top_k), dtype=getattr(torch, dt), device=x.device)
+            with _on(stream):
+                t = torch.zeros(shape(T, H, I, E, top_k), dtype=getattr(torch, dt), device=x.device)
             dumps[name] = t
             setattr(bufs, name, t.data_ptr())
     _lib.check(_lib.load().moe_w8a8_forward_fused(
@@ -282,8 +298,9 @@ def quantize_weights_smoothed(w, col_scale, stream=None):
     rows, K = w.shape
     _need(w, torch.float32, (rows, K), "w")
     _need(col_scale, torch.float32, (K,), "col_scale")
-    q = torch.empty((rows, K), dtype=torch.int8, device=w.device)
-    s = torch.empty((rows,), dtype=torch.float32, device=w.device)
+    with _on(stream):
+        q = torch.empty((rows, K), dtype=torch.int8, device=w.device)
+        s = torch.empty((rows,), dtype=torch.float32, device=w.device)
     _lib.check(_lib.load().moe_w8a8_quantize_weights_smoothed(_ptr(w), rows, K, _ptr(col_scale), _ptr(q), _ptr(s),
                                                               _stream(stream)), "moe_w8a8_quantize_weights_smoothed")
     return q, s
@@ -297,9 +314,10 @@ def forward_smooth(x, router_w, router_bias, smooth, w13_q, w13_scale, w2_q, w2_
     torch = _torch()
     T, H, I, E = _forward_args(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, top_k)
     _need(smooth, torch.float32, (E, H), "smooth")
-    if workspace is None:
-        workspace = new_workspace(workspace_size(T, H, I, E, top_k), x.device)
-    y = out if out is not None else torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    with _on(stream):
+        if workspace is None:
+            workspace = new_workspace(workspace_size(T, H, I, E, top_k), x.device)
+        y = out if out is not None else torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
     _need(y, torch.bfloat16, (T, H), "out")
     fields = tuple(_DEBUG_FIELDS) if fields is None else tuple(fields)
     bufs, dumps = None, {}
@@ -307,7 +325,8 @@ def forward_smooth(x, router_w, router_bias, smooth, w13_q, w13_scale, w2_q, w2_
         bufs = _lib.DebugBuffers()
         for name in fields:
             dt, shape = _DEBUG_FIELDS[name]
-            t = torch.zeros(shape(T, H, I, E, top_k), dtype=getattr(torch, dt), device=x.device)
+            with _on(stream):
+                t = torch.zeros(shape(T, H, I, E, top_k), dtype=getattr(torch, dt), device=x.device)
             dumps[name] = t
             setattr(bufs, name, t.data_ptr())
     _lib.check(_lib.load().moe_w8a8_forward_smooth(
@@ -332,9 +351,10 @@ def linear(x, w_q, w_scale, workspace=None, out=None, stream=None):
     _need(w_q, torch.int8, (N, K), "w_q")
     _need(w_scale, torch.float32, (N,), "w_scale")
     need = linear_workspace_size(M, N, K)
-    if workspace is None:
-        workspace = new_workspace(need, x.device)
-    y = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    with _on(stream):
+        if workspace is None:
+            workspace = new_workspace(need, x.device)
+        y = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     _need(y, torch.bfloat16, (M, N), "out")
     _lib.check(_lib.load().moe_w8a8_linear(_ptr(x), _ptr(w_q), _ptr(w_scale), M, N, K, _ptr(y), _ptr(workspace),
                                            workspace.numel() * workspace.element_size(), _stream(stream)),
@@ -355,8 +375,9 @@ def fp8_quantize_weights(w, stream=None):
     torch = _torch()
     rows, K = w.shape
     _need(w, torch.float32, (rows, K), "w")
-    q = torch.empty((rows, K), dtype=torch.uint8, device=w.device)
-    s = torch.empty((rows,), dtype=torch.float32, device=w.device)
+    with _on(stream):
+        q = torch.empty((rows, K), dtype=torch.uint8, device=w.device)
+        s = torch.empty((rows,), dtype=torch.float32, device=w.device)
     _lib.check(_lib.load().moe_w8a8_fp8_quantize_weights(_ptr(w), rows, K, _ptr(q), _ptr(s), _stream(stream)),
                "moe_w8a8_fp8_quantize_weights")
     return q, s
@@ -368,9 +389,10 @@ def fp8_forward(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, top_
     torch = _torch()
     T, H, I, E = _forward_args(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, top_k, torch.uint8)
     need = workspace_size(T, H, I, E, top_k)
-    if workspace is None:
-        workspace = new_workspace(need, x.device)
-    y = out if out is not None else torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    with _on(stream):
+        if workspace is None:
+            workspace = new_workspace(need, x.device)
+        y = out if out is not None else torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
     _need(y, torch.bfloat16, (T, H), "out")
     _lib.check(_lib.load().moe_w8a8_fp8_forward(
         _ptr(x), _ptr(router_w), _ptr(router_bias), _ptr(w13_q), _ptr(w13_scale), _ptr(w2_q), _ptr(w2_scale),
@@ -392,17 +414,18 @@ def fp8_forward_debug(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale
     torch = _torch()
     T, H, I, E = _forward_args(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, top_k, torch.uint8)
     need = workspace_size(T, H, I, E, top_k)
-    if workspace is None:
-        workspace = new_workspace(need, x.device)
     fields = tuple(_DEBUG_FIELDS_FP8) if fields is None else tuple(fields)
     bufs = _lib.DebugBuffers()
     out = {}
-    for name in fields:
-        dt, shape = _DEBUG_FIELDS_FP8[name]
-        t = torch.zeros(shape(T, H, I, E, top_k), dtype=getattr(torch, dt), device=x.device)
-        out[name] = t
-        setattr(bufs, name, t.data_ptr())
-    y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    with _on(stream):
+        if workspace is None:
+            workspace = new_workspace(need, x.device)
+        for name in fields:
+            dt, shape = _DEBUG_FIELDS_FP8[name]
+            t = torch.zeros(shape(T, H, I, E, top_k), dtype=getattr(torch, dt), device=x.device)
+            out[name] = t
+            setattr(bufs, name, t.data_ptr())
+        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
     _lib.check(_lib.load().moe_w8a8_fp8_forward_debug(
         _ptr(x), _ptr(router_w), _ptr(router_bias), _ptr(w13_q), _ptr(w13_scale), _ptr(w2_q), _ptr(w2_scale),
         T, H, I, E, top_k, _ptr(y), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -421,7 +444,8 @@ def fp8_forward_host(x_host, router_w, router_bias, w13_q, w13_scale, w2_q, w2_s
 
 # ---- block-scaled FP8 (E4M3, a scale per 128 channels) ---------------------
 # A decode step calls these with a few microseconds of GPU work each, so their
-# argument handling is kept short: _fits is the check, _need words its refusal.
+# argument handling is kept short: _fits is the check, _need words its refusal, and
+# only a call with a stream and something to allocate enters that stream's context.
 
 BLOCK = 128  # input channels, and output channels of a weight, that share a scale
 
@@ -455,8 +479,9 @@ def fp8_block_quantize_weights(w, stream=None):
         raise ValueError(f"w: expected 2 or 3 dimensions, got {w.dim()}")
     _need(w, torch.float32, w.shape, "w")
     groups, (rows, K) = (1 if w.dim() == 2 else w.shape[0]), w.shape[-2:]
-    q = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
-    s = torch.empty((*w.shape[:-2], _blocks(rows), _blocks(K)), dtype=torch.float32, device=w.device)
+    with _on(stream):
+        q = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
+        s = torch.empty((*w.shape[:-2], _blocks(rows), _blocks(K)), dtype=torch.float32, device=w.device)
     _lib.check(_lib.load().moe_w8a8_fp8_block_quantize_weights(w.data_ptr(), groups, rows, K, q.data_ptr(),
                                                                s.data_ptr(), _raw_stream(stream, w)),
                "moe_w8a8_fp8_block_quantize_weights")
@@ -473,6 +498,9 @@ def fp8_block_linear_workspace_size(M, N, K) -> int:
 def fp8_block_linear(x, w_q, w_scale, workspace=None, out=None, stream=None):
     """Block-scaled FP8 linear layer: bf16 x [M, K], E4M3 w_q [N, K] (uint8), fp32
     w_scale [ceil(N / 128), ceil(K / 128)] -> bf16 [M, N]."""
+    if stream is not None and (workspace is None or out is None):
+        with _on(stream):
+            return fp8_block_linear(x, w_q, w_scale, workspace, out)
     torch = _torch()
     bf16 = torch.bfloat16
     M, K = x.shape
@@ -506,6 +534,9 @@ def fp8_block_forward(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale
     """The MoE layer with block-scaled FP8 products: bf16 x [T, H] -> bf16 y [T, H];
     w13_q [E, 2I, H] and w2_q [E, H, I] E4M3 (uint8) with fp32 scales
     [E, 2I / 128, H / 128] and [E, H / 128, I / 128]."""
+    if stream is not None and (workspace is None or out is None):
+        with _on(stream):
+            return fp8_block_forward(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, top_k, workspace, out)
     torch = _torch()
     bf16, fp32, u8 = torch.bfloat16, torch.float32, torch.uint8
     T, H = shape = x.shape
@@ -546,6 +577,9 @@ def norm_residual(x, branch=None, post_w=None, gate=None, scale=1.0, pre_w=None,
 
     branch, weights and gate are bf16; gate is [H], [T, 1] or [T, H].  Returns
     (r, n): r in x's type (x itself without a branch; ``x_out`` may be x), n bf16."""
+    if stream is not None and (branch is not None and x_out is None or pre_w is not None and n_out is None):
+        with _on(stream):
+            return norm_residual(x, branch, post_w, gate, scale, pre_w, eps, x_out, n_out)
     torch = _torch()
     bf16 = torch.bfloat16
     fp32 = x.dtype is torch.float32
