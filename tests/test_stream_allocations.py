@@ -46,6 +46,7 @@ def allocations(monkeypatch):
     monkeypatch.setattr(moe, "_fits", lambda *a: True)
     monkeypatch.setattr(moe, "_raw_stream", lambda stream, t: 0)
     monkeypatch.setattr(moe, "_stream", lambda stream: 0)
+    monkeypatch.setattr(moe, "_room", lambda workspace: (0, workspace.nbytes))
     for name in ("empty", "zeros", "empty_like"):
         monkeypatch.setattr(torch, name, watched(name, getattr(torch, name)))
     return seen

@@ -63,6 +63,14 @@ def _need(t, dtype, shape, name):
                          f"{tuple(t.shape)} on {t.device}")
 
 
+def _room(workspace):
+    """Address and bytes of a workspace tensor."""
+    if not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError(f"workspace: expected a contiguous cuda tensor, got {tuple(workspace.shape)} with strides "
+                         f"{workspace.stride()} on {workspace.device}")
+    return workspace.data_ptr(), workspace.nbytes
+
+
 def version() -> int:
     return _lib.load().moe_w8a8_version()
 
@@ -142,7 +150,7 @@ def forward(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, top_k, w
     _need(y, torch.bfloat16, (T, H), "out")
     _lib.check(_lib.load().moe_w8a8_forward(
         _ptr(x), _ptr(router_w), _ptr(router_bias), _ptr(w13_q), _ptr(w13_scale), _ptr(w2_q), _ptr(w2_scale),
-        T, H, I, E, top_k, _ptr(y), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        T, H, I, E, top_k, _ptr(y), *_room(workspace),
         _stream(stream)), "moe_w8a8_forward")
     return y
 
@@ -192,8 +200,8 @@ def _forward_host(fn, name, code_dtype, x_host, router_w, router_bias, w13_q, w1
     cs = None if copy_stream is None else copy_stream.cuda_stream
     _lib.check(fn(
         _ptr(x_host), _ptr(router_w), _ptr(router_bias), _ptr(w13_q), _ptr(w13_scale), _ptr(w2_q), _ptr(w2_scale),
-        T, H, I, E, top_k, _ptr(y_host), _ptr(x_dev), _ptr(y_dev), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream), cs, int(chunks)), name)
+        T, H, I, E, top_k, _ptr(y_host), _ptr(x_dev), _ptr(y_dev), *_room(workspace), _stream(stream), cs,
+        int(chunks)), name)
     return y_host
 
 
@@ -249,7 +257,7 @@ def forward_debug(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, to
         y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
     _lib.check(_lib.load().moe_w8a8_forward_debug(
         _ptr(x), _ptr(router_w), _ptr(router_bias), _ptr(w13_q), _ptr(w13_scale), _ptr(w2_q), _ptr(w2_scale),
-        T, H, I, E, top_k, _ptr(y), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        T, H, I, E, top_k, _ptr(y), *_room(workspace),
         _stream(stream), ctypes.byref(bufs)), "moe_w8a8_forward_debug")
     return y, out
 
@@ -285,7 +293,7 @@ def forward_fused(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, to
             setattr(bufs, name, t.data_ptr())
     _lib.check(_lib.load().moe_w8a8_forward_fused(
         _ptr(x), _ptr(router_w), _ptr(router_bias), _ptr(w13_q), _ptr(w13_scale), _ptr(w2_q), _ptr(w2_scale),
-        T, H, I, E, top_k, _ptr(y), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        T, H, I, E, top_k, _ptr(y), *_room(workspace),
         _stream(stream), ctypes.byref(bufs) if bufs is not None else None), "moe_w8a8_forward_fused")
     return (y, dumps) if fields else y
 
@@ -331,7 +339,7 @@ def forward_smooth(x, router_w, router_bias, smooth, w13_q, w13_scale, w2_q, w2_
             setattr(bufs, name, t.data_ptr())
     _lib.check(_lib.load().moe_w8a8_forward_smooth(
         _ptr(x), _ptr(router_w), _ptr(router_bias), _ptr(smooth), _ptr(w13_q), _ptr(w13_scale), _ptr(w2_q),
-        _ptr(w2_scale), T, H, I, E, top_k, _ptr(y), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(w2_scale), T, H, I, E, top_k, _ptr(y), *_room(workspace),
         _stream(stream), ctypes.byref(bufs) if bufs is not None else None), "moe_w8a8_forward_smooth")
     return (y, dumps) if fields else y
 
@@ -356,9 +364,8 @@ def linear(x, w_q, w_scale, workspace=None, out=None, stream=None):
             workspace = new_workspace(need, x.device)
         y = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     _need(y, torch.bfloat16, (M, N), "out")
-    _lib.check(_lib.load().moe_w8a8_linear(_ptr(x), _ptr(w_q), _ptr(w_scale), M, N, K, _ptr(y), _ptr(workspace),
-                                           workspace.numel() * workspace.element_size(), _stream(stream)),
-               "moe_w8a8_linear")
+    _lib.check(_lib.load().moe_w8a8_linear(_ptr(x), _ptr(w_q), _ptr(w_scale), M, N, K, _ptr(y),
+                                           *_room(workspace), _stream(stream)), "moe_w8a8_linear")
     return y
 
 
@@ -396,7 +403,7 @@ def fp8_forward(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale, top_
     _need(y, torch.bfloat16, (T, H), "out")
     _lib.check(_lib.load().moe_w8a8_fp8_forward(
         _ptr(x), _ptr(router_w), _ptr(router_bias), _ptr(w13_q), _ptr(w13_scale), _ptr(w2_q), _ptr(w2_scale),
-        T, H, I, E, top_k, _ptr(y), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        T, H, I, E, top_k, _ptr(y), *_room(workspace),
         _stream(stream)), "moe_w8a8_fp8_forward")
     return y
 
@@ -428,7 +435,7 @@ def fp8_forward_debug(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale
         y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
     _lib.check(_lib.load().moe_w8a8_fp8_forward_debug(
         _ptr(x), _ptr(router_w), _ptr(router_bias), _ptr(w13_q), _ptr(w13_scale), _ptr(w2_q), _ptr(w2_scale),
-        T, H, I, E, top_k, _ptr(y), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        T, H, I, E, top_k, _ptr(y), *_room(workspace),
         _stream(stream), ctypes.byref(bufs)), "moe_w8a8_fp8_forward_debug")
     return y, out
 
@@ -515,8 +522,8 @@ def fp8_block_linear(x, w_q, w_scale, workspace=None, out=None, stream=None):
     if out is None:
         out = torch.empty((M, N), dtype=bf16, device=x.device)
     status = _lib.load().moe_w8a8_fp8_block_linear(
-        x.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), M, N, K, out.data_ptr(), workspace.data_ptr(),
-        workspace.nbytes, _raw_stream(stream, x))
+        x.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), M, N, K, out.data_ptr(), *_room(workspace),
+        _raw_stream(stream, x))
     if status:
         raise MoeError(status, "moe_w8a8_fp8_block_linear")
     return out
@@ -557,7 +564,7 @@ def fp8_block_forward(x, router_w, router_bias, w13_q, w13_scale, w2_q, w2_scale
         out = torch.empty_like(x)
     status = _lib.load().moe_w8a8_fp8_block_forward(
         x.data_ptr(), router_w.data_ptr(), _ptr(router_bias), w13_q.data_ptr(), w13_scale.data_ptr(), w2_q.data_ptr(),
-        w2_scale.data_ptr(), T, H, I, E, top_k, out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        w2_scale.data_ptr(), T, H, I, E, top_k, out.data_ptr(), *_room(workspace),
         _raw_stream(stream, x))
     if status:
         raise MoeError(status, "moe_w8a8_fp8_block_forward")
