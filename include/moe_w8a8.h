@@ -129,7 +129,8 @@ MOE_W8A8_API moe_status_t moe_w8a8_quantize_weights(const float* w, int64_t rows
  * 256 bytes hold the sticky device error word read by moe_w8a8_device_error
  * and a routing counter that every call leaves at zero; zero them once before
  * the first call on a new workspace.  Calls that share a workspace must not
- * overlap on the GPU.
+ * overlap on the GPU.  The size does not fall with T: a workspace for T tokens
+ * serves every call of at most T tokens with the same H, I, E and top_k.
  * ------------------------------------------------------------------------- */
 MOE_W8A8_API size_t moe_w8a8_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k);
 
@@ -482,7 +483,8 @@ MOE_W8A8_API moe_status_t moe_w8a8_fp8_block_linear(const uint16_t* x, const uin
  * block-scaled FP8 products.  Arguments, shapes and errors as
  * moe_w8a8_fp8_forward, with
  *   w13_scale fp32 [E][2I / 128][H / 128], w2_scale fp32 [E][H / 128][I / 128]
- *   workspace >= moe_w8a8_fp8_block_workspace_size(T, H, I, E, top_k) bytes
+ *   workspace >= moe_w8a8_fp8_block_workspace_size(T, H, I, E, top_k) bytes,
+ *             which does not fall with T either
  * Router, top-k, slots and combine are those of the other forms; x is
  * quantised per token and 128 channels, h per slot and 128 channels. */
 MOE_W8A8_API size_t moe_w8a8_fp8_block_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k);

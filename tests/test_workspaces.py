@@ -28,3 +28,28 @@ def test_a_strided_workspace_is_refused():
         is_contiguous, stride = staticmethod(lambda: False), staticmethod(lambda: (0,))
     with pytest.raises(ValueError, match="workspace: expected a contiguous cuda tensor"):
         moe._room(OnGpu())
+
+
+SHAPES = [(2048, 768, 8, 2), (4096, 1536, 64, 2), (4096, 1536, 2, 1), (1024, 256, 8, 1), (7168, 2048, 256, 8),
+          (128, 128, 256, 8), (16384, 128, 130, 4), (1408, 640, 1, 1), (4096, 256, 33, 5)]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from w8a8_quantised_moe_gb300 import build
+    build.build()
+    return _lib.load()
+
+
+@pytest.mark.parametrize("size", ["moe_w8a8_workspace_size", "moe_w8a8_fp8_block_workspace_size"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_a_workspace_for_more_tokens_serves_fewer(lib, size, shape):
+    need = [getattr(lib, size)(T, *shape) for T in [*range(0, 6000), 1 << 16, (1 << 16) + 1, 1 << 20]]
+    assert need[0] > 0 and all(a <= b for a, b in zip(need, need[1:]))
+
+
+def test_a_linear_workspace_for_more_rows_serves_fewer(lib):
+    for size in (lib.moe_w8a8_linear_workspace_size, lib.moe_w8a8_fp8_block_linear_workspace_size):
+        for N, K in ((128, 128), (4096, 4096)):
+            need = [size(M, N, K) for M in range(0, 3000)]
+            assert need[0] > 0 and all(a <= b for a, b in zip(need, need[1:]))

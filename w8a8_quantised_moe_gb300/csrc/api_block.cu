@@ -49,8 +49,9 @@ BlockFwdLayout block_fwd_layout(int64_t T, int64_t H, int64_t I, int64_t E, int6
     L.err = take(256);
     L.counts = take(2 * 4);
     L.wsplit = take((size_t)3 * rp.E_pad * H * 2);
-    const size_t few = block_few_tokens(T, E, k) ? block_route_scratch(T, H) : 0;
-    const size_t logits = (size_t)rp.KS * T * rp.E_pad * 4;
+    int64_t t_few = T < kFewTokens ? T : kFewTokens;  // the most tokens, up to T, of the form for a few
+    while (t_few > 0 && !block_few_tokens(t_few, E, k)) --t_few;
+    const size_t few = block_route_scratch(t_few, H, E), logits = router_scratch(T, H, E);
     L.logits = take(logits > few ? logits : few);
     L.topk_ids = take(S * 4);
     L.topk_w = take(S * 4);

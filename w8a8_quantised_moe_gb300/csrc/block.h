@@ -69,7 +69,7 @@ constexpr int kFewTokens = 8, kFewSlots = 32;
 constexpr int kRouterMaxSlicesFew = 128;   // slices of the router's rows, at most
 constexpr int kRouterMaxSliceRows = 128;   // rows of one (H <= 16384)
 bool block_few_tokens(int64_t T, int64_t E, int64_t k);
-size_t block_route_scratch(int64_t T, int64_t H);  // bytes of P
+size_t block_route_scratch(int64_t T, int64_t H, int64_t E);  // bytes of P
 struct BlockRouteArgs {
     const uint16_t* x;       // bf16 [T][H]
     const float *Wr, *bias;  // fp32 [H][E]; [E] or nullptr

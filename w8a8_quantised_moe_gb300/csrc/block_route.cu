@@ -139,7 +139,10 @@ int route_ctas(int H) {
 }
 }  // namespace
 
-size_t block_route_scratch(int64_t T, int64_t H) { return (size_t)route_ctas((int)H) / kRfCluster * T * 256 * 4; }
+size_t block_route_scratch(int64_t T, int64_t H, int64_t E) {
+    const int64_t cols = E <= 32 ? 32 : E <= 64 ? 64 : E <= 128 ? 128 : 256;
+    return (size_t)route_ctas((int)H) / kRfCluster * T * cols * 4;
+}
 
 bool block_few_tokens(int64_t T, int64_t E, int64_t k) {
     return T <= kFewTokens && T * k <= kFewSlots && T * ((E + 31) / 32 * 32) <= 512;

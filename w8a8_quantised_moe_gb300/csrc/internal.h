@@ -142,6 +142,9 @@ struct RouterPlan {
     bool small;  // CUDA-core router (T <= kRouterSmallT): no weight split
 };
 RouterPlan router_plan(int64_t T, int64_t H, int64_t E);
+// Bytes of the router's partial logits, the most of any call of up to T tokens
+// (fewer tokens can take more slices and so more room).
+size_t router_scratch(int64_t T, int64_t H, int64_t E);
 
 // Forward workspace layout (byte offsets; every region 256-byte aligned).
 struct FwdLayout {

@@ -394,6 +394,24 @@ RouterPlan router_plan(int64_t T, int64_t H, int64_t E) {
     return p;
 }
 
+size_t router_scratch(int64_t T, int64_t H, int64_t E) {
+    auto bytes = [&](int64_t t) {
+        const RouterPlan p = router_plan(t, H, E);
+        return (size_t)p.KS * t * p.E_pad * 4;
+    };
+    size_t most = bytes(T);
+    if (T <= kRouterSmallT) return most;
+    auto consider = [&](int64_t t) {
+        const size_t b = bytes(t);
+        if (b > most) most = b;
+    };
+    consider(kRouterSmallT);
+    // whole token tiles: between them the slices stay and the tokens grow, and
+    // from kRouterTargetCtas tiles on there is one slice
+    for (int64_t t = kRouterSmallT + kRTM; t < T && t <= (int64_t)kRouterTargetCtas * kRTM; t += kRTM) consider(t);
+    return most;
+}
+
 cudaError_t launch_router(const uint16_t* x, const float* Wr, const float* bias, int T, int H, int E, int k,
                           uint16_t* wsplit, float* P, int32_t* topk_ids, float* topk_w, int32_t* rank,
                           int32_t* hist, int32_t* offsets, int32_t* counts, unsigned int* ticket, int* error,
