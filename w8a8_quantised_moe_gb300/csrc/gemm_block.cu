@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kBgThreads, 1)
         tmem_relinquish();
     }
     pdl_wait();  // the previous kernel's outputs (offsets, codes, scales) are visible from here
-    pdl_trigger();
+    if (warp == 1) pdl_trigger();  // not before the tensor memory is this CTA's
     if (warp == 2) block_tile_table(args, kBgRows, bg_col_blocks<EPI>(args), tile_start, row_start, lane);
     tc_fence_before();
     __syncthreads();

@@ -61,6 +61,9 @@ __host__ __device__ inline LfLayout lf_layout(int ntok, bool fused, int len_max)
     L.scales = L.codes + (fused ? len_max * ntok * kBlk : 0);
     L.bars = L.scales + len_max * ntok * 4;
     L.total = L.bars + 160 + 1024;  // + alignment slack
+    // A CTA that holds all of the tensor memory takes the SM for itself: no CTA of
+    // another launch is to wait there for columns while its cluster holds other SMs.
+    if (ntok * kLfNS == 512 && L.total < kLfMaxSmem) L.total = kLfMaxSmem;
     return L;
 }
 
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(kLfThreads, NTOK <= 64 ? 2 : 1)
     }
     __syncwarp();
     pdl_wait();  // x, and its codes and scales, are visible from here; y is free
-    pdl_trigger();
+    if (warp == 8) pdl_trigger();  // not before the tensor memory is this CTA's
     const float* sw = a.w_scale + (size_t)tile * nkb + kb0;
     if (warp < 8 && !FUSED) {  // scales of x times the weights'; columns from M on are not stored
         for (int i = threadIdx.x; i < a.M * len; i += 256) {
