@@ -69,7 +69,7 @@ class ExactLayer:
 
 
 # tokens, experts: the form for a few tokens, few rows an expert, many rows
-FORMS = [(7, 2), (40, 16), (300, 2)]
+FORMS = [(7, 2), (40, 20), (300, 2)]
 
 
 def random_values(E, seed):

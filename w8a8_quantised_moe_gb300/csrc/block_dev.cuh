@@ -39,8 +39,12 @@ __device__ __forceinline__ uint32_t e4m3_quot4(float a, float b, float c, float 
 // so the quotient lies between the products with the reciprocal 2^-22 lower
 // and higher; where both round to the same codes, those are the quotients'.
 // Elsewhere (a quotient next to a midpoint of two codes) and for scales whose
-// reciprocal could overflow, be 0 or NaN, the divisions decide.  Measured in
-// the few-row linear layer, 64 x 4096 x 4096: 18.8 us with eight divisions.
+// reciprocal could overflow, be 0 or NaN, the divisions decide.  Worth it where a
+// thread has a row's 64 codes to form and nothing else to wait for, at the end of
+// the gate/up product: layer of 8192 tokens 522 us, 539 with divisions.  Where the
+// row's loads leave the time, divisions are not slower: quant8 in the linear layer,
+// 1 x 4096 x 4096 8.2 us with these products and 7.7 with divisions, 64 x 4096 x
+// 4096 10.5 and 10.3, 4096 x 16 x 8192 50.5 and 49.3.
 struct BlockQuot {
     float s, lo, hi;
     bool in_range;
@@ -74,9 +78,7 @@ __device__ __forceinline__ uint2 quant8(const float (&f)[8], float& s) {
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1) amax = amax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
     s = block_scale(amax);
-    uint32_t c[2];
-    BlockQuot(s).codes(f, c);
-    return make_uint2(c[0], c[1]);
+    return make_uint2(e4m3_quot4(f[0], f[1], f[2], f[3], s), e4m3_quot4(f[4], f[5], f[6], f[7], s));
 }
 
 __device__ __forceinline__ void bf16x8_to_f32(const uint4& v, float (&f)[8]) {

@@ -28,11 +28,19 @@
 namespace moe {
 namespace {
 
-// Rows a group on average up to which this kernel is taken.  (Layer of 64 experts,
-// H 4096, I 1536, top-2, cold, this kernel against gemm_block.cu, us: 16 tokens 108
-// and 112; 64 tokens, 2 rows a group, 200 and 200; 128 tokens 216 and 222; 256
-// tokens, 8 rows a group, 247 and 245; 512 tokens 290 and 247.)
-constexpr long kFewRowsMax = 4;
+// Rows a group on average up to which this kernel is taken.  Measured, the whole layer,
+// weights cold, this kernel / gemm_block.cu, us (E experts, top-k, H, I):
+//   rows  E 64, 2, 4096, 1536    E 128, 4, 2048, 768    E 256, 8, 7168, 2048
+//   1     156 / 156              94 / 108
+//   2     194 / 207              113 / 133              1458 / 1516
+//   4     214 / 219              125 / 140              1659 / 1688
+//   16    261 / 252              157 / 163              2203 / 1786
+// and with a Zipf(1.2) choice of experts, whose largest groups take many tiles of 16 rows:
+//   2     86 / 91                58 / 63                450 / 386
+//   4     127 / 97               75 / 71                700 / 483
+// Even loads gain 3 to 12 % at 4 rows, uneven ones lose up to 45 %; at 2 they gain 4 to 15 %
+// and lose at one shape.
+constexpr long kFewRowsMax = 2;
 // Activation rows of a tile then.  (32 of them leave room for a stage less: 64
 // tokens 206, 256 tokens 249.)
 constexpr int kFewTile = 16;
@@ -117,10 +125,9 @@ __device__ __forceinline__ void few_output(const BlockGemmArgs& args, int r, int
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) amax = amax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
         const float s = block_scale(amax);
-        uint32_t code[1];
-        BlockQuot(s).codes(h, code);
         const size_t n_ch = (size_t)args.up_offset;
-        *reinterpret_cast<uint32_t*>(args.q_out + (size_t)r * n_ch + cb * kBlk + lane * 4) = code[0];
+        *reinterpret_cast<uint32_t*>(args.q_out + (size_t)r * n_ch + cb * kBlk + lane * 4) =
+            e4m3_quot4(h[0], h[1], h[2], h[3], s);
         if (lane == 0) args.s_out[(size_t)r * (n_ch / kBlk) + cb] = s;
     } else {
 #pragma unroll

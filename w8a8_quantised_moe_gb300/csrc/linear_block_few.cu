@@ -9,11 +9,10 @@
 // from the start.
 //
 //   A  128 weight rows (the MMA's M) x 128 channels, by TMA
-//   B  NTOK >= M quantised rows of x (N) x 128 channels: up to 16 rows are
+//   B  NTOK >= M quantised rows of x (N) x 128 channels: up to kLfFusedRows rows are
 //      quantised here while the weights fly (FUSED: each CTA its part of K, written
 //      in the 128-byte swizzle); more come by TMA from the quantiser's launch
-//      before, which the weights' loads overlap.  (Measured at 64 x 4096 x 4096:
-//      quantised here 18.8 us, since each of the 32 tiles' clusters repeats it.)
+//      before, which the weights' loads overlap.
 //   D  one 128-channel block's sums, NTOK columns of tensor memory, four buffers
 //
 // The epilogue warps scale each block's sums by sx * sw (a column's scale, from
@@ -33,7 +32,13 @@ namespace {
 constexpr int kLfThreads = 320;
 constexpr int kLfNS = 4;                  // weight stages, and tensor-memory buffers
 constexpr int kLfStageA = kBlk * kBlk;    // 128 weight rows x 128 channels
-constexpr int kLfFusedRows = 16;          // up to this many rows are quantised here
+// Up to this many rows are quantised here.  Measured at N = K = 4096, quantised here /
+// by a launch before, us, from a graph: 1 row 7.6 / 8.0, 4 rows 8.3 / 8.2, 8 rows 9.1 /
+// 8.7, 12 rows 10.7 / 8.7, 16 rows 11.5 / 8.9 (13.0 / 9.0 at 16 x 2048 x 7168); called one
+// after the other from Python, where the second launch costs host time, 1 to 16 rows:
+// 11.3 to 13.6 / 14.0 to 14.7.  Beyond 8 rows each cluster's repeat of all of x costs a
+// graph more than the launch costs the host.
+constexpr int kLfFusedRows = 8;
 constexpr int kLfMaxSmem = 232448;
 
 struct LinFewArgs {
@@ -359,6 +364,11 @@ cudaError_t launch_lf(const CUtensorMap& tw, const CUtensorMap& tx, const LinFew
 
 bool block_linear_few_fused(int M) { return M <= kLfFusedRows; }
 
+// 128 rows are what four buffers of tensor memory hold.  This kernel / gemm_block.cu at
+// that limit, us, from a graph, weights cold: 128 x 4096 x 4096 12.7 / 18.6, 128 x 2048 x
+// 7168 13.6 / 27.8, 128 x 7168 x 2048 11.7 / 12.6, 128 x 8192 x 8192 26.2 / 32.4, 128 x
+// 7168 x 16384 44 / 59; a wide N alone goes the other way: 16384 x 4096 with 17 rows 18.9 /
+// 20.6, 64 rows 24.6 / 21.0, 128 rows 26.7 / 21.5.  (129 x 4096 x 4096: 18.5 there.)
 bool block_linear_few_supported(int M, int N, int K) {
     return M <= 128 && lf_cluster(lf_ntok(M), block_linear_few_fused(M), N, blocks_of(K)) > 0;
 }
