@@ -33,8 +33,8 @@ bool lin_shape_ok(int64_t M, int64_t N, int64_t K) {
 // Router and routing regions as the layer's other forms (FwdLayout); codes of
 // one byte, a scale per slot and 128 channels.
 struct BlockFwdLayout {
-    size_t err, counts, wsplit, logits, topk_ids, topk_w, rank, hist, offsets, slot_of, slot_token, q_x, s_x, q_h,
-        s_h, o, done, total;
+    size_t err, counts, wsplit, logits, topk_ids, topk_w, rank, hist, offsets, slot_of, q_x, s_x, q_h, s_h, o, done,
+        total;
 };
 BlockFwdLayout block_fwd_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
     BlockFwdLayout L{};
@@ -59,7 +59,6 @@ BlockFwdLayout block_fwd_layout(int64_t T, int64_t H, int64_t I, int64_t E, int6
     L.hist = take(nchunk * E * 4);
     L.offsets = take((E + 1) * 4);
     L.slot_of = take(S * 4);
-    L.slot_token = take(S * 4);
     L.q_x = take(S * H);
     L.s_x = take(S * (H / kBlk) * 4);
     L.q_h = take(S * I);
@@ -227,8 +226,7 @@ moe_status_t moe_w8a8_fp8_block_forward(const uint16_t* x, const float* router_w
         return from_cuda(e);
     e = launch_permute_quant_block(x, at<int32_t>(workspace, L.topk_ids), at<int32_t>(workspace, L.rank), hist,
                                    (int)T, (int)H, (int)E, (int)top_k, at<int32_t>(workspace, L.slot_of),
-                                   at<int32_t>(workspace, L.slot_token), at<uint8_t>(workspace, L.q_x),
-                                   at<float>(workspace, L.s_x), err, st, pdl);
+                                   at<uint8_t>(workspace, L.q_x), at<float>(workspace, L.s_x), err, st, pdl);
     if (e != cudaSuccess) return from_cuda(e);
 
     g.offsets = offsets;

@@ -62,7 +62,7 @@ template <bool SLOTS, int V>
 __global__ void __launch_bounds__(256) quantize_rows_block_kernel(
     const uint16_t* __restrict__ x, int M, int K, uint8_t* __restrict__ q, float* __restrict__ s_out,
     const int32_t* __restrict__ topk_ids, const int32_t* __restrict__ rank, const int32_t* __restrict__ base, int E,
-    int k, int32_t* __restrict__ slot_of, int32_t* __restrict__ slot_token, int* __restrict__ error) {
+    int k, int32_t* __restrict__ slot_of, int* __restrict__ error) {
     const int lane = threadIdx.x & 31;
     const int kb = blocks_of(K), parts = (kb + 2 * V - 1) / (2 * V);
     const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -83,10 +83,7 @@ __global__ void __launch_bounds__(256) quantize_rows_block_kernel(
         my_slot = in_range(e, 0, E, error) ? base[(size_t)(r / kRouterTokens) * E + e] + rank[(size_t)r * k + lane]
                                            : -1;  // -1: out of range (checked build), its writes skipped
         if (my_slot >= 0 && !in_range(my_slot, 0, (long long)M * k, error)) my_slot = -1;
-        if (part == 0) {
-            slot_of[(size_t)r * k + lane] = my_slot;
-            if (!kChecked || my_slot >= 0) slot_token[my_slot] = r;
-        }
+        if (part == 0) slot_of[(size_t)r * k + lane] = my_slot;
     }
     const int n = SLOTS ? k : 1;
 #pragma unroll
@@ -129,16 +126,14 @@ cudaError_t launch_quantize_weights_block(const float* w, int64_t groups, int ro
 
 cudaError_t launch_quantize_block(const uint16_t* x, int M, int K, uint8_t* q, float* s, cudaStream_t st, bool pdl) {
     if (M == 0) return cudaSuccess;
-    return launch_quantize_rows<false>(st, pdl, x, M, K, q, s, nullptr, nullptr, nullptr, 0, 1, nullptr, nullptr,
-                                       nullptr);
+    return launch_quantize_rows<false>(st, pdl, x, M, K, q, s, nullptr, nullptr, nullptr, 0, 1, nullptr, nullptr);
 }
 
 cudaError_t launch_permute_quant_block(const uint16_t* x, const int32_t* topk_ids, const int32_t* rank,
                                        const int32_t* base, int T, int H, int E, int k, int32_t* slot_of,
-                                       int32_t* slot_token, uint8_t* q, float* s, int* error, cudaStream_t st,
-                                       bool pdl) {
+                                       uint8_t* q, float* s, int* error, cudaStream_t st, bool pdl) {
     if (T == 0) return cudaSuccess;
-    return launch_quantize_rows<true>(st, pdl, x, T, H, q, s, topk_ids, rank, base, E, k, slot_of, slot_token, error);
+    return launch_quantize_rows<true>(st, pdl, x, T, H, q, s, topk_ids, rank, base, E, k, slot_of, error);
 }
 
 }  // namespace moe

@@ -95,8 +95,7 @@ cudaError_t launch_quantize_block(const uint16_t* x, int M, int K, uint8_t* q, f
 // found from the router's chunk ranks and bases.
 cudaError_t launch_permute_quant_block(const uint16_t* x, const int32_t* topk_ids, const int32_t* rank,
                                        const int32_t* base, int T, int H, int E, int k, int32_t* slot_of,
-                                       int32_t* slot_token, uint8_t* q, float* s, int* error, cudaStream_t st,
-                                       bool pdl);
+                                       uint8_t* q, float* s, int* error, cudaStream_t st, bool pdl);
 
 // Shape of the gate of norm_residual.
 enum class GateForm : int { None = 0, Channel = 1, Token = 2, Element = 3 };
