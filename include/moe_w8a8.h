@@ -445,12 +445,15 @@ MOE_W8A8_API int moe_w8a8_host_chunks(int64_t T, int64_t H, int64_t I, int64_t E
  * input channels, found once.  The last block of a dimension may be shorter.
  * A block's scale is s = amax * (1/448) (one binary32 product with the rounded
  * reciprocal) and its codes are the E4M3 values nearest to the binary32
- * quotients v / s, ties to even, saturated at +-448; a block of zeros has s = 0 and codes 0.  A NaN or an infinity
- * makes its block's scale non-finite and the results that use it NaN.  The
- * product is
+ * quotients v / s, ties to even, saturated at +-448; where s is 0 (a block of
+ * zeros, or of values so small that it rounds to 0) the codes are 0.  A NaN or
+ * an infinity makes its block's scale non-finite and the results that use it
+ * NaN.  The product is
  *   y[m][n] = sum_b s_x[m][b] * s_w[n / 128][b] * sum_{k in b} q_x[m][k] * q_w[n][k]
  * with exact E4M3 products summed in binary32 and each block's sum scaled
- * before it is added.  Scale factors of one block instead of a whole row: an
+ * before it is added, by the binary32 product of the two scales: block maxima
+ * whose product is below 2^-108 leave that product fewer than 24 bits, and
+ * above 2^145 it is infinite.  Scale factors of one block instead of a whole row: an
  * outlier channel costs precision in its own 128 channels only.  (Block scales
  * for the E4M3 operands of "DeepSeek V4 950 FP8 inference on H100", sections
  * 2.1-2.4.)
@@ -486,7 +489,8 @@ MOE_W8A8_API moe_status_t moe_w8a8_fp8_block_linear(const uint16_t* x, const uin
  *   workspace >= moe_w8a8_fp8_block_workspace_size(T, H, I, E, top_k) bytes,
  *             which does not fall with T either
  * Router, top-k, slots and combine are those of the other forms; x is
- * quantised per token and 128 channels, h per slot and 128 channels. */
+ * quantised per token and 128 channels, h per slot and 128 channels, from its
+ * binary32 value (within 5 * 2^-23, gates below -87.3 as 0).  o is binary32. */
 MOE_W8A8_API size_t moe_w8a8_fp8_block_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k);
 MOE_W8A8_API moe_status_t moe_w8a8_fp8_block_forward(const uint16_t* x, const float* router_w,
                                                      const float* router_bias, const uint8_t* w13_q,
@@ -498,7 +502,8 @@ MOE_W8A8_API moe_status_t moe_w8a8_fp8_block_forward(const uint16_t* x, const fl
 /* ---------------------------------------------------------------------------
  * moe_w8a8_norm_residual -- the norms around a block: the norm after it, its
  * gate, the residual scale and addition, and the norm before the next block,
- * in one pass.  Per row of H channels, in binary32:
+ * in one pass.  Per row of H channels, in binary32 (a row whose sum of squares
+ * passes binary32's range has a factor of 0):
  *   b     = branch * rsqrt(mean(branch^2) + eps) * post_w   (post_w NULL: b = branch)
  *   r     = x + scale * gate * b                            (branch NULL: r = x)
  *   n     = r * rsqrt(mean(r^2) + eps) * pre_w              (from the unrounded r)

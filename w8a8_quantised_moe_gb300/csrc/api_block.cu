@@ -149,7 +149,7 @@ moe_status_t moe_w8a8_fp8_block_forward(const uint16_t* x, const float* router_w
     if (gemm_path_forced()) return MOE_ERR_NOT_IMPLEMENTED;
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool pdl = pdl_default();  // every launch after the first
+    const bool pdl = pdl_default();  // every launch but the first of launch_router
     const int S = (int)(T * top_k), nchunk = (int)((T + kRouterTokens - 1) / kRouterTokens);
     int* err = at<int>(workspace, L.err);
     int32_t* hist = at<int32_t>(workspace, L.hist);

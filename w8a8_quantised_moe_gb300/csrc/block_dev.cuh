@@ -9,8 +9,9 @@ namespace moe {
 namespace {
 
 // A block's scale: its largest magnitude over 448, the largest E4M3 magnitude,
-// as one product with the binary32 reciprocal.  (The quotient of the largest
-// magnitude by its scale is 448 to within an ulp or two, so its code is 448.)
+// as one product with the binary32 reciprocal.  (For a normal scale the quotient
+// of the largest magnitude by it is 448 to within an ulp or two, and its code 448;
+// a subnormal one is coarser, and codes saturate or stay below.)
 __device__ __forceinline__ float block_scale(float amax) { return __fmul_rn(amax, 1.0f / 448.0f); }
 
 // Two E4M3 codes (lo in the low byte): round to nearest even, saturate.

@@ -13,7 +13,9 @@
 // per half and block: sx of its row times sw of the half.  GateUp's halves are 64
 // gate rows and the 64 up rows of the same channels, so the tile holds whole
 // scale blocks of h: each thread applies silu(gate) * up to its 64 + 64 columns
-// and h leaves the kernel as E4M3 codes with their scale, never as binary32.
+// and h leaves the kernel as E4M3 codes with their scale, never as binary32.  (The
+// second expert product's rows are binary32: fp16 rows with a scale per 128 columns
+// saved 33 us of 546 at 8192 tokens, and rounded y twice.)
 //   warp 0      TMA producer (ring of kBgNS stages: activation rows and four
 //               quarters of the weight rows, 128 bytes of K each)
 //   warp 1      MMA issuer (and TMEM allocator): four K = 32 MMAs a block into one
@@ -41,9 +43,9 @@
 // multiply-adds (540), tests of the next block's barriers ahead of time (504), row
 // scales read four blocks at a time (520) or stored block by block (617).  CTA
 // pairs (cta_group::2, 32 KB a CTA and block) came to 447 here, by drawing less
-// power, and to the same time at 4096^3, but a group's odd tile of 128 rows leaves a
-// CTA idle: 16 experts of 2048 rows took 992 against 837.  Weights multicast to two
-// CTAs: 483 against 490.
+// power, and to the same time at 4096^3; 16 experts of 2048 rows took 992 against 837,
+// which an idle CTA in each group's odd tile (one in 17 at most) does not explain: the
+// cause was not found.  Weights multicast to two CTAs: 483 against 490.
 #include <mutex>
 
 #include "block.h"

@@ -171,10 +171,16 @@ LinLayout lin_layout(int64_t M, int64_t N, int64_t K);
 // prefetch their first weights there; each grid still waits for its
 // predecessor's completion, and a dependent grid launches only once every
 // CTA of its predecessor is running, so no grid can hold the SMs that an
-// earlier one still needs.  The first kernel of each entry point is launched
-// without PDL (it then serialises like a plain launch).  The dp4a GEMM reads
-// the expert offsets and its weights before its wait (both complete before
-// its predecessor started).
+// earlier one still needs.  The first kernel of each entry point of the layers
+// is launched without PDL (it then serialises like a plain launch); the
+// block-scaled linear layer, the block-scaled layer's form for a few tokens and
+// the norms launch their first with it, which waits like any other.  The dp4a
+// GEMM reads the expert offsets and its weights before its wait, the few-row
+// block-scaled products their weights and the experts' ids or offsets (all
+// complete before its predecessor passed its own wait).  A kernel with tensor
+// memory must not trigger before it holds it: the next one on its SM could take
+// the columns and wait for it (the block-scaled ones trigger in the allocating
+// warp).
 #ifdef __CUDACC__
 // Checked build: true when lo <= v < hi, else records kErrDevice (when error
 // is given) and returns false.  Always true in the normal build.
