@@ -490,7 +490,8 @@ MOE_W8A8_API moe_status_t moe_w8a8_fp8_block_linear(const uint16_t* x, const uin
  *             which does not fall with T either
  * Router, top-k, slots and combine are those of the other forms; x is
  * quantised per token and 128 channels, h per slot and 128 channels, from its
- * binary32 value (within 5 * 2^-23, gates below -87.3 as 0).  o is binary32. */
+ * binary32 value (within 6 * 2^-23; exp(-|gate|) keeps fewer bits for gates
+ * below -87.3).  o is binary32. */
 MOE_W8A8_API size_t moe_w8a8_fp8_block_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k);
 MOE_W8A8_API moe_status_t moe_w8a8_fp8_block_forward(const uint16_t* x, const float* router_w,
                                                      const float* router_bias, const uint8_t* w13_q,

@@ -188,3 +188,34 @@ def test_codes_of_h_for_far_negative_gates(T, E):
     want = ref.e4m3_values()[code.long()] * s.double().repeat_interleave(128, 1) * 2.0**100
     assert (up > 0).sum() >= 8 * E
     assert ((y - want).abs() <= 2.0**-7 * want.abs()).all()
+
+
+@pytest.mark.parametrize("T,E", FORMS)
+def test_codes_of_h_where_the_exponential_nears_its_range(T, E):
+    """Gates of -86 to -95, where exp(-g) passes 2^126 and then binary32's range.  exp(g) is
+    subnormal there: an error of half 2^-149 of it, |g| times in silu's product, besides the
+    6 * 2^-23 of h and of its block's maximum, and half a unit each for scale and quotient.
+    Within that of a midpoint either code will do."""
+    layer = ExactLayer([[0] * I] * E, [1.0] * T)
+    w13, x = layer.args[3], layer.args[0]
+    codes = ref.e4m3_codes(torch.arange(16).float())
+    gen = torch.Generator().manual_seed(T)
+    gate = torch.randint(344, 381, (E, I), generator=gen)
+    up = torch.randint(0, 256, (E, I), generator=gen)
+    # gate / -4 in three weights
+    x[:, 2], x[:, 4], x[:, 5] = -64, -4, -0.25
+    w13[:, :I, 2] = codes[gate // 256].cuda()
+    w13[:, :I, 4], w13[:, :I, 5] = codes[gate // 16 % 16].cuda(), codes[gate % 16].cuda()
+    w13[:, I:, 0], w13[:, I:, 1] = codes[up // 16].cuda(), codes[up % 16].cuda()
+    layer.args[6][:] = 2.0**100
+    g, u = gate.double() / -4, up.double()
+    h = g / (1 + torch.exp(-g)) * u
+    layer.h = h[layer.e]
+    code, _ = layer.codes()
+    s = (layer.h.float().reshape(T, 2, 128).abs().amax(2) * ref.RECIPROCAL).double().repeat_interleave(128, 1)
+    q = layer.h / s
+    slack = q.abs() * 13 * 2.0**-23 + ((u * (g.abs() + 2))[layer.e] * 2.0**-149) / s
+    low, high = (ref.e4m3_values()[ref.e4m3_codes((q + d).clamp(-448, 448).float()).long()] for d in (-slack, slack))
+    y = moe.fp8_block_forward(*layer.args).double().cpu() / 2.0**100 / s
+    assert y.isfinite().all() and (code % 128 > 0).float().mean() > 0.5
+    assert ((y >= low - 2.0**-7 * low.abs()) & (y <= high + 2.0**-7 * high.abs())).all()

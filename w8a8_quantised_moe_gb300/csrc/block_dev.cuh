@@ -98,13 +98,17 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return r;
 }
 
-// h = g / (1 + exp(-g)) * u within 5 * 2^-23: expf to 2 ulp over its whole range,
-// the fast quotient to 2 ulp (it gives 0 for 1 + exp(-g) above 2^126, g below -87.3).
-// The fast exponential's error grows with its argument (2 + 1.17 |g| ulp) and so
-// moved codes of h for far negative gates; in its place, layer of 8192 tokens: 547
-// and 546 us.  A rounded quotient as well (the other layers' form): 636.
+// h = g / (1 + exp(-g)) * u within 6 * 2^-23, by exp(-|g|), which does not pass
+// binary32's range (where it is subnormal, |g| above 87.3, half of 2^-149 in it
+// adds to that): expf to 2 ulp over its whole range, the fast quotient by 1 to 2
+// to 2 ulp.  The fast exponential's error grows with its argument (2 + 1.17 |g|
+// ulp) and so moved codes of h for far negative gates, and the fast quotient by
+// 1 + exp(-g) gave 0 for gates below -87.3.  Layer of 8192 tokens: 546 us with both,
+// 547 with expf, the same in this form; 636 with a rounded quotient besides (the other
+// layers' form).
 __device__ __forceinline__ float silu_mul(float g, float u) {
-    return __fdividef(g, 1.0f + expf(-g)) * u;
+    const float t = expf(-fabsf(g));
+    return __fdividef(g < 0.f ? __fmul_rn(g, t) : g, 1.0f + t) * u;
 }
 
 // Two binary32 values in one 64-bit register, and the packed multiply-add on
