@@ -467,7 +467,7 @@ MOE_W8A8_API int moe_w8a8_host_chunks(int64_t T, int64_t H, int64_t I, int64_t E
  * moe_w8a8_fp8_block_linear: y = x W^T.
  *   x        bf16 [M][K]
  *   w_q      E4M3 [N][K], w_scale fp32 [ceil(N / 128)][ceil(K / 128)]
- *   y        bf16 [M][N], rounded once
+ *   y        bf16 [M][N], rounded once; not x's memory
  *   workspace >= moe_w8a8_fp8_block_linear_workspace_size(M, N, K) bytes, 256-byte
  *            aligned, its first 256 bytes zeroed once by the caller
  * Supported: 0 <= M <= 2^20; N, K multiples of 16 in [16, 65536].  M == 0 is a
