@@ -528,6 +528,110 @@ MOE_W8A8_API moe_status_t moe_w8a8_norm_residual(const void* x, int x_fp32, cons
                                                  void* x_out, uint16_t* n_out, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The paged key/value cache in 8 bits, and attention over it.
+ *
+ * A page holds `page` tokens of every key head.  A block of the cache is the
+ * tokens of one page and head: E4M3 codes and one binary32 scale, for keys and
+ * for values; a value is its code times its block's scale.  moe_w8a8_kv_append
+ * gives a block the scale 2^E, E the least integer >= -64 with
+ * max |value| <= 448 * 2^E, and the E4M3 codes nearest to value / 2^E (ties to
+ * even).  Where new tokens come into a page that holds tokens of their sequence
+ * already, the block keeps the larger of its scale and theirs, and where that
+ * grows the codes that it holds are rounded again, to E4M3(code * old / new):
+ * exact but for codes that become subnormal.  A value that is not finite makes
+ * its block's scale NaN (and the new codes 0) until the page is begun anew, and
+ * with it every result that sees a token of the block, no other.
+ *
+ * moe_w8a8_kv_cache_t: device memory of the caller.
+ *   k, v       E4M3 codes [n_pages][heads][page][dim], page_stride bytes (a
+ *              multiple of 16) from one page to the next, the rest contiguous
+ *   k_scale, v_scale  fp32 [n_pages][heads], scale_stride values from page to
+ *              page; positive (values' scales below 2^-64 count as 2^-64; a
+ *              value block whose scale is 0 is not seen)
+ *   page 16, 32, 64 or 128; dim 64 or 128; 1 <= heads <= 256.
+ *
+ * moe_w8a8_kv_batch_t: B sequences with T new tokens in all.
+ *   q_start    [B + 1], ascending: sequence b's new tokens are the rows
+ *              q_start[b] .. q_start[b + 1] - 1 of q, k and v.  Rows of no
+ *              sequence (behind the last) are not read and their results are
+ *              left as they are
+ *   lengths    [B]: the sequence's tokens in the cache, the new ones included
+ *              (they are its last).  New tokens of a sequence whose length is
+ *              smaller than their number have, as far as they do not fit, no
+ *              position: they are not stored and see nothing
+ *   page_table [B][table_stride]: the first max_pages of a row are the pages of
+ *              the sequence, in order; entries behind its last page are not read.
+ *              A page that is written belongs to one sequence; one that is only
+ *              read may belong to several
+ * The arrays are read on the device: a captured call follows their contents.
+ * Lengths beyond max_pages * page count as that; page ids outside [0, n_pages)
+ * are never followed: the tokens of such a page are not stored, or not seen, and
+ * the error word is set (MOE_ERR_DEVICE from moe_w8a8_device_error).
+ * 0 <= B, T <= 2^20; max_pages * page <= 2^30.  B == 0 or T == 0 is a no-op.
+ * Strides of q, k and v are elements from token to token, multiples of 8; a
+ * token's heads are contiguous.  Pointers are 16-byte aligned, those of scales,
+ * the batch's arrays and lse 4-byte.
+ *
+ * moe_w8a8_kv_append: stores k and v, bf16 [T][heads][dim], and turns keys and
+ * queries by their positions p (a token's place in its sequence, from 0):
+ *   a' = a cos - b sin, b' = b cos + a sin   for the pairs (a, b) of the first
+ *   rope_dim channels: (i, i + rope_dim / 2), or (2 i, 2 i + 1) if interleaved;
+ *   the other channels stay.
+ *   rope       fp32 [rope_rows][rope_dim]: row p has the rope_dim / 2 cosines,
+ *              then the sines; or NULL with rope_dim 0: nothing is turned.
+ *              rope_dim a multiple of 16, at most dim.  Tokens whose position is
+ *              not in the table are left out, and the error word is set
+ *   q, q_out   bf16 [T][q_heads][dim], q_out contiguous; q may be NULL (no
+ *              queries), q_out may be q where q is contiguous
+ *   workspace  256 bytes, zeroed once: the error word
+ * Codes are those of the exact products with the table's values; queries are
+ * turned in binary32 and rounded once.
+ *
+ * moe_w8a8_kv_attention: for new token i of n of a sequence of length L, and
+ * query head h of q_heads (a multiple of heads; key head h / (q_heads / heads)),
+ *   p = L - n + i,  s_j = scale <q, k_j> for 0 <= j <= p (and j > p - window),
+ *   out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)
+ *   q          bf16, turned already; out bf16 [T][q_heads][dim], rounded once,
+ *              not q's memory; lse fp32 [T][q_heads] or NULL
+ *   scale      positive; window 0: every key up to p
+ *   workspace  >= moe_w8a8_kv_attention_workspace_size(B, T, q_heads, heads,
+ *              dim) bytes, which do not fall with B or T; 256-byte aligned, the
+ *              first 256 bytes zeroed once
+ * A row that sees no key has out 0 and lse -inf.  Scores and sums are binary32
+ * of exact products (a query row to 2^-25 of its largest channel), the weights
+ * fp16.  Results depend in their last bits on the batch: where a sequence is cut
+ * into parts.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t n_pages, heads, page, dim;
+    int64_t page_stride;  /* bytes */
+    int64_t scale_stride; /* values */
+} moe_w8a8_kv_cache_t;
+
+typedef struct {
+    const int32_t* q_start;
+    const int32_t* lengths;
+    const int32_t* page_table;
+    int64_t B, T, max_pages, table_stride;
+} moe_w8a8_kv_batch_t;
+
+MOE_W8A8_API moe_status_t moe_w8a8_kv_append(const moe_w8a8_kv_cache_t* cache, const moe_w8a8_kv_batch_t* batch,
+                                             const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                                             int64_t v_stride, const uint16_t* q, int64_t q_stride, int64_t q_heads,
+                                             const float* rope, int64_t rope_rows, int64_t rope_dim, int interleaved,
+                                             uint16_t* q_out, void* workspace, size_t workspace_bytes, void* stream);
+MOE_W8A8_API size_t moe_w8a8_kv_attention_workspace_size(int64_t B, int64_t T, int64_t q_heads, int64_t kv_heads,
+                                                         int64_t dim);
+MOE_W8A8_API moe_status_t moe_w8a8_kv_attention(const moe_w8a8_kv_cache_t* cache, const moe_w8a8_kv_batch_t* batch,
+                                                const uint16_t* q, int64_t q_stride, int64_t q_heads, float scale,
+                                                int64_t window, uint16_t* out, float* lse, void* workspace,
+                                                size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * moe_w8a8_device_error -- synchronise `stream`, then read and clear the
  * sticky device error word in the first bytes of `workspace`.  Returns
  * MOE_OK, MOE_ERR_DEVICE_TIMEOUT (a pipeline wait inside a kernel gave up;

@@ -31,6 +31,7 @@ __all__ = [
     "fp8_quantize_weights", "fp8_forward", "fp8_forward_debug", "fp8_forward_host",
     "fp8_block_quantize_weights", "fp8_block_linear_workspace_size", "fp8_block_linear", "fp8_block_workspace_size",
     "fp8_block_forward", "norm_residual",
+    "KVCache", "new_kv_cache", "kv_append", "kv_attention_workspace_size", "kv_attention",
 ]
 
 
@@ -610,3 +611,162 @@ def norm_residual(x, branch=None, post_w=None, gate=None, scale=1.0, pre_w=None,
     if status:
         raise MoeError(status, "moe_w8a8_norm_residual")
     return r, n
+
+
+# ---- the paged key/value cache in 8 bits -------------------------------------
+
+class KVCache:
+    """Handle of a paged cache: E4M3 codes ``k``, ``v`` (uint8 [n_pages, heads, page,
+    dim]) and their blocks' scales ``k_scale``, ``v_scale`` (fp32 [n_pages, heads]).
+
+    Pages may lie further apart than they are large (one pool of many layers, keys
+    and values of a page next to each other); the rest is contiguous, and k and v,
+    and their scales, have the same strides.  The handle keeps the tensors, and 256
+    bytes for the error word of ``kv_append`` (``status``, read by
+    ``device_error(cache.status)``).  page 16, 32, 64 or 128; dim 64 or 128."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        torch = _torch()
+        if k.dim() != 4:
+            raise ValueError(f"k: expected 4 dimensions, got {k.dim()}")
+        n, heads, page, dim = shape = k.shape
+        for name, t, dtype, want in (("k", k, torch.uint8, shape), ("v", v, torch.uint8, shape),
+                                     ("k_scale", k_scale, torch.float32, shape[:2]),
+                                     ("v_scale", v_scale, torch.float32, shape[:2])):
+            if not (t.dtype is dtype and t.shape == want and t.is_cuda and t[:1].is_contiguous()
+                    and t.get_device() == k.get_device()):
+                raise ValueError(f"{name}: expected cuda {dtype} {tuple(want)} with contiguous pages, got {t.dtype} "
+                                 f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+        if n > 1 and (k.stride(0) != v.stride(0) or k_scale.stride(0) != v_scale.stride(0)):
+            raise ValueError("k and v, and their scales, have the same strides from page to page")
+        page_stride, scale_stride = (k.stride(0), k_scale.stride(0)) if n > 1 else (heads * page * dim, heads)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.heads, self.page, self.dim, self.device = heads, page, dim, k.device
+        self.status = new_workspace(256, k.device)
+        self._c = _lib.KvCacheT(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, heads, page,
+                                dim, page_stride, scale_stride)
+        self._at = ctypes.addressof(self._c)
+
+
+def new_kv_cache(n_pages, heads, dim, page=64, device="cuda"):
+    """An empty ``KVCache``."""
+    torch = _torch()
+    codes = [torch.zeros((n_pages, heads, page, dim), dtype=torch.uint8, device=device) for _ in range(2)]
+    scales = [torch.zeros((n_pages, heads), dtype=torch.float32, device=device) for _ in range(2)]
+    return KVCache(*codes, *scales)
+
+
+def _rows_fit(t, T, heads, dim):
+    """Whether t is bf16 [T, heads, dim] whose tokens' heads are contiguous."""
+    return (t.dtype is _torch().bfloat16 and t.shape == (T, heads, dim) and t.is_cuda and t.stride(2) == 1
+            and (heads == 1 or t.stride(1) == dim))
+
+
+def _need_rows(t, T, heads, dim, name):
+    if not _rows_fit(t, T, heads, dim):
+        raise ValueError(f"{name}: expected cuda torch.bfloat16 {(T, heads, dim)} with contiguous heads, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _row_stride(t, T, width):
+    return t.stride(0) if T > 1 else width
+
+
+def _kv_batch(q_start, lengths, page_table, T):
+    """The batch's description for a call (the tensors stay the caller's)."""
+    i32 = _torch().int32
+    B = lengths.shape[0] if lengths.dim() == 1 else -1
+    if not (_fits(q_start, i32, (B + 1,)) and _fits(lengths, i32, (B,)) and page_table.dtype is i32
+            and page_table.dim() == 2 and page_table.shape[0] == B and page_table.is_cuda
+            and (page_table.shape[1] <= 1 or page_table.stride(1) == 1)):
+        _need(lengths, i32, (max(B, 0),), "lengths")
+        _need(q_start, i32, (B + 1,), "q_start")
+        raise ValueError(f"page_table: expected cuda {i32} with {B} contiguous rows, got {page_table.dtype} "
+                         f"{tuple(page_table.shape)} with strides {page_table.stride()} on {page_table.device}")
+    pages = page_table.shape[1]
+    return _lib.KvBatchT(q_start.data_ptr(), lengths.data_ptr(), page_table.data_ptr(), B, T, pages,
+                         page_table.stride(0) if B > 1 else pages)
+
+
+def kv_append(cache, k, v, q_start, lengths, page_table, q=None, rope=None, interleaved=False, q_out=None,
+              stream=None):
+    """Stores new tokens' keys and values in their sequences' pages, keys and queries
+    turned by their positions on the way.
+
+    k, v [T, heads, dim] and q [T, q_heads, dim] bf16 (rows may be parts of wider ones);
+    q_start int32 [B + 1], lengths int32 [B] (with the new tokens) and page_table int32
+    [B, pages] as in include/moe_w8a8.h, on the device; rope fp32 [positions,
+    rope_dim]: cosines, then sines, of a position's angles, or None; interleaved:
+    pairs are neighbours, not half a rope_dim apart.  Returns the turned queries, bf16
+    [T, q_heads, dim] (``q_out`` where given), or None without q.  A bad page id or a
+    position outside the table is reported by ``device_error(cache.status)``."""
+    if stream is not None and q is not None and q_out is None:
+        with _on(stream):
+            return kv_append(cache, k, v, q_start, lengths, page_table, q, rope, interleaved)
+    torch = _torch()
+    T, heads, dim = k.shape[0], cache.heads, cache.dim
+    if not (_rows_fit(k, T, heads, dim) and _rows_fit(v, T, heads, dim)):
+        _need_rows(k, T, heads, dim, "k")
+        _need_rows(v, T, heads, dim, "v")
+    batch = _kv_batch(q_start, lengths, page_table, T)
+    q_heads = q_stride = rope_rows = rope_dim = 0
+    if q is not None:
+        if q.dim() != 3 or not _rows_fit(q, T, q.shape[1], dim):
+            _need_rows(q, T, q.shape[1] if q.dim() == 3 else 0, dim, "q")
+        q_heads = q.shape[1]
+        q_stride = _row_stride(q, T, q_heads * dim)
+        if q_out is None:
+            q_out = torch.empty((T, q_heads, dim), dtype=torch.bfloat16, device=q.device)
+        elif not _fits(q_out, torch.bfloat16, (T, q_heads, dim)):
+            _need(q_out, torch.bfloat16, (T, q_heads, dim), "q_out")
+    if rope is not None:
+        rope_rows, rope_dim = rope.shape
+        if not _fits(rope, torch.float32, (rope_rows, rope_dim)):
+            _need(rope, torch.float32, (rope_rows, rope_dim), "rope")
+    status = _lib.load().moe_w8a8_kv_append(
+        cache._at, ctypes.addressof(batch), k.data_ptr(), _row_stride(k, T, heads * dim), v.data_ptr(),
+        _row_stride(v, T, heads * dim), _ptr(q), q_stride, q_heads, _ptr(rope), rope_rows, rope_dim, interleaved,
+        _ptr(q_out) if q is not None else None, *_room(cache.status), _raw_stream(stream, k))
+    if status:
+        raise MoeError(status, "moe_w8a8_kv_append")
+    return q_out
+
+
+def kv_attention_workspace_size(B, T, q_heads, kv_heads, dim) -> int:
+    n = _lib.load().moe_w8a8_kv_attention_workspace_size(B, T, q_heads, kv_heads, dim)
+    if n == 0:
+        raise MoeError(-2, "moe_w8a8_kv_attention_workspace_size")
+    return int(n)
+
+
+def kv_attention(q, cache, q_start, lengths, page_table, scale=None, window=0, lse=None, workspace=None, out=None,
+                 stream=None):
+    """Causal attention of new tokens over the cached keys and values of their
+    sequences (stored before, their own among them): q bf16 [T, q_heads, dim], turned
+    already -> bf16 [T, q_heads, dim].  q_start, lengths and page_table as for
+    ``kv_append``; scale None: dim ** -0.5; window > 0: the last ``window`` keys only;
+    ``lse`` fp32 [T, q_heads] receives the rows' log sum exp.  Rows that see nothing
+    are 0, their lse -inf."""
+    if stream is not None and (workspace is None or out is None):
+        with _on(stream):
+            return kv_attention(q, cache, q_start, lengths, page_table, scale, window, lse, workspace, out)
+    torch = _torch()
+    dim = cache.dim
+    T, q_heads = q.shape[:2]
+    shape = (T, q_heads, dim)
+    if not (_rows_fit(q, T, q_heads, dim) and (out is None or _fits(out, torch.bfloat16, shape))
+            and (lse is None or _fits(lse, torch.float32, shape[:2]))):
+        _need_rows(q, T, q_heads, dim, "q")
+        _check_all(("out", out, torch.bfloat16, shape), ("lse", lse, torch.float32, shape[:2]))
+    batch = _kv_batch(q_start, lengths, page_table, T)
+    if workspace is None:
+        workspace = new_workspace(kv_attention_workspace_size(batch.B, T, q_heads, cache.heads, dim), q.device)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    status = _lib.load().moe_w8a8_kv_attention(
+        cache._at, ctypes.addressof(batch), q.data_ptr(), _row_stride(q, T, q_heads * dim), q_heads,
+        dim**-0.5 if scale is None else scale, window, out.data_ptr(), _ptr(lse), *_room(workspace),
+        _raw_stream(stream, q))
+    if status:
+        raise MoeError(status, "moe_w8a8_kv_attention")
+    return out

@@ -57,6 +57,9 @@ EXPORTS = (
     "moe_w8a8_fp8_block_workspace_size",
     "moe_w8a8_fp8_block_forward",
     "moe_w8a8_norm_residual",
+    "moe_w8a8_kv_append",
+    "moe_w8a8_kv_attention_workspace_size",
+    "moe_w8a8_kv_attention",
 )
 
 
@@ -70,6 +73,18 @@ class DebugBuffers(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in (
         "topk_ids", "topk_w", "offsets", "slot_of", "slot_token", "s_x", "q_x", "acc1", "h",
         "s_h", "q_h", "acc2", "o", "s_slot", "q_slot")]
+
+
+class KvCacheT(ctypes.Structure):
+    """moe_w8a8_kv_cache_t"""
+    _fields_ = [(name, ctypes.c_void_p) for name in ("k", "v", "k_scale", "v_scale")] + [
+        (name, ctypes.c_int64) for name in ("n_pages", "heads", "page", "dim", "page_stride", "scale_stride")]
+
+
+class KvBatchT(ctypes.Structure):
+    """moe_w8a8_kv_batch_t"""
+    _fields_ = [(name, ctypes.c_void_p) for name in ("q_start", "lengths", "page_table")] + [
+        (name, ctypes.c_int64) for name in ("B", "T", "max_pages", "table_stride")]
 
 
 _lock = threading.Lock()
@@ -138,6 +153,9 @@ def _declare(lib) -> None:
         "moe_w8a8_fp8_block_workspace_size": ([i64, i64, i64, i64, i64], sz),
         "moe_w8a8_fp8_block_forward": ([vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, sz, vp], i32),
         "moe_w8a8_norm_residual": ([vp, i32, vp, vp, vp, i32, f32, vp, f32, i64, i64, vp, vp, vp], i32),
+        "moe_w8a8_kv_append": ([vp, vp, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, i32, vp, vp, sz, vp], i32),
+        "moe_w8a8_kv_attention_workspace_size": ([i64, i64, i64, i64, i64], sz),
+        "moe_w8a8_kv_attention": ([vp, vp, vp, i64, i64, f32, i64, vp, vp, vp, sz, vp], i32),
     }
     for name, (args, res) in decl.items():
         fn = getattr(lib, name)

@@ -1,0 +1,62 @@
+// kv.h -- declarations of the paged 8-bit key/value cache: appending to it
+// (kv_append.cu) and attention over it (kv_attend_few.cu, kv_attend.cu).
+//
+// A block of the cache is the tokens of one page and head: E4M3 codes [page][dim]
+// and one binary32 scale, for keys and for values.
+#pragma once
+
+#include "internal.h"
+#include "kv_plan.h"
+
+namespace moe {
+
+struct KvCache {
+    uint8_t *k, *v;          // [n_pages][heads][page][dim], page_stride bytes from page to page
+    float *k_scale, *v_scale;  // [n_pages][heads], scale_stride values from page to page
+    int64_t page_stride, scale_stride;
+    int n_pages, heads, page, dim;
+};
+
+struct KvAppendArgs {
+    KvCache c;
+    KvBatch bt;
+    const uint16_t *k, *v, *q;  // bf16 rows of heads * dim (q: q_heads * dim) or nullptr (q)
+    int64_t k_stride, v_stride, q_stride;
+    int q_heads;
+    const float* rope;  // [rope_rows][rope_dim]: cosines, then sines
+    int rope_rows, rope_dim, interleaved;
+    uint16_t* q_out;    // [T][q_heads][dim]
+    int* error;
+    // set by the launch
+    int q_tokens;       // tokens of a block that turns queries
+    int store_blocks, task_blocks;
+};
+cudaError_t launch_kv_append(KvAppendArgs a, cudaStream_t st, bool pdl);
+
+struct KvAttendArgs {
+    KvCache c;
+    KvBatch bt;
+    KvShape sh;
+    const uint16_t* q;  // bf16 [T][q_heads][dim], q_stride elements from token to token
+    int64_t q_stride;
+    int q_heads;
+    float scale;
+    uint16_t* out;      // bf16 [T][q_heads][dim]
+    float* lse;         // [T][q_heads] or nullptr
+    int* error;
+    uint64_t timeout_ns;
+    int stall;          // test hook (MOE_INJECT=stall)
+    // workspace
+    int2* info;         // [T][q_heads]: where a row's parts are (kv_parts.cuh)
+    float* part_o;      // [slots][rows][dim]
+    float2* part_ml;    // [slots][rows]
+};
+// Row tiles of 16 rows on warp-level MMAs: few rows a sequence and key head.
+constexpr int kKvFewRows = 16, kKvFewTokens = 64, kKvFewWarps = 4;
+int kv_few_ctas();      // CTAs of its grid, at most
+cudaError_t launch_kv_attend_few(KvAttendArgs a, cudaStream_t st, bool pdl);
+
+// Joins the parts of rows whose units several CTAs had.
+cudaError_t launch_kv_join(const KvAttendArgs& a, cudaStream_t st, bool pdl);
+
+}  // namespace moe

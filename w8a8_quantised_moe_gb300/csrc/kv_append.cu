@@ -1,0 +1,307 @@
+// kv_append.cu -- new tokens' keys and values into the pages of the cache, keys and
+// queries turned by their positions on the way:
+//
+//   half-split pairs (i, i + R/2), neighbours (2 i, 2 i + 1):
+//     a' = a cos - b sin,  b' = b cos + a sin     (R rotated channels, then the rest)
+//   block (page, head): s = 2^E, E the least integer >= -64 with max |value| <= 448 2^E
+//     code = E4M3 nearest to value / s, ties to the even mantissa
+//   a page that holds tokens already: s' = max(s, the new tokens' s); where s' > s its
+//     codes are rounded again, E4M3(code s / s')
+//
+// A power of two costs nothing: E4M3 keeps the same relative precision at any scale,
+// quotients by it are exact, and rounding codes again is exact but for subnormals, so
+// that tokens that come one at a time and a whole prompt lead to nearly the same cache.
+// The turned keys keep what lies below their binary32 value in its last bit (rounding
+// to odd), so that the codes are those of the exact products with the table's values:
+// about 1 in 10^6 would differ by a step otherwise.
+//
+// Bound by HBM for a prompt (16-bit rows in, 8-bit pages and turned queries out), by
+// the latency of the lengths, the rows and the page's scale for single tokens.  A
+// block's task is one page run (the new tokens of one page), head and K or V: W warps
+// hold its values in registers, so that they are read and turned once.
+#include "block_dev.cuh"
+#include "kv_dev.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kApThreads = 256;
+
+// v rounded to odd: v is binary32, rest what lies between it and the exact value.
+__device__ __forceinline__ float to_odd(float v, float rest) {
+    const float hi = __fadd_rn(v, rest), lo = __fsub_rn(rest, __fsub_rn(hi, v));
+    uint32_t bits = __float_as_uint(hi);
+    if (lo != 0.f && !(bits & 1u)) bits += (lo > 0.f) == (hi > 0.f) ? 1u : ~0u;
+    return __uint_as_float(bits);
+}
+// a c + b s: exact products, their sum and what it leaves, rounded to odd.
+__device__ __forceinline__ float turn_odd(float a, float c, float b, float s) {
+    const float p = __fmul_rn(a, c), pe = fmaf(a, c, -p), w = __fmul_rn(b, s), we = fmaf(b, s, -w);
+    const float sum = __fadd_rn(p, w), bb = __fsub_rn(sum, p);
+    const float t = __fadd_rn(__fsub_rn(p, __fsub_rn(sum, bb)), __fsub_rn(w, bb));
+    return to_odd(sum, __fadd_rn(t, __fadd_rn(pe, we)));
+}
+__device__ __forceinline__ float turn_rn(float a, float c, float b, float s) { return fmaf(a, c, __fmul_rn(b, s)); }
+
+// 16 channels of a row that are turned together (or not at all): the two runs of 8.
+struct Unit {
+    int c0, c1, angle;  // first channels of the runs; first angle, or -1
+    bool pairs;
+    __device__ __forceinline__ Unit(int u, int rope_dim, int interleaved) {
+        const int turned = rope_dim / 16;
+        pairs = interleaved != 0;
+        angle = u < turned ? 8 * u : -1;
+        if (u < turned && !pairs) {
+            c0 = 8 * u;
+            c1 = rope_dim / 2 + 8 * u;
+        } else {
+            c0 = 16 * u;
+            c1 = c0 + 8;
+        }
+    }
+};
+
+template <bool ODD>
+__device__ __forceinline__ void turn_unit(float (&f)[16], const Unit& u, const float* row, int half) {
+    const float4* pc = reinterpret_cast<const float4*>(row + u.angle);
+    const float4* ps = reinterpret_cast<const float4*>(row + half + u.angle);
+    const float4 c0 = __ldg(pc), c1 = __ldg(pc + 1), s0 = __ldg(ps), s1 = __ldg(ps + 1);
+    const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+    const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+    auto turn = [&](float& a, float& b, int i) {
+        const float x = ODD ? turn_odd(a, c[i], -b, s[i]) : turn_rn(a, c[i], -b, s[i]);
+        const float y = ODD ? turn_odd(b, c[i], a, s[i]) : turn_rn(b, c[i], a, s[i]);
+        a = x;
+        b = y;
+    };
+    if (u.pairs) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) turn(f[2 * i], f[2 * i + 1], i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) turn(f[i], f[8 + i], i);
+    }
+}
+
+__device__ __forceinline__ void load16(const uint16_t* row, const Unit& u, float (&f)[16]) {
+    float lo[8], hi[8];
+    bf16x8_to_f32(*reinterpret_cast<const uint4*>(row + u.c0), lo);
+    bf16x8_to_f32(*reinterpret_cast<const uint4*>(row + u.c1), hi);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        f[i] = lo[i];
+        f[8 + i] = hi[i];
+    }
+}
+
+// The scale of a block whose largest magnitude is amax; NaN where that is not finite.
+__device__ __forceinline__ float pow2_scale(float amax) {
+    const uint32_t b = __float_as_uint(amax);
+    if (b >= 0x7f800000u) return __uint_as_float(0x7fffffffu);
+    int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);  // 448 = 1.75 * 2^8
+    if (e < -64) e = -64;
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// Codes of 4 values over the scale 1 / inv; inv 0 (a scale that is not finite): codes 0.
+__device__ __forceinline__ uint32_t codes4(const float* f, float inv) {
+    if (inv == 0.f) return 0u;
+    return e4m3_pair(f[0] * inv, f[1] * inv) | (e4m3_pair(f[2] * inv, f[3] * inv) << 16);
+}
+
+// One E4M3 code times `ratio`, rounded to E4M3.
+__device__ __forceinline__ uint32_t requant4(uint32_t w, float ratio) {
+    const uint32_t lo = e4m3x2_to_f16x2(w), hi = e4m3x2_to_f16x2_hi(w);
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const __half2 h = *reinterpret_cast<const __half2*>(i == 0 ? &lo : &hi);
+        f[2 * i] = __low2float(h) * ratio;
+        f[2 * i + 1] = __high2float(h) * ratio;
+    }
+    return e4m3_pair(f[0], f[1]) | (e4m3_pair(f[2], f[3]) << 16);
+}
+
+// Queries: the block's tokens [t0, t1), every head.
+__device__ __forceinline__ void turn_queries(const KvAppendArgs& a, int t0, int t1, int* seq) {
+    // sequence of t0: the entries of q_start[1..B] that are not above it
+    int count = 0;
+    for (int b = 1 + threadIdx.x; b <= a.bt.B; b += kApThreads) count += a.bt.q_start[b] <= t0;
+    count = __reduce_add_sync(0xffffffffu, count);
+    if (threadIdx.x == 0) *seq = 0;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0 && count) atomicAdd(seq, count);
+    __syncthreads();
+    int b = *seq;
+    const int D = a.c.dim, upr = D / 16, units = a.q_heads * upr;
+    for (int t = t0; t < t1; ++t) {
+        while (b < a.bt.B && a.bt.q_start[b + 1] <= t) ++b;
+        if (b >= a.bt.B) return;  // rows behind the last sequence
+        const KvSeq s = kv_seq(a.bt, b, a.c.page);
+        const int pos = s.len - s.n + t - s.q0;
+        if (t < s.q0 || pos < 0) continue;
+        if (a.rope_dim > 0 && pos >= a.rope_rows) {
+            if (threadIdx.x == 0) atomicOr(a.error, kErrDevice);
+            continue;
+        }
+        const uint16_t* in = a.q + t * a.q_stride;
+        uint16_t* out = a.q_out + (size_t)t * a.q_heads * D;
+        for (int i = threadIdx.x; i < units; i += kApThreads) {
+            const Unit u(i % upr, a.rope_dim, a.interleaved);
+            const int at = i / upr * D;
+            float f[16];
+            load16(in + at, u, f);
+            if (u.angle >= 0) turn_unit<false>(f, u, a.rope + (size_t)pos * a.rope_dim, a.rope_dim / 2);
+            *reinterpret_cast<uint4*>(out + at + u.c0) =
+                make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+            *reinterpret_cast<uint4*>(out + at + u.c1) = make_uint4(
+                bf16_pair(f[8], f[9]), bf16_pair(f[10], f[11]), bf16_pair(f[12], f[13]), bf16_pair(f[14], f[15]));
+        }
+    }
+}
+
+// W: warps of a task (1 or 8).  NU: units that a thread holds in registers; the
+// others (a page with many new tokens where few were expected) are read twice.
+template <int W, int NU>
+__global__ void __launch_bounds__(kApThreads) kv_append_kernel(const KvAppendArgs a) {
+    __shared__ int64_t red[kApThreads / 32];
+    __shared__ int run_b, run_page;
+    __shared__ float amax_s[kApThreads / 32];
+    pdl_wait();
+    pdl_trigger();
+    if ((int)blockIdx.x >= a.store_blocks) {
+        const int t0 = ((int)blockIdx.x - a.store_blocks) * a.q_tokens;
+        turn_queries(a, t0, kv_min(t0 + a.q_tokens, a.bt.T), &run_b);
+        return;
+    }
+    const int run = blockIdx.x / a.task_blocks, P = a.c.page, D = a.c.dim;
+    // the run's sequence and page
+    const int per = (a.bt.B + kApThreads - 1) / kApThreads;
+    const int b0 = kv_min((int)threadIdx.x * per, a.bt.B), b1 = kv_min(b0 + per, a.bt.B);
+    int64_t mine = 0, before;
+    for (int b = b0; b < b1; ++b) mine += kv_run_pages(kv_seq(a.bt, b, P), P);
+    if (run >= block_scan<kApThreads>(mine, before, red)) return;
+    if (run >= before && run < before + mine) {
+        int left = run - (int)before, b = b0;
+        for (;; ++b) {
+            const int n = kv_run_pages(kv_seq(a.bt, b, P), P);
+            if (left < n) break;
+            left -= n;
+        }
+        run_b = b;
+        run_page = left;
+    }
+    __syncthreads();
+    const KvSeq s = kv_seq(a.bt, run_b, P);
+    const int page = kv_first_page(s, P) + run_page;
+    // positions [lo, hi) of the page are new; those before lo are held already
+    int lo = kv_max(page * P, kv_max(s.len - s.n, 0)), hi = kv_min(page * P + P, s.len);
+    const int held = lo - page * P;
+    if (a.rope_dim > 0 && hi > a.rope_rows) {
+        if (threadIdx.x == 0) atomicOr(a.error, kErrDevice);
+        hi = a.rope_rows;
+    }
+    const int id = a.bt.page_table[run_b * a.bt.table_stride + page];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int task = (blockIdx.x % a.task_blocks) * (8 / W) + warp / W;
+    // a task of W warps ends as one: only whole blocks (W = 8) meet at barriers below
+    if (task >= 2 * a.c.heads || hi <= lo) return;
+    if ((unsigned)id >= (unsigned)a.c.n_pages) {
+        if (threadIdx.x == 0 || lane == 0) atomicOr(a.error, kErrDevice);
+        return;
+    }
+    const bool keys = task < a.c.heads;
+    const int head = keys ? task : task - a.c.heads;
+    const int upr = D / 16, units = (hi - lo) * upr, tid = W == 1 ? lane : (int)threadIdx.x;
+    const int64_t stride = keys ? a.k_stride : a.v_stride;
+    const int rope_dim = keys ? a.rope_dim : 0;
+    const uint16_t* in = (keys ? a.k : a.v) + (int64_t)(s.q0 + lo - (s.len - s.n)) * stride + head * D;
+    uint8_t* block = (keys ? a.c.k : a.c.v) + id * a.c.page_stride + (size_t)head * P * D;
+    float* scale = (keys ? a.c.k_scale : a.c.v_scale) + id * a.c.scale_stride + head;
+    const float before_s = held > 0 ? *scale : 0.f;
+
+    auto load = [&](int i, float(&f)[16]) {
+        const int r = i / upr;
+        const Unit u(i % upr, rope_dim, a.interleaved);
+        load16(in + r * stride, u, f);
+        if (u.angle >= 0) turn_unit<true>(f, u, a.rope + (size_t)(lo + r) * a.rope_dim, a.rope_dim / 2);
+    };
+    auto store = [&](int i, const float(&f)[16], float inv) {
+        const Unit u(i % upr, rope_dim, a.interleaved);
+        uint8_t* row = block + (size_t)(held + i / upr) * D;
+        *reinterpret_cast<uint2*>(row + u.c0) = make_uint2(codes4(f, inv), codes4(f + 4, inv));
+        *reinterpret_cast<uint2*>(row + u.c1) = make_uint2(codes4(f + 8, inv), codes4(f + 12, inv));
+    };
+    float held_f[NU][16];
+    float amax = 0.f;
+    auto largest = [&](const float(&f)[16]) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) amax = amax_nan(amax, f[j]);
+    };
+#pragma unroll
+    for (int k = 0; k < NU; ++k) {
+        const int i = tid + k * 32 * W;
+        if (i < units) {
+            load(i, held_f[k]);
+            largest(held_f[k]);
+        }
+    }
+    for (int i = tid + NU * 32 * W; i < units; i += 32 * W) {
+        float f[16];
+        load(i, f);
+        largest(f);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) amax = amax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    if (W > 1) {
+        if (lane == 0) amax_s[warp] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < W; ++w) amax = amax_nan(amax, amax_s[w]);
+    }
+    float now = pow2_scale(amax);
+    if (held > 0) now = now != now || before_s != before_s ? __uint_as_float(0x7fffffffu) : fmaxf(now, before_s);
+    const float inv = now == now ? __frcp_rn(now) : 0.f;
+#pragma unroll
+    for (int k = 0; k < NU; ++k) {
+        const int i = tid + k * 32 * W;
+        if (i < units) store(i, held_f[k], inv);
+    }
+    for (int i = tid + NU * 32 * W; i < units; i += 32 * W) {
+        float f[16];
+        load(i, f);
+        store(i, f, inv);
+    }
+    if (held > 0 && now > before_s) {
+        const float ratio = __fdiv_rn(before_s, now);
+        uint4* codes = reinterpret_cast<uint4*>(block);
+        for (int i = tid; i < held * D / 16; i += 32 * W) {
+            const uint4 w = codes[i];
+            codes[i] = make_uint4(requant4(w.x, ratio), requant4(w.y, ratio), requant4(w.z, ratio), requant4(w.w, ratio));
+        }
+    }
+    if (W > 1) __syncthreads();  // every thread has read the scale
+    else __syncwarp();
+    if (tid == 0) *scale = now;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(KvAppendArgs a, cudaStream_t st, bool pdl) {
+    const int64_t runs = kv_most_runs(a.bt.B, a.bt.T, a.c.page);
+    // A warp a task where a sequence brings a few tokens, eight where it brings pages.
+    const bool few = (int64_t)a.bt.T <= 4 * (int64_t)a.bt.B;
+    a.task_blocks = few ? (2 * a.c.heads + 7) / 8 : 2 * a.c.heads;
+    const int64_t store = runs * a.task_blocks;
+    a.q_tokens = 1;
+    while (a.q_tokens < 16 && (int64_t)a.bt.T / (2 * a.q_tokens) >= 8 * num_sms()) a.q_tokens *= 2;
+    const int64_t q_blocks = a.q != nullptr ? (a.bt.T + a.q_tokens - 1) / a.q_tokens : 0;
+    if (store + q_blocks > INT32_MAX) return cudaErrorInvalidValue;
+    a.store_blocks = (int)store;
+    const dim3 grid((unsigned)(store + q_blocks)), block(kApThreads);
+    if (few) return launch_kernel(kv_append_kernel<1, 1>, grid, block, 0, st, pdl, a);
+    if (a.c.page * a.c.dim <= 16 * kApThreads) return launch_kernel(kv_append_kernel<8, 1>, grid, block, 0, st, pdl, a);
+    return launch_kernel(kv_append_kernel<8, 4>, grid, block, 0, st, pdl, a);
+}
+
+}  // namespace moe
