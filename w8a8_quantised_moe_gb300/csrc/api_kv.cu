@@ -47,9 +47,16 @@ KvBatch batch_of(const moe_w8a8_kv_batch_t& b) {
 struct AttendLayout {
     size_t info, part_ml, part_o, total;
 };
-AttendLayout attend_layout(int64_t T, int64_t Hq, int64_t D) {
+// Rows (new token, query head of a key head) that B sequences have on average, from
+// which on row tiles of 256 are faster than those of 16.
+constexpr int64_t kManyRows = 32;
+bool many_rows(int64_t B, int64_t T, int64_t group) { return T * group > kManyRows * B; }
+
+AttendLayout attend_layout(int64_t T, int64_t Hq, int64_t Hkv, int64_t D) {
     AttendLayout L{};
-    const int64_t part_rows = 2 * (int64_t)kv_few_ctas() * kKvFewRows;
+    // room for the form with many rows where a batch of up to T tokens can take it
+    const int64_t few = 2 * (int64_t)kv_few_ctas() * kKvFewRows, many = 2 * (int64_t)kv_tc_ctas() * kKvRows;
+    const int64_t part_rows = many_rows(1, T, Hq / Hkv) && many > few ? many : few;
     L.info = 256;
     L.part_ml = L.info + align256((size_t)T * Hq * 8);
     L.part_o = L.part_ml + align256((size_t)part_rows * 8);
@@ -106,7 +113,7 @@ moe_status_t moe_w8a8_kv_append(const moe_w8a8_kv_cache_t* cache, const moe_w8a8
 }
 
 size_t moe_w8a8_kv_attention_workspace_size(int64_t B, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t dim) {
-    return attend_shape_ok(B, T, q_heads, kv_heads, dim) ? attend_layout(T, q_heads, dim).total : 0;
+    return attend_shape_ok(B, T, q_heads, kv_heads, dim) ? attend_layout(T, q_heads, kv_heads, dim).total : 0;
 }
 
 moe_status_t moe_w8a8_kv_attention(const moe_w8a8_kv_cache_t* cache, const moe_w8a8_kv_batch_t* batch,
@@ -123,7 +130,7 @@ moe_status_t moe_w8a8_kv_attention(const moe_w8a8_kv_cache_t* cache, const moe_w
                  {cache->k_scale, cache->v_scale, batch->q_start, batch->lengths, batch->page_table}) ||
         !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return MOE_ERR_INVALID_ARG;
-    const AttendLayout L = attend_layout(T, q_heads, D);
+    const AttendLayout L = attend_layout(T, q_heads, cache->heads, D);
     if (workspace_bytes < L.total || injected(kInjectWsShort)) return MOE_ERR_WORKSPACE_TOO_SMALL;
     KvAttendArgs a{};
     a.c = cache_of(*cache);
@@ -143,7 +150,9 @@ moe_status_t moe_w8a8_kv_attention(const moe_w8a8_kv_cache_t* cache, const moe_w
     a.info = at<int2>(workspace, L.info);
     a.part_ml = at<float2>(workspace, L.part_ml);
     a.part_o = at<float>(workspace, L.part_o);
-    return from_cuda(launch_kv_attend_few(a, static_cast<cudaStream_t>(stream), pdl_default()));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return from_cuda(many_rows(B, T, a.sh.group) ? launch_kv_attend(a, st, pdl_default())
+                                                 : launch_kv_attend_few(a, st, pdl_default()));
 }
 
 }  // extern "C"

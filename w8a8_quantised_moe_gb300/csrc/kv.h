@@ -56,6 +56,11 @@ constexpr int kKvFewRows = 16, kKvFewTokens = 64, kKvFewWarps = 4;
 int kv_few_ctas();      // CTAs of its grid, at most
 cudaError_t launch_kv_attend_few(KvAttendArgs a, cudaStream_t st, bool pdl);
 
+// Row tiles of 256 rows on tcgen05 (kv_attend.cu): many rows.
+constexpr int kKvRows = 256;
+int kv_tc_ctas();
+cudaError_t launch_kv_attend(KvAttendArgs a, cudaStream_t st, bool pdl);
+
 // Joins the parts of rows whose units several CTAs had.
 cudaError_t launch_kv_join(const KvAttendArgs& a, cudaStream_t st, bool pdl);
 

@@ -1,0 +1,692 @@
+// kv_attend.cu -- attention over the paged 8-bit cache for many rows a sequence and
+// key head (prompts, chunks of them, drafted tokens), on the tcgen05 tensor cores.
+// The mathematics is that of kv_attend_few.cu.
+//
+// A CTA has 256 rows (query token, head of the group) of one key head as two tiles of
+// 128, each an MMA's M, and 128 keys a step:
+//   S = Q1 K^T + Q2 K^T   kind::f8f6f4 on the cache's codes as they are.  A bf16 query
+//       channel has 8 significant bits, two E4M3 values of 4: Q1 = E4M3(q), Q2 =
+//       E4M3(q - Q1), the row scaled to 128 <= max < 256, is q but for what lies below
+//       2^-17 of the row's largest channel.  Both parts at twice the fp16 rate cost
+//       what one fp16 product would, and the keys need no conversion.
+//   O += P V              kind::f16: weights in fp16 (11 bits) from tensor memory,
+//       values converted to fp16 (exact).  E4M3 pairs would not do here: weights
+//       below 2^-18 of the largest would be lost, and long contexts are made of them.
+//   warps 0-3, 4-7   softmax of one tile each, a thread a row: scores from tensor
+//                    memory, weights back in their place; the maximum is corrected
+//                    only when it rises by more than 2^8, by the same threads
+//   warps 8-11       values: codes from global memory to fp16 in shared memory, keys'
+//                    and values' scales
+//   warp 12          keys: TMA, a box a page
+//   warp 13          MMA issuer (and TMEM allocator)
+// Work is dealt as in kv_attend_few.cu.  Every wait is bounded (ptx.cuh).
+#include <mutex>
+
+#include "block_dev.cuh"
+#include "block_tiles.cuh"
+#include "kv_dev.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kTcThreads = 512;
+constexpr int kTcTile = 128;      // rows of a tile, keys of a step
+constexpr int kTcKS = 3, kTcVS = 2;  // stages of keys, of values
+constexpr float kTcHeadroom = 8.f, kTcWeightBits = 6.f;  // as in kv_attend_few.cu
+constexpr uint32_t kTcCols = 512;
+
+// The launch gives every thread 128 registers: 2 x 128 x 192 + 128 x 80 + 128 x 48 of 512 x 128.
+__device__ __forceinline__ void tc_regs_softmax() { asm volatile("setmaxnreg.inc.sync.aligned.u32 192;"); }
+__device__ __forceinline__ void tc_regs_values() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
+__device__ __forceinline__ void tc_regs_few() { asm volatile("setmaxnreg.dec.sync.aligned.u32 48;"); }
+
+template <int D>
+struct Tc {
+    static constexpr int kPiece = kTcTile * D;        // bytes of a tile's rows in E4M3 (Q1, Q2; keys)
+    static constexpr int kValues = kTcTile * D * 2;   // of a step's values in fp16
+    static constexpr int kOffK = 4 * kPiece;          // after Q [tile][part]
+    static constexpr int kOffV = kOffK + kTcKS * kPiece;
+    static constexpr int kOffScales = kOffV + kTcVS * kValues;  // [stage][8 groups of 16 keys] (key, log2 value, 1 / value)
+    static constexpr int kOffBars = kOffScales + kTcVS * 8 * 16;
+    // q_full[2] k_full[KS] k_empty[KS] v_full[VS] v_empty[VS] s_full[2] p_full[2] pv_done[2] teardown stall
+    static constexpr int kNumBars = 2 + 2 * kTcKS + 2 * kTcVS + 6 + 2;
+    static constexpr int kOffWork = (kOffBars + kNumBars * 8 + 15) / 16 * 16;
+    static constexpr int kOffMisc = (kOffWork + (int)sizeof(KvWork) + 15) / 16 * 16;
+    static constexpr int kUsed = kOffMisc + 64 + kTcThreads / 32 * 8;
+    // more than half an SM's, so that the one CTA that holds the tensor memory is alone there
+    static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
+    static_assert(kSmem <= 232448, "shared memory budget");
+    // place of a 16-byte piece in a swizzled E4M3 tile (128-byte swizzle, 64-byte where rows are 64 bytes)
+    __device__ static __forceinline__ int place(int row, int c) {
+        return row * D + ((D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4);
+    }
+    __device__ static __forceinline__ uint64_t desc(uint32_t saddr) {
+        if (D == 128) return smem_desc_sw128(saddr);
+        uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+        d |= static_cast<uint64_t>(1) << 16;
+        d |= static_cast<uint64_t>(512 >> 4) << 32;  // 8 rows x 64 B
+        d |= static_cast<uint64_t>(1) << 46;
+        d |= static_cast<uint64_t>(4) << 61;  // 64-byte swizzle
+        return d;
+    }
+    // Values: channels contiguous ("MN-major"), 64 of them a 128-byte row, 8 keys a
+    // 1024-byte group; the next group of keys follows, the next 64 channels are 16 KB on.
+    __device__ static __forceinline__ uint64_t desc_values(uint32_t saddr) {
+        uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+        d |= static_cast<uint64_t>((kTcTile * 128) >> 4) << 16;
+        d |= static_cast<uint64_t>(1024 >> 4) << 32;
+        d |= static_cast<uint64_t>(1) << 46;
+        d |= static_cast<uint64_t>(2) << 61;
+        return d;
+    }
+    __device__ static __forceinline__ int place_value(int key, int c) {  // c: 8 channels
+        return (c >> 3) * (kTcTile * 128) + (key >> 3) * 1024 + (key & 7) * 128 + (((c & 7) ^ (key & 7)) << 4);
+    }
+};
+
+struct TcBars {
+    uint64_t *q_full, *k_full, *k_empty, *v_full, *v_empty, *s_full, *p_full, *pv_done, *teardown, *stall;
+    __device__ __forceinline__ explicit TcBars(uint8_t* at) {
+        uint64_t* b = reinterpret_cast<uint64_t*>(at);
+        q_full = b;
+        k_full = q_full + 2;
+        k_empty = k_full + kTcKS;
+        v_full = k_empty + kTcKS;
+        v_empty = v_full + kTcVS;
+        s_full = v_empty + kTcVS;
+        p_full = s_full + 2;
+        pv_done = p_full + 2;
+        teardown = pv_done + 2;
+        stall = teardown + 1;
+    }
+};
+
+// A CTA's run, cut at the borders of row tiles; every role walks through it.
+struct TcWalk {
+    KvPlace at;
+    int64_t left;
+    int n;        // steps here
+    bool first;
+    __device__ __forceinline__ explicit TcWalk(const KvWork& w) : at(w.at), left(w.u1 - w.u0), first(true) { count(); }
+    __device__ __forceinline__ void count() { n = left < at.end - at.unit ? (int)left : at.end - at.unit; }
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ void next(const KvAttendArgs& a) {
+        left -= n;
+        first = false;
+        if (left > 0) {
+            at.unit = at.end - 1;
+            kv_next(at, a.bt, a.sh, a.c.heads);
+            count();
+        }
+    }
+    // tiles of the row tile that have rows
+    __device__ __forceinline__ int tiles(const KvAttendArgs& a) const {
+        return at.s.n * a.sh.group - at.rt * a.sh.rows > kTcTile ? 2 : 1;
+    }
+};
+
+// A ring's stage and phase.
+struct TcRing {
+    uint32_t stage = 0, phase = 0;
+    __device__ __forceinline__ void step(uint32_t n) {
+        if (++stage == n) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// Pages of 16-key groups: group i of the step that begins at key k0; -1: none there.
+__device__ __forceinline__ int tc_page(const KvAttendArgs& a, const KvPlace& p, int k0, int i) {
+    const int k = k0 + 16 * i;
+    return k < p.s.len ? __ldg(a.bt.page_table + p.b * a.bt.table_stride + k / a.c.page) : -1;
+}
+
+// The registers of the tensor-memory loads before it: no use of them moves above.
+__device__ __forceinline__ void pin32(uint32_t (&r)[32]) {
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
+// Waits for the warp's tensor-memory loads; no use of the registers moves above it.
+__device__ __forceinline__ void tc_wait_ld_16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15])::"memory");
+}
+// Each thread of the warp writes 16 consecutive columns of its lane.
+__device__ __forceinline__ void tc_st_16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// a * b + c on pairs
+__device__ __forceinline__ f32x2 fma2_of(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// ------------------------------------------------------------------ softmax
+// One thread: row `row` of the CTA's 256, tile t.
+template <int D>
+struct TcRow {
+    float m, l, factor;
+    int pos;
+    bool valid;
+
+    // This row's query as two E4M3 parts in shared memory.
+    __device__ __forceinline__ void start(const KvAttendArgs& a, const KvPlace& p, int row, uint8_t* q_tile) {
+        const int r = p.rt * a.sh.rows + row, tok = r / a.sh.group;
+        valid = r < p.s.n * a.sh.group;
+        pos = valid ? p.s.len - p.s.n + tok : -1;
+        m = -INFINITY;
+        l = 0.f;
+        const int lrow = row & (kTcTile - 1);
+        uint4 w[D / 8];
+        uint32_t top = 0;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + (valid ? (int64_t)(p.s.q0 + tok) * a.q_stride + (p.head * a.sh.group + r % a.sh.group) * D : 0));
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            w[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                         __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu)));
+        }
+        top = max(top & 0xffffu, top >> 16);
+        int e = (int)(top >> 7) - 127 - 7;
+        if (e < -120) e = -120;
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+        factor = __fmul_rn(__fmul_rn(a.scale, kLog2e), __uint_as_float((uint32_t)(127 + e) << 23));
+        if (top >= 0x7f80u) factor = __uint_as_float(0x7fffffffu);  // a row that is not finite
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint4& v = w[2 * c + (j >> 1)];
+                const uint32_t x = j & 1 ? v.z : v.x, y = j & 1 ? v.w : v.y;
+                const float f[4] = {bf16_lo(x) * down, bf16_hi(x) * down, bf16_lo(y) * down, bf16_hi(y) * down};
+                hi[j] = e4m3_pair(f[0], f[1]) | (e4m3_pair(f[2], f[3]) << 16);
+                const uint32_t h0 = e4m3x2_to_f16x2(hi[j]), h1 = e4m3x2_to_f16x2_hi(hi[j]);
+                const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+                const float2 g1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+                lo[j] = e4m3_pair(f[0] - g0.x, f[1] - g0.y) | (e4m3_pair(f[2] - g1.x, f[3] - g1.y) << 16);
+            }
+            *reinterpret_cast<uint4*>(q_tile + Tc<D>::place(lrow, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(q_tile + Tc<D>::kPiece + Tc<D>::place(lrow, c)) =
+                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
+
+    // Sums at `o` (tensor memory) times `by`.
+    __device__ __forceinline__ void rescale(uint32_t o, float by) {
+#pragma unroll
+        for (int c = 0; c < D; c += 16) {
+            uint32_t r[16];
+            tmem_ld_16(o + c, r);
+            tc_wait_ld_16(r);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * by);
+            tc_st_16(o + c, r);
+        }
+        tmem_wait_st();
+    }
+
+    // One step: scores at `s` become weights there.  k0: first key; some: O holds sums.
+    __device__ __forceinline__ void step(const KvAttendArgs& a, uint32_t s, uint32_t o, const float4* scales, int k0,
+                                         bool some) {
+        uint32_t r[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld_32(s + 32 * i, r[i]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pin32(r[i]);
+        // keys [lo, hi] of the step are seen
+        const int hi = pos - k0, lo = a.sh.window > 0 ? pos - a.sh.window + 1 - k0 : 0;
+        const bool border = __any_sync(0xffffffffu, hi < kTcTile - 1 || lo > 0);
+        float top = -INFINITY;
+        if (border) {
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                const float4 sc = scales[g];
+                const float f = sc.x * factor;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int c = 16 * g + i;
+                    uint32_t& x = r[c >> 5][c & 31];
+                    const float v = c >= lo && c <= hi ? fmaf(__uint_as_float(x), f, sc.y) : -INFINITY;
+                    top = fmaxf(top, v);
+                    x = __float_as_uint(v);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                const float4 sc = scales[g];
+                float t = __uint_as_float(r[g >> 1][(g & 1) * 16]);
+#pragma unroll
+                for (int i = 1; i < 16; ++i) t = fmaxf(t, __uint_as_float(r[g >> 1][(g & 1) * 16 + i]));
+                top = fmaxf(top, fmaf(t, sc.x * factor, sc.y));
+            }
+        }
+        if (__any_sync(0xffffffffu, top > m + kTcHeadroom)) {
+            const float now = fmaxf(top, m), down = now == m ? 1.f : ex2(m - now);
+            m = now;
+            l *= down;
+            if (some) rescale(o, down);
+        }
+        if (border)
+            weights<true>(s, scales, r);
+        else
+            weights<false>(s, scales, r);
+        tmem_wait_st();
+    }
+
+    // Scores r (READY: scaled already) to weights at `s`, fp16 pairs, and their sum.
+    template <bool READY>
+    __device__ __forceinline__ void weights(uint32_t s, const float4* scales, const uint32_t (&r)[4][32]) {
+        const float base = m == -INFINITY ? 0.f : m - kTcWeightBits;
+        const f32x2 base2 = pack2(-base, -base);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {  // 32 keys: 16 columns of weights
+            uint32_t w[16];
+#pragma unroll
+            for (int gg = 0; gg < 2; ++gg) {
+                const float4 sc = scales[2 * h + gg];
+                const float f = sc.x * factor, shift = sc.y - base;
+                const f32x2 f2 = pack2(f, f), shift2 = pack2(shift, shift);
+                f32x2 sum = 0ull;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int c = 16 * gg + 2 * i;
+                    const f32x2 x = pack2(__uint_as_float(r[h][c]), __uint_as_float(r[h][c + 1]));
+                    float p0, p1;
+                    unpack2(READY ? add2(x, base2) : fma2_of(x, f2, shift2), p0, p1);
+                    p0 = ex2(p0);
+                    p1 = ex2(p1);
+                    sum = add2(sum, pack2(p0, p1));
+                    w[8 * gg + i] = f16_pair(p0, p1);
+                }
+                float s0, s1;
+                unpack2(sum, s0, s1);
+                s0 += s1;
+                if (s0 != 0.f) l = fmaf(s0, sc.z, l);  // unseen keys leave a block's NaN scale alone
+            }
+            tc_st_16(s + 16 * h, w);
+        }
+    }
+
+    // The sums to the output row, or to the CTA's part of it.
+    __device__ __forceinline__ void finish(const KvAttendArgs& a, const KvWork& work, const TcWalk& walk, int row,
+                                           uint32_t o) {
+        const KvPlace& p = walk.at;
+        const KvParts parts = kv_parts(work, p, walk.first);
+        const int r = p.rt * a.sh.rows + row;
+        const int64_t out_row =
+            (int64_t)(p.s.q0 + r / a.sh.group) * a.q_heads + p.head * a.sh.group + r % a.sh.group;
+        const float down = 0x1p-6f, sum = l * down;
+        const float by = parts.parts > 1 ? down : sum == 0.f ? 0.f : __fdiv_rn(down, sum);
+        float* part = a.part_o + ((size_t)parts.slot * a.sh.rows + row) * D;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+            uint32_t v[32];
+            tmem_ld_32(o + c, v);
+            tmem_wait_ld();
+            pin32(v);
+            if (!valid) continue;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * by);
+            if (parts.parts > 1) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<uint4*>(part + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    auto pair = [&](int k) { return bf16_pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])); };
+                    *reinterpret_cast<uint4*>(a.out + out_row * D + c + i) =
+                        make_uint4(pair(i), pair(i + 2), pair(i + 4), pair(i + 6));
+                }
+            }
+        }
+        if (!valid) return;
+        if (parts.parts > 1)
+            a.part_ml[(size_t)parts.slot * a.sh.rows + row] = make_float2(m, sum);
+        else if (a.lse != nullptr)
+            a.lse[out_row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+        if (parts.leader) a.info[out_row] = make_int2(parts.slot, parts.parts * 256 + row);
+    }
+};
+
+template <int D>
+__device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& work, uint8_t* smem, const TcBars& bar,
+                                           uint32_t tmem, const WaitCtl& ctl) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 2, row = threadIdx.x;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s = tmem + lanes + t * kTcTile, o = tmem + lanes + 2 * kTcTile + t * kTcTile;
+    uint8_t* q_tile = smem + t * 2 * Tc<D>::kPiece;
+    TcRing v;
+    uint32_t s_phase = 0, pv = 0;  // steps of this tile
+    TcRow<D> mine;
+    for (TcWalk walk(work); walk.more(); walk.next(a)) {
+        if (t >= walk.tiles(a)) {
+            for (int j = 0; j < walk.n; ++j) v.step(kTcVS);
+            continue;
+        }
+        mine.start(a, walk.at, row, q_tile);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.q_full[t]);
+        for (int j = 0; j < walk.n; ++j) {
+            if (!warp_wait(&bar.v_full[v.stage], v.phase, ctl) || !warp_wait(&bar.s_full[t], s_phase, ctl)) return;
+            tc_fence_after();
+            mine.step(a, s, o, reinterpret_cast<const float4*>(smem + Tc<D>::kOffScales) + 8 * v.stage,
+                      (walk.at.unit + j) * kTcTile, j > 0);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.p_full[t]);
+            v.step(kTcVS);
+            s_phase ^= 1u;
+        }
+        pv += walk.n;
+        if (!warp_wait(&bar.pv_done[t], (pv - 1) & 1u, ctl)) return;
+        tc_fence_after();
+        mine.finish(a, work, walk, row, o);
+        tc_fence_before();
+    }
+}
+
+// ------------------------------------------------------------------ values
+template <int D>
+__device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& work, uint8_t* smem, const TcBars& bar,
+                                          const WaitCtl& ctl) {
+    constexpr int kPerRow = D / 16, kRows = 128 / kPerRow, kPasses = kTcTile / kRows;  // rows of a pass
+    const int tid = threadIdx.x - 256, lane = tid & 31, c = tid % kPerRow;
+    uint4 w[kPasses];
+    float ks = 0.f, vs = 0.f;
+    TcWalk walk(work);
+    int j = 0;  // the step whose codes are loaded next
+    bool more = walk.more();
+    // the pages of that step, 16 keys a lane of the first eight
+    int ids = more ? tc_page(a, walk.at, walk.at.unit * kTcTile, lane & 7) : -1;
+    auto load = [&] {
+        const KvPlace& p = walk.at;
+        const int k0 = (p.unit + j) * kTcTile;
+        const int id = ids;
+        const bool there = (unsigned)id < (unsigned)a.c.n_pages;
+        if (!there && lane < 8 && k0 + 16 * lane < p.s.len) atomicOr(a.error, kErrDevice);
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int key = i * kRows + tid / kPerRow;
+            const int page = __shfl_sync(0xffffffffu, id, key >> 4);
+            const bool valid = (unsigned)page < (unsigned)a.c.n_pages && k0 + key < p.s.len;
+            const uint8_t* src =
+                a.c.v + page * a.c.page_stride + ((size_t)p.head * a.c.page + (k0 + key) % a.c.page) * D + c * 16;
+            w[i] = valid ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+        }
+        ks = 1.f;
+        vs = 0.f;
+        if (there && lane < 8) {
+            ks = __ldg(a.c.k_scale + id * a.c.scale_stride + p.head);
+            vs = __ldg(a.c.v_scale + id * a.c.scale_stride + p.head);
+        }
+        if (++j == walk.n) {
+            walk.next(a);
+            j = 0;
+        }
+        more = walk.more();
+        if (more) ids = tc_page(a, walk.at, (walk.at.unit + j) * kTcTile, lane & 7);
+    };
+    if (!more) return;
+    load();
+    TcRing v;
+    for (int64_t left = work.u1 - work.u0; left > 0; --left) {
+        if (!warp_wait(&bar.v_empty[v.stage], v.phase ^ 1u, ctl)) return;
+        uint8_t* dst = smem + Tc<D>::kOffV + v.stage * Tc<D>::kValues;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int key = i * kRows + tid / kPerRow;
+            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                h[2 * k] = e4m3x2_to_f16x2(x[k]);
+                h[2 * k + 1] = e4m3x2_to_f16x2_hi(x[k]);
+            }
+            // lanes of the second 64 channels begin with their other half: all banks at once
+            const bool swap = D == 128 && (c & 4);
+            const uint4 first = swap ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
+            const uint4 second = swap ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(h[4], h[5], h[6], h[7]);
+            *reinterpret_cast<uint4*>(dst + Tc<D>::place_value(key, 2 * c + (swap ? 1 : 0))) = first;
+            *reinterpret_cast<uint4*>(dst + Tc<D>::place_value(key, 2 * c + (swap ? 0 : 1))) = second;
+        }
+        if (tid < 8) {
+            float lg, inv;
+            value_scale(vs, lg, inv);
+            reinterpret_cast<float4*>(smem + Tc<D>::kOffScales)[8 * v.stage + tid] = make_float4(ks, lg, inv, 0.f);
+        }
+        if (more) load();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.v_full[v.stage]);
+        v.step(kTcVS);
+    }
+}
+
+// ------------------------------------------------------------------ keys
+template <int D>
+__device__ __forceinline__ void tc_keys(const KvAttendArgs& a, const KvWork& work, uint8_t* smem, const TcBars& bar,
+                                        const CUtensorMap* map, int no_page, const WaitCtl& ctl) {
+    const int lane = threadIdx.x & 31, boxes = kTcTile / a.c.page, groups = a.c.page / 16;
+    int ok = 1;
+    if (lane == 0) ok = !a.stall || mbar_wait(bar.stall, 0, ctl);  // the test hook's wait runs out
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    TcRing k;
+    uint32_t it = 0;
+    TcWalk walk(work);
+    int id = walk.more() && lane < boxes ? tc_page(a, walk.at, walk.at.unit * kTcTile, lane * groups) : -1;
+    for (; ok && walk.more(); walk.next(a)) {
+        for (int j = 0; j < walk.n; ++j, ++it) {
+            if (j == 0 && it != 0 && lane < boxes) id = tc_page(a, walk.at, walk.at.unit * kTcTile, lane * groups);
+            // a page that is not there is read as one behind the last: zeros
+            const int page = (unsigned)id < (unsigned)a.c.n_pages ? id : no_page;
+            if (lane < boxes && j + 1 < walk.n) id = tc_page(a, walk.at, (walk.at.unit + j + 1) * kTcTile, lane * groups);
+            if (lane == 0) {
+                ok = mbar_wait(&bar.k_empty[k.stage], k.phase ^ 1u, ctl);
+                if (ok) mbar_arrive_expect_tx(&bar.k_full[k.stage], Tc<D>::kPiece);
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            if (lane < boxes)
+                tma_load_3d(smem + Tc<D>::kOffK + k.stage * Tc<D>::kPiece + lane * a.c.page * D, map,
+                            &bar.k_full[k.stage], 0, walk.at.head * a.c.page, page);
+            k.step(kTcKS);
+        }
+        if (!ok) break;
+    }
+    // drain: every copy issued must land before the CTA may exit
+    if (lane == 0)
+        for (uint32_t st = 0; st < (uint32_t)kTcKS && st < it; ++st) {
+            const uint32_t last = it - 1 - ((it - 1 - st) % kTcKS);
+            mbar_wait_drain(&bar.k_full[st], (last / kTcKS) & 1u);
+        }
+}
+
+// ------------------------------------------------------------------ products
+template <int D>
+__device__ __forceinline__ void tc_products(const KvAttendArgs& a, const KvWork& work, uint8_t* smem,
+                                            const TcBars& bar, uint32_t tmem, const WaitCtl& ctl) {
+    constexpr uint32_t idesc_s = idesc_e4m3(kTcTile, kTcTile);
+    constexpr uint32_t idesc_o = idesc_f16_f32(kTcTile, D) | (1u << 16);  // values: channels contiguous
+    const uint64_t q0 = Tc<D>::desc(smem_u32(smem)), k0 = Tc<D>::desc(smem_u32(smem) + Tc<D>::kOffK);
+    const uint64_t v0 = Tc<D>::desc_values(smem_u32(smem) + Tc<D>::kOffV);
+    TcRing k, v;
+    uint32_t q_phase[2] = {0, 0}, steps[2] = {0, 0};  // segments, steps of a tile
+    // O of tile t += its weights times the values of the ring's stage
+    auto weighted = [&](int t, bool some, bool last) {
+        if (!mbar_wait(&bar.v_full[v.stage], v.phase, ctl) || !mbar_wait(&bar.p_full[t], steps[t] & 1u, ctl)) return false;
+        tc_fence_after();
+        const uint64_t b = v0 + (uint64_t)(v.stage * (Tc<D>::kValues >> 4));
+#pragma unroll
+        for (int i = 0; i < kTcTile / 16; ++i)
+            mma_f16_tmem_a(tmem + 2 * kTcTile + t * kTcTile, tmem + t * kTcTile + 8 * i, b + (uint64_t)(i * (2048 >> 4)),
+                           idesc_o, some || i != 0 ? 1u : 0u);
+        mma_commit(&bar.pv_done[t]);
+        if (last) mma_commit(&bar.v_empty[v.stage]);
+        ++steps[t];
+        return true;
+    };
+    bool ok = true;
+    for (TcWalk walk(work); ok && walk.more(); walk.next(a)) {
+        const int tiles = walk.tiles(a);
+        for (int t = 0; ok && t < tiles; ++t) {
+            ok = mbar_wait(&bar.q_full[t], q_phase[t], ctl);
+            q_phase[t] ^= 1u;
+        }
+        for (int j = 0; ok && j < walk.n; ++j) {
+            for (int t = 0; ok && t < tiles; ++t) {
+                if (j > 0) {
+                    ok = weighted(t, j > 1, t + 1 == tiles);
+                    // the scores take the weights' place: these must have been read
+                    ok = ok && mbar_wait(&bar.pv_done[t], (steps[t] - 1) & 1u, ctl);
+                }
+                if (t == 0) ok = ok && mbar_wait(&bar.k_full[k.stage], k.phase, ctl);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t q = q0 + (uint64_t)(t * 2 * (Tc<D>::kPiece >> 4));
+                const uint64_t b = k0 + (uint64_t)(k.stage * (Tc<D>::kPiece >> 4));
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i)  // 32 bytes of channels an MMA
+                        mma_e4m3(tmem + t * kTcTile, q + (uint64_t)(part * (Tc<D>::kPiece >> 4) + 2 * i),
+                                 b + (uint64_t)(2 * i), idesc_s, part != 0 || i != 0 ? 1u : 0u);
+                mma_commit(&bar.s_full[t]);
+            }
+            if (!ok) break;
+            mma_commit(&bar.k_empty[k.stage]);
+            k.step(kTcKS);
+            if (j > 0) v.step(kTcVS);
+        }
+        for (int t = 0; ok && t < tiles; ++t) ok = weighted(t, walk.n > 1, t + 1 == tiles);
+        v.step(kTcVS);
+    }
+    mma_commit(bar.teardown);
+    mbar_wait_drain(bar.teardown, 0);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    kv_attend_kernel(const __grid_constant__ CUtensorMap keys, const KvAttendArgs a, int no_page) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if ((smem_u32(smem) & 1023u) != 0u) {
+        if (threadIdx.x == 0) atomicOr(a.error, kErrDevice);
+        return;
+    }
+    const TcBars bar(smem + Tc<D>::kOffBars);
+    KvWork* work = reinterpret_cast<KvWork*>(smem + Tc<D>::kOffWork);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Tc<D>::kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Tc<D>::kOffMisc + 8);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&bar.q_full[t], 4);
+            mbar_init(&bar.s_full[t], 1);
+            mbar_init(&bar.p_full[t], 4);
+            mbar_init(&bar.pv_done[t], 1);
+        }
+        for (int i = 0; i < kTcKS; ++i) {
+            mbar_init(&bar.k_full[i], 1);
+            mbar_init(&bar.k_empty[i], 1);
+        }
+        for (int i = 0; i < kTcVS; ++i) {
+            mbar_init(&bar.v_full[i], 4);
+            mbar_init(&bar.v_empty[i], 1);
+        }
+        mbar_init(bar.teardown, 1);
+        mbar_init(bar.stall, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&keys);
+    }
+    if (warp == 13) {
+        tmem_alloc(tmem_slot, kTcCols);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    if (warp == 13) pdl_trigger();  // not before the tensor memory is this CTA's
+    kv_find_work<kTcThreads>(a, gridDim.x, 1, work, reinterpret_cast<int64_t*>(smem + Tc<D>::kOffMisc + 64));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtl ctl{abort_flag, a.error, a.timeout_ns, 0u};
+    if (work->u1 > work->u0) {
+        if (warp < 8) {
+            tc_regs_softmax();
+            tc_softmax<D>(a, *work, smem, bar, tmem, ctl);
+        } else if (warp < 12) {
+            tc_regs_values();
+            tc_values<D>(a, *work, smem, bar, ctl);
+        } else {
+            tc_regs_few();
+            if (warp == 12) tc_keys<D>(a, *work, smem, bar, &keys, no_page, ctl);
+            if (warp == 13 && lane == 0) tc_products<D>(a, *work, smem, bar, tmem, ctl);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 13) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTcCols);
+    }
+}
+
+template <int D>
+cudaError_t launch_tc(const KvAttendArgs& a, cudaStream_t st, bool pdl) {
+    auto kern = kv_attend_kernel<D>;
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    std::call_once(once, [&] {
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<D>::kSmem);
+    });
+    if (err != cudaSuccess) return err;
+    CUtensorMap keys;
+    const int pages = a.c.n_pages > 0 ? a.c.n_pages : 1;
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.c.heads * a.c.page, (uint64_t)pages};
+    const uint64_t strides[2] = {(uint64_t)D, (uint64_t)a.c.page_stride};
+    const uint32_t box[3] = {(uint32_t)D, (uint32_t)a.c.page, 1};
+    if (!make_tensor_map_3d(&keys, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.c.k, dims, strides, box,
+                            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+        return cudaErrorInvalidValue;
+    return launch_kernel(kern, dim3(kv_tc_ctas()), dim3(kTcThreads), Tc<D>::kSmem, st, pdl, keys, a, pages);
+}
+
+}  // namespace
+
+int kv_tc_ctas() { return num_sms(); }
+
+cudaError_t launch_kv_attend(KvAttendArgs a, cudaStream_t st, bool pdl) {
+    a.sh.rows = kKvRows;
+    a.sh.tokens = kTcTile;
+    const cudaError_t e = a.c.dim == 64 ? launch_tc<64>(a, st, pdl) : launch_tc<128>(a, st, pdl);
+    return e != cudaSuccess ? e : launch_kv_join(a, st, pdl);
+}
+
+}  // namespace moe
