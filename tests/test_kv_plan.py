@@ -62,6 +62,18 @@ int main() {
             U += kv_seq_units(kv_seq(bt, b, page), sh) * heads;
         }
         if (U == 0) continue;
+        for (int b = 0; b < B; ++b) {  // sums by formula and one by one
+            const KvSeq s = kv_seq(bt, b, page);
+            long long sum = 0;
+            for (int rt = 0; rt < kv_row_tiles(s, sh); ++rt) {
+                int first, count;
+                kv_units(s, sh, rt, first, count);
+                CHECK(first >= 0 && count >= 1);
+                CHECK(kv_units_before(s, sh, rt) == sum);
+                sum += count;
+            }
+            CHECK(kv_seq_units(s, sh) == sum);
+        }
         const int most = 1 + rnd(400), ctas = kv_ctas(U, most, 1 + rnd(4));
         CHECK(ctas >= 1 && ctas <= most && ctas <= U);
         std::map<std::tuple<int, int, int, int>, int> done;
@@ -75,7 +87,18 @@ int main() {
             while (b + 1 < B && before[b + 1] <= u0) ++b;
             while (kv_seq_units(kv_seq(bt, b, page), sh) == 0) --b;
             KvPlace p;
-            kv_locate(p, bt, sh, b, before[b], u0);
+            p.b = b;
+            p.s = kv_seq(bt, b, page);
+            const long long per = kv_seq_units(p.s, sh);
+            p.head = (int)((u0 - before[b]) / per);
+            int found = 0;
+            KvPlace q = p;
+            for (int rt = 0; rt < kv_row_tiles(q.s, sh); ++rt)
+                if (kv_enter_if(q, sh, rt, u0 - before[b] - p.head * per, before[b] + p.head * per)) {
+                    p = q;
+                    ++found;
+                }
+            CHECK(found == 1);
             for (long long u = u0; u < u1; ++u) {
                 CHECK(kv_owner(U, ctas, u) == c);
                 CHECK(p.b < B && p.head < heads && p.rt < kv_row_tiles(p.s, sh));

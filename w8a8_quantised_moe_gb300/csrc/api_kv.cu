@@ -37,8 +37,9 @@ bool bad_ptrs(std::initializer_list<const void*> by16, std::initializer_list<con
 }
 
 KvCache cache_of(const moe_w8a8_kv_cache_t& c) {
-    return {c.k, c.v, c.k_scale, c.v_scale, c.page_stride, c.scale_stride, (int)c.n_pages, (int)c.heads, (int)c.page,
-            (int)c.dim};
+    const int bits = c.page == 16 ? 4 : c.page == 32 ? 5 : c.page == 64 ? 6 : 7;
+    return {c.k,           c.v,          c.k_scale,    c.v_scale,   c.page_stride, c.scale_stride,
+            (int)c.n_pages, (int)c.heads, (int)c.page, (int)c.dim, bits};
 }
 KvBatch batch_of(const moe_w8a8_kv_batch_t& b) {
     return {b.q_start, b.lengths, b.page_table, b.table_stride, (int)b.B, (int)b.T, (int)b.max_pages};

@@ -15,6 +15,7 @@ struct KvCache {
     float *k_scale, *v_scale;  // [n_pages][heads], scale_stride values from page to page
     int64_t page_stride, scale_stride;
     int n_pages, heads, page, dim;
+    int page_bits;  // page = 1 << page_bits
 };
 
 struct KvAppendArgs {

@@ -35,11 +35,6 @@ constexpr int kTcKS = 3, kTcVS = 2;  // stages of keys, of values
 constexpr float kTcHeadroom = 8.f, kTcWeightBits = 6.f;  // as in kv_attend_few.cu
 constexpr uint32_t kTcCols = 512;
 
-// The launch gives every thread 128 registers: 2 x 128 x 192 + 128 x 80 + 128 x 48 of 512 x 128.
-__device__ __forceinline__ void tc_regs_softmax() { asm volatile("setmaxnreg.inc.sync.aligned.u32 192;"); }
-__device__ __forceinline__ void tc_regs_values() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
-__device__ __forceinline__ void tc_regs_few() { asm volatile("setmaxnreg.dec.sync.aligned.u32 48;"); }
-
 template <int D>
 struct Tc {
     static constexpr int kPiece = kTcTile * D;        // bytes of a tile's rows in E4M3 (Q1, Q2; keys)
@@ -139,17 +134,14 @@ struct TcRing {
 // Pages of 16-key groups: group i of the step that begins at key k0; -1: none there.
 __device__ __forceinline__ int tc_page(const KvAttendArgs& a, const KvPlace& p, int k0, int i) {
     const int k = k0 + 16 * i;
-    return k < p.s.len ? __ldg(a.bt.page_table + p.b * a.bt.table_stride + k / a.c.page) : -1;
+    return k < p.s.len ? __ldg(a.bt.page_table + p.b * a.bt.table_stride + (k >> a.c.page_bits)) : -1;
 }
 
-// The registers of the tensor-memory loads before it: no use of them moves above.
-__device__ __forceinline__ void pin32(uint32_t (&r)[32]) {
-    asm volatile(""
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+// max of three
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // Waits for the warp's tensor-memory loads; no use of the registers moves above it.
@@ -158,6 +150,14 @@ __device__ __forceinline__ void tc_wait_ld_16(uint32_t (&r)[16]) {
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
                    "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void tc_wait_ld_32(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
 // Each thread of the warp writes 16 consecutive columns of its lane.
 __device__ __forceinline__ void tc_st_16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -248,87 +248,90 @@ struct TcRow {
     }
 
     // One step: scores at `s` become weights there.  k0: first key; some: O holds sums.
+    // The scores are read twice, 32 keys at a time, rather than kept in 128 registers: a
+    // short loop, where the unrolled one waited for its instructions.
     __device__ __forceinline__ void step(const KvAttendArgs& a, uint32_t s, uint32_t o, const float4* scales, int k0,
                                          bool some) {
-        uint32_t r[4][32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld_32(s + 32 * i, r[i]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pin32(r[i]);
         // keys [lo, hi] of the step are seen
         const int hi = pos - k0, lo = a.sh.window > 0 ? pos - a.sh.window + 1 - k0 : 0;
-        const bool border = __any_sync(0xffffffffu, hi < kTcTile - 1 || lo > 0);
+        if (__any_sync(0xffffffffu, hi < kTcTile - 1 || lo > 0))
+            step_of<true>(s, o, scales, lo, hi, some);
+        else
+            step_of<false>(s, o, scales, lo, hi, some);
+    }
+
+    template <bool BORDER>
+    __device__ __forceinline__ void step_of(uint32_t s, uint32_t o, const float4* scales, int lo, int hi, bool some) {
         float top = -INFINITY;
-        if (border) {
+        uint32_t r[2][32];
+        tmem_ld_32(s, r[0]);
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {
-                const float4 sc = scales[g];
+        for (int h = 0; h < 4; ++h) {
+            tc_wait_ld_32(r[h & 1]);
+            if (h < 3) tmem_ld_32(s + 32 * (h + 1), r[(h + 1) & 1]);
+#pragma unroll
+            for (int gg = 0; gg < 2; ++gg) {
+                const float4 sc = scales[2 * h + gg];
                 const float f = sc.x * factor;
+                const uint32_t* x = r[h & 1] + 16 * gg;
+                if (BORDER) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int c = 16 * g + i;
-                    uint32_t& x = r[c >> 5][c & 31];
-                    const float v = c >= lo && c <= hi ? fmaf(__uint_as_float(x), f, sc.y) : -INFINITY;
-                    top = fmaxf(top, v);
-                    x = __float_as_uint(v);
+                    for (int i = 0; i < 16; ++i) {
+                        const int c = 32 * h + 16 * gg + i;
+                        top = fmaxf(top, c >= lo && c <= hi ? fmaf(__uint_as_float(x[i]), f, sc.y) : -INFINITY);
+                    }
+                } else {  // scales are positive: the largest product is the largest score's
+                    float t = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+#pragma unroll
+                    for (int i = 3; i < 15; i += 2) t = max3(t, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                    t = fmaxf(t, __uint_as_float(x[15]));
+                    top = fmaxf(top, fmaf(t, f, sc.y));
                 }
             }
-        } else {
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-                const float4 sc = scales[g];
-                float t = __uint_as_float(r[g >> 1][(g & 1) * 16]);
-#pragma unroll
-                for (int i = 1; i < 16; ++i) t = fmaxf(t, __uint_as_float(r[g >> 1][(g & 1) * 16 + i]));
-                top = fmaxf(top, fmaf(t, sc.x * factor, sc.y));
-            }
         }
+        tmem_ld_32(s, r[0]);
         if (__any_sync(0xffffffffu, top > m + kTcHeadroom)) {
             const float now = fmaxf(top, m), down = now == m ? 1.f : ex2(m - now);
             m = now;
             l *= down;
             if (some) rescale(o, down);
         }
-        if (border)
-            weights<true>(s, scales, r);
-        else
-            weights<false>(s, scales, r);
-        tmem_wait_st();
-    }
-
-    // Scores r (READY: scaled already) to weights at `s`, fp16 pairs, and their sum.
-    template <bool READY>
-    __device__ __forceinline__ void weights(uint32_t s, const float4* scales, const uint32_t (&r)[4][32]) {
         const float base = m == -INFINITY ? 0.f : m - kTcWeightBits;
-        const f32x2 base2 = pack2(-base, -base);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {  // 32 keys: 16 columns of weights
+        for (int h = 0; h < 4; ++h) {
+            tc_wait_ld_32(r[h & 1]);
+            if (h < 3) tmem_ld_32(s + 32 * (h + 1), r[(h + 1) & 1]);
             uint32_t w[16];
 #pragma unroll
             for (int gg = 0; gg < 2; ++gg) {
                 const float4 sc = scales[2 * h + gg];
                 const float f = sc.x * factor, shift = sc.y - base;
                 const f32x2 f2 = pack2(f, f), shift2 = pack2(shift, shift);
+                const uint32_t* x = r[h & 1] + 16 * gg;
                 f32x2 sum = 0ull;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int c = 16 * gg + 2 * i;
-                    const f32x2 x = pack2(__uint_as_float(r[h][c]), __uint_as_float(r[h][c + 1]));
+                for (int i = 0; i < 16; i += 2) {
                     float p0, p1;
-                    unpack2(READY ? add2(x, base2) : fma2_of(x, f2, shift2), p0, p1);
+                    unpack2(fma2_of(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), f2, shift2), p0, p1);
+                    if (BORDER) {
+                        const int c = 32 * h + 16 * gg + i;
+                        p0 = c >= lo && c <= hi ? p0 : -INFINITY;
+                        p1 = c + 1 >= lo && c + 1 <= hi ? p1 : -INFINITY;
+                    }
                     p0 = ex2(p0);
                     p1 = ex2(p1);
                     sum = add2(sum, pack2(p0, p1));
-                    w[8 * gg + i] = f16_pair(p0, p1);
+                    w[8 * gg + i / 2] = f16_pair(p0, p1);
                 }
                 float s0, s1;
                 unpack2(sum, s0, s1);
                 s0 += s1;
                 if (s0 != 0.f) l = fmaf(s0, sc.z, l);  // unseen keys leave a block's NaN scale alone
             }
+            // columns [16 h, 16 h + 16) are scores that have been read: 32 h is not below them
             tc_st_16(s + 16 * h, w);
         }
+        tmem_wait_st();
     }
 
     // The sums to the output row, or to the CTA's part of it.
@@ -346,8 +349,7 @@ struct TcRow {
         for (int c = 0; c < D; c += 32) {
             uint32_t v[32];
             tmem_ld_32(o + c, v);
-            tmem_wait_ld();
-            pin32(v);
+            tc_wait_ld_32(v);
             if (!valid) continue;
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * by);
@@ -383,15 +385,24 @@ __device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& 
     TcRing v;
     uint32_t s_phase = 0, pv = 0;  // steps of this tile
     TcRow<D> mine;
-    for (TcWalk walk(work); walk.more(); walk.next(a)) {
-        if (t >= walk.tiles(a)) {
-            for (int j = 0; j < walk.n; ++j) v.step(kTcVS);
-            continue;
-        }
-        mine.start(a, walk.at, row, q_tile);
+    TcWalk walk(work);
+    auto start = [&](TcRow<D>& r, const TcWalk& w) {
+        if (!w.more() || t >= w.tiles(a)) return;
+        r.start(a, w.at, row, q_tile);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.q_full[t]);
+    };
+    start(mine, walk);
+    while (walk.more()) {
+        TcWalk next = walk;
+        if (t >= walk.tiles(a)) {
+            for (int j = 0; j < walk.n; ++j) v.step(kTcVS);
+            next.next(a);
+            start(mine, next);
+            walk = next;
+            continue;
+        }
         for (int j = 0; j < walk.n; ++j) {
             if (!warp_wait(&bar.v_full[v.stage], v.phase, ctl) || !warp_wait(&bar.s_full[t], s_phase, ctl)) return;
             tc_fence_after();
@@ -403,11 +414,18 @@ __device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& 
             v.step(kTcVS);
             s_phase ^= 1u;
         }
+        // the last scores are there, so the queries have been read: the next row tile's
+        // take their place while the last product runs
+        TcRow<D> after = mine;
+        next.next(a);
+        start(after, next);
         pv += walk.n;
         if (!warp_wait(&bar.pv_done[t], (pv - 1) & 1u, ctl)) return;
         tc_fence_after();
         mine.finish(a, work, walk, row, o);
         tc_fence_before();
+        mine = after;
+        walk = next;
     }
 }
 
@@ -436,7 +454,7 @@ __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& w
             const int page = __shfl_sync(0xffffffffu, id, key >> 4);
             const bool valid = (unsigned)page < (unsigned)a.c.n_pages && k0 + key < p.s.len;
             const uint8_t* src =
-                a.c.v + page * a.c.page_stride + ((size_t)p.head * a.c.page + (k0 + key) % a.c.page) * D + c * 16;
+                a.c.v + page * a.c.page_stride + ((p.head << a.c.page_bits) + ((k0 + key) & (a.c.page - 1))) * D + c * 16;
             w[i] = valid ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
         }
         ks = 1.f;
@@ -480,11 +498,11 @@ __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& w
             value_scale(vs, lg, inv);
             reinterpret_cast<float4*>(smem + Tc<D>::kOffScales)[8 * v.stage + tid] = make_float4(ks, lg, inv, 0.f);
         }
-        if (more) load();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.v_full[v.stage]);
         v.step(kTcVS);
+        if (more) load();
     }
 }
 
@@ -528,26 +546,78 @@ __device__ __forceinline__ void tc_keys(const KvAttendArgs& a, const KvWork& wor
 }
 
 // ------------------------------------------------------------------ products
+// N MMAs of 32 channels each: D (+)= A B^T, E4M3, both operands advancing 32 bytes; the
+// first overwrites D where `accumulate` is 0.  One block, so that the issuing thread, which
+// waits for its issue slots among busy warps, has few instructions.
+template <int N>
+__device__ __forceinline__ void tc_mma_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    static_assert(N == 2 || N == 4, "D / 32");
+    if constexpr (N == 4)
+        asm volatile(
+            "{\n\t.reg .pred p, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
+            "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+            "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, t;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, t;\n\t.reg .b64 a1, b1;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
+            "add.s64 a1, %1, 2;\n\tadd.s64 b1, %2, 2;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, t;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// The eight MMAs of 16 keys of a step: O (+)= P V, weights 8 columns on each, values 2 KB.
+__device__ __forceinline__ void tc_mma_values(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, t;\n\t.reg .b64 b1, b2, b3, b4, b5, b6, b7;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
+        "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\tadd.s64 b4, %2, 512;\n\t"
+        "add.s64 b5, %2, 640;\n\tadd.s64 b6, %2, 768;\n\tadd.s64 b7, %2, 896;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\tadd.u32 a4, %1, 32;\n\t"
+        "add.u32 a5, %1, 40;\n\tadd.u32 a6, %1, 48;\n\tadd.u32 a7, %1, 56;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, t;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// The whole warp runs the loop, so that what the MMAs take stays uniform; lane 0 issues.
 template <int D>
 __device__ __forceinline__ void tc_products(const KvAttendArgs& a, const KvWork& work, uint8_t* smem,
                                             const TcBars& bar, uint32_t tmem, const WaitCtl& ctl) {
     constexpr uint32_t idesc_s = idesc_e4m3(kTcTile, kTcTile);
     constexpr uint32_t idesc_o = idesc_f16_f32(kTcTile, D) | (1u << 16);  // values: channels contiguous
+    const int lane = threadIdx.x & 31;
     const uint64_t q0 = Tc<D>::desc(smem_u32(smem)), k0 = Tc<D>::desc(smem_u32(smem) + Tc<D>::kOffK);
     const uint64_t v0 = Tc<D>::desc_values(smem_u32(smem) + Tc<D>::kOffV);
     TcRing k, v;
     uint32_t q_phase[2] = {0, 0}, steps[2] = {0, 0};  // segments, steps of a tile
     // O of tile t += its weights times the values of the ring's stage
     auto weighted = [&](int t, bool some, bool last) {
-        if (!mbar_wait(&bar.v_full[v.stage], v.phase, ctl) || !mbar_wait(&bar.p_full[t], steps[t] & 1u, ctl)) return false;
+        if (!warp_wait(&bar.v_full[v.stage], v.phase, ctl) || !warp_wait(&bar.p_full[t], steps[t] & 1u, ctl)) return false;
         tc_fence_after();
-        const uint64_t b = v0 + (uint64_t)(v.stage * (Tc<D>::kValues >> 4));
-#pragma unroll
-        for (int i = 0; i < kTcTile / 16; ++i)
-            mma_f16_tmem_a(tmem + 2 * kTcTile + t * kTcTile, tmem + t * kTcTile + 8 * i, b + (uint64_t)(i * (2048 >> 4)),
-                           idesc_o, some || i != 0 ? 1u : 0u);
-        mma_commit(&bar.pv_done[t]);
-        if (last) mma_commit(&bar.v_empty[v.stage]);
+        if (lane == 0) {
+            tc_mma_values(tmem + 2 * kTcTile + t * kTcTile, tmem + t * kTcTile,
+                          v0 + (uint64_t)(v.stage * (Tc<D>::kValues >> 4)), idesc_o, some ? 1u : 0u);
+            mma_commit(&bar.pv_done[t]);
+            if (last) mma_commit(&bar.v_empty[v.stage]);
+        }
+        __syncwarp();
         ++steps[t];
         return true;
     };
@@ -555,39 +625,42 @@ __device__ __forceinline__ void tc_products(const KvAttendArgs& a, const KvWork&
     for (TcWalk walk(work); ok && walk.more(); walk.next(a)) {
         const int tiles = walk.tiles(a);
         for (int t = 0; ok && t < tiles; ++t) {
-            ok = mbar_wait(&bar.q_full[t], q_phase[t], ctl);
+            ok = warp_wait(&bar.q_full[t], q_phase[t], ctl);
             q_phase[t] ^= 1u;
         }
         for (int j = 0; ok && j < walk.n; ++j) {
-            for (int t = 0; ok && t < tiles; ++t) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (t >= tiles || !ok) break;
                 if (j > 0) {
                     ok = weighted(t, j > 1, t + 1 == tiles);
                     // the scores take the weights' place: these must have been read
-                    ok = ok && mbar_wait(&bar.pv_done[t], (steps[t] - 1) & 1u, ctl);
+                    ok = ok && warp_wait(&bar.pv_done[t], (steps[t] - 1) & 1u, ctl);
                 }
-                if (t == 0) ok = ok && mbar_wait(&bar.k_full[k.stage], k.phase, ctl);
+                if (t == 0) ok = ok && warp_wait(&bar.k_full[k.stage], k.phase, ctl);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t q = q0 + (uint64_t)(t * 2 * (Tc<D>::kPiece >> 4));
-                const uint64_t b = k0 + (uint64_t)(k.stage * (Tc<D>::kPiece >> 4));
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i)  // 32 bytes of channels an MMA
-                        mma_e4m3(tmem + t * kTcTile, q + (uint64_t)(part * (Tc<D>::kPiece >> 4) + 2 * i),
-                                 b + (uint64_t)(2 * i), idesc_s, part != 0 || i != 0 ? 1u : 0u);
-                mma_commit(&bar.s_full[t]);
+                if (lane == 0) {
+                    const uint64_t q = q0 + (uint64_t)(t * 2 * (Tc<D>::kPiece >> 4));
+                    const uint64_t b = k0 + (uint64_t)(k.stage * (Tc<D>::kPiece >> 4));
+                    tc_mma_scores<D / 32>(tmem + t * kTcTile, q, b, idesc_s, 0u);
+                    tc_mma_scores<D / 32>(tmem + t * kTcTile, q + (uint64_t)(Tc<D>::kPiece >> 4), b, idesc_s, 1u);
+                    mma_commit(&bar.s_full[t]);
+                    if (t + 1 == tiles) mma_commit(&bar.k_empty[k.stage]);
+                }
+                __syncwarp();
             }
             if (!ok) break;
-            mma_commit(&bar.k_empty[k.stage]);
             k.step(kTcKS);
             if (j > 0) v.step(kTcVS);
         }
         for (int t = 0; ok && t < tiles; ++t) ok = weighted(t, walk.n > 1, t + 1 == tiles);
         v.step(kTcVS);
     }
-    mma_commit(bar.teardown);
-    mbar_wait_drain(bar.teardown, 0);
+    if (lane == 0) {
+        mma_commit(bar.teardown);
+        mbar_wait_drain(bar.teardown, 0);
+    }
 }
 
 template <int D>
@@ -602,7 +675,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     KvWork* work = reinterpret_cast<KvWork*>(smem + Tc<D>::kOffWork);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Tc<D>::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Tc<D>::kOffMisc + 8);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bar.q_full[t], 4);
@@ -638,15 +711,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const WaitCtl ctl{abort_flag, a.error, a.timeout_ns, 0u};
     if (work->u1 > work->u0) {
         if (warp < 8) {
-            tc_regs_softmax();
             tc_softmax<D>(a, *work, smem, bar, tmem, ctl);
         } else if (warp < 12) {
-            tc_regs_values();
             tc_values<D>(a, *work, smem, bar, ctl);
         } else {
-            tc_regs_few();
             if (warp == 12) tc_keys<D>(a, *work, smem, bar, &keys, no_page, ctl);
-            if (warp == 13 && lane == 0) tc_products<D>(a, *work, smem, bar, tmem, ctl);
+            if (warp == 13) tc_products<D>(a, *work, smem, bar, tmem, ctl);
         }
     }
     __syncwarp();

@@ -86,7 +86,7 @@ struct FewCopies {
     __device__ __forceinline__ int key0() const { return at.unit * kKvFewTokens + (int)(threadIdx.x >> 5) * kFewKeys; }
     __device__ __forceinline__ void look_up(const KvAttendArgs& a) {
         const int k0 = key0();
-        id = k0 < at.s.len ? __ldg(a.bt.page_table + at.b * a.bt.table_stride + k0 / a.c.page) : -1;
+        id = k0 < at.s.len ? __ldg(a.bt.page_table + at.b * a.bt.table_stride + (k0 >> a.c.page_bits)) : -1;
     }
     __device__ __forceinline__ void start(const KvAttendArgs& a, const KvWork& w) {
         at = w.at;
@@ -99,7 +99,7 @@ struct FewCopies {
         if (left > 0) {
             const int lane = threadIdx.x & 31, k0 = key0();
             const bool there = k0 < at.s.len && kv_page_ok(a.c, id, a.error);
-            const int in_page = k0 % a.c.page;
+            const int in_page = k0 & (a.c.page - 1);
             const size_t off = there ? id * a.c.page_stride + ((size_t)at.head * a.c.page + in_page) * D : 0;
             constexpr int kPer = 32 / Few<D>::kChunks;  // rows of an instruction
             const int c = lane % Few<D>::kChunks;

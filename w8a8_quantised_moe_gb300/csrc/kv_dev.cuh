@@ -84,12 +84,13 @@ __device__ __forceinline__ int64_t block_scan(int64_t mine, int64_t& before, int
 
 // What a CTA does of the batch's units: [u0, u1) of U, dealt to `ctas`, from `at` on.
 struct KvWork {
-    int64_t U, u0, u1;
-    int ctas;
+    int64_t U, u0, u1, base;  // base: number of the first unit of sequence b
+    int ctas, b;
     KvPlace at;
 };
 // Every thread of the block calls it; `work` is shared memory.  Each thread counts
-// the units of consecutive sequences; the one that has the CTA's first finds its place.
+// the units of consecutive sequences; the one whose the CTA's first unit is names the
+// sequence, in which every thread looks at row tiles of its own.
 template <int THREADS>
 __device__ __forceinline__ void kv_find_work(const KvAttendArgs& a, int most_ctas, int least_units, KvWork* work,
                                              int64_t* red) {
@@ -107,17 +108,28 @@ __device__ __forceinline__ void kv_find_work(const KvAttendArgs& a, int most_cta
         work->ctas = ctas;
     }
     if (u0 < u1 && u0 >= before && u0 < before + mine) {
-        for (int b = b0; b < b1; ++b) {
+        int b = b0;
+        for (; b < b1 - 1; ++b) {
             const int64_t units = kv_seq_units(kv_seq(a.bt, b, a.sh.page), a.sh) * a.c.heads;
-            if (u0 < before + units) {
-                KvPlace p;
-                kv_locate(p, a.bt, a.sh, b, before, u0);
-                work->at = p;
-                break;
-            }
+            if (u0 < before + units) break;
             before += units;
         }
+        work->b = b;
+        work->base = before;
     }
+    __syncthreads();
+    if (u0 >= u1) return;
+    KvPlace p;
+    p.b = work->b;
+    p.s = kv_seq(a.bt, p.b, a.sh.page);
+    const int64_t per_head = kv_seq_units(p.s, a.sh);
+    p.head = (int)((u0 - work->base) / per_head);
+    const int64_t head_base = work->base + p.head * per_head;
+    for (int rt = threadIdx.x, tiles = kv_row_tiles(p.s, a.sh); rt < tiles; rt += THREADS)
+        if (kv_enter_if(p, a.sh, rt, u0 - head_base, head_base)) {
+            work->at = p;
+            break;
+        }
     __syncthreads();
 }
 

@@ -60,25 +60,62 @@ KV_HD int64_t kv_most_runs(int64_t B, int64_t T, int64_t page) {
 struct KvShape {
     int group, rows, tokens, window, page;
 };
-KV_HD int kv_row_tiles(const KvSeq& s, const KvShape& sh) { return (int)(((int64_t)s.n * sh.group + sh.rows - 1) / sh.rows); }
+KV_HD int kv_row_tiles(const KvSeq& s, const KvShape& sh) { return (s.n * sh.group + sh.rows - 1) / sh.rows; }
 KV_HD void kv_units(const KvSeq& s, const KvShape& sh, int rt, int& first, int& count) {
-    const int64_t r0 = (int64_t)rt * sh.rows, all = (int64_t)s.n * sh.group;
-    const int64_t r1 = (r0 + sh.rows < all ? r0 + sh.rows : all) - 1;
-    const int p0 = s.len - s.n + (int)(r0 / sh.group), p1 = s.len - s.n + (int)(r1 / sh.group);
-    const int lo = sh.window > 0 && p0 >= sh.window ? p0 - sh.window + 1 : 0;
-    first = lo / sh.tokens;
-    count = kv_max(p1 < 0 ? 0 : p1 / sh.tokens + 1 - first, 1);
+    const int c = s.len - s.n, r0 = rt * sh.rows, r1 = kv_min(r0 + sh.rows, s.n * sh.group) - 1;
+    const int p0 = c + r0 / sh.group, p1 = c + r1 / sh.group;
+    first = sh.window > 0 && p0 >= sh.window ? (p0 - sh.window + 1) / sh.tokens : 0;
+    count = p1 < 0 ? 1 : p1 / sh.tokens + 1 - first;
+}
+
+// sum of floor((a i + b) / m) over 0 <= i < n, for a, b >= 0 and m > 0: the points of the
+// lattice under a line.  Whole parts of the slope and of b are counted at once; what
+// is left is counted along the other axis, where the slope is m / a.
+KV_HD int64_t kv_floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+    int64_t sum = 0;
+    while (n > 0) {
+        sum += (a / m) * (n * (n - 1) / 2) + (b / m) * n;
+        a %= m;
+        b %= m;
+        const int64_t top = a * n + b;  // m times the height at i = n
+        if (top < m) break;
+        n = top / m;
+        b = top % m;
+        const int64_t t = m;
+        m = a;
+        a = t;
+    }
+    return sum;
+}
+// Units of a sequence's row tiles before rt, for one key head, 0 <= rt <= its row tiles.
+// The last row of a tile but the last is at position c + floor(((rt + 1) rows - 1) / group),
+// so that its last unit is the floor of a linear function of rt, as is the first.
+KV_HD int64_t kv_units_before(const KvSeq& s, const KvShape& sh, int rt) {
+    const int64_t c = s.len - s.n, g = sh.group, R = sh.rows, m = g * sh.tokens;
+    int64_t sum = 0;
+    int whole = rt;
+    if (rt > 0 && rt == kv_row_tiles(s, sh)) {
+        int first, count;
+        kv_units(s, sh, --whole, first, count);
+        sum = count;
+    }
+    sum += whole;  // one unit each, and those before the last
+    int64_t i0 = c < 0 ? -c * g / R : 0;  // the row tiles before see no key
+    if (i0 < whole) sum += kv_floor_sum(whole - i0, m, R, c * g + (i0 + 1) * R - 1);
+    if (sh.window > 0) {
+        const int64_t past = (sh.window - c) * g;  // rows from which on the window cuts
+        i0 = past > 0 ? (past + R - 1) / R : 0;
+        if (i0 < whole) sum -= kv_floor_sum(whole - i0, m, R, i0 * R + (c - sh.window + 1) * g);
+    }
+    return sum;
 }
 // Units of a sequence and one key head.
 KV_HD int64_t kv_seq_units(const KvSeq& s, const KvShape& sh) {
-    int64_t sum = 0;
     const int tiles = kv_row_tiles(s, sh);
-    for (int rt = 0; rt < tiles; ++rt) {
-        int first, count;
-        kv_units(s, sh, rt, first, count);
-        sum += count;
-    }
-    return sum;
+    if (tiles > 1) return kv_units_before(s, sh, tiles);
+    int first = 0, count = 0;
+    if (tiles == 1) kv_units(s, sh, 0, first, count);
+    return count;
 }
 
 // The batch's U units, in the order (sequence, key head, row tile, unit), are dealt
@@ -104,21 +141,16 @@ KV_HD void kv_enter(KvPlace& p, const KvShape& sh) {
     p.unit = p.first;
     p.end = p.first + count;
 }
-// The unit `u` of sequence b, whose first is number `base` (u - base < heads * its units a head).
-KV_HD void kv_locate(KvPlace& p, const KvBatch& bt, const KvShape& sh, int b, int64_t base, int64_t u) {
-    p.b = b;
-    p.s = kv_seq(bt, b, sh.page);
-    const int64_t per = kv_seq_units(p.s, sh);
-    p.head = (int)((u - base) / per);
-    p.base = base + p.head * per;
-    p.rt = 0;
+// Whether unit `u`, counted within one key head of p's sequence, is of row tile rt; if so, p is there.
+KV_HD bool kv_enter_if(KvPlace& p, const KvShape& sh, int rt, int64_t u, int64_t head_base) {
+    const int64_t before = kv_units_before(p.s, sh, rt);
+    if (u < before) return false;
+    p.rt = rt;
     kv_enter(p, sh);
-    while (u - p.base >= p.end - p.first) {
-        p.base += p.end - p.first;
-        ++p.rt;
-        kv_enter(p, sh);
-    }
-    p.unit = p.first + (int)(u - p.base);
+    if (u >= before + (p.end - p.first)) return false;
+    p.base = head_base + before;
+    p.unit = p.first + (int)(u - before);
+    return true;
 }
 // The next unit; there must be one.
 KV_HD void kv_next(KvPlace& p, const KvBatch& bt, const KvShape& sh, int heads) {
