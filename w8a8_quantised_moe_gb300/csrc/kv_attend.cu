@@ -197,15 +197,20 @@ struct TcRow {
         m = -INFINITY;
         l = 0.f;
         const int lrow = row & (kTcTile - 1);
-        uint4 w[D / 8];
         uint32_t top = 0;
         const uint4* src = reinterpret_cast<const uint4*>(
             a.q + (valid ? (int64_t)(p.s.q0 + tok) * a.q_stride + (p.head * a.sh.group + r % a.sh.group) * D : 0));
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        // Short loops: code that runs once a row tile waits for its instructions.
+#pragma unroll 1
+        for (int i = 0; i < D / 8; i += 8) {
+            uint4 w[8];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            w[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
-                                         __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu)));
+            for (int k = 0; k < 8; ++k) w[k] = valid ? __ldg(src + i + k) : none;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)  // magnitudes of bf16 pairs, compared as whole numbers
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[k].x & 0x7fff7fffu, w[k].y & 0x7fff7fffu),
+                                             __vmaxu2(w[k].z & 0x7fff7fffu, w[k].w & 0x7fff7fffu)));
         }
         top = max(top & 0xffffu, top >> 16);
         int e = (int)(top >> 7) - 127 - 7;
@@ -213,13 +218,13 @@ struct TcRow {
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
         factor = __fmul_rn(__fmul_rn(a.scale, kLog2e), __uint_as_float((uint32_t)(127 + e) << 23));
         if (top >= 0x7f80u) factor = __uint_as_float(0x7fffffffu);  // a row that is not finite
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
+            const uint4 w[2] = {valid ? __ldg(src + 2 * c) : none, valid ? __ldg(src + 2 * c + 1) : none};
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint4& v = w[2 * c + (j >> 1)];
-                const uint32_t x = j & 1 ? v.z : v.x, y = j & 1 ? v.w : v.y;
+                const uint32_t x = j & 1 ? w[j >> 1].z : w[j >> 1].x, y = j & 1 ? w[j >> 1].w : w[j >> 1].y;
                 const float f[4] = {bf16_lo(x) * down, bf16_hi(x) * down, bf16_lo(y) * down, bf16_hi(y) * down};
                 hi[j] = e4m3_pair(f[0], f[1]) | (e4m3_pair(f[2], f[3]) << 16);
                 const uint32_t h0 = e4m3x2_to_f16x2(hi[j]), h1 = e4m3x2_to_f16x2_hi(hi[j]);
@@ -227,15 +232,15 @@ struct TcRow {
                 const float2 g1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
                 lo[j] = e4m3_pair(f[0] - g0.x, f[1] - g0.y) | (e4m3_pair(f[2] - g1.x, f[3] - g1.y) << 16);
             }
-            *reinterpret_cast<uint4*>(q_tile + Tc<D>::place(lrow, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(q_tile + Tc<D>::kPiece + Tc<D>::place(lrow, c)) =
-                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            uint8_t* at = q_tile + Tc<D>::place(lrow, c);
+            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(at + Tc<D>::kPiece) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     }
 
     // Sums at `o` (tensor memory) times `by`.
     __device__ __forceinline__ void rescale(uint32_t o, float by) {
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D; c += 16) {
             uint32_t r[16];
             tmem_ld_16(o + c, r);
@@ -248,90 +253,133 @@ struct TcRow {
     }
 
     // One step: scores at `s` become weights there.  k0: first key; some: O holds sums.
-    // The scores are read twice, 32 keys at a time, rather than kept in 128 registers: a
-    // short loop, where the unrolled one waited for its instructions.
+    // The scores are read twice, 32 keys at a time, rather than kept in 128 registers, and
+    // the loops are short: unrolled over the whole step, the warps waited for instructions.
     __device__ __forceinline__ void step(const KvAttendArgs& a, uint32_t s, uint32_t o, const float4* scales, int k0,
                                          bool some) {
         // keys [lo, hi] of the step are seen
         const int hi = pos - k0, lo = a.sh.window > 0 ? pos - a.sh.window + 1 - k0 : 0;
-        if (__any_sync(0xffffffffu, hi < kTcTile - 1 || lo > 0))
-            step_of<true>(s, o, scales, lo, hi, some);
-        else
-            step_of<false>(s, o, scales, lo, hi, some);
-    }
-
-    template <bool BORDER>
-    __device__ __forceinline__ void step_of(uint32_t s, uint32_t o, const float4* scales, int lo, int hi, bool some) {
+        const bool border = __any_sync(0xffffffffu, hi < kTcTile - 1 || lo > 0);
         float top = -INFINITY;
-        uint32_t r[2][32];
-        tmem_ld_32(s, r[0]);
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            tc_wait_ld_32(r[h & 1]);
-            if (h < 3) tmem_ld_32(s + 32 * (h + 1), r[(h + 1) & 1]);
-#pragma unroll
-            for (int gg = 0; gg < 2; ++gg) {
-                const float4 sc = scales[2 * h + gg];
-                const float f = sc.x * factor;
-                const uint32_t* x = r[h & 1] + 16 * gg;
-                if (BORDER) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int c = 32 * h + 16 * gg + i;
-                        top = fmaxf(top, c >= lo && c <= hi ? fmaf(__uint_as_float(x[i]), f, sc.y) : -INFINITY);
-                    }
-                } else {  // scales are positive: the largest product is the largest score's
-                    float t = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
-#pragma unroll
-                    for (int i = 3; i < 15; i += 2) t = max3(t, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-                    t = fmaxf(t, __uint_as_float(x[15]));
-                    top = fmaxf(top, fmaf(t, f, sc.y));
-                }
+        if (border) {
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {
+                uint32_t r[32];
+                tmem_ld_32(s + 32 * h, r);
+                tc_wait_ld_32(r);
+                float2 sc[2];
+                hide(r, sc, scales + 2 * h, lo - 32 * h, hi - 32 * h);
+                top = fmaxf(top, fmaxf(fmaf(largest(r), sc[0].x, sc[0].y), fmaf(largest(r + 16), sc[1].x, sc[1].y)));
             }
+        } else {
+            uint32_t r[2][32];
+            tmem_ld_32(s, r[0]);
+#pragma unroll 1
+            for (int h = 0; h < 4; h += 2)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    tc_wait_ld_32(r[b]);
+                    if (b == 0 || h == 0) tmem_ld_32(s + 32 * (h + b + 1), r[b ^ 1]);
+                    const float4 s0 = scales[2 * (h + b)], s1 = scales[2 * (h + b) + 1];
+                    // scales are positive: the largest product is the largest score's
+                    top = max3(top, fmaf(largest(r[b]), s0.x * factor, s0.y),
+                               fmaf(largest(r[b] + 16), s1.x * factor, s1.y));
+                }
         }
-        tmem_ld_32(s, r[0]);
         if (__any_sync(0xffffffffu, top > m + kTcHeadroom)) {
             const float now = fmaxf(top, m), down = now == m ? 1.f : ex2(m - now);
             m = now;
             l *= down;
             if (some) rescale(o, down);
         }
+        // weights: columns [16 h, 16 h + 16) are scores that have been read
         const float base = m == -INFINITY ? 0.f : m - kTcWeightBits;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            tc_wait_ld_32(r[h & 1]);
-            if (h < 3) tmem_ld_32(s + 32 * (h + 1), r[(h + 1) & 1]);
-            uint32_t w[16];
-#pragma unroll
-            for (int gg = 0; gg < 2; ++gg) {
-                const float4 sc = scales[2 * h + gg];
-                const float f = sc.x * factor, shift = sc.y - base;
-                const f32x2 f2 = pack2(f, f), shift2 = pack2(shift, shift);
-                const uint32_t* x = r[h & 1] + 16 * gg;
-                f32x2 sum = 0ull;
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    float p0, p1;
-                    unpack2(fma2_of(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), f2, shift2), p0, p1);
-                    if (BORDER) {
-                        const int c = 32 * h + 16 * gg + i;
-                        p0 = c >= lo && c <= hi ? p0 : -INFINITY;
-                        p1 = c + 1 >= lo && c + 1 <= hi ? p1 : -INFINITY;
-                    }
-                    p0 = ex2(p0);
-                    p1 = ex2(p1);
-                    sum = add2(sum, pack2(p0, p1));
-                    w[8 * gg + i / 2] = f16_pair(p0, p1);
-                }
-                float s0, s1;
-                unpack2(sum, s0, s1);
-                s0 += s1;
-                if (s0 != 0.f) l = fmaf(s0, sc.z, l);  // unseen keys leave a block's NaN scale alone
+        if (border) {
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {
+                uint32_t r[32];
+                tmem_ld_32(s + 32 * h, r);
+                tc_wait_ld_32(r);
+                float2 sc[2];
+                hide(r, sc, scales + 2 * h, lo - 32 * h, hi - 32 * h);
+                weights(r, sc[0], sc[1], scales[2 * h].z, scales[2 * h + 1].z, base, s + 16 * h);
             }
-            // columns [16 h, 16 h + 16) are scores that have been read: 32 h is not below them
-            tc_st_16(s + 16 * h, w);
+        } else {
+            uint32_t r[2][32];
+            tmem_ld_32(s, r[0]);
+#pragma unroll 1
+            for (int h = 0; h < 4; h += 2)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    tc_wait_ld_32(r[b]);
+                    if (b == 0 || h == 0) tmem_ld_32(s + 32 * (h + b + 1), r[b ^ 1]);
+                    const float4 s0 = scales[2 * (h + b)], s1 = scales[2 * (h + b) + 1];
+                    weights(r[b], make_float2(s0.x * factor, s0.y), make_float2(s1.x * factor, s1.y), s0.z, s1.z, base,
+                            s + 16 * (h + b));
+                }
         }
         tmem_wait_st();
+    }
+
+    // Largest of 16 scores.
+    __device__ static __forceinline__ float largest(const uint32_t* x) {
+        float t = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+        float u = max3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
+#pragma unroll
+        for (int i = 6; i < 14; i += 4) {
+            t = max3(t, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            u = max3(u, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+        }
+        t = max3(t, __uint_as_float(x[14]), __uint_as_float(x[15]));
+        return fmaxf(t, u);
+    }
+
+    // 32 scores of which [lo, hi] are seen: the others to -inf.  sc: a group's factor and
+    // addend, such that -inf stays so whatever the scales are.  A group with a factor that
+    // is not a number passes that on to the scores that are seen.
+    __device__ __forceinline__ void hide(uint32_t (&r)[32], float2 (&sc)[2], const float4* scales, int lo, int hi) const {
+        lo = max(lo, 0);
+        hi = min(hi, 31);
+        const uint32_t seen = hi < lo ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
+        const uint32_t none = __float_as_uint(-INFINITY);
+#pragma unroll
+        for (int gg = 0; gg < 2; ++gg) {
+            const float4 x = scales[gg];
+            const float f = x.x * factor;
+            const bool bad = !(f == f) || !(x.y == x.y);
+            sc[gg] = bad ? make_float2(1.f, 0.f) : make_float2(fmaxf(f, 0x1p-126f), x.y);
+#pragma unroll
+            for (int i = 16 * gg; i < 16 * gg + 16; ++i) {
+                if (bad) r[i] = 0x7fffffffu;
+                r[i] = seen & (1u << i) ? r[i] : none;
+            }
+        }
+    }
+
+    // 32 scores to weights, fp16 pairs, at `dst`, and their sums (inv0, inv1: 1 / the values' scales).
+    __device__ __forceinline__ void weights(const uint32_t (&r)[32], float2 sc0, float2 sc1, float inv0, float inv1,
+                                            float base, uint32_t dst) {
+        uint32_t w[16];
+#pragma unroll
+        for (int gg = 0; gg < 2; ++gg) {
+            const float f = gg ? sc1.x : sc0.x, shift = (gg ? sc1.y : sc0.y) - base;
+            const f32x2 f2 = pack2(f, f), shift2 = pack2(shift, shift);
+            f32x2 sum = 0ull;
+#pragma unroll
+            for (int i = 16 * gg; i < 16 * gg + 16; i += 2) {
+                float p0, p1;
+                unpack2(fma2_of(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2, shift2), p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                sum = add2(sum, pack2(p0, p1));
+                w[i / 2] = f16_pair(p0, p1);
+            }
+            float s0, s1;
+            unpack2(sum, s0, s1);
+            s0 += s1;
+            if (s0 != 0.f) l = fmaf(s0, gg ? inv1 : inv0, l);  // unseen keys leave a block's NaN scale alone
+        }
+        tc_st_16(dst, w);
     }
 
     // The sums to the output row, or to the CTA's part of it.
@@ -345,7 +393,7 @@ struct TcRow {
         const float down = 0x1p-6f, sum = l * down;
         const float by = parts.parts > 1 ? down : sum == 0.f ? 0.f : __fdiv_rn(down, sum);
         float* part = a.part_o + ((size_t)parts.slot * a.sh.rows + row) * D;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
             uint32_t v[32];
             tmem_ld_32(o + c, v);
