@@ -482,7 +482,11 @@ template <int D>
 __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& work, uint8_t* smem, const TcBars& bar,
                                           const WaitCtl& ctl) {
     constexpr int kPerRow = D / 16, kRows = 128 / kPerRow, kPasses = kTcTile / kRows;  // rows of a pass
-    const int tid = threadIdx.x - 256, lane = tid & 31, c = tid % kPerRow;
+    const int tid = threadIdx.x - 256, lane = tid & 31;
+    // A lane's 16 channels and key of a pass: 8 lanes that store together have two keys
+    // and pieces 0, 2, 4, 6 of 128 bytes, which the swizzle puts into all banks.
+    const int c = D == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
+    const int row = (tid >> 5) * (kRows / 4) + (D == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane >> 2);
     uint4 w[kPasses];
     float ks = 0.f, vs = 0.f;
     TcWalk walk(work);
@@ -498,7 +502,7 @@ __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& w
         if (!there && lane < 8 && k0 + 16 * lane < p.s.len) atomicOr(a.error, kErrDevice);
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
-            const int key = i * kRows + tid / kPerRow;
+            const int key = i * kRows + row;
             const int page = __shfl_sync(0xffffffffu, id, key >> 4);
             const bool valid = (unsigned)page < (unsigned)a.c.n_pages && k0 + key < p.s.len;
             const uint8_t* src =
@@ -526,7 +530,7 @@ __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& w
         uint8_t* dst = smem + Tc<D>::kOffV + v.stage * Tc<D>::kValues;
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
-            const int key = i * kRows + tid / kPerRow;
+            const int key = i * kRows + row;
             const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
             uint32_t h[8];
 #pragma unroll
@@ -534,12 +538,8 @@ __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& w
                 h[2 * k] = e4m3x2_to_f16x2(x[k]);
                 h[2 * k + 1] = e4m3x2_to_f16x2_hi(x[k]);
             }
-            // lanes of the second 64 channels begin with their other half: all banks at once
-            const bool swap = D == 128 && (c & 4);
-            const uint4 first = swap ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
-            const uint4 second = swap ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(h[4], h[5], h[6], h[7]);
-            *reinterpret_cast<uint4*>(dst + Tc<D>::place_value(key, 2 * c + (swap ? 1 : 0))) = first;
-            *reinterpret_cast<uint4*>(dst + Tc<D>::place_value(key, 2 * c + (swap ? 0 : 1))) = second;
+            *reinterpret_cast<uint4*>(dst + Tc<D>::place_value(key, 2 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(dst + Tc<D>::place_value(key, 2 * c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         if (tid < 8) {
             float lg, inv;
@@ -594,78 +594,70 @@ __device__ __forceinline__ void tc_keys(const KvAttendArgs& a, const KvWork& wor
 }
 
 // ------------------------------------------------------------------ products
-// N MMAs of 32 channels each: D (+)= A B^T, E4M3, both operands advancing 32 bytes; the
-// first overwrites D where `accumulate` is 0.  One block, so that the issuing thread, which
-// waits for its issue slots among busy warps, has few instructions.
-template <int N>
-__device__ __forceinline__ void tc_mma_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    static_assert(N == 2 || N == 4, "D / 32");
-    if constexpr (N == 4)
+// The MMAs' operands are constants but for the low words of the descriptors, and one lane
+// of the whole warp issues under a predicate, without a branch: what an MMA takes stays in
+// uniform registers.  (64-bit descriptors in a branch of lane 0 cost 100 clocks an MMA,
+// which itself is 64.)  The tensor memory's address is 0: the CTA has all of it.
+#define TC_SCORE_MMA(A, B, ACC)                                                              \
+    "add.u32 x, %1, " #A ";\n\tmov.b64 a, {x, %4};\n\tadd.u32 x, %2, " #B                    \
+    ";\n\tmov.b64 b, {x, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, " #ACC ";\n\t"
+// S = Q1 K^T + Q2 K^T at column `d`: 32 bytes of channels an MMA; q, k: low words of the
+// descriptors; the second part is a tile's bytes on.
+template <int D>
+__device__ __forceinline__ void tc_mma_scores(uint32_t d, uint32_t q, uint32_t k, uint32_t hi) {
+    if constexpr (D == 128)
         asm volatile(
-            "{\n\t.reg .pred p, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
-            "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
-            "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, t;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, t;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-            : "memory");
+            "{\n\t.reg .pred e, n, t;\n\t.reg .b64 a, b;\n\t.reg .b32 x;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 n, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
+            TC_SCORE_MMA(0, 0, n) TC_SCORE_MMA(2, 2, t) TC_SCORE_MMA(4, 4, t) TC_SCORE_MMA(6, 6, t)
+            TC_SCORE_MMA(1024, 0, t) TC_SCORE_MMA(1026, 2, t) TC_SCORE_MMA(1028, 4, t) TC_SCORE_MMA(1030, 6, t)
+            "}" ::"r"(d), "r"(q), "r"(k), "r"(idesc_e4m3(kTcTile, kTcTile)), "r"(hi) : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p, t;\n\t.reg .b64 a1, b1;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
-            "add.s64 a1, %1, 2;\n\tadd.s64 b1, %2, 2;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, t;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-            : "memory");
+            "{\n\t.reg .pred e, n, t;\n\t.reg .b64 a, b;\n\t.reg .b32 x;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 n, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
+            TC_SCORE_MMA(0, 0, n) TC_SCORE_MMA(2, 2, t) TC_SCORE_MMA(512, 0, t) TC_SCORE_MMA(514, 2, t)
+            "}" ::"r"(d), "r"(q), "r"(k), "r"(idesc_e4m3(kTcTile, kTcTile)), "r"(hi) : "memory");
 }
+static_assert(kTcTile * 128 / 16 == 1024 && kTcTile * 64 / 16 == 512, "a tile's bytes in the descriptors' units");
 
-// The eight MMAs of 16 keys of a step: O (+)= P V, weights 8 columns on each, values 2 KB.
-__device__ __forceinline__ void tc_mma_values(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+#define TC_VALUE_MMA(A, B, ACC)                                                                  \
+    "add.u32 x, %2, " #B ";\n\tmov.b64 b, {x, %4};\n\tadd.u32 y, %1, " #A                        \
+    ";\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], b, %3, " #ACC ";\n\t"
+// O (+)= P V at column `d`: 16 keys an MMA, 8 columns of weights and 2 KB of values.
+template <int D>
+__device__ __forceinline__ void tc_mma_values(uint32_t d, uint32_t p, uint32_t v, uint32_t hi, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, t;\n\t.reg .b64 b1, b2, b3, b4, b5, b6, b7;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
-        "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\tadd.s64 b4, %2, 512;\n\t"
-        "add.s64 b5, %2, 640;\n\tadd.s64 b6, %2, 768;\n\tadd.s64 b7, %2, 896;\n\t"
-        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\tadd.u32 a4, %1, 32;\n\t"
-        "add.u32 a5, %1, 40;\n\tadd.u32 a6, %1, 48;\n\tadd.u32 a7, %1, 56;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, t;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, t;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, t;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, t;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred e, n, t;\n\t.reg .b64 b;\n\t.reg .b32 x, y;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 n, %5, 0;\n\tsetp.eq.b32 t, %3, %3;\n\t"
+        TC_VALUE_MMA(0, 0, n) TC_VALUE_MMA(8, 128, t) TC_VALUE_MMA(16, 256, t) TC_VALUE_MMA(24, 384, t)
+        TC_VALUE_MMA(32, 512, t) TC_VALUE_MMA(40, 640, t) TC_VALUE_MMA(48, 768, t) TC_VALUE_MMA(56, 896, t)
+        "}" ::"r"(d), "r"(p), "r"(v), "r"(idesc_f16_f32(kTcTile, D) | (1u << 16)),  // values: channels contiguous
+        "r"(hi), "r"(accumulate) : "memory");
+}
+// Arrives on `bar` when the MMAs issued so far are done.
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
 }
 
-// The whole warp runs the loop, so that what the MMAs take stays uniform; lane 0 issues.
 template <int D>
 __device__ __forceinline__ void tc_products(const KvAttendArgs& a, const KvWork& work, uint8_t* smem,
-                                            const TcBars& bar, uint32_t tmem, const WaitCtl& ctl) {
-    constexpr uint32_t idesc_s = idesc_e4m3(kTcTile, kTcTile);
-    constexpr uint32_t idesc_o = idesc_f16_f32(kTcTile, D) | (1u << 16);  // values: channels contiguous
-    const int lane = threadIdx.x & 31;
-    const uint64_t q0 = Tc<D>::desc(smem_u32(smem)), k0 = Tc<D>::desc(smem_u32(smem) + Tc<D>::kOffK);
-    const uint64_t v0 = Tc<D>::desc_values(smem_u32(smem) + Tc<D>::kOffV);
+                                            const TcBars& bar, const WaitCtl& ctl) {
+    const uint64_t q_desc = Tc<D>::desc(smem_u32(smem)), v_desc = Tc<D>::desc_values(smem_u32(smem) + Tc<D>::kOffV);
+    const uint32_t q0 = (uint32_t)q_desc, k0 = q0 + (Tc<D>::kOffK >> 4), v0 = (uint32_t)v_desc;
     TcRing k, v;
     uint32_t q_phase[2] = {0, 0}, steps[2] = {0, 0};  // segments, steps of a tile
     // O of tile t += its weights times the values of the ring's stage
     auto weighted = [&](int t, bool some, bool last) {
         if (!warp_wait(&bar.v_full[v.stage], v.phase, ctl) || !warp_wait(&bar.p_full[t], steps[t] & 1u, ctl)) return false;
         tc_fence_after();
-        if (lane == 0) {
-            tc_mma_values(tmem + 2 * kTcTile + t * kTcTile, tmem + t * kTcTile,
-                          v0 + (uint64_t)(v.stage * (Tc<D>::kValues >> 4)), idesc_o, some ? 1u : 0u);
-            mma_commit(&bar.pv_done[t]);
-            if (last) mma_commit(&bar.v_empty[v.stage]);
-        }
-        __syncwarp();
+        tc_mma_values<D>(2 * kTcTile + t * kTcTile, t * kTcTile, v0 + v.stage * (Tc<D>::kValues >> 4),
+                         (uint32_t)(v_desc >> 32), some ? 1u : 0u);
+        tc_commit(&bar.pv_done[t]);
+        if (last) tc_commit(&bar.v_empty[v.stage]);
         ++steps[t];
         return true;
     };
@@ -688,15 +680,10 @@ __device__ __forceinline__ void tc_products(const KvAttendArgs& a, const KvWork&
                 if (t == 0) ok = ok && warp_wait(&bar.k_full[k.stage], k.phase, ctl);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t q = q0 + (uint64_t)(t * 2 * (Tc<D>::kPiece >> 4));
-                    const uint64_t b = k0 + (uint64_t)(k.stage * (Tc<D>::kPiece >> 4));
-                    tc_mma_scores<D / 32>(tmem + t * kTcTile, q, b, idesc_s, 0u);
-                    tc_mma_scores<D / 32>(tmem + t * kTcTile, q + (uint64_t)(Tc<D>::kPiece >> 4), b, idesc_s, 1u);
-                    mma_commit(&bar.s_full[t]);
-                    if (t + 1 == tiles) mma_commit(&bar.k_empty[k.stage]);
-                }
-                __syncwarp();
+                tc_mma_scores<D>(t * kTcTile, q0 + t * 2 * (Tc<D>::kPiece >> 4), k0 + k.stage * (Tc<D>::kPiece >> 4),
+                                 (uint32_t)(q_desc >> 32));
+                tc_commit(&bar.s_full[t]);
+                if (t + 1 == tiles) tc_commit(&bar.k_empty[k.stage]);
             }
             if (!ok) break;
             k.step(kTcKS);
@@ -705,10 +692,8 @@ __device__ __forceinline__ void tc_products(const KvAttendArgs& a, const KvWork&
         for (int t = 0; ok && t < tiles; ++t) ok = weighted(t, walk.n > 1, t + 1 == tiles);
         v.step(kTcVS);
     }
-    if (lane == 0) {
-        mma_commit(bar.teardown);
-        mbar_wait_drain(bar.teardown, 0);
-    }
+    tc_commit(bar.teardown);
+    if ((threadIdx.x & 31) == 0) mbar_wait_drain(bar.teardown, 0);
 }
 
 template <int D>
@@ -757,14 +742,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const WaitCtl ctl{abort_flag, a.error, a.timeout_ns, 0u};
-    if (work->u1 > work->u0) {
+    if (tmem != 0u && threadIdx.x == 0) atomicOr(a.error, kErrDevice);  // all columns begin at 0
+    if (work->u1 > work->u0 && tmem == 0u) {
         if (warp < 8) {
             tc_softmax<D>(a, *work, smem, bar, tmem, ctl);
         } else if (warp < 12) {
             tc_values<D>(a, *work, smem, bar, ctl);
         } else {
             if (warp == 12) tc_keys<D>(a, *work, smem, bar, &keys, no_page, ctl);
-            if (warp == 13) tc_products<D>(a, *work, smem, bar, tmem, ctl);
+            if (warp == 13) tc_products<D>(a, *work, smem, bar, ctl);
         }
     }
     __syncwarp();
