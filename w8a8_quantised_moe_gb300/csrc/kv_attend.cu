@@ -18,7 +18,7 @@
 //   warps 8-11       values: codes from global memory to fp16 in shared memory, keys'
 //                    and values' scales
 //   warp 12          keys: TMA, a box a page
-//   warp 13          MMA issuer (and TMEM allocator)
+//   warps 13, 14     MMA issuers, a tile each (13 also holds the tensor memory)
 // Work is dealt as in kv_attend_few.cu.  Every wait is bounded (ptx.cuh).
 #include <mutex>
 
@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kTcThreads = 512;
 constexpr int kTcTile = 128;      // rows of a tile, keys of a step
+constexpr int kTcHalf = 64;       // keys of half a step, whose scores are one of a tile's two buffers
 constexpr int kTcKS = 3, kTcVS = 2;  // stages of keys, of values
 constexpr float kTcHeadroom = 8.f, kTcWeightBits = 6.f;  // as in kv_attend_few.cu
 constexpr uint32_t kTcCols = 512;
@@ -43,8 +44,8 @@ struct Tc {
     static constexpr int kOffV = kOffK + kTcKS * kPiece;
     static constexpr int kOffScales = kOffV + kTcVS * kValues;  // [stage][8 groups of 16 keys] (key, log2 value, 1 / value)
     static constexpr int kOffBars = kOffScales + kTcVS * 8 * 16;
-    // q_full[2] k_full[KS] k_empty[KS] v_full[VS] v_empty[VS] s_full[2] p_full[2] pv_done[2] teardown stall
-    static constexpr int kNumBars = 2 + 2 * kTcKS + 2 * kTcVS + 6 + 2;
+    // q_full[2] k_full[KS] k_empty[KS] v_full[VS] v_empty[VS] s_full[2][2] p_full[2][2] pv_done[2] teardown[2] stall
+    static constexpr int kNumBars = 2 + 2 * kTcKS + 2 * kTcVS + 10 + 3;
     static constexpr int kOffWork = (kOffBars + kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kOffMisc = (kOffWork + (int)sizeof(KvWork) + 15) / 16 * 16;
     static constexpr int kUsed = kOffMisc + 64 + kTcThreads / 32 * 8;
@@ -89,10 +90,10 @@ struct TcBars {
         v_full = k_empty + kTcKS;
         v_empty = v_full + kTcVS;
         s_full = v_empty + kTcVS;
-        p_full = s_full + 2;
-        pv_done = p_full + 2;
+        p_full = s_full + 4;
+        pv_done = p_full + 4;
         teardown = pv_done + 2;
-        stall = teardown + 1;
+        stall = teardown + 2;
     }
 };
 
@@ -252,73 +253,48 @@ struct TcRow {
         tmem_wait_st();
     }
 
-    // One step: scores at `s` become weights there.  k0: first key; some: O holds sums.
-    // The scores are read twice, 32 keys at a time, rather than kept in 128 registers, and
-    // the loops are short: unrolled over the whole step, the warps waited for instructions.
-    __device__ __forceinline__ void step(const KvAttendArgs& a, uint32_t s, uint32_t o, const float4* scales, int k0,
-                                         bool some) {
-        // keys [lo, hi] of the step are seen
+    // Half a step: scores at `s` become weights there.  k0: first key; some: O holds sums,
+    // which are all there once `summed` is true.
+    template <class Summed>
+    __device__ __forceinline__ bool step(const KvAttendArgs& a, uint32_t s, uint32_t o, const float4* scales, int k0,
+                                         bool some, Summed summed) {
+        uint32_t r[2][32];
+        tmem_ld_32(s, r[0]);
+        tmem_ld_32(s + 32, r[1]);
+        // keys [lo, hi] of the half are seen
         const int hi = pos - k0, lo = a.sh.window > 0 ? pos - a.sh.window + 1 - k0 : 0;
-        const bool border = __any_sync(0xffffffffu, hi < kTcTile - 1 || lo > 0);
-        float top = -INFINITY;
-        if (border) {
-#pragma unroll 1
-            for (int h = 0; h < 4; ++h) {
-                uint32_t r[32];
-                tmem_ld_32(s + 32 * h, r);
-                tc_wait_ld_32(r);
-                float2 sc[2];
-                hide(r, sc, scales + 2 * h, lo - 32 * h, hi - 32 * h);
-                top = fmaxf(top, fmaxf(fmaf(largest(r), sc[0].x, sc[0].y), fmaf(largest(r + 16), sc[1].x, sc[1].y)));
-            }
-        } else {
-            uint32_t r[2][32];
-            tmem_ld_32(s, r[0]);
-#pragma unroll 1
-            for (int h = 0; h < 4; h += 2)
+        const bool border = __any_sync(0xffffffffu, hi < kTcHalf - 1 || lo > 0);
+        float2 sc[4];
+        float inv[4];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    tc_wait_ld_32(r[b]);
-                    if (b == 0 || h == 0) tmem_ld_32(s + 32 * (h + b + 1), r[b ^ 1]);
-                    const float4 s0 = scales[2 * (h + b)], s1 = scales[2 * (h + b) + 1];
-                    // scales are positive: the largest product is the largest score's
-                    top = max3(top, fmaf(largest(r[b]), s0.x * factor, s0.y),
-                               fmaf(largest(r[b] + 16), s1.x * factor, s1.y));
-                }
+        for (int g = 0; g < 4; ++g) {
+            const float4 x = scales[g];
+            sc[g] = make_float2(x.x * factor, x.y);
+            inv[g] = x.z;
         }
+        tc_wait_ld_32(r[0]);
+        tc_wait_ld_32(r[1]);
+        if (border) {
+            hide(r[0], sc, lo, hi);
+            hide(r[1], sc + 2, lo - 32, hi - 32);
+        }
+        // scales are positive: the largest product is the largest score's
+        const float top = max3(fmaf(largest(r[0]), sc[0].x, sc[0].y), fmaf(largest(r[0] + 16), sc[1].x, sc[1].y),
+                               fmaxf(fmaf(largest(r[1]), sc[2].x, sc[2].y), fmaf(largest(r[1] + 16), sc[3].x, sc[3].y)));
         if (__any_sync(0xffffffffu, top > m + kTcHeadroom)) {
             const float now = fmaxf(top, m), down = now == m ? 1.f : ex2(m - now);
             m = now;
             l *= down;
-            if (some) rescale(o, down);
-        }
-        // weights: columns [16 h, 16 h + 16) are scores that have been read
-        const float base = m == -INFINITY ? 0.f : m - kTcWeightBits;
-        if (border) {
-#pragma unroll 1
-            for (int h = 0; h < 4; ++h) {
-                uint32_t r[32];
-                tmem_ld_32(s + 32 * h, r);
-                tc_wait_ld_32(r);
-                float2 sc[2];
-                hide(r, sc, scales + 2 * h, lo - 32 * h, hi - 32 * h);
-                weights(r, sc[0], sc[1], scales[2 * h].z, scales[2 * h + 1].z, base, s + 16 * h);
+            if (some) {
+                if (!summed()) return false;
+                rescale(o, down);
             }
-        } else {
-            uint32_t r[2][32];
-            tmem_ld_32(s, r[0]);
-#pragma unroll 1
-            for (int h = 0; h < 4; h += 2)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    tc_wait_ld_32(r[b]);
-                    if (b == 0 || h == 0) tmem_ld_32(s + 32 * (h + b + 1), r[b ^ 1]);
-                    const float4 s0 = scales[2 * (h + b)], s1 = scales[2 * (h + b) + 1];
-                    weights(r[b], make_float2(s0.x * factor, s0.y), make_float2(s1.x * factor, s1.y), s0.z, s1.z, base,
-                            s + 16 * (h + b));
-                }
         }
+        const float base = m == -INFINITY ? 0.f : m - kTcWeightBits;
+        weights(r[0], sc[0], sc[1], inv[0], inv[1], base, s);
+        weights(r[1], sc[2], sc[3], inv[2], inv[3], base, s + 16);
         tmem_wait_st();
+        return true;
     }
 
     // Largest of 16 scores.
@@ -335,19 +311,17 @@ struct TcRow {
     }
 
     // 32 scores of which [lo, hi] are seen: the others to -inf.  sc: a group's factor and
-    // addend, such that -inf stays so whatever the scales are.  A group with a factor that
-    // is not a number passes that on to the scores that are seen.
-    __device__ __forceinline__ void hide(uint32_t (&r)[32], float2 (&sc)[2], const float4* scales, int lo, int hi) const {
+    // addend, made such that -inf stays so whatever the scales are.  A group with a factor
+    // that is not a number passes that on to the scores that are seen.
+    __device__ static __forceinline__ void hide(uint32_t (&r)[32], float2* sc, int lo, int hi) {
         lo = max(lo, 0);
         hi = min(hi, 31);
         const uint32_t seen = hi < lo ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
         const uint32_t none = __float_as_uint(-INFINITY);
 #pragma unroll
         for (int gg = 0; gg < 2; ++gg) {
-            const float4 x = scales[gg];
-            const float f = x.x * factor;
-            const bool bad = !(f == f) || !(x.y == x.y);
-            sc[gg] = bad ? make_float2(1.f, 0.f) : make_float2(fmaxf(f, 0x1p-126f), x.y);
+            const bool bad = !(sc[gg].x == sc[gg].x) || !(sc[gg].y == sc[gg].y);
+            sc[gg] = bad ? make_float2(1.f, 0.f) : make_float2(fmaxf(sc[gg].x, 0x1p-126f), sc[gg].y);
 #pragma unroll
             for (int i = 16 * gg; i < 16 * gg + 16; ++i) {
                 if (bad) r[i] = 0x7fffffffu;
@@ -431,7 +405,7 @@ __device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& 
     const uint32_t s = tmem + lanes + t * kTcTile, o = tmem + lanes + 2 * kTcTile + t * kTcTile;
     uint8_t* q_tile = smem + t * 2 * Tc<D>::kPiece;
     TcRing v;
-    uint32_t s_phase = 0, pv = 0;  // steps of this tile
+    uint32_t s_phase = 0, pv = 0;  // steps; halves handed over
     TcRow<D> mine;
     TcWalk walk(work);
     auto start = [&](TcRow<D>& r, const TcWalk& w) {
@@ -452,13 +426,24 @@ __device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& 
             continue;
         }
         for (int j = 0; j < walk.n; ++j) {
-            if (!warp_wait(&bar.v_full[v.stage], v.phase, ctl) || !warp_wait(&bar.s_full[t], s_phase, ctl)) return;
-            tc_fence_after();
-            mine.step(a, s, o, reinterpret_cast<const float4*>(smem + Tc<D>::kOffScales) + 8 * v.stage,
-                      (walk.at.unit + j) * kTcTile, j > 0);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.p_full[t]);
+            if (!warp_wait(&bar.v_full[v.stage], v.phase, ctl)) return;  // its scales
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                if (!warp_wait(&bar.s_full[2 * t + h], s_phase, ctl)) return;
+                tc_fence_after();
+                const bool ok = mine.step(
+                    a, s + h * kTcHalf, o, reinterpret_cast<const float4*>(smem + Tc<D>::kOffScales) + 8 * v.stage + 4 * h,
+                    (walk.at.unit + j) * kTcTile + h * kTcHalf, j + h > 0, [&] {
+                        const bool summed = warp_wait(&bar.pv_done[t], (pv - 1) & 1u, ctl);
+                        tc_fence_after();
+                        return summed;
+                    });
+                if (!ok) return;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.p_full[2 * t + h]);
+                ++pv;
+            }
             v.step(kTcVS);
             s_phase ^= 1u;
         }
@@ -467,7 +452,6 @@ __device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& 
         TcRow<D> after = mine;
         next.next(a);
         start(after, next);
-        pv += walk.n;
         if (!warp_wait(&bar.pv_done[t], (pv - 1) & 1u, ctl)) return;
         tc_fence_after();
         mine.finish(a, work, walk, row, o);
@@ -496,18 +480,23 @@ __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& w
     int ids = more ? tc_page(a, walk.at, walk.at.unit * kTcTile, lane & 7) : -1;
     auto load = [&] {
         const KvPlace& p = walk.at;
-        const int k0 = (p.unit + j) * kTcTile;
+        const int k0 = (p.unit + j) * kTcTile, keys = p.s.len - k0;  // keys of the step that are there
         const int id = ids;
         const bool there = (unsigned)id < (unsigned)a.c.n_pages;
-        if (!there && lane < 8 && k0 + 16 * lane < p.s.len) atomicOr(a.error, kErrDevice);
+        if (!there && lane < 8 && 16 * lane < keys) atomicOr(a.error, kErrDevice);
+        // where this lane's group begins (a page that is not there: nothing)
+        const int in_page = (16 * (lane & 7)) & (a.c.page - 1);
+        const uint8_t* group = a.c.v + (there ? id * a.c.page_stride + ((p.head << a.c.page_bits) + in_page) * D : 0);
+        const uint32_t lo = (uint32_t)reinterpret_cast<uintptr_t>(group),
+                       hi = (uint32_t)(reinterpret_cast<uintptr_t>(group) >> 32);
+        const uint32_t ok = __ballot_sync(0xffffffffu, there);
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
-            const int key = i * kRows + row;
-            const int page = __shfl_sync(0xffffffffu, id, key >> 4);
-            const bool valid = (unsigned)page < (unsigned)a.c.n_pages && k0 + key < p.s.len;
-            const uint8_t* src =
-                a.c.v + page * a.c.page_stride + ((p.head << a.c.page_bits) + ((k0 + key) & (a.c.page - 1))) * D + c * 16;
-            w[i] = valid ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+            const int key = i * kRows + row, g = D == 128 ? i : key >> 4;
+            const uint64_t at = (uint64_t)__shfl_sync(0xffffffffu, hi, g) << 32 | __shfl_sync(0xffffffffu, lo, g);
+            w[i] = make_uint4(0, 0, 0, 0);
+            if ((ok >> g & 1) && key < keys)
+                w[i] = __ldg(reinterpret_cast<const uint4*>(at + ((key & 15) * D + c * 16)));
         }
         ks = 1.f;
         vs = 0.f;
@@ -601,8 +590,8 @@ __device__ __forceinline__ void tc_keys(const KvAttendArgs& a, const KvWork& wor
 #define TC_SCORE_MMA(A, B, ACC)                                                              \
     "add.u32 x, %1, " #A ";\n\tmov.b64 a, {x, %4};\n\tadd.u32 x, %2, " #B                    \
     ";\n\tmov.b64 b, {x, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, " #ACC ";\n\t"
-// S = Q1 K^T + Q2 K^T at column `d`: 32 bytes of channels an MMA; q, k: low words of the
-// descriptors; the second part is a tile's bytes on.
+// S = Q1 K^T + Q2 K^T of 64 keys at column `d`: 32 bytes of channels an MMA; q, k: low words
+// of the descriptors; the second part is a tile's bytes on.
 template <int D>
 __device__ __forceinline__ void tc_mma_scores(uint32_t d, uint32_t q, uint32_t k, uint32_t hi) {
     if constexpr (D == 128)
@@ -611,27 +600,26 @@ __device__ __forceinline__ void tc_mma_scores(uint32_t d, uint32_t q, uint32_t k
             "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 n, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
             TC_SCORE_MMA(0, 0, n) TC_SCORE_MMA(2, 2, t) TC_SCORE_MMA(4, 4, t) TC_SCORE_MMA(6, 6, t)
             TC_SCORE_MMA(1024, 0, t) TC_SCORE_MMA(1026, 2, t) TC_SCORE_MMA(1028, 4, t) TC_SCORE_MMA(1030, 6, t)
-            "}" ::"r"(d), "r"(q), "r"(k), "r"(idesc_e4m3(kTcTile, kTcTile)), "r"(hi) : "memory");
+            "}" ::"r"(d), "r"(q), "r"(k), "r"(idesc_e4m3(kTcTile, kTcHalf)), "r"(hi) : "memory");
     else
         asm volatile(
             "{\n\t.reg .pred e, n, t;\n\t.reg .b64 a, b;\n\t.reg .b32 x;\n\t"
             "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 n, %3, %3;\n\tsetp.eq.b32 t, %3, %3;\n\t"
             TC_SCORE_MMA(0, 0, n) TC_SCORE_MMA(2, 2, t) TC_SCORE_MMA(512, 0, t) TC_SCORE_MMA(514, 2, t)
-            "}" ::"r"(d), "r"(q), "r"(k), "r"(idesc_e4m3(kTcTile, kTcTile)), "r"(hi) : "memory");
+            "}" ::"r"(d), "r"(q), "r"(k), "r"(idesc_e4m3(kTcTile, kTcHalf)), "r"(hi) : "memory");
 }
 static_assert(kTcTile * 128 / 16 == 1024 && kTcTile * 64 / 16 == 512, "a tile's bytes in the descriptors' units");
 
 #define TC_VALUE_MMA(A, B, ACC)                                                                  \
     "add.u32 x, %2, " #B ";\n\tmov.b64 b, {x, %4};\n\tadd.u32 y, %1, " #A                        \
     ";\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], b, %3, " #ACC ";\n\t"
-// O (+)= P V at column `d`: 16 keys an MMA, 8 columns of weights and 2 KB of values.
+// O (+)= P V of 64 keys at column `d`: 16 keys an MMA, 8 columns of weights and 2 KB of values.
 template <int D>
 __device__ __forceinline__ void tc_mma_values(uint32_t d, uint32_t p, uint32_t v, uint32_t hi, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred e, n, t;\n\t.reg .b64 b;\n\t.reg .b32 x, y;\n\t"
         "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 n, %5, 0;\n\tsetp.eq.b32 t, %3, %3;\n\t"
         TC_VALUE_MMA(0, 0, n) TC_VALUE_MMA(8, 128, t) TC_VALUE_MMA(16, 256, t) TC_VALUE_MMA(24, 384, t)
-        TC_VALUE_MMA(32, 512, t) TC_VALUE_MMA(40, 640, t) TC_VALUE_MMA(48, 768, t) TC_VALUE_MMA(56, 896, t)
         "}" ::"r"(d), "r"(p), "r"(v), "r"(idesc_f16_f32(kTcTile, D) | (1u << 16)),  // values: channels contiguous
         "r"(hi), "r"(accumulate) : "memory");
 }
@@ -643,57 +631,83 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
         : "memory");
 }
 
+// A warp a tile.  A step is two halves of 64 keys, each with a buffer of its own for its
+// scores, whose place the weights take: the scores of a half are asked for before the
+// weights of the half before are there, so that the softmax finds them done.  (With one
+// buffer a step of 128 keys was a chain of scores, softmax and weighted values, 4800
+// clocks; one warp for both tiles was no different.)
+// The ring of values needs no wait of its own: the softmax has waited for the stage before
+// it hands over the weights.
 template <int D>
 __device__ __forceinline__ void tc_products(const KvAttendArgs& a, const KvWork& work, uint8_t* smem,
-                                            const TcBars& bar, const WaitCtl& ctl) {
+                                            const TcBars& bar, int t, const WaitCtl& ctl) {
     const uint64_t q_desc = Tc<D>::desc(smem_u32(smem)), v_desc = Tc<D>::desc_values(smem_u32(smem) + Tc<D>::kOffV);
-    const uint32_t q0 = (uint32_t)q_desc, k0 = q0 + (Tc<D>::kOffK >> 4), v0 = (uint32_t)v_desc;
+    const uint32_t q0 = (uint32_t)q_desc + t * 2 * (Tc<D>::kPiece >> 4), k0 = (uint32_t)q_desc + (Tc<D>::kOffK >> 4);
+    const uint32_t v0 = (uint32_t)v_desc;
+    const int lane = threadIdx.x & 31;
     TcRing k, v;
-    uint32_t q_phase[2] = {0, 0}, steps[2] = {0, 0};  // segments, steps of a tile
-    // O of tile t += its weights times the values of the ring's stage
-    auto weighted = [&](int t, bool some, bool last) {
-        if (!warp_wait(&bar.v_full[v.stage], v.phase, ctl) || !warp_wait(&bar.p_full[t], steps[t] & 1u, ctl)) return false;
+    uint32_t q_phase = 0, p_phase = 0, done = 0;  // row tiles; steps; weighted halves issued
+    auto scores = [&](int half) {
         tc_fence_after();
-        tc_mma_values<D>(2 * kTcTile + t * kTcTile, t * kTcTile, v0 + v.stage * (Tc<D>::kValues >> 4),
-                         (uint32_t)(v_desc >> 32), some ? 1u : 0u);
+        tc_mma_scores<D>(t * kTcTile + half * kTcHalf, q0,
+                         k0 + k.stage * (Tc<D>::kPiece >> 4) + half * (Tc<D>::kPiece >> 5), (uint32_t)(q_desc >> 32));
+        tc_commit(&bar.s_full[2 * t + half]);
+        if (half == 1) {
+            tc_commit(&bar.k_empty[k.stage]);
+            k.step(kTcKS);
+        }
+    };
+    auto weighted = [&](int half, bool some) {
+        if (!warp_wait(&bar.p_full[2 * t + half], p_phase, ctl)) return false;
+        tc_fence_after();
+        tc_mma_values<D>(2 * kTcTile + t * kTcTile, t * kTcTile + half * kTcHalf,
+                         v0 + v.stage * (Tc<D>::kValues >> 4) + half * (kTcHalf * 128 >> 4), (uint32_t)(v_desc >> 32),
+                         some ? 1u : 0u);
         tc_commit(&bar.pv_done[t]);
-        if (last) tc_commit(&bar.v_empty[v.stage]);
-        ++steps[t];
+        ++done;
+        if (half == 1) {
+            tc_commit(&bar.v_empty[v.stage]);
+            v.step(kTcVS);
+            p_phase ^= 1u;
+        }
         return true;
     };
+    // the weights in a buffer have been read: all halves issued so far are done
+    auto free_buffer = [&] { return warp_wait(&bar.pv_done[t], (done - 1) & 1u, ctl); };
     bool ok = true;
     for (TcWalk walk(work); ok && walk.more(); walk.next(a)) {
-        const int tiles = walk.tiles(a);
-        for (int t = 0; ok && t < tiles; ++t) {
-            ok = warp_wait(&bar.q_full[t], q_phase[t], ctl);
-            q_phase[t] ^= 1u;
-        }
-        for (int j = 0; ok && j < walk.n; ++j) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (t >= tiles || !ok) break;
-                if (j > 0) {
-                    ok = weighted(t, j > 1, t + 1 == tiles);
-                    // the scores take the weights' place: these must have been read
-                    ok = ok && warp_wait(&bar.pv_done[t], (steps[t] - 1) & 1u, ctl);
+        if (t >= walk.tiles(a)) {  // no rows: the other tile's stages are free as far as this one goes
+            for (int j = 0; ok && j < walk.n; ++j) {
+                ok = warp_wait(&bar.k_full[k.stage], k.phase, ctl) && warp_wait(&bar.v_full[v.stage], v.phase, ctl);
+                if (ok && lane == 0) {
+                    mbar_arrive(&bar.k_empty[k.stage]);
+                    mbar_arrive(&bar.v_empty[v.stage]);
                 }
-                if (t == 0) ok = ok && warp_wait(&bar.k_full[k.stage], k.phase, ctl);
-                if (!ok) break;
-                tc_fence_after();
-                tc_mma_scores<D>(t * kTcTile, q0 + t * 2 * (Tc<D>::kPiece >> 4), k0 + k.stage * (Tc<D>::kPiece >> 4),
-                                 (uint32_t)(q_desc >> 32));
-                tc_commit(&bar.s_full[t]);
-                if (t + 1 == tiles) tc_commit(&bar.k_empty[k.stage]);
+                k.step(kTcKS);
+                v.step(kTcVS);
             }
-            if (!ok) break;
-            k.step(kTcKS);
-            if (j > 0) v.step(kTcVS);
+            continue;
         }
-        for (int t = 0; ok && t < tiles; ++t) ok = weighted(t, walk.n > 1, t + 1 == tiles);
-        v.step(kTcVS);
+        ok = warp_wait(&bar.q_full[t], q_phase, ctl) && warp_wait(&bar.k_full[k.stage], k.phase, ctl) &&
+             (done == 0 || free_buffer());
+        q_phase ^= 1u;
+        if (!ok) break;
+        scores(0);
+        scores(1);
+        ok = weighted(0, false);
+        for (int j = 1; ok && j < walk.n; ++j) {
+            ok = warp_wait(&bar.k_full[k.stage], k.phase, ctl) && free_buffer();
+            if (!ok) break;
+            scores(0);
+            ok = weighted(1, true) && free_buffer();
+            if (!ok) break;
+            scores(1);
+            ok = weighted(0, true);
+        }
+        ok = ok && weighted(1, true);
     }
-    tc_commit(bar.teardown);
-    if ((threadIdx.x & 31) == 0) mbar_wait_drain(bar.teardown, 0);
+    tc_commit(&bar.teardown[t]);
+    if (lane == 0) mbar_wait_drain(&bar.teardown[t], 0);
 }
 
 template <int D>
@@ -712,19 +726,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bar.q_full[t], 4);
-            mbar_init(&bar.s_full[t], 1);
-            mbar_init(&bar.p_full[t], 4);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&bar.s_full[2 * t + h], 1);
+                mbar_init(&bar.p_full[2 * t + h], 4);
+            }
             mbar_init(&bar.pv_done[t], 1);
+            mbar_init(&bar.teardown[t], 1);
         }
         for (int i = 0; i < kTcKS; ++i) {
             mbar_init(&bar.k_full[i], 1);
-            mbar_init(&bar.k_empty[i], 1);
+            mbar_init(&bar.k_empty[i], 2);
         }
         for (int i = 0; i < kTcVS; ++i) {
             mbar_init(&bar.v_full[i], 4);
-            mbar_init(&bar.v_empty[i], 1);
+            mbar_init(&bar.v_empty[i], 2);
         }
-        mbar_init(bar.teardown, 1);
         mbar_init(bar.stall, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -750,7 +766,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc_values<D>(a, *work, smem, bar, ctl);
         } else {
             if (warp == 12) tc_keys<D>(a, *work, smem, bar, &keys, no_page, ctl);
-            if (warp == 13) tc_products<D>(a, *work, smem, bar, ctl);
+            if (warp >= 13 && warp < 15) tc_products<D>(a, *work, smem, bar, warp - 13, ctl);
         }
     }
     __syncwarp();
