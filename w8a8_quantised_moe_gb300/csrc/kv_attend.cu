@@ -33,7 +33,7 @@ constexpr int kTcThreads = 512;
 constexpr int kTcTile = 128;      // rows of a tile, keys of a step
 constexpr int kTcHalf = 64;       // keys of half a step, whose scores are one of a tile's two buffers
 constexpr int kTcKS = 3, kTcVS = 2;  // stages of keys, of values
-constexpr float kTcHeadroom = 8.f, kTcWeightBits = 6.f;  // as in kv_attend_few.cu
+constexpr float kTcWeightBits = 6.f;  // weights are 2^6 at the maximum, as in kv_attend_few.cu
 constexpr uint32_t kTcCols = 512;
 
 template <int D>
@@ -188,7 +188,7 @@ template <int D>
 struct TcRow {
     float m, l, factor;
     int pos;
-    bool valid;
+    bool valid, fresh;  // fresh: has seen no key yet
 
     // This row's query as two E4M3 parts in shared memory.
     __device__ __forceinline__ void start(const KvAttendArgs& a, const KvPlace& p, int row, uint8_t* q_tile) {
@@ -219,6 +219,7 @@ struct TcRow {
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
         factor = __fmul_rn(__fmul_rn(a.scale, kLog2e), __uint_as_float((uint32_t)(127 + e) << 23));
         if (top >= 0x7f80u) factor = __uint_as_float(0x7fffffffu);  // a row that is not finite
+        fresh = valid && top < 0x7f80u;
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
             const uint4 w[2] = {valid ? __ldg(src + 2 * c) : none, valid ? __ldg(src + 2 * c + 1) : none};
@@ -278,21 +279,37 @@ struct TcRow {
             hide(r[0], sc, lo, hi);
             hide(r[1], sc + 2, lo - 32, hi - 32);
         }
-        // scales are positive: the largest product is the largest score's
-        const float top = max3(fmaf(largest(r[0]), sc[0].x, sc[0].y), fmaf(largest(r[0] + 16), sc[1].x, sc[1].y),
-                               fmaxf(fmaf(largest(r[1]), sc[2].x, sc[2].y), fmaf(largest(r[1] + 16), sc[3].x, sc[3].y)));
-        if (__any_sync(0xffffffffu, top > m + kTcHeadroom)) {
-            const float now = fmaxf(top, m), down = now == m ? 1.f : ex2(m - now);
-            m = now;
-            l *= down;
-            if (some) {
-                if (!summed()) return false;
-                rescale(o, down);
+        // The weights are formed for the maximum so far.  Where one comes out above 2^14 (2^8
+        // above that maximum; fp16 ends at 2^16), or a row has no maximum yet, that is brought
+        // up to date and they are formed once more.
+        // (Row by row: no row's bits depend on another's.)
+        bool need = fresh, renew = __any_sync(0xffffffffu, need);
+        float sum;
+        for (int round = 0;; ++round) {
+            if (renew) {
+                // scales are positive: the largest product is the largest score's
+                const float top =
+                    max3(fmaf(largest(r[0]), sc[0].x, sc[0].y), fmaf(largest(r[0] + 16), sc[1].x, sc[1].y),
+                         fmaxf(fmaf(largest(r[1]), sc[2].x, sc[2].y), fmaf(largest(r[1] + 16), sc[3].x, sc[3].y)));
+                const float now = need ? fmaxf(top, m) : m, down = now == m ? 1.f : ex2(m - now);
+                m = now;
+                fresh = fresh && m == -INFINITY;
+                l *= down;
+                if (some) {
+                    if (!summed()) return false;
+                    rescale(o, down);
+                }
             }
+            const float base = m == -INFINITY ? 0.f : m - kTcWeightBits;
+            sum = 0.f;
+            need = weights(r[0], sc[0], sc[1], inv[0], inv[1], base, s, sum);
+            need = weights(r[1], sc[2], sc[3], inv[2], inv[3], base, s + 16, sum) || need;
+            // (a row that has just been brought up to date has weights of 2^6 at most)
+            if (round == 2 || !__any_sync(0xffffffffu, need)) break;
+            renew = true;
+            tmem_wait_st();  // the weights take the place of those just written
         }
-        const float base = m == -INFINITY ? 0.f : m - kTcWeightBits;
-        weights(r[0], sc[0], sc[1], inv[0], inv[1], base, s);
-        weights(r[1], sc[2], sc[3], inv[2], inv[3], base, s + 16);
+        l += sum;
         tmem_wait_st();
         return true;
     }
@@ -330,10 +347,12 @@ struct TcRow {
         }
     }
 
-    // 32 scores to weights, fp16 pairs, at `dst`, and their sums (inv0, inv1: 1 / the values' scales).
-    __device__ __forceinline__ void weights(const uint32_t (&r)[32], float2 sc0, float2 sc1, float inv0, float inv1,
-                                            float base, uint32_t dst) {
+    // 32 scores to weights, fp16 pairs, at `dst`; their sums times inv0 and inv1 (1 / the
+    // values' scales) are added to `total`.  Whether one may be above 2^14.
+    __device__ static __forceinline__ bool weights(const uint32_t (&r)[32], float2 sc0, float2 sc1, float inv0,
+                                                   float inv1, float base, uint32_t dst, float& total) {
         uint32_t w[16];
+        bool large = false;
 #pragma unroll
         for (int gg = 0; gg < 2; ++gg) {
             const float f = gg ? sc1.x : sc0.x, shift = (gg ? sc1.y : sc0.y) - base;
@@ -351,9 +370,11 @@ struct TcRow {
             float s0, s1;
             unpack2(sum, s0, s1);
             s0 += s1;
-            if (s0 != 0.f) l = fmaf(s0, gg ? inv1 : inv0, l);  // unseen keys leave a block's NaN scale alone
+            large = large || s0 > 0x1p14f;
+            if (s0 != 0.f) total = fmaf(s0, gg ? inv1 : inv0, total);  // unseen keys leave a block's NaN scale alone
         }
         tc_st_16(dst, w);
+        return large;
     }
 
     // The sums to the output row, or to the CTA's part of it.
