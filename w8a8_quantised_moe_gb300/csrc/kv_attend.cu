@@ -12,13 +12,13 @@
 //   O += P V              kind::f16: weights in fp16 (11 bits) from tensor memory,
 //       values converted to fp16 (exact).  E4M3 pairs would not do here: weights
 //       below 2^-18 of the largest would be lost, and long contexts are made of them.
-//   warps 0-3, 4-7   softmax of one tile each, a thread a row: scores from tensor
-//                    memory, weights back in their place; the maximum is corrected
-//                    only when it rises by more than 2^8, by the same threads
-//   warps 8-11       values: codes from global memory to fp16 in shared memory, keys'
+//   warps 0-7, 8-15  softmax of one tile each, two threads a row: scores from tensor memory,
+//                    weights back in their place; the maximum is corrected only when it
+//                    rises by more than 2^8, by the same threads
+//   warps 16-19      values: codes from global memory to fp16 in shared memory, keys'
 //                    and values' scales
-//   warp 12          keys: TMA, a box a page
-//   warps 13, 14     MMA issuers, a tile each (13 also holds the tensor memory)
+//   warp 20          keys: TMA, a box a page
+//   warps 21, 22     MMA issuers, a tile each (21 also holds the tensor memory)
 // Work is dealt as in kv_attend_few.cu.  Every wait is bounded (ptx.cuh).
 #include <mutex>
 
@@ -29,11 +29,12 @@
 namespace moe {
 namespace {
 
-constexpr int kTcThreads = 512;
+constexpr int kTcThreads = 768;
+constexpr int kTcValues0 = 16, kTcKeys0 = 20, kTcProducts0 = 21;  // first warps of the roles behind the softmax's 16
 constexpr int kTcTile = 128;      // rows of a tile, keys of a step
 constexpr int kTcHalf = 64;       // keys of half a step, whose scores are one of a tile's two buffers
 constexpr int kTcKS = 3, kTcVS = 2;  // stages of keys, of values
-constexpr float kTcWeightBits = 6.f;  // weights are 2^6 at the maximum, as in kv_attend_few.cu
+constexpr float kTcHeadroom = 8.f, kTcWeightBits = 6.f;  // as in kv_attend_few.cu
 constexpr uint32_t kTcCols = 512;
 
 template <int D>
@@ -43,9 +44,11 @@ struct Tc {
     static constexpr int kOffK = 4 * kPiece;          // after Q [tile][part]
     static constexpr int kOffV = kOffK + kTcKS * kPiece;
     static constexpr int kOffScales = kOffV + kTcVS * kValues;  // [stage][8 groups of 16 keys] (key, log2 value, 1 / value)
-    static constexpr int kOffBars = kOffScales + kTcVS * 8 * 16;
-    // q_full[2] k_full[KS] k_empty[KS] v_full[VS] v_empty[VS] s_full[2][2] p_full[2][2] pv_done[2] teardown[2] stall
-    static constexpr int kNumBars = 2 + 2 * kTcKS + 2 * kTcVS + 10 + 3;
+    static constexpr int kOffStage = kOffScales + kTcVS * 8 * 16;  // 2 KB a softmax warp
+    static constexpr int kOffShared = kOffStage + 32 * 1024;       // [use][tile][row][part], what a row's two threads tell each other
+    static constexpr int kOffBars = kOffShared + 3 * 2 * kTcTile * 8;
+    // q_full[2] k_full[KS] k_empty[KS] v_full[VS] v_empty[VS] s_full[2][2] p_full[2][2] pv_done[2][2] teardown[2] stall
+    static constexpr int kNumBars = 2 + 2 * kTcKS + 2 * kTcVS + 12 + 3;
     static constexpr int kOffWork = (kOffBars + kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kOffMisc = (kOffWork + (int)sizeof(KvWork) + 15) / 16 * 16;
     static constexpr int kUsed = kOffMisc + 64 + kTcThreads / 32 * 8;
@@ -92,7 +95,7 @@ struct TcBars {
         s_full = v_empty + kTcVS;
         p_full = s_full + 4;
         pv_done = p_full + 4;
-        teardown = pv_done + 2;
+        teardown = pv_done + 4;
         stall = teardown + 2;
     }
 };
@@ -183,50 +186,85 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
 }
 
 // ------------------------------------------------------------------ softmax
-// One thread: row `row` of the CTA's 256, tile t.
+// Barrier of the two warps of a row group, and the OR of their conditions.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+
+// A thread of the softmax: row `row` of tile t's 128, keys [32 part, 32 part + 32) of every
+// half, channels [D/2 part, D/2 part + D/2) of queries and output.  Two warps share 32 rows
+// (and the tensor memory's lanes): a warp alone is a chain of latencies, and with one warp
+// a row group the softmax of a half took 1250 clocks where its exponentials need 256.
+// Their barriers are not bounded, so neither leaves the other: a warp whose wait gave up
+// goes on, and both return at the next pair_any.
 template <int D>
 struct TcRow {
+    static constexpr int kCols = D / 2;  // channels of a part
     float m, l, factor;
-    int pos;
-    bool valid, fresh;  // fresh: has seen no key yet
+    int pos, pos_first, pos_last;  // position; those of the warp's first and last row
+    bool valid;
 
-    // This row's query as two E4M3 parts in shared memory.
-    __device__ __forceinline__ void start(const KvAttendArgs& a, const KvPlace& p, int row, uint8_t* q_tile) {
-        const int r = p.rt * a.sh.rows + row, tok = r / a.sh.group;
-        valid = r < p.s.n * a.sh.group;
-        pos = valid ? p.s.len - p.s.n + tok : -1;
+    // The warp's 32 rows x its channels of the queries, as two E4M3 parts in shared memory.
+    // Lanes side by side load a row; its largest magnitude is that of both warps.
+    __device__ __forceinline__ void start(const KvAttendArgs& a, const KvPlace& p, int t, int row, int part,
+                                          uint8_t* q_tile, uint32_t* shared, int pair) {
+        constexpr int kLanes = kCols / 8, kRows = 32 / kLanes, kLoads = 32 / kRows;  // lanes of a row, rows of a load
+        const int lane = threadIdx.x & 31, group = a.sh.group, rows = p.s.n * group;
+        const int r0 = p.rt * a.sh.rows + t * kTcTile + (row & ~31), c = p.s.len - p.s.n;  // the warp's first row
+        uint4 w[kLoads];
+        uint32_t top[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = r0 + i * kRows + lane / kLanes, tok = r / group;
+            const uint16_t* src = a.q + (int64_t)(p.s.q0 + tok) * a.q_stride +
+                                  (p.head * group + r - tok * group) * D + part * kCols + lane % kLanes * 8;
+            w[i] = make_uint4(0, 0, 0, 0);
+            if (r < rows) w[i] = __ldg(reinterpret_cast<const uint4*>(src));
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            // magnitudes of bf16 pairs, compared as whole numbers
+            uint32_t x = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                  __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+            x = max(x & 0xffffu, x >> 16);
+#pragma unroll
+            for (int off = kLanes / 2; off > 0; off >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, off));
+            if (lane % kLanes == 0) shared[2 * ((row & ~31) + i * kRows + lane / kLanes) + part] = x;
+        }
+        pair_sync(pair);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint2 x = reinterpret_cast<const uint2*>(shared)[(row & ~31) + i * kRows + lane / kLanes];
+            top[i] = max(x.x, x.y);
+        }
+        const uint2 own = reinterpret_cast<const uint2*>(shared)[row];
+        // a row's scale 2^-e: e = the exponent of its largest magnitude less 7
+        auto exponent = [](uint32_t x) { return max((int)(x >> 7) - 127 - 7, -120); };
+        auto power = [](int e) { return __uint_as_float((uint32_t)(127 + e) << 23); };
+        const uint32_t mine = max(own.x, own.y);
+        factor = __fmul_rn(__fmul_rn(a.scale, kLog2e), power(exponent(mine)));
+        if (mine >= 0x7f80u) factor = __uint_as_float(0x7fffffffu);  // a row that is not finite
+        const int r = r0 + (row & 31);
+        valid = r < rows;
+        pos = valid ? c + r / group : -1;
+        pos_first = r0 < rows ? c + r0 / group : -1;
+        pos_last = r0 + 31 < rows ? c + (r0 + 31) / group : -1;
         m = -INFINITY;
         l = 0.f;
-        const int lrow = row & (kTcTile - 1);
-        uint32_t top = 0;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + (valid ? (int64_t)(p.s.q0 + tok) * a.q_stride + (p.head * a.sh.group + r % a.sh.group) * D : 0));
-        const uint4 none = make_uint4(0, 0, 0, 0);
-        // Short loops: code that runs once a row tile waits for its instructions.
-#pragma unroll 1
-        for (int i = 0; i < D / 8; i += 8) {
-            uint4 w[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = valid ? __ldg(src + i + k) : none;
+        for (int i = 0; i < kLoads; ++i) {
+            const float down = power(-exponent(top[i]));
+            uint32_t hi[2], lo[2];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)  // magnitudes of bf16 pairs, compared as whole numbers
-                top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[k].x & 0x7fff7fffu, w[k].y & 0x7fff7fffu),
-                                             __vmaxu2(w[k].z & 0x7fff7fffu, w[k].w & 0x7fff7fffu)));
-        }
-        top = max(top & 0xffffu, top >> 16);
-        int e = (int)(top >> 7) - 127 - 7;
-        if (e < -120) e = -120;
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        factor = __fmul_rn(__fmul_rn(a.scale, kLog2e), __uint_as_float((uint32_t)(127 + e) << 23));
-        if (top >= 0x7f80u) factor = __uint_as_float(0x7fffffffu);  // a row that is not finite
-        fresh = valid && top < 0x7f80u;
-#pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
-            const uint4 w[2] = {valid ? __ldg(src + 2 * c) : none, valid ? __ldg(src + 2 * c + 1) : none};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t x = j & 1 ? w[j >> 1].z : w[j >> 1].x, y = j & 1 ? w[j >> 1].w : w[j >> 1].y;
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t x = j ? w[i].z : w[i].x, y = j ? w[i].w : w[i].y;
                 const float f[4] = {bf16_lo(x) * down, bf16_hi(x) * down, bf16_lo(y) * down, bf16_hi(y) * down};
                 hi[j] = e4m3_pair(f[0], f[1]) | (e4m3_pair(f[2], f[3]) << 16);
                 const uint32_t h0 = e4m3x2_to_f16x2(hi[j]), h1 = e4m3x2_to_f16x2_hi(hi[j]);
@@ -234,16 +272,17 @@ struct TcRow {
                 const float2 g1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
                 lo[j] = e4m3_pair(f[0] - g0.x, f[1] - g0.y) | (e4m3_pair(f[2] - g1.x, f[3] - g1.y) << 16);
             }
-            uint8_t* at = q_tile + Tc<D>::place(lrow, c);
-            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(at + Tc<D>::kPiece) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            const int at = part * kCols + lane % kLanes * 8;
+            uint8_t* dst = q_tile + Tc<D>::place((row & ~31) + i * kRows + lane / kLanes, at >> 4) + (at & 8);
+            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(dst + Tc<D>::kPiece) = make_uint2(lo[0], lo[1]);
         }
     }
 
-    // Sums at `o` (tensor memory) times `by`.
+    // This part's sums at `o` (tensor memory) times `by`.
     __device__ __forceinline__ void rescale(uint32_t o, float by) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
+        for (int c = 0; c < kCols; c += 16) {
             uint32_t r[16];
             tmem_ld_16(o + c, r);
             tc_wait_ld_16(r);
@@ -254,62 +293,65 @@ struct TcRow {
         tmem_wait_st();
     }
 
-    // Half a step: scores at `s` become weights there.  k0: first key; some: O holds sums,
-    // which are all there once `summed` is true.
+    // 32 keys of a half: scores at `s` become weights at `dst`.  k0: the first key; o: this
+    // part's sums, which hold something where `some`, and everything handed over so far once
+    // `summed` has run.  False: one of the two warps has failed.
     template <class Summed>
-    __device__ __forceinline__ bool step(const KvAttendArgs& a, uint32_t s, uint32_t o, const float4* scales, int k0,
-                                         bool some, Summed summed) {
-        uint32_t r[2][32];
-        tmem_ld_32(s, r[0]);
-        tmem_ld_32(s + 32, r[1]);
-        // keys [lo, hi] of the half are seen
-        const int hi = pos - k0, lo = a.sh.window > 0 ? pos - a.sh.window + 1 - k0 : 0;
-        const bool border = __any_sync(0xffffffffu, hi < kTcHalf - 1 || lo > 0);
-        float2 sc[4];
-        float inv[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const float4 x = scales[g];
-            sc[g] = make_float2(x.x * factor, x.y);
-            inv[g] = x.z;
-        }
-        tc_wait_ld_32(r[0]);
-        tc_wait_ld_32(r[1]);
-        if (border) {
-            hide(r[0], sc, lo, hi);
-            hide(r[1], sc + 2, lo - 32, hi - 32);
-        }
-        // The weights are formed for the maximum so far.  Where one comes out above 2^14 (2^8
-        // above that maximum; fp16 ends at 2^16), or a row has no maximum yet, that is brought
-        // up to date and they are formed once more.
-        // (Row by row: no row's bits depend on another's.)
-        bool need = fresh, renew = __any_sync(0xffffffffu, need);
-        float sum;
-        for (int round = 0;; ++round) {
-            if (renew) {
-                // scales are positive: the largest product is the largest score's
-                const float top =
-                    max3(fmaf(largest(r[0]), sc[0].x, sc[0].y), fmaf(largest(r[0] + 16), sc[1].x, sc[1].y),
-                         fmaxf(fmaf(largest(r[1]), sc[2].x, sc[2].y), fmaf(largest(r[1] + 16), sc[3].x, sc[3].y)));
-                const float now = need ? fmaxf(top, m) : m, down = now == m ? 1.f : ex2(m - now);
-                m = now;
-                fresh = fresh && m == -INFINITY;
-                l *= down;
-                if (some) {
-                    if (!summed()) return false;
-                    rescale(o, down);
-                }
+    __device__ __forceinline__ bool step(const KvAttendArgs& a, uint32_t s, uint32_t dst, uint32_t o,
+                                         const float4* scales, int k0, bool some, bool failed, int row, int part,
+                                         float* shared, int pair, Summed summed) {
+        uint32_t r[32];
+        tmem_ld_32(s, r);
+        const float4 x0 = scales[0], x1 = scales[1];
+        float2 sc[2] = {make_float2(x0.x * factor, x0.y), make_float2(x1.x * factor, x1.y)};
+        const int window = a.sh.window;
+        const bool border = pos_first < k0 + 31 || pos_last < 0 || (window > 0 && pos_last - window >= k0);
+        tc_wait_ld_32(r);
+        if (border) hide(r, sc, window > 0 ? pos - window + 1 - k0 : 0, pos - k0);
+        // scales are positive: the largest product is the largest score's
+        const float top = fmaxf(fmaf(largest(r), sc[0].x, sc[0].y), fmaf(largest(r + 16), sc[1].x, sc[1].y));
+        // The maximum follows when it is behind by more than 2^8, row by row: no row's bits depend on another's.
+        const bool behind = top > m + kTcHeadroom;
+        tc_fence_before();
+        const bool renew = pair_any(pair, behind || failed);
+        tc_fence_after();
+        if (renew) {
+            constexpr uint32_t kFailed = 0x7fc0dead;  // no score's bits
+            shared[2 * row + part] = failed ? __uint_as_float(kFailed) : top;
+            pair_sync(pair);
+            const float2 both = reinterpret_cast<const float2*>(shared)[row];
+            if (__float_as_uint(both.x) == kFailed || __float_as_uint(both.y) == kFailed) return false;
+            const float most = fmaxf(both.x, both.y), now = most > m + kTcHeadroom ? most : m;
+            const float down = now == m ? 1.f : ex2(m - now);
+            m = now;
+            l *= down;
+            if (some) {
+                summed();
+                rescale(o, down);
             }
-            const float base = m == -INFINITY ? 0.f : m - kTcWeightBits;
-            sum = 0.f;
-            need = weights(r[0], sc[0], sc[1], inv[0], inv[1], base, s, sum);
-            need = weights(r[1], sc[2], sc[3], inv[2], inv[3], base, s + 16, sum) || need;
-            // (a row that has just been brought up to date has weights of 2^6 at most)
-            if (round == 2 || !__any_sync(0xffffffffu, need)) break;
-            renew = true;
-            tmem_wait_st();  // the weights take the place of those just written
         }
-        l += sum;
+        const float base = m == -INFINITY ? 0.f : m - kTcWeightBits;
+        uint32_t w[16];
+#pragma unroll
+        for (int gg = 0; gg < 2; ++gg) {
+            const float f = sc[gg].x, shift = sc[gg].y - base;
+            const f32x2 f2 = pack2(f, f), shift2 = pack2(shift, shift);
+            f32x2 sum = 0ull;
+#pragma unroll
+            for (int i = 16 * gg; i < 16 * gg + 16; i += 2) {
+                float p0, p1;
+                unpack2(fma2_of(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2, shift2), p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                sum = add2(sum, pack2(p0, p1));
+                w[i / 2] = f16_pair(p0, p1);
+            }
+            float s0, s1;
+            unpack2(sum, s0, s1);
+            s0 += s1;
+            if (s0 != 0.f) l = fmaf(s0, gg ? x1.z : x0.z, l);  // unseen keys leave a block's NaN scale alone
+        }
+        tc_st_16(dst, w);  // (both warps have read their scores: pair_any)
         tmem_wait_st();
         return true;
     }
@@ -330,7 +372,7 @@ struct TcRow {
     // 32 scores of which [lo, hi] are seen: the others to -inf.  sc: a group's factor and
     // addend, made such that -inf stays so whatever the scales are.  A group with a factor
     // that is not a number passes that on to the scores that are seen.
-    __device__ static __forceinline__ void hide(uint32_t (&r)[32], float2* sc, int lo, int hi) {
+    __device__ static __forceinline__ void hide(uint32_t (&r)[32], float2 (&sc)[2], int lo, int hi) {
         lo = max(lo, 0);
         hi = min(hi, 31);
         const uint32_t seen = hi < lo ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
@@ -347,91 +389,84 @@ struct TcRow {
         }
     }
 
-    // 32 scores to weights, fp16 pairs, at `dst`; their sums times inv0 and inv1 (1 / the
-    // values' scales) are added to `total`.  Whether one may be above 2^14.
-    __device__ static __forceinline__ bool weights(const uint32_t (&r)[32], float2 sc0, float2 sc1, float inv0,
-                                                   float inv1, float base, uint32_t dst, float& total) {
-        uint32_t w[16];
-        bool large = false;
-#pragma unroll
-        for (int gg = 0; gg < 2; ++gg) {
-            const float f = gg ? sc1.x : sc0.x, shift = (gg ? sc1.y : sc0.y) - base;
-            const f32x2 f2 = pack2(f, f), shift2 = pack2(shift, shift);
-            f32x2 sum = 0ull;
-#pragma unroll
-            for (int i = 16 * gg; i < 16 * gg + 16; i += 2) {
-                float p0, p1;
-                unpack2(fma2_of(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2, shift2), p0, p1);
-                p0 = ex2(p0);
-                p1 = ex2(p1);
-                sum = add2(sum, pack2(p0, p1));
-                w[i / 2] = f16_pair(p0, p1);
-            }
-            float s0, s1;
-            unpack2(sum, s0, s1);
-            s0 += s1;
-            large = large || s0 > 0x1p14f;
-            if (s0 != 0.f) total = fmaf(s0, gg ? inv1 : inv0, total);  // unseen keys leave a block's NaN scale alone
-        }
-        tc_st_16(dst, w);
-        return large;
-    }
-
-    // The sums to the output row, or to the CTA's part of it.
-    __device__ __forceinline__ void finish(const KvAttendArgs& a, const KvWork& work, const TcWalk& walk, int row,
-                                           uint32_t o) {
+    // This part's sums (tensor memory `o`) to the output row, or to the CTA's part of it, 64
+    // bytes a row at a time through shared memory (`stage`, 2 KB a warp), so that an instruction
+    // writes 8 rows' pieces and not 16 bytes of 32.
+    __device__ __forceinline__ void finish(const KvAttendArgs& a, const KvWork& work, const TcWalk& walk, int t, int row,
+                                           int part, uint32_t o, float* shared, int pair, uint8_t* stage) {
+        const int lane = threadIdx.x & 31;
+        shared[2 * row + part] = l;
+        pair_sync(pair);
+        const float2 both = reinterpret_cast<const float2*>(shared)[row];
         const KvPlace& p = walk.at;
         const KvParts parts = kv_parts(work, p, walk.first);
-        const int r = p.rt * a.sh.rows + row;
-        const int64_t out_row =
-            (int64_t)(p.s.q0 + r / a.sh.group) * a.q_heads + p.head * a.sh.group + r % a.sh.group;
-        const float down = 0x1p-6f, sum = l * down;
-        const float by = parts.parts > 1 ? down : sum == 0.f ? 0.f : __fdiv_rn(down, sum);
-        float* part = a.part_o + ((size_t)parts.slot * a.sh.rows + row) * D;
+        const bool whole = parts.parts == 1;
+        const int group = a.sh.group, rows = p.s.n * group, in_tile = t * kTcTile + row;
+        const int r0 = p.rt * a.sh.rows + in_tile - lane;  // the warp's first row
+        auto out_row = [&](int r) { return (int64_t)(p.s.q0 + r / group) * a.q_heads + p.head * group + r % group; };
+        const float down = 0x1p-6f, sum = (both.x + both.y) * down;
+        const float by = !whole ? down : sum == 0.f ? 0.f : __fdiv_rn(down, sum);
+        const int cols = whole ? 32 : 16;  // channels of 64 bytes
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-            uint32_t v[32];
-            tmem_ld_32(o + c, v);
-            tc_wait_ld_32(v);
-            if (!valid) continue;
+        for (int c = 0; c < kCols; c += cols) {
+            uint32_t v[16];
+            if (whole) {
+                uint32_t x[32];
+                tmem_ld_32(o + c, x);
+                tc_wait_ld_32(x);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * by);
-            if (parts.parts > 1) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    *reinterpret_cast<uint4*>(part + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                for (int i = 0; i < 16; ++i)
+                    v[i] = bf16_pair(__uint_as_float(x[2 * i]) * by, __uint_as_float(x[2 * i + 1]) * by);
             } else {
+                tmem_ld_16(o + c, v);
+                tc_wait_ld_16(v);
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    auto pair = [&](int k) { return bf16_pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])); };
-                    *reinterpret_cast<uint4*>(a.out + out_row * D + c + i) =
-                        make_uint4(pair(i), pair(i + 2), pair(i + 4), pair(i + 6));
-                }
+                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * by);
+            }
+            auto place = [&](int r, int q) { return reinterpret_cast<uint4*>(stage + r * 64 + ((q ^ (r >> 1 & 3)) << 4)); };
+            __syncwarp();  // the previous piece has been read
+#pragma unroll
+            for (int q = 0; q < 4; ++q) *place(lane, q) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int rr = i * 8 + (lane >> 2), q = lane & 3, col = part * kCols + c;
+                if (r0 + rr >= rows) continue;
+                uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(a.out + out_row(r0 + rr) * D + col)
+                                     : reinterpret_cast<uint8_t*>(
+                                           a.part_o + ((size_t)parts.slot * a.sh.rows + in_tile - lane + rr) * D + col);
+                reinterpret_cast<uint4*>(dst)[q] = *place(rr, q);
             }
         }
-        if (!valid) return;
-        if (parts.parts > 1)
-            a.part_ml[(size_t)parts.slot * a.sh.rows + row] = make_float2(m, sum);
+        if (!valid || part != 0) return;
+        const int64_t at = out_row(r0 + lane);
+        if (!whole)
+            a.part_ml[(size_t)parts.slot * a.sh.rows + in_tile] = make_float2(m, sum);
         else if (a.lse != nullptr)
-            a.lse[out_row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
-        if (parts.leader) a.info[out_row] = make_int2(parts.slot, parts.parts * 256 + row);
+            a.lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+        if (parts.leader) a.info[at] = make_int2(parts.slot, parts.parts * 256 + in_tile);
     }
 };
 
 template <int D>
 __device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& work, uint8_t* smem, const TcBars& bar,
                                            uint32_t tmem, const WaitCtl& ctl) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 2, row = threadIdx.x;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s = tmem + lanes + t * kTcTile, o = tmem + lanes + 2 * kTcTile + t * kTcTile;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = warp >> 3, part = warp >> 2 & 1, row = (warp & 3) * 32 + lane, pair = 1 + t * 4 + (warp & 3);
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s = lanes + t * kTcTile, o = lanes + 2 * kTcTile + t * kTcTile + part * (D / 2);
     uint8_t* q_tile = smem + t * 2 * Tc<D>::kPiece;
+    uint8_t* stage = smem + Tc<D>::kOffStage + warp * 2048;
+    float* shared = reinterpret_cast<float*>(smem + Tc<D>::kOffShared) + t * 2 * kTcTile;  // [row][part]
+    constexpr int kUse = 4 * kTcTile;  // each of its three uses has a place of its own
     TcRing v;
-    uint32_t s_phase = 0, pv = 0;  // steps; halves handed over
+    uint32_t s_phase = 0;  // steps
+    bool failed = false;   // a wait gave up
     TcRow<D> mine;
     TcWalk walk(work);
     auto start = [&](TcRow<D>& r, const TcWalk& w) {
         if (!w.more() || t >= w.tiles(a)) return;
-        r.start(a, w.at, row, q_tile);
+        r.start(a, w.at, t, row, part, q_tile, reinterpret_cast<uint32_t*>(shared + kUse), pair);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.q_full[t]);
@@ -447,23 +482,24 @@ __device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& 
             continue;
         }
         for (int j = 0; j < walk.n; ++j) {
-            if (!warp_wait(&bar.v_full[v.stage], v.phase, ctl)) return;  // its scales
+            failed = !warp_wait(&bar.v_full[v.stage], v.phase, ctl) || failed;  // its scales
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-                if (!warp_wait(&bar.s_full[2 * t + h], s_phase, ctl)) return;
+                failed = !warp_wait(&bar.s_full[2 * t + h], s_phase, ctl) || failed;
                 tc_fence_after();
+                const float4* scales =
+                    reinterpret_cast<const float4*>(smem + Tc<D>::kOffScales) + 8 * v.stage + 4 * h + 2 * part;
                 const bool ok = mine.step(
-                    a, s + h * kTcHalf, o, reinterpret_cast<const float4*>(smem + Tc<D>::kOffScales) + 8 * v.stage + 4 * h,
-                    (walk.at.unit + j) * kTcTile + h * kTcHalf, j + h > 0, [&] {
-                        const bool summed = warp_wait(&bar.pv_done[t], (pv - 1) & 1u, ctl);
+                    a, s + h * kTcHalf + 32 * part, s + h * kTcHalf + 16 * part, o, scales,
+                    (walk.at.unit + j) * kTcTile + h * kTcHalf + 32 * part, j + h > 0, failed, row, part, shared, pair,
+                    [&] {  // the half before, and with it all others
+                        failed = !warp_wait(&bar.pv_done[2 * t + (h ^ 1)], h ? s_phase : s_phase ^ 1u, ctl) || failed;
                         tc_fence_after();
-                        return summed;
                     });
                 if (!ok) return;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_full[2 * t + h]);
-                ++pv;
             }
             v.step(kTcVS);
             s_phase ^= 1u;
@@ -473,9 +509,9 @@ __device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& 
         TcRow<D> after = mine;
         next.next(a);
         start(after, next);
-        if (!warp_wait(&bar.pv_done[t], (pv - 1) & 1u, ctl)) return;
+        failed = !warp_wait(&bar.pv_done[2 * t + 1], s_phase ^ 1u, ctl) || failed;
         tc_fence_after();
-        mine.finish(a, work, walk, row, o);
+        mine.finish(a, work, walk, t, row, part, o, shared + 2 * kUse, pair, stage);
         tc_fence_before();
         mine = after;
         walk = next;
@@ -487,7 +523,7 @@ template <int D>
 __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& work, uint8_t* smem, const TcBars& bar,
                                           const WaitCtl& ctl) {
     constexpr int kPerRow = D / 16, kRows = 128 / kPerRow, kPasses = kTcTile / kRows;  // rows of a pass
-    const int tid = threadIdx.x - 256, lane = tid & 31;
+    const int tid = threadIdx.x - 32 * kTcValues0, lane = tid & 31;
     // A lane's 16 channels and key of a pass: 8 lanes that store together have two keys
     // and pieces 0, 2, 4, 6 of 128 bytes, which the swizzle puts into all banks.
     const int c = D == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
@@ -667,7 +703,8 @@ __device__ __forceinline__ void tc_products(const KvAttendArgs& a, const KvWork&
     const uint32_t v0 = (uint32_t)v_desc;
     const int lane = threadIdx.x & 31;
     TcRing k, v;
-    uint32_t q_phase = 0, p_phase = 0, done = 0;  // row tiles; steps; weighted halves issued
+    uint32_t q_phase = 0, p_phase = 0;  // row tiles; steps
+    uint32_t done[2] = {0, 0};          // weighted halves issued
     auto scores = [&](int half) {
         tc_fence_after();
         tc_mma_scores<D>(t * kTcTile + half * kTcHalf, q0,
@@ -684,8 +721,8 @@ __device__ __forceinline__ void tc_products(const KvAttendArgs& a, const KvWork&
         tc_mma_values<D>(2 * kTcTile + t * kTcTile, t * kTcTile + half * kTcHalf,
                          v0 + v.stage * (Tc<D>::kValues >> 4) + half * (kTcHalf * 128 >> 4), (uint32_t)(v_desc >> 32),
                          some ? 1u : 0u);
-        tc_commit(&bar.pv_done[t]);
-        ++done;
+        tc_commit(&bar.pv_done[2 * t + half]);
+        ++done[half];
         if (half == 1) {
             tc_commit(&bar.v_empty[v.stage]);
             v.step(kTcVS);
@@ -693,8 +730,11 @@ __device__ __forceinline__ void tc_products(const KvAttendArgs& a, const KvWork&
         }
         return true;
     };
-    // the weights in a buffer have been read: all halves issued so far are done
-    auto free_buffer = [&] { return warp_wait(&bar.pv_done[t], (done - 1) & 1u, ctl); };
+    // the weights in a half's buffer have been read.  (A barrier a half: with one for both, the
+    // wait for the second could take the end of the one before the first for it.)
+    auto free_buffer = [&](int half) {
+        return done[half] == 0 || warp_wait(&bar.pv_done[2 * t + half], (done[half] - 1) & 1u, ctl);
+    };
     bool ok = true;
     for (TcWalk walk(work); ok && walk.more(); walk.next(a)) {
         if (t >= walk.tiles(a)) {  // no rows: the other tile's stages are free as far as this one goes
@@ -710,17 +750,17 @@ __device__ __forceinline__ void tc_products(const KvAttendArgs& a, const KvWork&
             continue;
         }
         ok = warp_wait(&bar.q_full[t], q_phase, ctl) && warp_wait(&bar.k_full[k.stage], k.phase, ctl) &&
-             (done == 0 || free_buffer());
+             free_buffer(0) && free_buffer(1);
         q_phase ^= 1u;
         if (!ok) break;
         scores(0);
         scores(1);
         ok = weighted(0, false);
         for (int j = 1; ok && j < walk.n; ++j) {
-            ok = warp_wait(&bar.k_full[k.stage], k.phase, ctl) && free_buffer();
+            ok = warp_wait(&bar.k_full[k.stage], k.phase, ctl) && free_buffer(0);
             if (!ok) break;
             scores(0);
-            ok = weighted(1, true) && free_buffer();
+            ok = weighted(1, true) && free_buffer(1);
             if (!ok) break;
             scores(1);
             ok = weighted(0, true);
@@ -746,12 +786,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&bar.q_full[t], 4);
+            mbar_init(&bar.q_full[t], 8);
             for (int h = 0; h < 2; ++h) {
                 mbar_init(&bar.s_full[2 * t + h], 1);
-                mbar_init(&bar.p_full[2 * t + h], 4);
+                mbar_init(&bar.p_full[2 * t + h], 8);
+                mbar_init(&bar.pv_done[2 * t + h], 1);
             }
-            mbar_init(&bar.pv_done[t], 1);
             mbar_init(&bar.teardown[t], 1);
         }
         for (int i = 0; i < kTcKS; ++i) {
@@ -767,12 +807,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         fence_barrier_init();
         tma_prefetch_desc(&keys);
     }
-    if (warp == 13) {
+    if (warp == kTcProducts0) {
         tmem_alloc(tmem_slot, kTcCols);
         tmem_relinquish();
     }
     pdl_wait();
-    if (warp == 13) pdl_trigger();  // not before the tensor memory is this CTA's
+    if (warp == kTcProducts0) pdl_trigger();  // not before the tensor memory is this CTA's
     kv_find_work<kTcThreads>(a, gridDim.x, 1, work, reinterpret_cast<int64_t*>(smem + Tc<D>::kOffMisc + 64));
     tc_fence_before();
     __syncthreads();
@@ -781,19 +821,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const WaitCtl ctl{abort_flag, a.error, a.timeout_ns, 0u};
     if (tmem != 0u && threadIdx.x == 0) atomicOr(a.error, kErrDevice);  // all columns begin at 0
     if (work->u1 > work->u0 && tmem == 0u) {
-        if (warp < 8) {
+        if (warp < kTcValues0)
             tc_softmax<D>(a, *work, smem, bar, tmem, ctl);
-        } else if (warp < 12) {
+        else if (warp < kTcKeys0)
             tc_values<D>(a, *work, smem, bar, ctl);
-        } else {
-            if (warp == 12) tc_keys<D>(a, *work, smem, bar, &keys, no_page, ctl);
-            if (warp >= 13 && warp < 15) tc_products<D>(a, *work, smem, bar, warp - 13, ctl);
-        }
+        else if (warp == kTcKeys0)
+            tc_keys<D>(a, *work, smem, bar, &keys, no_page, ctl);
+        else if (warp < kTcProducts0 + 2)
+            tc_products<D>(a, *work, smem, bar, warp - kTcProducts0, ctl);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 13) {
+    if (warp == kTcProducts0) {
         tc_fence_after();
         tmem_dealloc(tmem, kTcCols);
     }
