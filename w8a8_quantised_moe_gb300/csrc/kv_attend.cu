@@ -100,6 +100,38 @@ struct TcBars {
     }
 };
 
+// warp_wait (gemm_common.cuh) for warps that share their schedulers with busy ones: a thread
+// that waits is suspended for up to 20 us at a time, where the plain test came back some five
+// times a wait and took a third of the issue slots.
+__device__ __forceinline__ bool tc_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
+    if (__all_sync(0xffffffffu, tc_test(bar, parity))) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        if (__all_sync(0xffffffffu, tc_test(bar, parity))) return true;
+        int give_up = 0;
+        if ((threadIdx.x & 31) == 0) {
+            if (*ctl.abort) {
+                give_up = 1;
+            } else if (global_timer_ns() - t0 > ctl.timeout_ns) {
+                give_up_timeout(ctl);
+                give_up = 1;
+            }
+        }
+        if (__shfl_sync(0xffffffffu, give_up, 0)) return false;
+    }
+}
+
 // A CTA's run, cut at the borders of row tiles; every role walks through it.
 struct TcWalk {
     KvPlace at;
@@ -482,10 +514,10 @@ __device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& 
             continue;
         }
         for (int j = 0; j < walk.n; ++j) {
-            failed = !warp_wait(&bar.v_full[v.stage], v.phase, ctl) || failed;  // its scales
+            failed = !tc_wait(&bar.v_full[v.stage], v.phase, ctl) || failed;  // its scales
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-                failed = !warp_wait(&bar.s_full[2 * t + h], s_phase, ctl) || failed;
+                failed = !tc_wait(&bar.s_full[2 * t + h], s_phase, ctl) || failed;
                 tc_fence_after();
                 const float4* scales =
                     reinterpret_cast<const float4*>(smem + Tc<D>::kOffScales) + 8 * v.stage + 4 * h + 2 * part;
@@ -493,7 +525,7 @@ __device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& 
                     a, s + h * kTcHalf + 32 * part, s + h * kTcHalf + 16 * part, o, scales,
                     (walk.at.unit + j) * kTcTile + h * kTcHalf + 32 * part, j + h > 0, failed, row, part, shared, pair,
                     [&] {  // the half before, and with it all others
-                        failed = !warp_wait(&bar.pv_done[2 * t + (h ^ 1)], h ? s_phase : s_phase ^ 1u, ctl) || failed;
+                        failed = !tc_wait(&bar.pv_done[2 * t + (h ^ 1)], h ? s_phase : s_phase ^ 1u, ctl) || failed;
                         tc_fence_after();
                     });
                 if (!ok) return;
@@ -509,7 +541,7 @@ __device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& 
         TcRow<D> after = mine;
         next.next(a);
         start(after, next);
-        failed = !warp_wait(&bar.pv_done[2 * t + 1], s_phase ^ 1u, ctl) || failed;
+        failed = !tc_wait(&bar.pv_done[2 * t + 1], s_phase ^ 1u, ctl) || failed;
         tc_fence_after();
         mine.finish(a, work, walk, t, row, part, o, shared + 2 * kUse, pair, stage);
         tc_fence_before();
@@ -572,7 +604,7 @@ __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& w
     load();
     TcRing v;
     for (int64_t left = work.u1 - work.u0; left > 0; --left) {
-        if (!warp_wait(&bar.v_empty[v.stage], v.phase ^ 1u, ctl)) return;
+        if (!tc_wait(&bar.v_empty[v.stage], v.phase ^ 1u, ctl)) return;
         uint8_t* dst = smem + Tc<D>::kOffV + v.stage * Tc<D>::kValues;
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
@@ -716,7 +748,7 @@ __device__ __forceinline__ void tc_products(const KvAttendArgs& a, const KvWork&
         }
     };
     auto weighted = [&](int half, bool some) {
-        if (!warp_wait(&bar.p_full[2 * t + half], p_phase, ctl)) return false;
+        if (!tc_wait(&bar.p_full[2 * t + half], p_phase, ctl)) return false;
         tc_fence_after();
         tc_mma_values<D>(2 * kTcTile + t * kTcTile, t * kTcTile + half * kTcHalf,
                          v0 + v.stage * (Tc<D>::kValues >> 4) + half * (kTcHalf * 128 >> 4), (uint32_t)(v_desc >> 32),
@@ -733,13 +765,13 @@ __device__ __forceinline__ void tc_products(const KvAttendArgs& a, const KvWork&
     // the weights in a half's buffer have been read.  (A barrier a half: with one for both, the
     // wait for the second could take the end of the one before the first for it.)
     auto free_buffer = [&](int half) {
-        return done[half] == 0 || warp_wait(&bar.pv_done[2 * t + half], (done[half] - 1) & 1u, ctl);
+        return done[half] == 0 || tc_wait(&bar.pv_done[2 * t + half], (done[half] - 1) & 1u, ctl);
     };
     bool ok = true;
     for (TcWalk walk(work); ok && walk.more(); walk.next(a)) {
         if (t >= walk.tiles(a)) {  // no rows: the other tile's stages are free as far as this one goes
             for (int j = 0; ok && j < walk.n; ++j) {
-                ok = warp_wait(&bar.k_full[k.stage], k.phase, ctl) && warp_wait(&bar.v_full[v.stage], v.phase, ctl);
+                ok = tc_wait(&bar.k_full[k.stage], k.phase, ctl) && tc_wait(&bar.v_full[v.stage], v.phase, ctl);
                 if (ok && lane == 0) {
                     mbar_arrive(&bar.k_empty[k.stage]);
                     mbar_arrive(&bar.v_empty[v.stage]);
@@ -749,7 +781,7 @@ __device__ __forceinline__ void tc_products(const KvAttendArgs& a, const KvWork&
             }
             continue;
         }
-        ok = warp_wait(&bar.q_full[t], q_phase, ctl) && warp_wait(&bar.k_full[k.stage], k.phase, ctl) &&
+        ok = tc_wait(&bar.q_full[t], q_phase, ctl) && tc_wait(&bar.k_full[k.stage], k.phase, ctl) &&
              free_buffer(0) && free_buffer(1);
         q_phase ^= 1u;
         if (!ok) break;
@@ -757,7 +789,7 @@ __device__ __forceinline__ void tc_products(const KvAttendArgs& a, const KvWork&
         scores(1);
         ok = weighted(0, false);
         for (int j = 1; ok && j < walk.n; ++j) {
-            ok = warp_wait(&bar.k_full[k.stage], k.phase, ctl) && free_buffer(0);
+            ok = tc_wait(&bar.k_full[k.stage], k.phase, ctl) && free_buffer(0);
             if (!ok) break;
             scores(0);
             ok = weighted(1, true) && free_buffer(1);
