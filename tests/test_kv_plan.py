@@ -54,7 +54,7 @@ int main() {
         if (!wild) CHECK(runs <= kv_most_runs(B, T, page));
         // attention
         const int row_choice[2] = {16, 256}, tok_choice[2] = {64, 128};
-        KvShape sh{1 + rnd(rnd(2) ? 20 : 3), row_choice[rnd(2)], tok_choice[rnd(2)], rnd(2) ? 0 : 1 + rnd(300), page};
+        KvShape sh{1 + rnd(rnd(2) ? 20 : 3), row_choice[rnd(2)], tok_choice[rnd(2)], rnd(2) ? 0 : 1 + rnd(300), page, rnd(3) ? rnd(6) : 0};
         long long U = 0;
         std::vector<long long> before;
         for (int b = 0; b < B; ++b) {
@@ -70,7 +70,7 @@ int main() {
                 kv_units(s, sh, rt, first, count);
                 CHECK(first >= 0 && count >= 1);
                 CHECK(kv_units_before(s, sh, rt) == sum);
-                sum += count;
+                sum += count + sh.extra;
             }
             CHECK(kv_seq_units(s, sh) == sum);
         }
@@ -78,7 +78,7 @@ int main() {
         CHECK(ctas >= 1 && ctas <= most && ctas <= U);
         std::map<std::tuple<int, int, int, int>, int> done;
         std::map<std::tuple<int, int, int>, std::vector<int>> parts;
-        long long last = 0;
+        long long last = 0, units = 0;
         for (int c = 0; c < ctas; ++c) {
             const long long u0 = kv_deal(U, ctas, c), u1 = kv_deal(U, ctas, c + 1);
             CHECK(u0 == last && u1 > u0);
@@ -99,19 +99,26 @@ int main() {
                     ++found;
                 }
             CHECK(found == 1);
-            for (long long u = u0; u < u1; ++u) {
+            for (;;) {
+                const long long u = p.base + (p.unit - p.first);
+                CHECK(u >= u0);
+                if (u >= u1) break;
                 CHECK(kv_owner(U, ctas, u) == c);
                 CHECK(p.b < B && p.head < heads && p.rt < kv_row_tiles(p.s, sh));
-                CHECK(p.base + (p.unit - p.first) == u);
                 CHECK(p.unit >= 0 && (long long)p.unit * sh.tokens <= kv_max(p.s.len - 1, 0));
+                ++units;
                 ++done[std::make_tuple(p.b, p.head, p.rt, p.unit)];
                 auto& list = parts[std::make_tuple(p.b, p.head, p.rt)];
                 if (list.empty() || list.back() != c) list.push_back(c);
                 CHECK(list.front() == kv_owner(U, ctas, p.base));
-                if (u + 1 < u1) kv_next(p, bt, sh, heads);
+                if (p.unit + 1 == p.end) CHECK(c == kv_owner(U, ctas, p.base + (p.end - p.first) - 1));
+                if (u1 <= p.base + (p.end - p.first) && p.unit + 1 == p.end) break;
+                kv_next(p, bt, sh, heads);
             }
         }
-        CHECK(last == U && (long long)done.size() == U);
+        long long tiles = 0;
+        for (int b = 0; b < B; ++b) tiles += (long long)kv_row_tiles(kv_seq(bt, b, page), sh) * heads;
+        CHECK(last == U && (long long)done.size() == units && units == U - tiles * sh.extra);
         for (auto& d : done) CHECK(d.second == 1);
         for (auto& l : parts)
             for (size_t i = 0; i < l.second.size(); ++i) CHECK(l.second[i] == l.second[0] + (int)i);

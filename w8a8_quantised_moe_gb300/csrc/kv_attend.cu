@@ -29,6 +29,9 @@
 namespace moe {
 namespace {
 
+#ifndef KV_EXTRA
+#define KV_EXTRA 4
+#endif
 #ifndef KV_PARTS
 #define KV_PARTS 1
 #endif
@@ -140,16 +143,21 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, const Wa
 // A CTA's run, cut at the borders of row tiles; every role walks through it.
 struct TcWalk {
     KvPlace at;
-    int64_t left;
-    int n;        // steps here
+    int64_t end;  // of the run
+    int n;        // steps here; 0: no more
     bool first;
-    __device__ __forceinline__ explicit TcWalk(const KvWork& w) : at(w.at), left(w.u1 - w.u0), first(true) { count(); }
-    __device__ __forceinline__ void count() { n = left < at.end - at.unit ? (int)left : at.end - at.unit; }
-    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ explicit TcWalk(const KvWork& w) : at(w.at), end(w.u1), first(true) { count(); }
+    __device__ __forceinline__ void count() {
+        const int64_t left = end - (at.base + (at.unit - at.first));
+        n = left <= 0 ? 0 : left < at.end - at.unit ? (int)left : at.end - at.unit;
+    }
+    __device__ __forceinline__ bool more() const { return n > 0; }
+    __device__ __forceinline__ bool whole() const { return n == at.end - at.first; }  // the row tile is this CTA's alone
     __device__ __forceinline__ void next(const KvAttendArgs& a) {
-        left -= n;
         first = false;
-        if (left > 0) {
+        if (end <= at.base + (at.end - at.first)) {  // the run ends with this row tile, or in it
+            n = 0;
+        } else {
             at.unit = at.end - 1;
             kv_next(at, a.bt, a.sh, a.c.heads);
             count();
@@ -159,6 +167,25 @@ struct TcWalk {
     __device__ __forceinline__ int tiles(const KvAttendArgs& a) const {
         return at.s.n * a.sh.group - at.rt * a.sh.rows > kTcTile ? 2 : 1;
     }
+};
+
+// Rows r0 .. r0 + 31 of a sequence and key head: their token and query head, by one division
+// and a product (x / group = x * ceil(2^21 / group) / 2^21 for x < 2^11, group <= 2^10).
+struct TcRows {
+    const KvAttendArgs& a;
+    const KvPlace& p;
+    int r0, tok0, rest0;
+    uint32_t inverse;
+    __device__ __forceinline__ TcRows(const KvAttendArgs& args, const KvPlace& place, int row)
+        : a(args), p(place), r0(row), tok0(row / args.sh.group), rest0(row - row / args.sh.group * args.sh.group),
+          inverse(((1u << 21) + args.sh.group - 1) / args.sh.group) {}
+    __device__ __forceinline__ int token(int i) const { return tok0 + (int)(((uint32_t)(rest0 + i) * inverse) >> 21); }
+    __device__ __forceinline__ int64_t row(int i, int64_t tokens, int heads) const {  // tokens: from one to the next
+        const int more = (int)(((uint32_t)(rest0 + i) * inverse) >> 21);
+        return (p.s.q0 + tok0 + more) * tokens + (int64_t)(p.head * a.sh.group + rest0 + i - more * a.sh.group) * heads;
+    }
+    __device__ __forceinline__ int64_t q_row(int i) const { return row(i, a.q_stride, a.c.dim); }
+    __device__ __forceinline__ int64_t out_row(int i) const { return row(i, a.q_heads, 1); }
 };
 
 // A ring's stage and phase.
@@ -260,12 +287,12 @@ struct TcRow {
                                           uint8_t* q_tile, uint32_t* shared, int pair) {
         constexpr int kLanes = kCols / 8, kRows = 32 / kLanes, kLoads = 32 / kRows;  // lanes of a row, rows of a load
         const int lane = threadIdx.x & 31, group = a.sh.group, rows = p.s.n * group;
-        const int r0 = p.rt * a.sh.rows + t * kTcTile + (row & ~31), c = p.s.len - p.s.n;  // the warp's first row
+        const TcRows of(a, p, p.rt * a.sh.rows + t * kTcTile + (row & ~31));  // the warp's rows
+        const int r0 = of.r0, c = p.s.len - p.s.n;
         auto source = [&](int i) {
-            const int r = r0 + i * kRows + lane / kLanes, tok = r / group;
-            const uint16_t* src = a.q + (int64_t)(p.s.q0 + tok) * a.q_stride +
-                                  (p.head * group + r - tok * group) * D + part * kCols + lane % kLanes * 8;
-            return r < rows ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+            const int rr = i * kRows + lane / kLanes;
+            const uint16_t* src = a.q + of.q_row(rr) + part * kCols + lane % kLanes * 8;
+            return r0 + rr < rows ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
         };
         constexpr int kBatch = 8;  // loads in flight; code that runs once a row tile is short, or waits for its instructions
 #pragma unroll 1
@@ -297,9 +324,9 @@ struct TcRow {
         if (mine >= 0x7f80u) factor = __uint_as_float(0x7fffffffu);  // a row that is not finite
         const int r = r0 + (row & 31);
         valid = r < rows;
-        pos = valid ? c + r / group : -1;
-        pos_first = r0 < rows ? c + r0 / group : -1;
-        pos_last = r0 + 31 < rows ? c + (r0 + 31) / group : -1;
+        pos = valid ? c + of.token(row & 31) : -1;
+        pos_first = r0 < rows ? c + of.token(0) : -1;
+        pos_last = r0 + 31 < rows ? c + of.token(31) : -1;
         m = -INFINITY;
         l = 0.f;
 #pragma unroll 1
@@ -474,11 +501,12 @@ struct TcRow {
         pair_sync(pair);
         const float2 both = reinterpret_cast<const float2*>(shared)[row];
         const KvPlace& p = walk.at;
-        const KvParts parts = kv_parts(work, p, walk.first);
-        const bool whole = parts.parts == 1;
+        const bool whole = walk.whole();
+        KvParts parts{0, 1, true};
+        if (!whole) parts = kv_parts(work, p, walk.first);
         const int group = a.sh.group, rows = p.s.n * group, in_tile = t * kTcTile + row;
-        const int r0 = p.rt * a.sh.rows + in_tile - lane;  // the warp's first row
-        auto out_row = [&](int r) { return (int64_t)(p.s.q0 + r / group) * a.q_heads + p.head * group + r % group; };
+        const TcRows of(a, p, p.rt * a.sh.rows + in_tile - lane);  // the warp's rows
+        const int r0 = of.r0;
         const float down = 0x1p-6f, sum = (kTcParts == 1 ? both.x : both.x + both.y) * down;
         const float by = !whole ? down : sum == 0.f ? 0.f : __fdiv_rn(down, sum);
         const int cols = whole ? 32 : 16;  // channels of 64 bytes
@@ -507,14 +535,14 @@ struct TcRow {
             for (int i = 0; i < 4; ++i) {
                 const int rr = i * 8 + (lane >> 2), q = lane & 3, col = part * kCols + c;
                 if (r0 + rr >= rows) continue;
-                uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(a.out + out_row(r0 + rr) * D + col)
+                uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(a.out + of.out_row(rr) * D + col)
                                      : reinterpret_cast<uint8_t*>(
                                            a.part_o + ((size_t)parts.slot * a.sh.rows + in_tile - lane + rr) * D + col);
                 reinterpret_cast<uint4*>(dst)[q] = *place(rr, q);
             }
         }
         if (!valid || part != 0) return;
-        const int64_t at = out_row(r0 + lane);
+        const int64_t at = of.out_row(lane);
         if (!whole)
             a.part_ml[(size_t)parts.slot * a.sh.rows + in_tile] = make_float2(m, sum);
         else if (a.lse != nullptr)
@@ -646,7 +674,8 @@ __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& w
     if (!more) return;
     load();
     TcRing v;
-    for (int64_t left = work.u1 - work.u0; left > 0; --left) {
+    for (bool last = false; !last;) {
+        last = !more;
         if (!tc_wait(&bar.v_empty[v.stage], v.phase ^ 1u, ctl)) return;
         uint8_t* dst = smem + Tc<D>::kOffV + v.stage * Tc<D>::kValues;
 #pragma unroll
@@ -941,6 +970,7 @@ int kv_tc_ctas() { return num_sms(); }
 cudaError_t launch_kv_attend(KvAttendArgs a, cudaStream_t st, bool pdl) {
     a.sh.rows = kKvRows;
     a.sh.tokens = kTcTile;
+    a.sh.extra = KV_EXTRA;
     const cudaError_t e = a.c.dim == 64 ? launch_tc<64>(a, st, pdl) : launch_tc<128>(a, st, pdl);
     return e != cudaSuccess ? e : launch_kv_join(a, st, pdl);
 }

@@ -455,6 +455,7 @@ int kv_few_ctas() { return 2 * num_sms(); }
 cudaError_t launch_kv_attend_few(KvAttendArgs a, cudaStream_t st, bool pdl) {
     a.sh.rows = kKvFewRows;
     a.sh.tokens = kKvFewTokens;
+    a.sh.extra = 0;
     const cudaError_t e = a.c.dim == 64 ? launch_few<64>(a, st, pdl) : launch_few<128>(a, st, pdl);
     return e != cudaSuccess ? e : launch_kv_join(a, st, pdl);
 }

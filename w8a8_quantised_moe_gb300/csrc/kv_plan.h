@@ -57,8 +57,10 @@ KV_HD int64_t kv_most_runs(int64_t B, int64_t T, int64_t page) {
 // tile is `rows` of them.  A unit is `tokens` keys against one row tile.  Row tile
 // rt of the sequence sees the units [first, first + count): at least one, which
 // may hold no key that it sees.
+// In the deal a row tile counts `extra` units more than it has, before its first: what
+// it costs to begin and end one.
 struct KvShape {
-    int group, rows, tokens, window, page;
+    int group, rows, tokens, window, page, extra;
 };
 KV_HD int kv_row_tiles(const KvSeq& s, const KvShape& sh) { return (s.n * sh.group + sh.rows - 1) / sh.rows; }
 KV_HD void kv_units(const KvSeq& s, const KvShape& sh, int rt, int& first, int& count) {
@@ -87,17 +89,17 @@ KV_HD int64_t kv_floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
     }
     return sum;
 }
-// Units of a sequence's row tiles before rt, for one key head, 0 <= rt <= its row tiles.
+// Units of a sequence's row tiles before rt as they count, for one key head, 0 <= rt <= its row tiles.
 // The last row of a tile but the last is at position c + floor(((rt + 1) rows - 1) / group),
 // so that its last unit is the floor of a linear function of rt, as is the first.
 KV_HD int64_t kv_units_before(const KvSeq& s, const KvShape& sh, int rt) {
     const int64_t c = s.len - s.n, g = sh.group, R = sh.rows, m = g * sh.tokens;
-    int64_t sum = 0;
+    int64_t sum = (int64_t)rt * sh.extra;
     int whole = rt;
     if (rt > 0 && rt == kv_row_tiles(s, sh)) {
         int first, count;
         kv_units(s, sh, --whole, first, count);
-        sum = count;
+        sum += count;
     }
     sum += whole;  // one unit each, and those before the last
     int64_t i0 = c < 0 ? -c * g / R : 0;  // the row tiles before see no key
@@ -109,13 +111,14 @@ KV_HD int64_t kv_units_before(const KvSeq& s, const KvShape& sh, int rt) {
     }
     return sum;
 }
-// Units of a sequence and one key head.
+// Units of a sequence and one key head, as they count.
 KV_HD int64_t kv_seq_units(const KvSeq& s, const KvShape& sh) {
     const int tiles = kv_row_tiles(s, sh);
     if (tiles > 1) return kv_units_before(s, sh, tiles);
     int first = 0, count = 0;
-    if (tiles == 1) kv_units(s, sh, 0, first, count);
-    return count;
+    if (tiles == 0) return 0;
+    kv_units(s, sh, 0, first, count);
+    return count + sh.extra;
 }
 
 // The batch's U units, in the order (sequence, key head, row tile, unit), are dealt
@@ -143,19 +146,19 @@ KV_HD void kv_enter(KvPlace& p, const KvShape& sh) {
 }
 // Whether unit `u`, counted within one key head of p's sequence, is of row tile rt; if so, p is there.
 KV_HD bool kv_enter_if(KvPlace& p, const KvShape& sh, int rt, int64_t u, int64_t head_base) {
-    const int64_t before = kv_units_before(p.s, sh, rt);
-    if (u < before) return false;
+    const int64_t before = kv_units_before(p.s, sh, rt) + sh.extra;  // of the row tile's first unit
+    if (u < before - sh.extra) return false;
     p.rt = rt;
     kv_enter(p, sh);
     if (u >= before + (p.end - p.first)) return false;
     p.base = head_base + before;
-    p.unit = p.first + (int)(u - before);
+    p.unit = u < before ? p.first : p.first + (int)(u - before);
     return true;
 }
-// The next unit; there must be one.
+// The next unit; there must be one in the batch.  (Its number is base + unit - first.)
 KV_HD void kv_next(KvPlace& p, const KvBatch& bt, const KvShape& sh, int heads) {
     if (++p.unit < p.end) return;
-    p.base += p.end - p.first;
+    p.base += p.end - p.first + sh.extra;
     ++p.rt;
     if (p.rt >= kv_row_tiles(p.s, sh)) {
         p.rt = 0;
