@@ -29,19 +29,15 @@
 namespace moe {
 namespace {
 
-#ifndef KV_EXTRA
-#define KV_EXTRA 4
-#endif
-#ifndef KV_PARTS
-#define KV_PARTS 1
-#endif
-constexpr int kTcParts = KV_PARTS;  // warps that share the softmax of 32 rows, each with its part of the keys and channels
-// first warps of the roles behind the softmax
-constexpr int kTcValues0 = 8 * kTcParts, kTcKeys0 = kTcValues0 + 4, kTcProducts0 = kTcKeys0 + 1;
-constexpr int kTcThreads = 32 * (kTcValues0 + 8);
+constexpr int kTcThreads = 768;
+constexpr int kTcValues0 = 16, kTcKeys0 = 20, kTcProducts0 = 21;  // first warps of the roles behind the softmax's 16
 constexpr int kTcTile = 128;      // rows of a tile, keys of a step
 constexpr int kTcHalf = 64;       // keys of half a step, whose scores are one of a tile's two buffers
-constexpr int kTcKS = 3, kTcVS = 2;  // stages of keys, of values
+constexpr int kTcKS = 2, kTcVS = 2;  // stages of keys, of values (three of keys: the same times)
+// What beginning and ending a row tile costs, in steps, for the deal.  A prompt of 8192
+// tokens, 0 / 2 / 4 / 6 / 8: 809 / 706 / 590 / 581 / 593 us (the CTAs with a head's first row
+// tiles have up to 29 of them).
+constexpr int kTcExtra = 6;
 constexpr float kTcHeadroom = 8.f, kTcWeightBits = 6.f;  // as in kv_attend_few.cu
 constexpr uint32_t kTcCols = 512;
 
@@ -53,7 +49,7 @@ struct Tc {
     static constexpr int kOffV = kOffK + kTcKS * kPiece;
     static constexpr int kOffScales = kOffV + kTcVS * kValues;  // [stage][8 groups of 16 keys] (key, log2 value, 1 / value)
     static constexpr int kOffStage = kOffScales + kTcVS * 8 * 16;  // 2 KB a softmax warp
-    static constexpr int kOffShared = kOffStage + 8 * kTcParts * 2048;       // [use][tile][row][part], what a row's two threads tell each other
+    static constexpr int kOffShared = kOffStage + 16 * 2048;       // [use][tile][row][part], what a row's two threads tell each other
     static constexpr int kOffBars = kOffShared + 3 * 2 * kTcTile * 8;
     // q_full[2] k_full[KS] k_empty[KS] v_full[VS] v_empty[VS] s_full[2][2] p_full[2][2] pv_done[2][2] teardown[2] stall
     static constexpr int kNumBars = 2 + 2 * kTcKS + 2 * kTcVS + 12 + 3;
@@ -251,14 +247,8 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
 
 // ------------------------------------------------------------------ softmax
 // Barrier of the two warps of a row group, and the OR of their conditions.
-__device__ __forceinline__ void pair_sync(int id) {
-    if (kTcParts == 1)
-        __syncwarp();
-    else
-        asm volatile("barrier.sync %0, 64;" ::"r"(id) : "memory");
-}
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.sync %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ bool pair_any(int id, bool x) {
-    if (kTcParts == 1) return __any_sync(0xffffffffu, x);
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
@@ -276,7 +266,7 @@ __device__ __forceinline__ bool pair_any(int id, bool x) {
 // goes on, and both return at the next pair_any.
 template <int D>
 struct TcRow {
-    static constexpr int kCols = D / kTcParts, kChunks = 2 / kTcParts;  // channels of a part; its 32s of keys of a half
+    static constexpr int kCols = D / 2;  // channels of a part
     float m, l, factor;
     int pos, pos_first, pos_last;  // position; those of the warp's first and last row
     bool valid;
@@ -294,27 +284,23 @@ struct TcRow {
             const uint16_t* src = a.q + of.q_row(rr) + part * kCols + lane % kLanes * 8;
             return r0 + rr < rows ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
         };
-        constexpr int kBatch = 8;  // loads in flight; code that runs once a row tile is short, or waits for its instructions
-#pragma unroll 1
-        for (int i0 = 0; i0 < kLoads; i0 += kBatch) {
-            uint4 w[kBatch];
+        uint4 w[kLoads];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) w[i] = source(i0 + i);
+        for (int i = 0; i < kLoads; ++i) w[i] = source(i);
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                // magnitudes of bf16 pairs, compared as whole numbers
-                uint32_t x = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
-                                      __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
-                x = max(x & 0xffffu, x >> 16);
+        for (int i = 0; i < kLoads; ++i) {
+            // magnitudes of bf16 pairs, compared as whole numbers
+            uint32_t x = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                  __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+            x = max(x & 0xffffu, x >> 16);
 #pragma unroll
-                for (int off = kLanes / 2; off > 0; off >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, off));
-                if (lane % kLanes == 0) shared[2 * ((row & ~31) + (i0 + i) * kRows + lane / kLanes) + part] = x;
-            }
+            for (int off = kLanes / 2; off > 0; off >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, off));
+            if (lane % kLanes == 0) shared[2 * ((row & ~31) + i * kRows + lane / kLanes) + part] = x;
         }
         pair_sync(pair);
         auto largest_of = [&](int rr) {
             const uint2 x = reinterpret_cast<const uint2*>(shared)[rr];
-            return kTcParts == 1 ? x.x : max(x.x, x.y);
+            return max(x.x, x.y);
         };
         // a row's scale 2^-e: e = the exponent of its largest magnitude less 7
         auto exponent = [](uint32_t x) { return max((int)(x >> 7) - 127 - 7, -120); };
@@ -329,31 +315,25 @@ struct TcRow {
         pos_last = r0 + 31 < rows ? c + of.token(31) : -1;
         m = -INFINITY;
         l = 0.f;
-#pragma unroll 1
-        for (int i0 = 0; i0 < kLoads; i0 += kBatch) {
-            uint4 w[kBatch];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) w[i] = source(i0 + i);
+        for (int i = 0; i < kLoads; ++i) {
+            const int rr = (row & ~31) + i * kRows + lane / kLanes;
+            const float down = power(-exponent(largest_of(rr)));
+            uint32_t hi[2], lo[2];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int rr = (row & ~31) + (i0 + i) * kRows + lane / kLanes;
-                const float down = power(-exponent(largest_of(rr)));
-                uint32_t hi[2], lo[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t x = j ? w[i].z : w[i].x, y = j ? w[i].w : w[i].y;
-                    const float f[4] = {bf16_lo(x) * down, bf16_hi(x) * down, bf16_lo(y) * down, bf16_hi(y) * down};
-                    hi[j] = e4m3_pair(f[0], f[1]) | (e4m3_pair(f[2], f[3]) << 16);
-                    const uint32_t h0 = e4m3x2_to_f16x2(hi[j]), h1 = e4m3x2_to_f16x2_hi(hi[j]);
-                    const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-                    const float2 g1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-                    lo[j] = e4m3_pair(f[0] - g0.x, f[1] - g0.y) | (e4m3_pair(f[2] - g1.x, f[3] - g1.y) << 16);
-                }
-                const int at = part * kCols + lane % kLanes * 8;
-                uint8_t* dst = q_tile + Tc<D>::place(rr, at >> 4) + (at & 8);
-                *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2*>(dst + Tc<D>::kPiece) = make_uint2(lo[0], lo[1]);
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t x = j ? w[i].z : w[i].x, y = j ? w[i].w : w[i].y;
+                const float f[4] = {bf16_lo(x) * down, bf16_hi(x) * down, bf16_lo(y) * down, bf16_hi(y) * down};
+                hi[j] = e4m3_pair(f[0], f[1]) | (e4m3_pair(f[2], f[3]) << 16);
+                const uint32_t h0 = e4m3x2_to_f16x2(hi[j]), h1 = e4m3x2_to_f16x2_hi(hi[j]);
+                const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+                const float2 g1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+                lo[j] = e4m3_pair(f[0] - g0.x, f[1] - g0.y) | (e4m3_pair(f[2] - g1.x, f[3] - g1.y) << 16);
             }
+            const int at = part * kCols + lane % kLanes * 8;
+            uint8_t* dst = q_tile + Tc<D>::place(rr, at >> 4) + (at & 8);
+            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(dst + Tc<D>::kPiece) = make_uint2(lo[0], lo[1]);
         }
     }
 
@@ -371,55 +351,35 @@ struct TcRow {
         tmem_wait_st();
     }
 
-    // The part's keys of a half: scores at `s` become weights at `dst`.  k0: the first key; o:
+    // The part's 32 keys of a half: scores at `s` become weights at `dst`.  k0: the first key; o:
     // this part's sums, which hold something where `some`, and everything handed over so far
     // once `summed` has run.  False: one of the row group's warps has failed.
     template <class Summed>
     __device__ __forceinline__ bool step(const KvAttendArgs& a, uint32_t s, uint32_t dst, uint32_t o,
                                          const float4* scales, int k0, bool some, bool failed, int row, int part,
                                          float* shared, int pair, Summed summed) {
-        uint32_t r[kChunks][32];
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) tmem_ld_32(s + 32 * i, r[i]);
-        float2 sc[2 * kChunks];
-        float inv[2 * kChunks];
-#pragma unroll
-        for (int g = 0; g < 2 * kChunks; ++g) {
-            const float4 x = scales[g];
-            sc[g] = make_float2(x.x * factor, x.y);
-            inv[g] = x.z;
-        }
+        uint32_t r[32];
+        tmem_ld_32(s, r);
+        const float4 x0 = scales[0], x1 = scales[1];
+        float2 sc[2] = {make_float2(x0.x * factor, x0.y), make_float2(x1.x * factor, x1.y)};
         const int window = a.sh.window;
-        const bool border = pos_first < k0 + 32 * kChunks - 1 || pos_last < 0 || (window > 0 && pos_last - window >= k0);
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) tc_wait_ld_32(r[i]);
-        if (border)
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i)
-                hide(r[i], sc[2 * i], sc[2 * i + 1], window > 0 ? pos - window + 1 - k0 - 32 * i : 0, pos - k0 - 32 * i);
+        const bool border = pos_first < k0 + 31 || pos_last < 0 || (window > 0 && pos_last - window >= k0);
+        tc_wait_ld_32(r);
+        if (border) hide(r, sc[0], sc[1], window > 0 ? pos - window + 1 - k0 : 0, pos - k0);
         // scales are positive: the largest product is the largest score's
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i)
-            top = max3(top, fmaf(largest(r[i]), sc[2 * i].x, sc[2 * i].y),
-                       fmaf(largest(r[i] + 16), sc[2 * i + 1].x, sc[2 * i + 1].y));
+        const float top = fmaxf(fmaf(largest(r), sc[0].x, sc[0].y), fmaf(largest(r + 16), sc[1].x, sc[1].y));
         // The maximum follows when it is behind by more than 2^8, row by row: no row's bits depend on another's.
         const bool behind = top > m + kTcHeadroom;
-        if (kTcParts > 1) tc_fence_before();
+        tc_fence_before();
         const bool renew = pair_any(pair, behind || failed);
-        if (kTcParts > 1) tc_fence_after();
+        tc_fence_after();
         if (renew) {
             constexpr uint32_t kFailed = 0x7fc0dead;  // no score's bits
-            float most = top;
-            if (kTcParts > 1) {
-                shared[2 * row + part] = failed ? __uint_as_float(kFailed) : top;
-                pair_sync(pair);
-                const float2 both = reinterpret_cast<const float2*>(shared)[row];
-                if (__float_as_uint(both.x) == kFailed || __float_as_uint(both.y) == kFailed) return false;
-                most = fmaxf(both.x, both.y);
-            } else if (failed) {
-                return false;
-            }
+            shared[2 * row + part] = failed ? __uint_as_float(kFailed) : top;
+            pair_sync(pair);
+            const float2 both = reinterpret_cast<const float2*>(shared)[row];
+            if (__float_as_uint(both.x) == kFailed || __float_as_uint(both.y) == kFailed) return false;
+            const float most = fmaxf(both.x, both.y);
             const float now = most > m + kTcHeadroom ? most : m, down = now == m ? 1.f : ex2(m - now);
             m = now;
             l *= down;
@@ -429,30 +389,27 @@ struct TcRow {
             }
         }
         const float base = m == -INFINITY ? 0.f : m - kTcWeightBits;
+        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            uint32_t w[16];
+        for (int gg = 0; gg < 2; ++gg) {
+            const float f = sc[gg].x, shift = sc[gg].y - base;
+            const f32x2 f2 = pack2(f, f), shift2 = pack2(shift, shift);
+            f32x2 sum = 0ull;
 #pragma unroll
-            for (int gg = 0; gg < 2; ++gg) {
-                const float f = sc[2 * i + gg].x, shift = sc[2 * i + gg].y - base;
-                const f32x2 f2 = pack2(f, f), shift2 = pack2(shift, shift);
-                f32x2 sum = 0ull;
-#pragma unroll
-                for (int k = 16 * gg; k < 16 * gg + 16; k += 2) {
-                    float p0, p1;
-                    unpack2(fma2_of(pack2(__uint_as_float(r[i][k]), __uint_as_float(r[i][k + 1])), f2, shift2), p0, p1);
-                    p0 = ex2(p0);
-                    p1 = ex2(p1);
-                    sum = add2(sum, pack2(p0, p1));
-                    w[k / 2] = f16_pair(p0, p1);
-                }
-                float s0, s1;
-                unpack2(sum, s0, s1);
-                s0 += s1;
-                if (s0 != 0.f) l = fmaf(s0, inv[2 * i + gg], l);  // unseen keys leave a block's NaN scale alone
+            for (int k = 16 * gg; k < 16 * gg + 16; k += 2) {
+                float p0, p1;
+                unpack2(fma2_of(pack2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), f2, shift2), p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                sum = add2(sum, pack2(p0, p1));
+                w[k / 2] = f16_pair(p0, p1);
             }
-            tc_st_16(dst + 16 * i, w);  // (scores there have been read: by the other part's warp, pair_any)
+            float s0, s1;
+            unpack2(sum, s0, s1);
+            s0 += s1;
+            if (s0 != 0.f) l = fmaf(s0, gg ? x1.z : x0.z, l);  // unseen keys leave a block's NaN scale alone
         }
+        tc_st_16(dst, w);  // (scores there have been read: by the other part's warp, pair_any)
         tmem_wait_st();
         return true;
     }
@@ -507,7 +464,7 @@ struct TcRow {
         const int group = a.sh.group, rows = p.s.n * group, in_tile = t * kTcTile + row;
         const TcRows of(a, p, p.rt * a.sh.rows + in_tile - lane);  // the warp's rows
         const int r0 = of.r0;
-        const float down = 0x1p-6f, sum = (kTcParts == 1 ? both.x : both.x + both.y) * down;
+        const float down = 0x1p-6f, sum = (both.x + both.y) * down;
         const float by = !whole ? down : sum == 0.f ? 0.f : __fdiv_rn(down, sum);
         const int cols = whole ? 32 : 16;  // channels of 64 bytes
 #pragma unroll 1
@@ -555,9 +512,9 @@ template <int D>
 __device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& work, uint8_t* smem, const TcBars& bar,
                                            uint32_t tmem, const WaitCtl& ctl) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = warp / (4 * kTcParts), part = (warp >> 2) % kTcParts, row = (warp & 3) * 32 + lane, pair = 1 + t * 4 + (warp & 3);
+    const int t = warp >> 3, part = warp >> 2 & 1, row = (warp & 3) * 32 + lane, pair = 1 + t * 4 + (warp & 3);
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t s = lanes + t * kTcTile, o = lanes + 2 * kTcTile + t * kTcTile + part * (D / kTcParts);
+    const uint32_t s = lanes + t * kTcTile, o = lanes + 2 * kTcTile + t * kTcTile + part * (D / 2);
     uint8_t* q_tile = smem + t * 2 * Tc<D>::kPiece;
     uint8_t* stage = smem + Tc<D>::kOffStage + warp * 2048;
     float* shared = reinterpret_cast<float*>(smem + Tc<D>::kOffShared) + t * 2 * kTcTile;  // [row][part]
@@ -591,10 +548,10 @@ __device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& 
                 failed = !tc_wait(&bar.s_full[2 * t + h], s_phase, ctl) || failed;
                 tc_fence_after();
                 const float4* scales =
-                    reinterpret_cast<const float4*>(smem + Tc<D>::kOffScales) + 8 * v.stage + 4 * h + 4 / kTcParts * part;
+                    reinterpret_cast<const float4*>(smem + Tc<D>::kOffScales) + 8 * v.stage + 4 * h + 2 * part;
                 const bool ok = mine.step(
                     a, s + h * kTcHalf + 32 * part, s + h * kTcHalf + 16 * part, o, scales,
-                    (walk.at.unit + j) * kTcTile + h * kTcHalf + kTcHalf / kTcParts * part, j + h > 0, failed, row, part, shared, pair,
+                    (walk.at.unit + j) * kTcTile + h * kTcHalf + 32 * part, j + h > 0, failed, row, part, shared, pair,
                     [&] {  // the half before, and with it all others
                         failed = !tc_wait(&bar.pv_done[2 * t + (h ^ 1)], h ? s_phase : s_phase ^ 1u, ctl) || failed;
                         tc_fence_after();
@@ -890,10 +847,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&bar.q_full[t], 4 * kTcParts);
+            mbar_init(&bar.q_full[t], 8);
             for (int h = 0; h < 2; ++h) {
                 mbar_init(&bar.s_full[2 * t + h], 1);
-                mbar_init(&bar.p_full[2 * t + h], 4 * kTcParts);
+                mbar_init(&bar.p_full[2 * t + h], 8);
                 mbar_init(&bar.pv_done[2 * t + h], 1);
             }
             mbar_init(&bar.teardown[t], 1);
@@ -970,7 +927,7 @@ int kv_tc_ctas() { return num_sms(); }
 cudaError_t launch_kv_attend(KvAttendArgs a, cudaStream_t st, bool pdl) {
     a.sh.rows = kKvRows;
     a.sh.tokens = kTcTile;
-    a.sh.extra = KV_EXTRA;
+    a.sh.extra = kTcExtra;
     const cudaError_t e = a.c.dim == 64 ? launch_tc<64>(a, st, pdl) : launch_tc<128>(a, st, pdl);
     return e != cudaSuccess ? e : launch_kv_join(a, st, pdl);
 }
