@@ -53,7 +53,7 @@ struct KvAttendArgs {
     float2* part_ml;    // [slots][rows]
 };
 // Row tiles of 16 rows on warp-level MMAs: few rows a sequence and key head.
-constexpr int kKvFewRows = 16, kKvFewTokens = 64, kKvFewWarps = 4;
+constexpr int kKvFewRows = 16, kKvFewTokens = 128, kKvFewWarps = 4;
 int kv_few_ctas();      // CTAs of its grid, at most
 cudaError_t launch_kv_attend_few(KvAttendArgs a, cudaStream_t st, bool pdl);
 

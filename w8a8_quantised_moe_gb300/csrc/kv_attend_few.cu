@@ -36,8 +36,9 @@ namespace moe {
 namespace {
 
 constexpr int kFewThreads = 32 * kKvFewWarps;
-constexpr int kFewKeys = 16;      // keys of a warp's step
-constexpr int kFewStages = 4;     // steps whose copies are under way or in use
+constexpr int kFewKeys = 16;      // keys of a copy: they lie in one page
+constexpr int kFewStep = 2;       // copies of a warp's step
+constexpr int kFewStages = 6;     // copies under way or in use
 constexpr int kFewLeast = 2;      // units of a CTA, at least (where there are that many)
 constexpr float kHeadroom = 8.f;  // the maximum may lag behind by this much (base 2)
 constexpr float kWeightBits = 6.f;  // weights are 2^6 at the maximum
@@ -61,10 +62,10 @@ struct Few {
     static constexpr int kHalf = kFewKeys * D;                // bytes of a step's keys (or values)
     static constexpr int kStage = 2 * kHalf + 16;             // and the two scales
     static constexpr int kRing = kFewStages * kStage;         // a warp's
-    static constexpr int kOffO = kKvFewWarps * kRing;         // [warps][16][D] binary32
-    static constexpr int kOffMl = kOffO + kKvFewWarps * 16 * D * 4;  // [warps][16] maxima, sums
+    static constexpr int kOffO = kKvFewWarps * kRing;         // [16][D] binary32
+    static constexpr int kOffMl = kOffO + 16 * D * 4;         // [warps][16] maxima, sums
     static constexpr int kOffWork = kOffMl + kKvFewWarps * 16 * 8;
-    static constexpr int kSmem = kOffWork + (int)sizeof(KvWork) + 8 * kKvFewWarps + 16;
+    static constexpr int kSmem = kOffWork + (int)sizeof(KvWork);
     static_assert(kOffWork % 16 == 0 && kStage % 16 == 0, "alignment");
     __device__ static __forceinline__ int place(int row, int chunk) {
         return row * D + ((D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3)) << 4);
@@ -76,40 +77,44 @@ struct Few {
     }
 };
 
-// The steps of a CTA's run, as one warp copies them: the page of the next one is
-// looked up a step ahead.
+// The steps of a CTA's run, as one warp copies them, 16 keys at a time: the page of the
+// next copy is looked up a copy ahead.
 template <int D>
 struct FewCopies {
     KvPlace at;
-    int64_t left;
-    int id;
-    __device__ __forceinline__ int key0() const { return at.unit * kKvFewTokens + (int)(threadIdx.x >> 5) * kFewKeys; }
+    int64_t left;  // copies
+    int id, half;
+    __device__ __forceinline__ int key0() const {
+        return at.unit * kKvFewTokens + ((int)(threadIdx.x >> 5) * kFewStep + half) * kFewKeys;
+    }
     __device__ __forceinline__ void look_up(const KvAttendArgs& a) {
         const int k0 = key0();
         id = k0 < at.s.len ? __ldg(a.bt.page_table + at.b * a.bt.table_stride + (k0 >> a.c.page_bits)) : -1;
     }
     __device__ __forceinline__ void start(const KvAttendArgs& a, const KvWork& w) {
         at = w.at;
-        left = w.u1 - w.u0;
+        left = (w.u1 - w.u0) * kFewStep;
+        half = 0;
         if (left > 0) look_up(a);
     }
-    // Copies the step's keys, values and scales to `stage`; what is not there
+    // Copies 16 keys, their values and the two scales to `stage`; what is not there
     // (behind the sequence, another's page) becomes 0, its scales too.
     __device__ __forceinline__ void issue(const KvAttendArgs& a, uint8_t* stage) {
         if (left > 0) {
-            const int lane = threadIdx.x & 31, k0 = key0();
-            const bool there = k0 < at.s.len && kv_page_ok(a.c, id, a.error);
-            const int in_page = k0 & (a.c.page - 1);
-            const size_t off = there ? id * a.c.page_stride + ((size_t)at.head * a.c.page + in_page) * D : 0;
+            const int lane = threadIdx.x & 31, k0 = key0(), there_are = at.s.len - k0;
+            const bool there = there_are > 0 && kv_page_ok(a.c, id, a.error);
             constexpr int kPer = 32 / Few<D>::kChunks;  // rows of an instruction
-            const int c = lane % Few<D>::kChunks;
+            const int c = lane % Few<D>::kChunks, row = lane / Few<D>::kChunks;
+            const int64_t off =
+                there ? id * a.c.page_stride + (((int64_t)at.head << a.c.page_bits) + (k0 & (a.c.page - 1)) + row) * D + c * 16
+                      : 0;
+            const uint8_t *k = a.c.k + off, *v = a.c.v + off;
 #pragma unroll
             for (int i = 0; i < kFewKeys / kPer; ++i) {
-                const int r = i * kPer + lane / Few<D>::kChunks;
-                const bool valid = there && k0 + r < at.s.len;
-                const size_t o = valid ? off + r * D + c * 16 : 0;
-                cp_async16_zfill(stage + Few<D>::place(r, c), a.c.k + o, valid);
-                cp_async16_zfill(stage + Few<D>::kHalf + Few<D>::place(r, c), a.c.v + o, valid);
+                const bool valid = there && i * kPer + row < there_are;
+                uint8_t* dst = stage + Few<D>::place(i * kPer + row, c);
+                cp_async16_zfill(dst, k + (valid ? i * kPer * D : 0), valid);
+                cp_async16_zfill(dst + Few<D>::kHalf, v + (valid ? i * kPer * D : 0), valid);
             }
             if (lane < 2) {
                 const float* s = (lane == 0 ? a.c.k_scale : a.c.v_scale) + (there ? id * a.c.scale_stride + at.head : 0);
@@ -119,7 +124,10 @@ struct FewCopies {
                              : "memory");
             }
             if (--left > 0) {
-                kv_next(at, a.bt, a.sh, a.c.heads);
+                if (++half == kFewStep) {
+                    half = 0;
+                    kv_next(at, a.bt, a.sh, a.c.heads);
+                }
                 look_up(a);
             }
         }
@@ -180,51 +188,69 @@ struct FewRows {
             for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     }
 
-    // One step: 16 keys from k0 on, at `stage`.
-    __device__ __forceinline__ void step(const KvAttendArgs& a, const uint8_t* stage, int k0) {
+    // One step: 32 keys from k0 on, 16 at each of stage[0] and stage[1].
+    __device__ __forceinline__ void step(const KvAttendArgs& a, const uint8_t* const (&stage)[kFewStep], int k0) {
+        constexpr int J = 2 * kFewStep;  // column tiles of 8 keys
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        float s[2][4];
+        float s[J][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < J; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[j][i] = 0.f;
-            const int row = key_row(j, g);
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                const uint4 k4 = *reinterpret_cast<const uint4*>(stage + Few<D>::place(row, 4 * c + t));
-                const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
+        for (int c = 0; c < D / 64; ++c) {
+            uint4 k4[J];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mma16816(s[j], q[4 * c + i], e4m3x2_to_f16x2(w[i]), e4m3x2_to_f16x2_hi(w[i]));
-            }
+            for (int j = 0; j < J; ++j)
+                k4[j] = *reinterpret_cast<const uint4*>(stage[j >> 1] + Few<D>::place(key_row(j & 1, g), 4 * c + t));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < J; ++j) {  // the column tiles' chains side by side
+                    const uint32_t w = i == 0 ? k4[j].x : i == 1 ? k4[j].y : i == 2 ? k4[j].z : k4[j].w;
+                    mma16816(s[j], q[4 * c + i], e4m3x2_to_f16x2(w), e4m3x2_to_f16x2_hi(w));
+                }
         }
-        const float2 sc = *reinterpret_cast<const float2*>(stage + 2 * Few<D>::kHalf);
-        float lg, inv;
-        value_scale(sc.y, lg, inv);
-        const float f[2] = {sc.x * factor[0], sc.x * factor[1]};
+        float inv[kFewStep];
+        bool gone = false;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int h = 0; h < kFewStep; ++h) {
+            const float2 sc = *reinterpret_cast<const float2*>(stage[h] + 2 * Few<D>::kHalf);
+            float lg;
+            value_scale(sc.y, lg, inv[h]);
+            gone = gone || sc.y == 0.f;
+            const float f[2] = {sc.x * factor[0], sc.x * factor[1]};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[j][i] = fmaf(s[j][i], f[i >> 1], lg);
+            for (int j = 2 * h; j < 2 * h + 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[j][i] = fmaf(s[j][i], f[i >> 1], lg);
+        }
         const int window = a.sh.window;
-        if (k0 + kFewKeys - 1 > pos_min || (window > 0 && k0 <= pos_max - window) || sc.y == 0.f) {
+        if (k0 + kFewStep * kFewKeys - 1 > pos_min || (window > 0 && k0 <= pos_max - window) || gone) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < J; ++j) {
+                const bool none = inv[j >> 1] == 0.f;  // a block that is not there
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int key = k0 + key_row(j, 2 * t + (i & 1)), p = pos[i >> 1];
-                    if (key > p || (window > 0 && key <= p - window) || sc.y == 0.f) s[j][i] = -INFINITY;
+                    const int key = k0 + (j >> 1) * kFewKeys + key_row(j & 1, 2 * t + (i & 1)), p = pos[i >> 1];
+                    if (key > p || (window > 0 && key <= p - window) || none) s[j][i] = -INFINITY;
                 }
+            }
         }
         float top[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            top[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+        for (int h = 0; h < 2; ++h) {
+            top[h] = fmaxf(s[0][2 * h], s[0][2 * h + 1]);
+#pragma unroll
+            for (int j = 1; j < J; ++j) top[h] = fmaxf(top[h], fmaxf(s[j][2 * h], s[j][2 * h + 1]));
+        }
         if (__any_sync(0xffffffffu, top[0] > m[0] + kHeadroom || top[1] > m[1] + kHeadroom)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float v = fmaxf(top[h], m[h]);
                 v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
                 v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                v = v > m[h] + kHeadroom ? v : m[h];  // row by row: no row's bits depend on another's
                 const float down = m[h] == v ? 1.f : ex2(m[h] - v);
                 m[h] = v;
                 l[h] *= down;
@@ -235,41 +261,47 @@ struct FewRows {
                 }
             }
         }
-        uint32_t p[4];
+        uint32_t p[kFewStep][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const float base = m[h] == -INFINITY ? 0.f : m[h] - kWeightBits;
-            float w[4], sum = 0.f;
+#pragma unroll
+            for (int b = 0; b < kFewStep; ++b) {
+                float w[4], sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[i] = ex2(s[2 * b + (i >> 1)][2 * h + (i & 1)] - base);
+                    sum += w[i];
+                }
+                if (sum != 0.f) l[h] = fmaf(sum, inv[b], l[h]);  // unseen keys leave a block's NaN scale alone
+                p[b][h] = f16_pair(w[0], w[1]);
+                p[b][2 + h] = f16_pair(w[2], w[3]);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < kFewStep; ++b) {
+            const uint8_t* values = stage[b] + Few<D>::kHalf;
+            uint32_t v[4][kTiles / 4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                w[i] = ex2(s[i >> 1][2 * h + (i & 1)] - base);
-                sum += w[i];
+                const int row = key_row(i >> 1, 2 * t + (i & 1));
+                if (D == 128) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(values + Few<D>::place(row, g));
+                    v[i][0] = x.x, v[i][1] = x.y, v[i][2 % (kTiles / 4)] = x.z, v[i][3 % (kTiles / 4)] = x.w;
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2*>(values + Few<D>::place(row, g >> 1) + (g & 1) * 8);
+                    v[i][0] = x.x, v[i][1] = x.y;
+                }
             }
-            if (sum != 0.f) l[h] = fmaf(sum, inv, l[h]);  // unseen keys leave a block's NaN scale alone
-            p[h] = f16_pair(w[0], w[1]);
-            p[2 + h] = f16_pair(w[2], w[3]);
-        }
-        const uint8_t* values = stage + Few<D>::kHalf;
-        uint32_t v[4][kTiles / 4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = key_row(i >> 1, 2 * t + (i & 1));
-            if (D == 128) {
-                const uint4 x = *reinterpret_cast<const uint4*>(values + Few<D>::place(row, g));
-                v[i][0] = x.x, v[i][1] = x.y, v[i][2 % (kTiles / 4)] = x.z, v[i][3 % (kTiles / 4)] = x.w;
-            } else {
-                const uint2 x = *reinterpret_cast<const uint2*>(values + Few<D>::place(row, g >> 1) + (g & 1) * 8);
-                v[i][0] = x.x, v[i][1] = x.y;
+            for (int w = 0; w < kTiles / 4; ++w) {
+                const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140), a1 = __byte_perm(v[0][w], v[1][w], 0x7362);
+                const uint32_t b0 = __byte_perm(v[2][w], v[3][w], 0x5140), b1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+                mma16816(o[4 * w], p[b], e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(b0));
+                mma16816(o[4 * w + 1], p[b], e4m3x2_to_f16x2_hi(a0), e4m3x2_to_f16x2_hi(b0));
+                mma16816(o[4 * w + 2], p[b], e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(b1));
+                mma16816(o[4 * w + 3], p[b], e4m3x2_to_f16x2_hi(a1), e4m3x2_to_f16x2_hi(b1));
             }
-        }
-#pragma unroll
-        for (int w = 0; w < kTiles / 4; ++w) {
-            const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140), a1 = __byte_perm(v[0][w], v[1][w], 0x7362);
-            const uint32_t b0 = __byte_perm(v[2][w], v[3][w], 0x5140), b1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-            mma16816(o[4 * w], p, e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(b0));
-            mma16816(o[4 * w + 1], p, e4m3x2_to_f16x2_hi(a0), e4m3x2_to_f16x2_hi(b0));
-            mma16816(o[4 * w + 2], p, e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(b1));
-            mma16816(o[4 * w + 3], p, e4m3x2_to_f16x2_hi(a1), e4m3x2_to_f16x2_hi(b1));
         }
     }
 };
@@ -300,26 +332,29 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv_attend_few_kernel(const KvA
     FewCopies<D> copies;
     copies.start(a, *work);
 #pragma unroll
-    for (int i = 0; i < kFewStages - 1; ++i) copies.issue(a, ring + i * F::kStage);
+    for (int i = 0; i < kFewStages - kFewStep; ++i) copies.issue(a, ring + i * F::kStage);
     KvPlace at = work->at;
     FewRows<D> rows;
     rows.start(a, at);
     bool first_segment = true;
-    int stage = 0;
+    int stage = 0;  // of the step, and of the copies asked for next
+    auto next_stage = [](int st) { return st + kFewStep == kFewStages ? 0 : st + kFewStep; };
+    int ahead = kFewStages - kFewStep;
     for (int64_t u = 0; u < units; ++u) {
-        int ahead = stage + kFewStages - 1;
-        if (ahead >= kFewStages) ahead -= kFewStages;
-        copies.issue(a, ring + ahead * F::kStage);
-        cp_async_wait<kFewStages - 1>();
+#pragma unroll
+        for (int i = 0; i < kFewStep; ++i) copies.issue(a, ring + (ahead + i) * F::kStage);
+        ahead = next_stage(ahead);
+        cp_async_wait<kFewStages - kFewStep>();
         __syncwarp();
-        rows.step(a, ring + stage * F::kStage, at.unit * kKvFewTokens + warp * kFewKeys);
-        __syncwarp();  // the stage may be written again
-        if (++stage == kFewStages) stage = 0;
+        const uint8_t* const in[kFewStep] = {ring + stage * F::kStage, ring + (stage + 1) * F::kStage};
+        rows.step(a, in, at.unit * kKvFewTokens + warp * kFewStep * kFewKeys);
+        __syncwarp();  // the stages may be written again
+        stage = next_stage(stage);
         if (at.unit + 1 == at.end || u + 1 == units) {
             // the end of the row tile, or of the CTA's run in it: the warps' sums together
             const KvParts parts = kv_parts(*work, at, first_segment);
             const int g = lane >> 2, t = lane & 3;
-            float* o_w = reinterpret_cast<float*>(smem + F::kOffO + warp * 16 * D * 4);
+            uint8_t* sums = smem + F::kOffO;
             __syncthreads();  // the previous row tile's have been read
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -330,27 +365,48 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv_attend_few_kernel(const KvA
                     ml[warp * 16 + g + 8 * h] = rows.m[h];
                     ml[kKvFewWarps * 16 + warp * 16 + g + 8 * h] = l;
                 }
-                // lane's channels D/4 t .. : tile i's two columns are D/8 apart
-#pragma unroll
-                for (int col = 0; col < 2; ++col)
-#pragma unroll
-                    for (int i = 0; i < D / 8; i += 4)
-                        *reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(o_w) +
-                                                   F::place_o(g + 8 * h, (D / 4 * t + D / 8 * col + i) / 4)) =
-                            make_float4(rows.o[i][2 * h + col], rows.o[i + 1][2 * h + col], rows.o[i + 2][2 * h + col],
-                                        rows.o[i + 3][2 * h + col]);
             }
             __syncthreads();
+            float f[2];  // what brings this warp's sums to the largest maximum
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float m = ml[g + 8 * h];
+#pragma unroll
+                for (int w = 1; w < kKvFewWarps; ++w) m = fmaxf(m, ml[w * 16 + g + 8 * h]);
+                f[h] = rows.m[h] == m ? 1.f : ex2(rows.m[h] - m);
+            }
+            // one warp after the other, so that one row tile's room is enough
+#pragma unroll 1
+            for (int w = 0; w < kKvFewWarps; ++w) {
+                if (w == warp) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        // lane's channels D/4 t ..: tile i's two columns are D/8 apart
+#pragma unroll
+                        for (int col = 0; col < 2; ++col)
+#pragma unroll
+                            for (int i = 0; i < D / 8; i += 4) {
+                                float4* at4 = reinterpret_cast<float4*>(
+                                    sums + F::place_o(g + 8 * h, (D / 4 * t + D / 8 * col + i) / 4));
+                                float4 x = w == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *at4;
+                                x.x = fmaf(f[h], rows.o[i][2 * h + col], x.x);
+                                x.y = fmaf(f[h], rows.o[i + 1][2 * h + col], x.y);
+                                x.z = fmaf(f[h], rows.o[i + 2][2 * h + col], x.z);
+                                x.w = fmaf(f[h], rows.o[i + 3][2 * h + col], x.w);
+                                *at4 = x;
+                            }
+                }
+                __syncthreads();
+            }
             // 8 threads a row
             const int row = threadIdx.x >> 3, all = at.s.n * a.sh.group, r = at.rt * kKvFewRows + row;
-            float m = ml[row], f[kKvFewWarps], l = 0.f;
+            float m = ml[row], l = 0.f;
 #pragma unroll
             for (int w = 1; w < kKvFewWarps; ++w) m = fmaxf(m, ml[w * 16 + row]);
 #pragma unroll
             for (int w = 0; w < kKvFewWarps; ++w) {
                 const float mw = ml[w * 16 + row];
-                f[w] = mw == m ? 1.f : ex2(mw - m);
-                l = fmaf(f[w], ml[kKvFewWarps * 16 + w * 16 + row], l);
+                l = fmaf(mw == m ? 1.f : ex2(mw - m), ml[kKvFewWarps * 16 + w * 16 + row], l);
             }
             // undo the weights' 2^6 (a row that has seen nothing has m = -inf, l = 0)
             const float down = 0x1p-6f;
@@ -361,15 +417,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv_attend_few_kernel(const KvA
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     const int c = i * 8 + (threadIdx.x & 7);
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int w = 0; w < kKvFewWarps; ++w) {
-                        const float4 x = *reinterpret_cast<const float4*>(smem + F::kOffO + w * 16 * D * 4 + F::place_o(row, c));
-                        o.x = fmaf(f[w], x.x, o.x);
-                        o.y = fmaf(f[w], x.y, o.y);
-                        o.z = fmaf(f[w], x.z, o.z);
-                        o.w = fmaf(f[w], x.w, o.w);
-                    }
+                    float4 o = *reinterpret_cast<const float4*>(sums + F::place_o(row, c));
                     o = make_float4(o.x * down, o.y * down, o.z * down, o.w * down);
                     if (parts.parts == 1)
                         write_out4(a, out_row, D, c * 4, o, m, l);
@@ -410,28 +458,34 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttendArgs a, int 
         const int2 info = a.info[r0];
         const int parts = info.y >> 8, row = info.y & 255, c0 = info.x >> 1;
         if (parts <= 1) continue;
+        auto slot = [&](int i) { return (size_t)(i == 0 ? info.x : 2 * (c0 + i)) * a.sh.rows + row; };
         float m = -INFINITY, l = 0.f;
-        for (int i = lane; i < parts; i += 32) {
-            const int slot = i == 0 ? info.x : 2 * (c0 + i);
-            m = fmaxf(m, a.part_ml[(size_t)slot * a.sh.rows + row].x);
-        }
+        for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.part_ml[slot(i)].x);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = 0; i < parts; ++i) {
-            const size_t slot = (size_t)(i == 0 ? info.x : 2 * (c0 + i)) * a.sh.rows + row;
-            const float2 x = a.part_ml[slot];
-            const float f = x.x == m ? 1.f : ex2(x.x - m);
-            l = fmaf(f, x.y, l);
-            if (lane * 4 < D) {
-                const float4 v = *reinterpret_cast<const float4*>(a.part_o + slot * D + lane * 4);
-                o.x = fmaf(f, v.x, o.x);
-                o.y = fmaf(f, v.y, o.y);
-                o.z = fmaf(f, v.z, o.z);
-                o.w = fmaf(f, v.w, o.w);
+        for (int i0 = 0; i0 < parts; i0 += 32) {  // a lane a part's maximum and sum, then the parts' rows
+            const int some = kv_min(32, parts - i0);
+            float f = 0.f;
+            if (lane < some) {
+                const float2 x = a.part_ml[slot(i0 + lane)];
+                f = x.x == m ? 1.f : ex2(x.x - m);
+                l = fmaf(f, x.y, l);
+            }
+#pragma unroll 8
+            for (int i = 0; i < some; ++i) {
+                const float fi = __shfl_sync(0xffffffffu, f, i);
+                if (lane * 4 < D) {
+                    const float4 v = *reinterpret_cast<const float4*>(a.part_o + slot(i0 + i) * D + lane * 4);
+                    o.x = fmaf(fi, v.x, o.x);
+                    o.y = fmaf(fi, v.y, o.y);
+                    o.z = fmaf(fi, v.z, o.z);
+                    o.w = fmaf(fi, v.w, o.w);
+                }
             }
         }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
         if (lane * 4 < D) write_out4(a, r0, D, lane * 4, o, m, l);
     }
 }
