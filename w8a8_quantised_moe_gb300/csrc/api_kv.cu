@@ -56,7 +56,7 @@ bool many_rows(int64_t B, int64_t T, int64_t group) { return T * group > kManyRo
 AttendLayout attend_layout(int64_t T, int64_t Hq, int64_t Hkv, int64_t D) {
     AttendLayout L{};
     // room for the form with many rows where a batch of up to T tokens can take it
-    const int64_t few = 2 * (int64_t)kv_few_ctas() * kKvFewRows, many = 2 * (int64_t)kv_tc_ctas() * kKvRows;
+    const int64_t few = kv_few_part_rows(), many = 2 * (int64_t)kv_tc_ctas() * kKvRows;
     const int64_t part_rows = many_rows(1, T, Hq / Hkv) && many > few ? many : few;
     L.info = 256;
     L.part_ml = L.info + align256((size_t)T * Hq * 8);

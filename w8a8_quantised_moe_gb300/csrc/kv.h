@@ -52,9 +52,9 @@ struct KvAttendArgs {
     float* part_o;      // [slots][rows][dim]
     float2* part_ml;    // [slots][rows]
 };
-// Row tiles of 16 rows on warp-level MMAs: few rows a sequence and key head.
-constexpr int kKvFewRows = 16, kKvFewTokens = 128, kKvFewWarps = 4;
-int kv_few_ctas();      // CTAs of its grid, at most
+// Row tiles of 8 or 16 rows on warp-level MMAs: few rows a sequence and key head.
+constexpr int kKvFewTokens = 128, kKvFewWarps = 4;
+int64_t kv_few_part_rows();
 cudaError_t launch_kv_attend_few(KvAttendArgs a, cudaStream_t st, bool pdl);
 
 // Row tiles of 256 rows on tcgen05 (kv_attend.cu): many rows.

@@ -8,22 +8,27 @@
 // is taken up by the weight's exponent, so that the products see the codes alone; the
 // denominator divides it out again (exactly where it is a power of two).
 //
-// Bound by HBM: every cached byte is used by at most 16 rows.  A warp has 16 keys at
-// a time and all their channels: m16n8k16 MMAs with fp16 operands, rows = the queries
-// (head, token) of one key head.  E4M3 is exact in fp16; a query row is scaled by a
-// power of two to 2^8 <= max < 2^9, so that fp16 holds its bf16 values exactly but for
-// those 2^25 times smaller than the largest; weights are rounded to fp16 (11 bits, with
-// 6 bits of headroom below and 8 above the maximum that is corrected lazily).  Warp-level
-// MMAs rather than tcgen05: 16 rows of a 128-row tile are all that a decode step has,
-// and the codes can go from their registers into the operands without a detour through
-// shared memory as fp16.
+// Bound by HBM: every cached byte is used by a few rows only.  A warp has 32 keys at a
+// time and all their channels, in m16n8k16 MMAs with fp16 operands whose M are the keys
+// and then the values' channels, N the rows (head, token) of one key head:
+//   S^T = K Q^T,  O^T += V^T P^T
+// so that 8 rows fill an MMA, the codes are converted once for all rows, and a row costs
+// no more registers than it has to.  (Rows as M: 16 of them, three quarters empty where 4
+// heads share a key head, with twice the MMAs, exponentials and registers.)  P^T is S^T's
+// 8 x 8 blocks transposed, one movmatrix each.
+// E4M3 is exact in fp16; a query row is scaled by a power of two to 2^8 <= max < 2^9, so
+// that fp16 holds its bf16 values exactly but for those 2^25 times smaller than the largest;
+// weights are rounded to fp16 (11 bits, with 6 bits of headroom below and 8 above the maximum
+// that is corrected lazily).  Warp-level MMAs rather than tcgen05: a decode step has a few
+// rows of a 128-row tile, and the codes can go from their registers into the operands
+// without a detour through shared memory as fp16.
 //
 // The order of channels inside a product, and of keys, is free; it is chosen so that a
-// lane reads 16 bytes of a row at a time, for keys (its B operand: 4 channels of one
-// key per word) and values (4 channels of 4 keys, paired by byte permutes), without
-// bank conflicts: place(row, chunk) = chunk ^ (row & 7), lane's keys as in key_row().
+// lane reads 16 bytes of a row at a time, for keys (4 channels of one key per word) and
+// values (4 channels of 4 keys, paired by byte permutes), without bank conflicts:
+// place(row, chunk) = chunk ^ (row & 7), lane's keys as in key_row().
 //
-// Work: the batch's units of 64 keys (16 a warp) are dealt to the CTAs in equal runs,
+// Work: the batch's units of 128 keys (32 a warp) are dealt to the CTAs in equal runs,
 // whatever the lengths of the sequences (kv_plan.h); a run that starts or ends inside
 // a row tile leaves its part in the workspace, and kv_join_kernel adds the parts in
 // their order.  Copies run ahead over the borders of row tiles.
@@ -38,7 +43,7 @@ namespace {
 constexpr int kFewThreads = 32 * kKvFewWarps;
 constexpr int kFewKeys = 16;      // keys of a copy: they lie in one page
 constexpr int kFewStep = 2;       // copies of a warp's step
-constexpr int kFewStages = 6;     // copies under way or in use
+constexpr int kFewStages = 4;     // copies under way or in use
 constexpr int kFewLeast = 2;      // units of a CTA, at least (where there are that many)
 constexpr float kHeadroom = 8.f;  // the maximum may lag behind by this much (base 2)
 constexpr float kWeightBits = 6.f;  // weights are 2^6 at the maximum
@@ -49,6 +54,13 @@ __device__ __forceinline__ int key_row(int j, int n) {
     return 8 * j + (((t >> 1) ^ b) << 2 | (t & 1) << 1 | b);
 }
 
+// The 8 x 8 block of fp16 whose row lane / 4 this lane has two elements of, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -56,24 +68,22 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D>
+// D channels, NR n-tiles of 8 rows.
+template <int D, int NR>
 struct Few {
+    static constexpr int kRows = 8 * NR;                      // of a row tile
     static constexpr int kChunks = D / 16;                    // 16-byte pieces of a row
-    static constexpr int kHalf = kFewKeys * D;                // bytes of a step's keys (or values)
+    static constexpr int kHalf = kFewKeys * D;                // bytes of a copy's keys (or values)
     static constexpr int kStage = 2 * kHalf + 16;             // and the two scales
     static constexpr int kRing = kFewStages * kStage;         // a warp's
-    static constexpr int kOffO = kKvFewWarps * kRing;         // [16][D] binary32
-    static constexpr int kOffMl = kOffO + 16 * D * 4;         // [warps][16] maxima, sums
-    static constexpr int kOffWork = kOffMl + kKvFewWarps * 16 * 8;
+    static constexpr int kOffO = kKvFewWarps * kRing;         // [rows][D] binary32
+    static constexpr int kOffMl = kOffO + kRows * D * 4;      // [warps][rows] maxima, then sums
+    static constexpr int kOffWork = kOffMl + kKvFewWarps * kRows * 8;
     static constexpr int kSmem = kOffWork + (int)sizeof(KvWork);
-    static_assert(kOffWork % 16 == 0 && kStage % 16 == 0, "alignment");
+    static constexpr int kCtas = NR == 1 ? 3 : 2;             // on an SM
+    static_assert(kOffWork % 16 == 0 && kStage % 16 == 0 && kCtas * (kSmem + 1024) <= 233472, "shared memory");
     __device__ static __forceinline__ int place(int row, int chunk) {
         return row * D + ((D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3)) << 4);
-    }
-    // 16-byte piece of a binary32 row of sums
-    __device__ static __forceinline__ int place_o(int row, int c) {
-        const int f = D == 128 ? ((c >> 3) << 1) | (row & 1) : (c >> 3) | (row & 1) << 1;
-        return row * D * 4 + ((c ^ f) << 4);
     }
 };
 
@@ -81,6 +91,7 @@ struct Few {
 // next copy is looked up a copy ahead.
 template <int D>
 struct FewCopies {
+    using F = Few<D, 1>;  // (a copy is the same for any rows)
     KvPlace at;
     int64_t left;  // copies
     int id, half;
@@ -103,23 +114,32 @@ struct FewCopies {
         if (left > 0) {
             const int lane = threadIdx.x & 31, k0 = key0(), there_are = at.s.len - k0;
             const bool there = there_are > 0 && kv_page_ok(a.c, id, a.error);
-            constexpr int kPer = 32 / Few<D>::kChunks;  // rows of an instruction
-            const int c = lane % Few<D>::kChunks, row = lane / Few<D>::kChunks;
+            constexpr int kPer = 32 / F::kChunks;  // rows of an instruction
+            const int c = lane % F::kChunks, row = lane / F::kChunks;
             const int64_t off =
                 there ? id * a.c.page_stride + (((int64_t)at.head << a.c.page_bits) + (k0 & (a.c.page - 1)) + row) * D + c * 16
                       : 0;
             const uint8_t *k = a.c.k + off, *v = a.c.v + off;
+            if (there && there_are >= kFewKeys) {
 #pragma unroll
-            for (int i = 0; i < kFewKeys / kPer; ++i) {
-                const bool valid = there && i * kPer + row < there_are;
-                uint8_t* dst = stage + Few<D>::place(i * kPer + row, c);
-                cp_async16_zfill(dst, k + (valid ? i * kPer * D : 0), valid);
-                cp_async16_zfill(dst + Few<D>::kHalf, v + (valid ? i * kPer * D : 0), valid);
+                for (int i = 0; i < kFewKeys / kPer; ++i) {
+                    uint8_t* dst = stage + F::place(i * kPer + row, c);
+                    cp_async16(dst, k + i * kPer * D);
+                    cp_async16(dst + F::kHalf, v + i * kPer * D);
+                }
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < kFewKeys / kPer; ++i) {
+                    const bool valid = there && i * kPer + row < there_are;
+                    uint8_t* dst = stage + F::place(i * kPer + row, c);
+                    cp_async16_zfill(dst, k + (valid ? i * kPer * D : 0), valid);
+                    cp_async16_zfill(dst + F::kHalf, v + (valid ? i * kPer * D : 0), valid);
+                }
             }
             if (lane < 2) {
                 const float* s = (lane == 0 ? a.c.k_scale : a.c.v_scale) + (there ? id * a.c.scale_stride + at.head : 0);
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(static_cast<uint32_t>(
-                                 __cvta_generic_to_shared(stage + 2 * Few<D>::kHalf + 4 * lane))),
+                                 __cvta_generic_to_shared(stage + 2 * F::kHalf + 4 * lane))),
                              "l"(s), "r"(there ? 4 : 0)
                              : "memory");
             }
@@ -135,28 +155,29 @@ struct FewCopies {
     }
 };
 
-// A warp's part of a row tile: lane (g, t) = (lane / 4, lane % 4) has rows g and g + 8.
-template <int D>
+// A warp's part of a row tile: lane (g, t) = (lane / 4, lane % 4) has, of every n-tile, the
+// rows 2 t and 2 t + 1 (index h) and of their sums the channels [D/8 g, D/8 g + D/8).
+template <int D, int NR>
 struct FewRows {
-    static constexpr int kSteps = D / 16, kTiles = D / 8;
-    uint32_t q[kSteps][4];
-    float o[kTiles][4], m[2], l[2], factor[2];
-    int pos[2], pos_min, pos_max;
+    using F = Few<D, NR>;
+    static constexpr int kSteps = D / 16, kTiles = D / 16;
+    uint32_t q[NR][kSteps][2];
+    float o[NR][kTiles][4], m[NR][2], l[NR][2], factor[NR][2];
+    int pos[NR][2], pos_min, pos_max;
 
     // Query rows of the row tile to fp16, the sums to 0.
     __device__ __forceinline__ void start(const KvAttendArgs& a, const KvPlace& p) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        const int rows = p.s.n * a.sh.group, r0 = p.rt * kKvFewRows;
-        const int last = kv_min(r0 + kKvFewRows, rows) - 1;
+        const int rows = p.s.n * a.sh.group, r0 = p.rt * F::kRows;
+        const int last = kv_min(r0 + F::kRows, rows) - 1;
         pos_min = p.s.len - p.s.n + r0 / a.sh.group;
         pos_max = p.s.len - p.s.n + last / a.sh.group;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = kv_min(r0 + g + 8 * h, last);  // rows behind the last repeat it
-            const int tok = r / a.sh.group;
-            pos[h] = p.s.len - p.s.n + tok;
+        for (int n = 0; n < NR; ++n) {
+            const int r = kv_min(r0 + 8 * n + g, last);  // rows behind the last repeat it
+            const int tok = r / a.sh.group, at = p.s.len - p.s.n + tok;
             const uint16_t* row =
-                a.q + (int64_t)(p.s.q0 + tok) * a.q_stride + (p.head * a.sh.group + r % a.sh.group) * D;
+                a.q + (int64_t)(p.s.q0 + tok) * a.q_stride + (p.head * a.sh.group + r - tok * a.sh.group) * D;
             uint2 w[kSteps];
             uint32_t top = 0;
 #pragma unroll
@@ -173,135 +194,158 @@ struct FewRows {
             if (top >= 0x7f80u) e = 0;
             if (e < -120) e = -120;
             const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-            factor[h] = __fmul_rn(__fmul_rn(a.scale, kLog2e), __uint_as_float((uint32_t)(127 + e) << 23));
+            const float f = __fmul_rn(__fmul_rn(a.scale, kLog2e), __uint_as_float((uint32_t)(127 + e) << 23));
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
-                q[s][h] = f16_pair(bf16_lo(w[s].x) * down, bf16_hi(w[s].x) * down);
-                q[s][2 + h] = f16_pair(bf16_lo(w[s].y) * down, bf16_hi(w[s].y) * down);
+                q[n][s][0] = f16_pair(bf16_lo(w[s].x) * down, bf16_hi(w[s].x) * down);
+                q[n][s][1] = f16_pair(bf16_lo(w[s].y) * down, bf16_hi(w[s].y) * down);
             }
-            m[h] = -INFINITY;
-            l[h] = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // row 2 t + h is lane group 2 t + h's
+                factor[n][h] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + h));
+                pos[n][h] = __shfl_sync(0xffffffffu, at, 4 * (2 * t + h));
+                m[n][h] = -INFINITY;
+                l[n][h] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
         }
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     }
 
     // One step: 32 keys from k0 on, 16 at each of stage[0] and stage[1].
     __device__ __forceinline__ void step(const KvAttendArgs& a, const uint8_t* const (&stage)[kFewStep], int k0) {
-        constexpr int J = 2 * kFewStep;  // column tiles of 8 keys
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        float s[J][4];
+        // scores [16 keys][n-tile]: of the keys key_row(0, g) (elements 0, 1) and key_row(1, g) (2, 3)
+        // with the rows 2 t, 2 t + 1
+        float s[kFewStep][NR][4];
 #pragma unroll
-        for (int j = 0; j < J; ++j)
+        for (int b = 0; b < kFewStep; ++b)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[j][i] = 0.f;
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[b][n][i] = 0.f;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-            uint4 k4[J];
+            uint4 k4[kFewStep][2];
 #pragma unroll
-            for (int j = 0; j < J; ++j)
-                k4[j] = *reinterpret_cast<const uint4*>(stage[j >> 1] + Few<D>::place(key_row(j & 1, g), 4 * c + t));
+            for (int b = 0; b < kFewStep; ++b)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    k4[b][j] = *reinterpret_cast<const uint4*>(stage[b] + F::place(key_row(j, g), 4 * c + t));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < J; ++j) {  // the column tiles' chains side by side
-                    const uint32_t w = i == 0 ? k4[j].x : i == 1 ? k4[j].y : i == 2 ? k4[j].z : k4[j].w;
-                    mma16816(s[j], q[4 * c + i], e4m3x2_to_f16x2(w), e4m3x2_to_f16x2_hi(w));
+                for (int b = 0; b < kFewStep; ++b) {  // the chains of sums side by side
+                    auto word = [&](const uint4& v) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
+                    const uint32_t x = word(k4[b][0]), y = word(k4[b][1]);
+                    const uint32_t key[4] = {e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y), e4m3x2_to_f16x2_hi(x),
+                                             e4m3x2_to_f16x2_hi(y)};
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) mma16816(s[b][n], key, q[n][4 * c + i][0], q[n][4 * c + i][1]);
                 }
         }
         float inv[kFewStep];
         bool gone = false;
 #pragma unroll
-        for (int h = 0; h < kFewStep; ++h) {
-            const float2 sc = *reinterpret_cast<const float2*>(stage[h] + 2 * Few<D>::kHalf);
+        for (int b = 0; b < kFewStep; ++b) {
+            const float2 sc = *reinterpret_cast<const float2*>(stage[b] + 2 * F::kHalf);
             float lg;
-            value_scale(sc.y, lg, inv[h]);
+            value_scale(sc.y, lg, inv[b]);
             gone = gone || sc.y == 0.f;
-            const float f[2] = {sc.x * factor[0], sc.x * factor[1]};
 #pragma unroll
-            for (int j = 2 * h; j < 2 * h + 2; ++j)
+            for (int n = 0; n < NR; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[j][i] = fmaf(s[j][i], f[i >> 1], lg);
+                for (int i = 0; i < 4; ++i) s[b][n][i] = fmaf(s[b][n][i], sc.x * factor[n][i & 1], lg);
         }
         const int window = a.sh.window;
         if (k0 + kFewStep * kFewKeys - 1 > pos_min || (window > 0 && k0 <= pos_max - window) || gone) {
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const bool none = inv[j >> 1] == 0.f;  // a block that is not there
+            for (int b = 0; b < kFewStep; ++b) {
+                const bool none = inv[b] == 0.f;  // a block that is not there
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = k0 + (j >> 1) * kFewKeys + key_row(j & 1, 2 * t + (i & 1)), p = pos[i >> 1];
-                    if (key > p || (window > 0 && key <= p - window) || none) s[j][i] = -INFINITY;
-                }
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = k0 + b * kFewKeys + key_row(i >> 1, g), p = pos[n][i & 1];
+                        if (key > p || (window > 0 && key <= p - window) || none) s[b][n][i] = -INFINITY;
+                    }
             }
         }
-        float top[2];
+        bool behind = false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            top[h] = fmaxf(s[0][2 * h], s[0][2 * h + 1]);
-#pragma unroll
-            for (int j = 1; j < J; ++j) top[h] = fmaxf(top[h], fmaxf(s[j][2 * h], s[j][2 * h + 1]));
-        }
-        if (__any_sync(0xffffffffu, top[0] > m[0] + kHeadroom || top[1] > m[1] + kHeadroom)) {
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float v = fmaxf(top[h], m[h]);
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                v = v > m[h] + kHeadroom ? v : m[h];  // row by row: no row's bits depend on another's
-                const float down = m[h] == v ? 1.f : ex2(m[h] - v);
-                m[h] = v;
-                l[h] *= down;
-#pragma unroll
-                for (int i = 0; i < kTiles; ++i) {
-                    o[i][2 * h] *= down;
-                    o[i][2 * h + 1] *= down;
-                }
+                const float top = fmaxf(fmaxf(s[0][n][h], s[0][n][h + 2]), fmaxf(s[1][n][h], s[1][n][h + 2]));
+                behind = behind || top > m[n][h] + kHeadroom;
             }
-        }
-        uint32_t p[kFewStep][4];
+        if (__any_sync(0xffffffffu, behind)) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float base = m[h] == -INFINITY ? 0.f : m[h] - kWeightBits;
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float v = fmaxf(fmaxf(s[0][n][h], s[0][n][h + 2]), fmaxf(s[1][n][h], s[1][n][h + 2]));
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+                    v = v > m[n][h] + kHeadroom ? v : m[n][h];  // row by row: no row's bits depend on another's
+                    const float down = m[n][h] == v ? 1.f : ex2(m[n][h] - v);
+                    m[n][h] = v;
+                    l[n][h] *= down;
+#pragma unroll
+                    for (int i = 0; i < kTiles; ++i) {
+                        o[n][i][h] *= down;
+                        o[n][i][h + 2] *= down;
+                    }
+                }
+        }
+        uint32_t p[kFewStep][NR][2];  // weights as the products' operand
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            float base[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) base[h] = m[n][h] == -INFINITY ? 0.f : m[n][h] - kWeightBits;
 #pragma unroll
             for (int b = 0; b < kFewStep; ++b) {
-                float w[4], sum = 0.f;
+                float w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    w[i] = ex2(s[2 * b + (i >> 1)][2 * h + (i & 1)] - base);
-                    sum += w[i];
+                for (int i = 0; i < 4; ++i) w[i] = ex2(s[b][n][i] - base[i & 1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float sum = w[h] + w[h + 2];
+                    if (sum != 0.f) l[n][h] = fmaf(sum, inv[b], l[n][h]);  // unseen keys leave a block's NaN scale alone
                 }
-                if (sum != 0.f) l[h] = fmaf(sum, inv[b], l[h]);  // unseen keys leave a block's NaN scale alone
-                p[b][h] = f16_pair(w[0], w[1]);
-                p[b][2 + h] = f16_pair(w[2], w[3]);
+                p[b][n][0] = transposed(f16_pair(w[0], w[1]));
+                p[b][n][1] = transposed(f16_pair(w[2], w[3]));
             }
         }
 #pragma unroll
         for (int b = 0; b < kFewStep; ++b) {
-            const uint8_t* values = stage[b] + Few<D>::kHalf;
-            uint32_t v[4][kTiles / 4];
+            const uint8_t* values = stage[b] + F::kHalf;
+            uint32_t v[4][D / 32];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int row = key_row(i >> 1, 2 * t + (i & 1));
                 if (D == 128) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(values + Few<D>::place(row, g));
-                    v[i][0] = x.x, v[i][1] = x.y, v[i][2 % (kTiles / 4)] = x.z, v[i][3 % (kTiles / 4)] = x.w;
+                    const uint4 x = *reinterpret_cast<const uint4*>(values + F::place(row, g));
+                    v[i][0] = x.x, v[i][1] = x.y, v[i][2 % (D / 32)] = x.z, v[i][3 % (D / 32)] = x.w;
                 } else {
-                    const uint2 x = *reinterpret_cast<const uint2*>(values + Few<D>::place(row, g >> 1) + (g & 1) * 8);
+                    const uint2 x = *reinterpret_cast<const uint2*>(values + F::place(row, g >> 1) + (g & 1) * 8);
                     v[i][0] = x.x, v[i][1] = x.y;
                 }
             }
 #pragma unroll
-            for (int w = 0; w < kTiles / 4; ++w) {
-                const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140), a1 = __byte_perm(v[0][w], v[1][w], 0x7362);
-                const uint32_t b0 = __byte_perm(v[2][w], v[3][w], 0x5140), b1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-                mma16816(o[4 * w], p[b], e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(b0));
-                mma16816(o[4 * w + 1], p[b], e4m3x2_to_f16x2_hi(a0), e4m3x2_to_f16x2_hi(b0));
-                mma16816(o[4 * w + 2], p[b], e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(b1));
-                mma16816(o[4 * w + 3], p[b], e4m3x2_to_f16x2_hi(a1), e4m3x2_to_f16x2_hi(b1));
-            }
+            for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {  // channels 4 w + 2 half and the next of this lane's
+                    const uint32_t sel = half ? 0x7362 : 0x5140;
+                    const uint32_t x = __byte_perm(v[0][w], v[1][w], sel), y = __byte_perm(v[2][w], v[3][w], sel);
+                    const uint32_t value[4] = {e4m3x2_to_f16x2(x), e4m3x2_to_f16x2_hi(x), e4m3x2_to_f16x2(y),
+                                               e4m3x2_to_f16x2_hi(y)};
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) mma16816(o[n][2 * w + half], value, p[b][n][0], p[b][n][1]);
+                }
         }
     }
 };
@@ -315,13 +359,14 @@ __device__ __forceinline__ void write_out4(const KvAttendArgs& a, int64_t row, i
     if (c == 0 && a.lse != nullptr) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kFewThreads, 2) kv_attend_few_kernel(const KvAttendArgs a) {
-    using F = Few<D>;
+template <int D, int NR>
+__global__ void __launch_bounds__(kFewThreads, Few<D, NR>::kCtas) kv_attend_few_kernel(const KvAttendArgs a) {
+    using F = Few<D, NR>;
+    constexpr int kRows = F::kRows;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t* ring = smem + warp * F::kRing;
-    float* ml = reinterpret_cast<float*>(smem + F::kOffMl);  // maxima [warps][16], sums [warps][16]
+    float* ml = reinterpret_cast<float*>(smem + F::kOffMl);  // maxima [warps][rows], sums [warps][rows]
     KvWork* work = reinterpret_cast<KvWork*>(smem + F::kOffWork);
     pdl_wait();
     pdl_trigger();
@@ -334,7 +379,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv_attend_few_kernel(const KvA
 #pragma unroll
     for (int i = 0; i < kFewStages - kFewStep; ++i) copies.issue(a, ring + i * F::kStage);
     KvPlace at = work->at;
-    FewRows<D> rows;
+    FewRows<D, NR> rows;
     rows.start(a, at);
     bool first_segment = true;
     int stage = 0;  // of the step, and of the copies asked for next
@@ -354,78 +399,85 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv_attend_few_kernel(const KvA
             // the end of the row tile, or of the CTA's run in it: the warps' sums together
             const KvParts parts = kv_parts(*work, at, first_segment);
             const int g = lane >> 2, t = lane & 3;
-            uint8_t* sums = smem + F::kOffO;
+            float* sums = reinterpret_cast<float*>(smem + F::kOffO);
             __syncthreads();  // the previous row tile's have been read
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float l = rows.l[h];
-                l += __shfl_xor_sync(0xffffffffu, l, 1);
-                l += __shfl_xor_sync(0xffffffffu, l, 2);
-                if (t == 0) {
-                    ml[warp * 16 + g + 8 * h] = rows.m[h];
-                    ml[kKvFewWarps * 16 + warp * 16 + g + 8 * h] = l;
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float l = rows.l[n][h];
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+                    if (g == 0) {
+                        ml[warp * kRows + 8 * n + 2 * t + h] = rows.m[n][h];
+                        ml[(kKvFewWarps + warp) * kRows + 8 * n + 2 * t + h] = l;
+                    }
                 }
-            }
             __syncthreads();
-            float f[2];  // what brings this warp's sums to the largest maximum
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float m = ml[g + 8 * h];
-#pragma unroll
-                for (int w = 1; w < kKvFewWarps; ++w) m = fmaxf(m, ml[w * 16 + g + 8 * h]);
-                f[h] = rows.m[h] == m ? 1.f : ex2(rows.m[h] - m);
-            }
             // one warp after the other, so that one row tile's room is enough
 #pragma unroll 1
             for (int w = 0; w < kKvFewWarps; ++w) {
                 if (w == warp) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        // lane's channels D/4 t ..: tile i's two columns are D/8 apart
+                    for (int n = 0; n < NR; ++n)
 #pragma unroll
-                        for (int col = 0; col < 2; ++col)
+                        for (int h = 0; h < 2; ++h) {
+                            const int row = 8 * n + 2 * t + h;
+                            float m = ml[row];  // the largest maximum
 #pragma unroll
-                            for (int i = 0; i < D / 8; i += 4) {
-                                float4* at4 = reinterpret_cast<float4*>(
-                                    sums + F::place_o(g + 8 * h, (D / 4 * t + D / 8 * col + i) / 4));
-                                float4 x = w == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *at4;
-                                x.x = fmaf(f[h], rows.o[i][2 * h + col], x.x);
-                                x.y = fmaf(f[h], rows.o[i + 1][2 * h + col], x.y);
-                                x.z = fmaf(f[h], rows.o[i + 2][2 * h + col], x.z);
-                                x.w = fmaf(f[h], rows.o[i + 3][2 * h + col], x.w);
-                                *at4 = x;
+                            for (int k = 1; k < kKvFewWarps; ++k) m = fmaxf(m, ml[k * kRows + row]);
+                            const float f = rows.m[n][h] == m ? 1.f : ex2(rows.m[n][h] - m);
+                            float4* at4 = reinterpret_cast<float4*>(sums + row * D) + D / 32 * g;
+#pragma unroll
+                            for (int i = 0; i < D / 32; ++i) {  // tiles 2 i, 2 i + 1: four channels
+                                const int c = (i + g + t) % (D / 32);  // spread over the banks
+                                float4 x = w == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : at4[c];
+                                float v[4];
+#pragma unroll
+                                for (int k = 0; k < D / 32; ++k)
+                                    if (k == c) {
+                                        v[0] = rows.o[n][2 * k][h], v[1] = rows.o[n][2 * k][h + 2];
+                                        v[2] = rows.o[n][2 * k + 1][h], v[3] = rows.o[n][2 * k + 1][h + 2];
+                                    }
+                                x.x = fmaf(f, v[0], x.x);
+                                x.y = fmaf(f, v[1], x.y);
+                                x.z = fmaf(f, v[2], x.z);
+                                x.w = fmaf(f, v[3], x.w);
+                                at4[c] = x;
                             }
+                        }
                 }
                 __syncthreads();
             }
-            // 8 threads a row
-            const int row = threadIdx.x >> 3, all = at.s.n * a.sh.group, r = at.rt * kKvFewRows + row;
+            // 128 / rows threads a row
+            constexpr int kPer = kFewThreads / kRows;
+            const int row = threadIdx.x / kPer, all = at.s.n * a.sh.group, r = at.rt * kRows + row;
             float m = ml[row], l = 0.f;
 #pragma unroll
-            for (int w = 1; w < kKvFewWarps; ++w) m = fmaxf(m, ml[w * 16 + row]);
+            for (int w = 1; w < kKvFewWarps; ++w) m = fmaxf(m, ml[w * kRows + row]);
 #pragma unroll
             for (int w = 0; w < kKvFewWarps; ++w) {
-                const float mw = ml[w * 16 + row];
-                l = fmaf(mw == m ? 1.f : ex2(mw - m), ml[kKvFewWarps * 16 + w * 16 + row], l);
+                const float mw = ml[w * kRows + row];
+                l = fmaf(mw == m ? 1.f : ex2(mw - m), ml[(kKvFewWarps + w) * kRows + row], l);
             }
             // undo the weights' 2^6 (a row that has seen nothing has m = -inf, l = 0)
             const float down = 0x1p-6f;
             l *= down;
             if (r < all) {
                 const int tok = r / a.sh.group;
-                const int64_t out_row = (int64_t)(at.s.q0 + tok) * a.q_heads + at.head * a.sh.group + r % a.sh.group;
+                const int64_t out_row = (int64_t)(at.s.q0 + tok) * a.q_heads + at.head * a.sh.group + r - tok * a.sh.group;
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const int c = i * 8 + (threadIdx.x & 7);
-                    float4 o = *reinterpret_cast<const float4*>(sums + F::place_o(row, c));
+                for (int i = 0; i < D / 4 / kPer; ++i) {
+                    const int c = i * kPer + threadIdx.x % kPer;
+                    float4 o = *(reinterpret_cast<const float4*>(sums + row * D) + c);
                     o = make_float4(o.x * down, o.y * down, o.z * down, o.w * down);
                     if (parts.parts == 1)
                         write_out4(a, out_row, D, c * 4, o, m, l);
                     else
-                        *reinterpret_cast<float4*>(a.part_o + ((size_t)parts.slot * kKvFewRows + row) * D + c * 4) = o;
+                        *reinterpret_cast<float4*>(a.part_o + ((size_t)parts.slot * kRows + row) * D + c * 4) = o;
                 }
-                if ((threadIdx.x & 7) == 0) {
-                    if (parts.parts > 1) a.part_ml[(size_t)parts.slot * kKvFewRows + row] = make_float2(m, l);
+                if (threadIdx.x % kPer == 0) {
+                    if (parts.parts > 1) a.part_ml[(size_t)parts.slot * kRows + row] = make_float2(m, l);
                     if (parts.leader) a.info[out_row] = make_int2(parts.slot, parts.parts * 256 + row);
                 }
             }
@@ -490,27 +542,33 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttendArgs a, int 
     }
 }
 
-template <int D>
-cudaError_t launch_few(const KvAttendArgs& a, cudaStream_t st, bool pdl) {
-    auto kern = kv_attend_few_kernel<D>;
+template <int D, int NR>
+cudaError_t launch_few(KvAttendArgs& a, cudaStream_t st, bool pdl) {
+    using F = Few<D, NR>;
+    auto kern = kv_attend_few_kernel<D, NR>;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     std::call_once(once, [&] {
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<D>::kSmem);
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
     });
     if (err != cudaSuccess) return err;
-    return launch_kernel(kern, dim3(kv_few_ctas()), dim3(kFewThreads), Few<D>::kSmem, st, pdl, a);
+    a.sh.rows = F::kRows;
+    return launch_kernel(kern, dim3(F::kCtas * num_sms()), dim3(kFewThreads), F::kSmem, st, pdl, a);
 }
 
 }  // namespace
 
-int kv_few_ctas() { return 2 * num_sms(); }
+// Rows of the parts that a grid of either form leaves, at most two a CTA.
+int64_t kv_few_part_rows() { return 2 * (int64_t)num_sms() * (3 * 8 > 2 * 16 ? 3 * 8 : 2 * 16); }
 
 cudaError_t launch_kv_attend_few(KvAttendArgs a, cudaStream_t st, bool pdl) {
-    a.sh.rows = kKvFewRows;
     a.sh.tokens = kKvFewTokens;
     a.sh.extra = 0;
-    const cudaError_t e = a.c.dim == 64 ? launch_few<64>(a, st, pdl) : launch_few<128>(a, st, pdl);
+    // 8 rows a row tile where sequences and key heads have up to 8 on average, 16 elsewhere.
+    const bool eight = (int64_t)a.bt.T * a.sh.group <= 8 * (int64_t)a.bt.B;
+    const bool d64 = a.c.dim == 64;
+    const cudaError_t e = eight ? (d64 ? launch_few<64, 1>(a, st, pdl) : launch_few<128, 1>(a, st, pdl))
+                                : (d64 ? launch_few<64, 2>(a, st, pdl) : launch_few<128, 2>(a, st, pdl));
     return e != cudaSuccess ? e : launch_kv_join(a, st, pdl);
 }
 
