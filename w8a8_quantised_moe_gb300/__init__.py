@@ -645,7 +645,7 @@ class KVCache:
         self.status = new_workspace(256, k.device)
         self._c = _lib.KvCacheT(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, heads, page,
                                 dim, page_stride, scale_stride)
-        self._at = ctypes.addressof(self._c)
+        self._at, self._status_at = ctypes.addressof(self._c), self.status.data_ptr()
 
 
 def new_kv_cache(n_pages, heads, dim, page=64, device="cuda"):
@@ -656,36 +656,33 @@ def new_kv_cache(n_pages, heads, dim, page=64, device="cuda"):
     return KVCache(*codes, *scales)
 
 
-def _rows_fit(t, T, heads, dim):
+def _rows_fit(t, shape, dim, strides):
     """Whether t is bf16 [T, heads, dim] whose tokens' heads are contiguous."""
-    return (t.dtype is _torch().bfloat16 and t.shape == (T, heads, dim) and t.is_cuda and t.stride(2) == 1
-            and (heads == 1 or t.stride(1) == dim))
+    return (t.dtype is _torch().bfloat16 and t.shape == shape and t.is_cuda
+            and (strides[1:] == (dim, 1) or shape[1] == 1 and strides[2] == 1))
 
 
 def _need_rows(t, T, heads, dim, name):
-    if not _rows_fit(t, T, heads, dim):
+    if t.dim() != 3 or not _rows_fit(t, (T, heads, dim), dim, t.stride()):
         raise ValueError(f"{name}: expected cuda torch.bfloat16 {(T, heads, dim)} with contiguous heads, got {t.dtype} "
                          f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
-
-
-def _row_stride(t, T, width):
-    return t.stride(0) if T > 1 else width
 
 
 def _kv_batch(q_start, lengths, page_table, T):
     """The batch's description for a call (the tensors stay the caller's)."""
     i32 = _torch().int32
     B = lengths.shape[0] if lengths.dim() == 1 else -1
+    table = page_table.shape
+    strides = page_table.stride()
     if not (_fits(q_start, i32, (B + 1,)) and _fits(lengths, i32, (B,)) and page_table.dtype is i32
-            and page_table.dim() == 2 and page_table.shape[0] == B and page_table.is_cuda
-            and (page_table.shape[1] <= 1 or page_table.stride(1) == 1)):
+            and len(table) == 2 and table[0] == B and page_table.is_cuda and (strides[1] == 1 or table[1] <= 1)):
         _need(lengths, i32, (max(B, 0),), "lengths")
         _need(q_start, i32, (B + 1,), "q_start")
         raise ValueError(f"page_table: expected cuda {i32} with {B} contiguous rows, got {page_table.dtype} "
-                         f"{tuple(page_table.shape)} with strides {page_table.stride()} on {page_table.device}")
-    pages = page_table.shape[1]
+                         f"{tuple(table)} with strides {strides} on {page_table.device}")
+    pages = table[1]
     return _lib.KvBatchT(q_start.data_ptr(), lengths.data_ptr(), page_table.data_ptr(), B, T, pages,
-                         page_table.stride(0) if B > 1 else pages)
+                         strides[0] if B > 1 else pages)
 
 
 def kv_append(cache, k, v, q_start, lengths, page_table, q=None, rope=None, interleaved=False, q_out=None,
@@ -705,28 +702,37 @@ def kv_append(cache, k, v, q_start, lengths, page_table, q=None, rope=None, inte
             return kv_append(cache, k, v, q_start, lengths, page_table, q, rope, interleaved)
     torch = _torch()
     T, heads, dim = k.shape[0], cache.heads, cache.dim
-    if not (_rows_fit(k, T, heads, dim) and _rows_fit(v, T, heads, dim)):
+    shape, k_strides, v_strides = (T, heads, dim), k.stride(), v.stride()
+    if not (_rows_fit(k, shape, dim, k_strides) and _rows_fit(v, shape, dim, v_strides)):
         _need_rows(k, T, heads, dim, "k")
         _need_rows(v, T, heads, dim, "v")
     batch = _kv_batch(q_start, lengths, page_table, T)
     q_heads = q_stride = rope_rows = rope_dim = 0
+    q_at = q_out_at = None
     if q is not None:
-        if q.dim() != 3 or not _rows_fit(q, T, q.shape[1], dim):
-            _need_rows(q, T, q.shape[1] if q.dim() == 3 else 0, dim, "q")
-        q_heads = q.shape[1]
-        q_stride = _row_stride(q, T, q_heads * dim)
+        q_shape, q_strides = q.shape, q.stride()
+        q_heads = q_shape[1] if len(q_shape) == 3 else 0
+        if not _rows_fit(q, (T, q_heads, dim), dim, q_strides):
+            _need_rows(q, T, q_heads, dim, "q")
         if q_out is None:
-            q_out = torch.empty((T, q_heads, dim), dtype=torch.bfloat16, device=q.device)
-        elif not _fits(q_out, torch.bfloat16, (T, q_heads, dim)):
-            _need(q_out, torch.bfloat16, (T, q_heads, dim), "q_out")
+            q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=cache.device)
+        elif not _fits(q_out, torch.bfloat16, q_shape):
+            _need(q_out, torch.bfloat16, q_shape, "q_out")
+        q_stride = q_strides[0] if T > 1 else q_heads * dim
+        q_at, q_out_at = q.data_ptr(), q_out.data_ptr()
+    else:
+        q_out = None
+    rope_at = None
     if rope is not None:
         rope_rows, rope_dim = rope.shape
-        if not _fits(rope, torch.float32, (rope_rows, rope_dim)):
+        if not _fits(rope, torch.float32, rope.shape):
             _need(rope, torch.float32, (rope_rows, rope_dim), "rope")
+        rope_at = rope.data_ptr()
+    width = heads * dim
     status = _lib.load().moe_w8a8_kv_append(
-        cache._at, ctypes.addressof(batch), k.data_ptr(), _row_stride(k, T, heads * dim), v.data_ptr(),
-        _row_stride(v, T, heads * dim), _ptr(q), q_stride, q_heads, _ptr(rope), rope_rows, rope_dim, interleaved,
-        _ptr(q_out) if q is not None else None, *_room(cache.status), _raw_stream(stream, k))
+        cache._at, ctypes.addressof(batch), k.data_ptr(), k_strides[0] if T > 1 else width, v.data_ptr(),
+        v_strides[0] if T > 1 else width, q_at, q_stride, q_heads, rope_at, rope_rows, rope_dim, interleaved, q_out_at,
+        cache._status_at, 256, _raw_stream(stream, k))
     if status:
         raise MoeError(status, "moe_w8a8_kv_append")
     return q_out
@@ -751,22 +757,22 @@ def kv_attention(q, cache, q_start, lengths, page_table, scale=None, window=0, l
         with _on(stream):
             return kv_attention(q, cache, q_start, lengths, page_table, scale, window, lse, workspace, out)
     torch = _torch()
-    dim = cache.dim
-    T, q_heads = q.shape[:2]
-    shape = (T, q_heads, dim)
-    if not (_rows_fit(q, T, q_heads, dim) and (out is None or _fits(out, torch.bfloat16, shape))
+    dim, bf16 = cache.dim, torch.bfloat16
+    shape, strides = q.shape, q.stride()
+    T, q_heads = shape[0], shape[1] if len(shape) == 3 else 0
+    if not (_rows_fit(q, (T, q_heads, dim), dim, strides) and (out is None or _fits(out, bf16, shape))
             and (lse is None or _fits(lse, torch.float32, shape[:2]))):
         _need_rows(q, T, q_heads, dim, "q")
-        _check_all(("out", out, torch.bfloat16, shape), ("lse", lse, torch.float32, shape[:2]))
+        _check_all(("out", out, bf16, shape), ("lse", lse, torch.float32, shape[:2]))
     batch = _kv_batch(q_start, lengths, page_table, T)
     if workspace is None:
-        workspace = new_workspace(kv_attention_workspace_size(batch.B, T, q_heads, cache.heads, dim), q.device)
+        workspace = new_workspace(kv_attention_workspace_size(batch.B, T, q_heads, cache.heads, dim), cache.device)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty(shape, dtype=bf16, device=cache.device)
     status = _lib.load().moe_w8a8_kv_attention(
-        cache._at, ctypes.addressof(batch), q.data_ptr(), _row_stride(q, T, q_heads * dim), q_heads,
-        dim**-0.5 if scale is None else scale, window, out.data_ptr(), _ptr(lse), *_room(workspace),
-        _raw_stream(stream, q))
+        cache._at, ctypes.addressof(batch), q.data_ptr(), strides[0] if T > 1 else q_heads * dim, q_heads,
+        dim**-0.5 if scale is None else scale, window, out.data_ptr(), None if lse is None else lse.data_ptr(),
+        *_room(workspace), _raw_stream(stream, q))
     if status:
         raise MoeError(status, "moe_w8a8_kv_attention")
     return out

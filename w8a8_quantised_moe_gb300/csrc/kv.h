@@ -51,6 +51,7 @@ struct KvAttendArgs {
     int2* info;         // [T][q_heads]: where a row's parts are (kv_parts.cuh)
     float* part_o;      // [slots][rows][dim]
     float2* part_ml;    // [slots][rows]
+    int slots;          // two a CTA of the grid; set by the launch
 };
 // Row tiles of 8 or 16 rows on warp-level MMAs: few rows a sequence and key head.
 constexpr int kKvFewTokens = 128, kKvFewWarps = 4;

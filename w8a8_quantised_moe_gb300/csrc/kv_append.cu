@@ -122,56 +122,83 @@ __device__ __forceinline__ uint32_t requant4(uint32_t w, float ratio) {
     return e4m3_pair(f[0], f[1]) | (e4m3_pair(f[2], f[3]) << 16);
 }
 
-// Queries: the block's tokens [t0, t1), every head.
-__device__ __forceinline__ void turn_queries(const KvAppendArgs& a, int t0, int t1, int* seq) {
-    // sequence of t0: the entries of q_start[1..B] that are not above it
-    int count = 0;
-    for (int b = 1 + threadIdx.x; b <= a.bt.B; b += kApThreads) count += a.bt.q_start[b] <= t0;
-    count = __reduce_add_sync(0xffffffffu, count);
-    if (threadIdx.x == 0) *seq = 0;
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0 && count) atomicAdd(seq, count);
-    __syncthreads();
-    int b = *seq;
-    const int D = a.c.dim, upr = D / 16, units = a.q_heads * upr;
-    for (int t = t0; t < t1; ++t) {
-        while (b < a.bt.B && a.bt.q_start[b + 1] <= t) ++b;
-        if (b >= a.bt.B) return;  // rows behind the last sequence
-        const KvSeq s = kv_seq(a.bt, b, a.c.page);
-        const int pos = s.len - s.n + t - s.q0;
-        if (t < s.q0 || pos < 0) continue;
-        if (a.rope_dim > 0 && pos >= a.rope_rows) {
-            if (threadIdx.x == 0) atomicOr(a.error, kErrDevice);
-            continue;
+// Queries: the block's tokens [t0, t1), every head; two units of a thread in flight (four: 55 us for
+// a prompt of 8192 tokens, two 53).
+constexpr int kApTokens = 16;  // of such a block, at most
+__device__ __forceinline__ void turn_queries(const KvAppendArgs& a, int t0, int t1, int* pos) {
+    // the tokens' positions; -1: none to turn
+    if ((int)threadIdx.x < t1 - t0) {
+        const int t = t0 + threadIdx.x;
+        int lo = 0, hi = a.bt.B;  // the entries of q_start[1..B] that are not above t
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (a.bt.q_start[mid + 1] <= t) lo = mid + 1;
+            else hi = mid;
         }
-        const uint16_t* in = a.q + t * a.q_stride;
-        uint16_t* out = a.q_out + (size_t)t * a.q_heads * D;
-        for (int i = threadIdx.x; i < units; i += kApThreads) {
-            const Unit u(i % upr, a.rope_dim, a.interleaved);
-            const int at = i / upr * D;
-            float f[16];
-            load16(in + at, u, f);
-            if (u.angle >= 0) turn_unit<false>(f, u, a.rope + (size_t)pos * a.rope_dim, a.rope_dim / 2);
-            *reinterpret_cast<uint4*>(out + at + u.c0) =
-                make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
-            *reinterpret_cast<uint4*>(out + at + u.c1) = make_uint4(
-                bf16_pair(f[8], f[9]), bf16_pair(f[10], f[11]), bf16_pair(f[12], f[13]), bf16_pair(f[14], f[15]));
+        int p = -1;
+        if (lo < a.bt.B) {  // else a row behind the last sequence
+            const KvSeq s = kv_seq(a.bt, lo, a.c.page);
+            if (t >= s.q0) p = s.len - s.n + t - s.q0;
+        }
+        if (a.rope_dim > 0 && p >= a.rope_rows) {
+            atomicOr(a.error, kErrDevice);
+            p = -1;
+        }
+        pos[threadIdx.x] = p;
+    }
+    __syncthreads();
+    const int D = a.c.dim, upr = D / 16, bits = D == 128 ? 3 : 2, units = a.q_heads * upr, all = (t1 - t0) * units;
+    constexpr int kFlight = 2;
+    for (int i0 = threadIdx.x; i0 < all; i0 += kFlight * kApThreads) {
+        uint4 w[kFlight][2];
+        int p[kFlight];
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
+            const int i = i0 + k * kApThreads, tok = i / units;
+            p[k] = i < all ? pos[tok] : -1;
+            const uint16_t* row = a.q + (t0 + tok) * a.q_stride + ((i - tok * units) >> bits) * D;
+            const Unit u(i & (upr - 1), a.rope_dim, a.interleaved);
+            if (p[k] >= 0) {
+                w[k][0] = *reinterpret_cast<const uint4*>(row + u.c0);
+                w[k][1] = *reinterpret_cast<const uint4*>(row + u.c1);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
+            if (p[k] < 0) continue;
+            const int i = i0 + k * kApThreads, tok = i / units;
+            const Unit u(i & (upr - 1), a.rope_dim, a.interleaved);
+            float lo[8], hi[8], x[16];
+            bf16x8_to_f32(w[k][0], lo);
+            bf16x8_to_f32(w[k][1], hi);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[j] = lo[j];
+                x[8 + j] = hi[j];
+            }
+            if (u.angle >= 0) turn_unit<false>(x, u, a.rope + (size_t)p[k] * a.rope_dim, a.rope_dim / 2);
+            uint16_t* out = a.q_out + (size_t)(t0 + tok) * a.q_heads * D + ((i - tok * units) >> bits) * D;
+            *reinterpret_cast<uint4*>(out + u.c0) =
+                make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+            *reinterpret_cast<uint4*>(out + u.c1) = make_uint4(
+                bf16_pair(x[8], x[9]), bf16_pair(x[10], x[11]), bf16_pair(x[12], x[13]), bf16_pair(x[14], x[15]));
         }
     }
 }
 
-// W: warps of a task (1 or 8).  NU: units that a thread holds in registers; the
-// others (a page with many new tokens where few were expected) are read twice.
+// W: warps of a task (1, 2, 4 or 8; 8 / W tasks of a run a block).  NU: units that a thread
+// holds in registers; the others (a page with many new tokens where few were expected, the
+// second half of one of 128 tokens) are read twice.
 template <int W, int NU>
-__global__ void __launch_bounds__(kApThreads) kv_append_kernel(const KvAppendArgs a) {
+__global__ void __launch_bounds__(kApThreads, 4) kv_append_kernel(const KvAppendArgs a) {
     __shared__ int64_t red[kApThreads / 32];
-    __shared__ int run_b, run_page;
+    __shared__ int run_b, run_page, pos[kApTokens];
     __shared__ float amax_s[kApThreads / 32];
     pdl_wait();
     pdl_trigger();
     if ((int)blockIdx.x >= a.store_blocks) {
         const int t0 = ((int)blockIdx.x - a.store_blocks) * a.q_tokens;
-        turn_queries(a, t0, kv_min(t0 + a.q_tokens, a.bt.T), &run_b);
+        turn_queries(a, t0, kv_min(t0 + a.q_tokens, a.bt.T), pos);
         return;
     }
     const int run = blockIdx.x / a.task_blocks, P = a.c.page, D = a.c.dim;
@@ -201,36 +228,24 @@ __global__ void __launch_bounds__(kApThreads) kv_append_kernel(const KvAppendArg
         if (threadIdx.x == 0) atomicOr(a.error, kErrDevice);
         hi = a.rope_rows;
     }
-    const int id = a.bt.page_table[run_b * a.bt.table_stride + page];
+    const int id = a.bt.page_table[run_b * a.bt.table_stride + page];  // not waited for before the rows are there
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int task = (blockIdx.x % a.task_blocks) * (8 / W) + warp / W;
-    // a task of W warps ends as one: only whole blocks (W = 8) meet at barriers below
+    // the warps of a task end as one, so that they meet at their barriers
     if (task >= 2 * a.c.heads || hi <= lo) return;
-    if ((unsigned)id >= (unsigned)a.c.n_pages) {
-        if (threadIdx.x == 0 || lane == 0) atomicOr(a.error, kErrDevice);
-        return;
-    }
     const bool keys = task < a.c.heads;
     const int head = keys ? task : task - a.c.heads;
-    const int upr = D / 16, units = (hi - lo) * upr, tid = W == 1 ? lane : (int)threadIdx.x;
+    const int upr = D / 16, bits = D == 128 ? 3 : 2, units = (hi - lo) * upr;
+    const int tid = (int)threadIdx.x & (32 * W - 1);
     const int64_t stride = keys ? a.k_stride : a.v_stride;
     const int rope_dim = keys ? a.rope_dim : 0;
     const uint16_t* in = (keys ? a.k : a.v) + (int64_t)(s.q0 + lo - (s.len - s.n)) * stride + head * D;
-    uint8_t* block = (keys ? a.c.k : a.c.v) + id * a.c.page_stride + (size_t)head * P * D;
-    float* scale = (keys ? a.c.k_scale : a.c.v_scale) + id * a.c.scale_stride + head;
-    const float before_s = held > 0 ? *scale : 0.f;
 
     auto load = [&](int i, float(&f)[16]) {
-        const int r = i / upr;
-        const Unit u(i % upr, rope_dim, a.interleaved);
+        const int r = i >> bits;
+        const Unit u(i & (upr - 1), rope_dim, a.interleaved);
         load16(in + r * stride, u, f);
         if (u.angle >= 0) turn_unit<true>(f, u, a.rope + (size_t)(lo + r) * a.rope_dim, a.rope_dim / 2);
-    };
-    auto store = [&](int i, const float(&f)[16], float inv) {
-        const Unit u(i % upr, rope_dim, a.interleaved);
-        uint8_t* row = block + (size_t)(held + i / upr) * D;
-        *reinterpret_cast<uint2*>(row + u.c0) = make_uint2(codes4(f, inv), codes4(f + 4, inv));
-        *reinterpret_cast<uint2*>(row + u.c1) = make_uint2(codes4(f + 8, inv), codes4(f + 12, inv));
     };
     float held_f[NU][16];
     float amax = 0.f;
@@ -253,12 +268,31 @@ __global__ void __launch_bounds__(kApThreads) kv_append_kernel(const KvAppendArg
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) amax = amax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    auto task_sync = [&] {
+        if (W == 1)
+            __syncwarp();
+        else
+            asm volatile("barrier.sync %0, %1;" ::"r"(1 + warp / W), "n"(32 * W) : "memory");
+    };
     if (W > 1) {
         if (lane == 0) amax_s[warp] = amax;
-        __syncthreads();
+        task_sync();
 #pragma unroll
-        for (int w = 0; w < W; ++w) amax = amax_nan(amax, amax_s[w]);
+        for (int w = 0; w < W; ++w) amax = amax_nan(amax, amax_s[warp / W * W + w]);
     }
+    if ((unsigned)id >= (unsigned)a.c.n_pages) {
+        if (tid == 0) atomicOr(a.error, kErrDevice);
+        return;
+    }
+    uint8_t* block = (keys ? a.c.k : a.c.v) + id * a.c.page_stride + (size_t)head * P * D;
+    float* scale = (keys ? a.c.k_scale : a.c.v_scale) + id * a.c.scale_stride + head;
+    const float before_s = held > 0 ? *scale : 0.f;
+    auto store = [&](int i, const float(&f)[16], float inv) {
+        const Unit u(i & (upr - 1), rope_dim, a.interleaved);
+        uint8_t* row = block + (size_t)(held + (i >> bits)) * D;
+        *reinterpret_cast<uint2*>(row + u.c0) = make_uint2(codes4(f, inv), codes4(f + 4, inv));
+        *reinterpret_cast<uint2*>(row + u.c1) = make_uint2(codes4(f + 8, inv), codes4(f + 12, inv));
+    };
     float now = pow2_scale(amax);
     if (held > 0) now = now != now || before_s != before_s ? __uint_as_float(0x7fffffffu) : fmaxf(now, before_s);
     const float inv = now == now ? __frcp_rn(now) : 0.f;
@@ -280,8 +314,7 @@ __global__ void __launch_bounds__(kApThreads) kv_append_kernel(const KvAppendArg
             codes[i] = make_uint4(requant4(w.x, ratio), requant4(w.y, ratio), requant4(w.z, ratio), requant4(w.w, ratio));
         }
     }
-    if (W > 1) __syncthreads();  // every thread has read the scale
-    else __syncwarp();
+    if (held > 0) task_sync();  // every thread has read the scale
     if (tid == 0) *scale = now;
 }
 
@@ -289,19 +322,24 @@ __global__ void __launch_bounds__(kApThreads) kv_append_kernel(const KvAppendArg
 
 cudaError_t launch_kv_append(KvAppendArgs a, cudaStream_t st, bool pdl) {
     const int64_t runs = kv_most_runs(a.bt.B, a.bt.T, a.c.page);
-    // A warp a task where a sequence brings a few tokens, eight where it brings pages.
-    const bool few = (int64_t)a.bt.T <= 4 * (int64_t)a.bt.B;
-    a.task_blocks = few ? (2 * a.c.heads + 7) / 8 : 2 * a.c.heads;
+    // A warp a task where a sequence brings a few tokens; else as many as hold a page of
+    // new tokens, two units a thread.
+    const int page_units = a.c.page * a.c.dim / 16;
+    const int W = (int64_t)a.bt.T <= 4 * (int64_t)a.bt.B ? 1 : page_units <= 64 ? 1 : page_units <= 128 ? 2 : page_units <= 256 ? 4 : 8;
+    a.task_blocks = (2 * a.c.heads * W + 7) / 8;
     const int64_t store = runs * a.task_blocks;
     a.q_tokens = 1;
-    while (a.q_tokens < 16 && (int64_t)a.bt.T / (2 * a.q_tokens) >= 8 * num_sms()) a.q_tokens *= 2;
+    while (a.q_tokens < kApTokens && (int64_t)a.bt.T / (2 * a.q_tokens) >= 8 * num_sms()) a.q_tokens *= 2;
     const int64_t q_blocks = a.q != nullptr ? (a.bt.T + a.q_tokens - 1) / a.q_tokens : 0;
     if (store + q_blocks > INT32_MAX) return cudaErrorInvalidValue;
     a.store_blocks = (int)store;
     const dim3 grid((unsigned)(store + q_blocks)), block(kApThreads);
-    if (few) return launch_kernel(kv_append_kernel<1, 1>, grid, block, 0, st, pdl, a);
-    if (a.c.page * a.c.dim <= 16 * kApThreads) return launch_kernel(kv_append_kernel<8, 1>, grid, block, 0, st, pdl, a);
-    return launch_kernel(kv_append_kernel<8, 4>, grid, block, 0, st, pdl, a);
+    switch (W) {
+        case 1: return launch_kernel(kv_append_kernel<1, 2>, grid, block, 0, st, pdl, a);
+        case 2: return launch_kernel(kv_append_kernel<2, 2>, grid, block, 0, st, pdl, a);
+        case 4: return launch_kernel(kv_append_kernel<4, 2>, grid, block, 0, st, pdl, a);
+        default: return launch_kernel(kv_append_kernel<8, 2>, grid, block, 0, st, pdl, a);
+    }
 }
 
 }  // namespace moe

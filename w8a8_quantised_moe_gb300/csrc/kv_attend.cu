@@ -928,6 +928,7 @@ cudaError_t launch_kv_attend(KvAttendArgs a, cudaStream_t st, bool pdl) {
     a.sh.rows = kKvRows;
     a.sh.tokens = kTcTile;
     a.sh.extra = kTcExtra;
+    a.slots = 2 * kv_tc_ctas();
     const cudaError_t e = a.c.dim == 64 ? launch_tc<64>(a, st, pdl) : launch_tc<128>(a, st, pdl);
     return e != cudaSuccess ? e : launch_kv_join(a, st, pdl);
 }

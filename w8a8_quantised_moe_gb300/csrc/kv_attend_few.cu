@@ -502,14 +502,18 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttendArgs a, int 
     const int64_t all = (int64_t)a.bt.T * a.q_heads;
     pdl_wait();
     pdl_trigger();
-    const int64_t lo = (int64_t)kv_clamp(a.bt.q_start[0], 0, a.bt.T) * a.q_heads;
-    int64_t hi = lo;  // the rows of sequences are [lo, hi)
-    hi = (int64_t)kv_max(kv_clamp(a.bt.q_start[a.bt.B], 0, a.bt.T), (int)(lo / a.q_heads)) * a.q_heads;
-    for (int64_t r0 = warp * per_warp; r0 < kv_min64(warp * per_warp + per_warp, all); ++r0) {
-        if (r0 < lo || r0 >= hi) continue;
+    const int first = a.bt.q_start[0], end = a.bt.q_start[a.bt.B];
+    const int64_t r1 = kv_min64(warp * per_warp + per_warp, all);
+    for (int64_t r0 = warp * per_warp; r0 < r1; ++r0) {
         const int2 info = a.info[r0];
+        // the rows of sequences; others' info is an earlier call's
+        const int token = (int)(r0 / a.q_heads);
+        if (token < first || token >= end) continue;
         const int parts = info.y >> 8, row = info.y & 255, c0 = info.x >> 1;
-        if (parts <= 1) continue;
+        // (a row tile given up after a timeout may have left anything)
+        if (parts <= 1 || (unsigned)info.x >= (unsigned)a.slots || parts > a.slots || 2 * (c0 + parts - 1) >= a.slots ||
+            row >= a.sh.rows)
+            continue;
         auto slot = [&](int i) { return (size_t)(i == 0 ? info.x : 2 * (c0 + i)) * a.sh.rows + row; };
         float m = -INFINITY, l = 0.f;
         for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.part_ml[slot(i)].x);
@@ -553,6 +557,7 @@ cudaError_t launch_few(KvAttendArgs& a, cudaStream_t st, bool pdl) {
     });
     if (err != cudaSuccess) return err;
     a.sh.rows = F::kRows;
+    a.slots = 2 * F::kCtas * num_sms();
     return launch_kernel(kern, dim3(F::kCtas * num_sms()), dim3(kFewThreads), F::kSmem, st, pdl, a);
 }
 

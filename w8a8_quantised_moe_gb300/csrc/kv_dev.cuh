@@ -123,7 +123,7 @@ __device__ __forceinline__ void kv_find_work(const KvAttendArgs& a, int most_cta
     p.b = work->b;
     p.s = kv_seq(a.bt, p.b, a.sh.page);
     const int64_t per_head = kv_seq_units(p.s, a.sh);
-    p.head = (int)((u0 - work->base) / per_head);
+    p.head = (int)kv_quotient(u0 - work->base, per_head);
     const int64_t head_base = work->base + p.head * per_head;
     for (int rt = threadIdx.x, tiles = kv_row_tiles(p.s, a.sh); rt < tiles; rt += THREADS)
         if (kv_enter_if(p, a.sh, rt, u0 - head_base, head_base)) {

@@ -123,10 +123,14 @@ KV_HD int64_t kv_seq_units(const KvSeq& s, const KvShape& sh) {
 
 // The batch's U units, in the order (sequence, key head, row tile, unit), are dealt
 // to C CTAs in runs that differ by one at most.
-KV_HD int64_t kv_deal(int64_t U, int C, int c) { return U * c / C; }
-KV_HD int kv_owner(int64_t U, int C, int64_t u) { return (int)(((u + 1) * C - 1) / U); }
+// (In 32 bits where they are enough: a 64-bit division is a chain of a hundred instructions.)
+KV_HD int64_t kv_quotient(int64_t a, int64_t b) {
+    return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+KV_HD int64_t kv_deal(int64_t U, int C, int c) { return kv_quotient(U * c, C); }
+KV_HD int kv_owner(int64_t U, int C, int64_t u) { return (int)kv_quotient((u + 1) * C - 1, U); }
 KV_HD int kv_ctas(int64_t U, int most, int least_units) {
-    const int64_t c = (U + least_units - 1) / least_units;
+    const int64_t c = kv_quotient(U + least_units - 1, least_units);
     return (int)(c < 1 ? 1 : c < most ? c : most);
 }
 
