@@ -49,8 +49,8 @@
  *     "bad_ptr": the pointer check fails as if a data pointer were null
  *     (MOE_ERR_INVALID_ARG); "launch_fail": every kernel launch fails before
  *     anything is queued (MOE_ERR_CUDA).  On the GPU: "stall": every
- *     tensor-core expert or linear GEMM launch starts with its producer
- *     waiting, within the wait limit (moe_w8a8_set_wait_timeout_ns), on a
+ *     tensor-core expert or linear GEMM launch, and every attention launch
+ *     for many rows, starts with its producer waiting, within the wait limit (moe_w8a8_set_wait_timeout_ns), on a
  *     barrier that nothing completes, so that the limit runs out and the
  *     kernel takes its abort path (MOE_ERR_DEVICE_TIMEOUT from
  *     moe_w8a8_device_error; outputs undefined).  "bad_slot", honoured only
@@ -597,10 +597,11 @@ MOE_W8A8_API moe_status_t moe_w8a8_norm_residual(const void* x, int x_fp32, cons
  *   workspace  >= moe_w8a8_kv_attention_workspace_size(B, T, q_heads, heads,
  *              dim) bytes, which do not fall with B or T; 256-byte aligned, the
  *              first 256 bytes zeroed once
- * A row that sees no key has out 0 and lse -inf.  Scores and sums are binary32
- * of exact products (a query row to 2^-25 of its largest channel), the weights
- * fp16.  Results depend in their last bits on the batch: where a sequence is cut
- * into parts.
+ * A row that sees no key has out 0 and lse -inf.  Scores are binary32 sums of
+ * exact products (of a query row to 2^-17 of its largest channel), weights fp16
+ * (11 bits), sums binary32.  Results depend in their last bits on the batch:
+ * where a sequence is cut into parts, and which form of row tiles its average
+ * number of rows takes.  One launch, and one that joins the parts.
  * ------------------------------------------------------------------------- */
 typedef struct {
     uint8_t* k;

@@ -122,12 +122,25 @@ def test_python_refusals():
         moe.kv_attention_workspace_size(1, 1, 3, 2, 64)
 
     class Handle:
-        heads, page, dim = 2, 16, 64
+        heads, page, dim, device, _index = 2, 16, 64, "cuda:0", 0
     x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     ints = torch.zeros(3, dtype=torch.int32)
-    with pytest.raises(ValueError, match="k: expected cuda torch.bfloat16"):
+    with pytest.raises(ValueError, match="k: expected torch.bfloat16"):
         moe.kv_append(Handle, x, x, ints, ints[:2], ints[:2, None])
-    with pytest.raises(ValueError, match="q: expected cuda torch.bfloat16"):
+    with pytest.raises(ValueError, match="q: expected torch.bfloat16"):
         moe.kv_attention(x, Handle, ints, ints[:2], ints[:2, None])
-    with pytest.raises(ValueError, match="lengths: expected contiguous cuda"):
-        moe._kv_batch(ints, ints[:2], ints[:2, None], 4)
+    with pytest.raises(ValueError, match="lengths: expected contiguous torch.int32"):
+        moe._kv_batch(ints, ints[:2], ints[:2, None], 4, Handle)
+    Handle._index = -1  # the host's tensors pass, but for what is wrong with each
+    with pytest.raises(ValueError, match="v: expected torch.bfloat16"):
+        moe.kv_append(Handle, x, x[:, :1], ints, ints[:2], ints[:2, None])
+    with pytest.raises(ValueError, match="q_start: expected"):
+        moe.kv_append(Handle, x, x, ints[:2], ints[:2], ints[:2, None])
+    with pytest.raises(ValueError, match="page_table: expected"):
+        moe.kv_append(Handle, x, x, ints, ints[:2], ints[:1, None])
+    with pytest.raises(ValueError, match="rope: expected"):
+        moe.kv_append(Handle, x, x, ints, ints[:2], ints[:2, None], rope=torch.zeros(4, 4, dtype=torch.float64))
+    with pytest.raises(ValueError, match="q_out: expected"):
+        moe.kv_append(Handle, x, x, ints, ints[:2], ints[:2, None], q=x, q_out=x[:2])
+    with pytest.raises(ValueError, match="lse: expected"):
+        moe.kv_attention(x, Handle, ints, ints[:2], ints[:2, None], lse=torch.zeros(4, 3))

@@ -27,7 +27,7 @@ BATCH = (INTS, INTS[:2], INTS[:2, None])
 def stand_ins(monkeypatch):
     monkeypatch.setattr(_lib, "load", lambda: calls.FakeLibrary())
     monkeypatch.setattr(moe, "_rows_fit", lambda *a: True)
-    monkeypatch.setattr(moe, "_fits", lambda *a: True)
+    monkeypatch.setattr(moe, "_fits_cache", lambda *a: True)
     monkeypatch.setattr(moe, "_raw_stream", lambda stream, t: 0)
     monkeypatch.setattr(moe, "_kv_batch", lambda *a: _lib.KvBatchT(0, 0, 0, 2, 3, 1, 1))
 

@@ -641,7 +641,7 @@ class KVCache:
             raise ValueError("k and v, and their scales, have the same strides from page to page")
         page_stride, scale_stride = (k.stride(0), k_scale.stride(0)) if n > 1 else (heads * page * dim, heads)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.heads, self.page, self.dim, self.device = heads, page, dim, k.device
+        self.heads, self.page, self.dim, self.device, self._index = heads, page, dim, k.device, k.get_device()
         self.status = new_workspace(256, k.device)
         self._c = _lib.KvCacheT(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, heads, page,
                                 dim, page_stride, scale_stride)
@@ -656,30 +656,41 @@ def new_kv_cache(n_pages, heads, dim, page=64, device="cuda"):
     return KVCache(*codes, *scales)
 
 
-def _rows_fit(t, shape, dim, strides):
-    """Whether t is bf16 [T, heads, dim] whose tokens' heads are contiguous."""
-    return (t.dtype is _torch().bfloat16 and t.shape == shape and t.is_cuda
+def _rows_fit(t, shape, dim, strides, cache):
+    """Whether t is bf16 [T, heads, dim] on the cache's device, a token's heads contiguous."""
+    return (t.dtype is _torch().bfloat16 and t.shape == shape and t.get_device() == cache._index
             and (strides[1:] == (dim, 1) or shape[1] == 1 and strides[2] == 1))
 
 
-def _need_rows(t, T, heads, dim, name):
-    if t.dim() != 3 or not _rows_fit(t, (T, heads, dim), dim, t.stride()):
-        raise ValueError(f"{name}: expected cuda torch.bfloat16 {(T, heads, dim)} with contiguous heads, got {t.dtype} "
-                         f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+def _need_rows(t, T, heads, cache, name):
+    if t.dim() != 3 or not _rows_fit(t, (T, heads, cache.dim), cache.dim, t.stride(), cache):
+        raise ValueError(f"{name}: expected torch.bfloat16 {(T, heads, cache.dim)} with contiguous heads on "
+                         f"{cache.device}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def _kv_batch(q_start, lengths, page_table, T):
+def _fits_cache(t, dtype, shape, cache):
+    return t.dtype is dtype and t.shape == shape and t.get_device() == cache._index and t.is_contiguous()
+
+
+def _need_cache(t, dtype, shape, cache, name):
+    if not _fits_cache(t, dtype, shape, cache):
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {cache.device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+
+
+def _kv_batch(q_start, lengths, page_table, T, cache):
     """The batch's description for a call (the tensors stay the caller's)."""
     i32 = _torch().int32
     B = lengths.shape[0] if lengths.dim() == 1 else -1
     table = page_table.shape
     strides = page_table.stride()
-    if not (_fits(q_start, i32, (B + 1,)) and _fits(lengths, i32, (B,)) and page_table.dtype is i32
-            and len(table) == 2 and table[0] == B and page_table.is_cuda and (strides[1] == 1 or table[1] <= 1)):
-        _need(lengths, i32, (max(B, 0),), "lengths")
-        _need(q_start, i32, (B + 1,), "q_start")
-        raise ValueError(f"page_table: expected cuda {i32} with {B} contiguous rows, got {page_table.dtype} "
-                         f"{tuple(table)} with strides {strides} on {page_table.device}")
+    if not (_fits_cache(q_start, i32, (B + 1,), cache) and _fits_cache(lengths, i32, (B,), cache)
+            and page_table.dtype is i32 and len(table) == 2 and table[0] == B
+            and page_table.get_device() == cache._index and (strides[1] == 1 or table[1] <= 1)):
+        _need_cache(lengths, i32, (max(B, 0),), cache, "lengths")
+        _need_cache(q_start, i32, (B + 1,), cache, "q_start")
+        raise ValueError(f"page_table: expected {i32} with {B} contiguous rows on {cache.device}, got "
+                         f"{page_table.dtype} {tuple(table)} with strides {strides} on {page_table.device}")
     pages = table[1]
     return _lib.KvBatchT(q_start.data_ptr(), lengths.data_ptr(), page_table.data_ptr(), B, T, pages,
                          strides[0] if B > 1 else pages)
@@ -703,21 +714,21 @@ def kv_append(cache, k, v, q_start, lengths, page_table, q=None, rope=None, inte
     torch = _torch()
     T, heads, dim = k.shape[0], cache.heads, cache.dim
     shape, k_strides, v_strides = (T, heads, dim), k.stride(), v.stride()
-    if not (_rows_fit(k, shape, dim, k_strides) and _rows_fit(v, shape, dim, v_strides)):
-        _need_rows(k, T, heads, dim, "k")
-        _need_rows(v, T, heads, dim, "v")
-    batch = _kv_batch(q_start, lengths, page_table, T)
+    if not (_rows_fit(k, shape, dim, k_strides, cache) and _rows_fit(v, shape, dim, v_strides, cache)):
+        _need_rows(k, T, heads, cache, "k")
+        _need_rows(v, T, heads, cache, "v")
+    batch = _kv_batch(q_start, lengths, page_table, T, cache)
     q_heads = q_stride = rope_rows = rope_dim = 0
     q_at = q_out_at = None
     if q is not None:
         q_shape, q_strides = q.shape, q.stride()
         q_heads = q_shape[1] if len(q_shape) == 3 else 0
-        if not _rows_fit(q, (T, q_heads, dim), dim, q_strides):
-            _need_rows(q, T, q_heads, dim, "q")
+        if not _rows_fit(q, (T, q_heads, dim), dim, q_strides, cache):
+            _need_rows(q, T, q_heads, cache, "q")
         if q_out is None:
             q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=cache.device)
-        elif not _fits(q_out, torch.bfloat16, q_shape):
-            _need(q_out, torch.bfloat16, q_shape, "q_out")
+        elif not _fits_cache(q_out, torch.bfloat16, q_shape, cache):
+            _need_cache(q_out, torch.bfloat16, q_shape, cache, "q_out")
         q_stride = q_strides[0] if T > 1 else q_heads * dim
         q_at, q_out_at = q.data_ptr(), q_out.data_ptr()
     else:
@@ -725,8 +736,8 @@ def kv_append(cache, k, v, q_start, lengths, page_table, q=None, rope=None, inte
     rope_at = None
     if rope is not None:
         rope_rows, rope_dim = rope.shape
-        if not _fits(rope, torch.float32, rope.shape):
-            _need(rope, torch.float32, (rope_rows, rope_dim), "rope")
+        if not _fits_cache(rope, torch.float32, rope.shape, cache):
+            _need_cache(rope, torch.float32, (rope_rows, rope_dim), cache, "rope")
         rope_at = rope.data_ptr()
     width = heads * dim
     status = _lib.load().moe_w8a8_kv_append(
@@ -760,11 +771,14 @@ def kv_attention(q, cache, q_start, lengths, page_table, scale=None, window=0, l
     dim, bf16 = cache.dim, torch.bfloat16
     shape, strides = q.shape, q.stride()
     T, q_heads = shape[0], shape[1] if len(shape) == 3 else 0
-    if not (_rows_fit(q, (T, q_heads, dim), dim, strides) and (out is None or _fits(out, bf16, shape))
-            and (lse is None or _fits(lse, torch.float32, shape[:2]))):
-        _need_rows(q, T, q_heads, dim, "q")
-        _check_all(("out", out, bf16, shape), ("lse", lse, torch.float32, shape[:2]))
-    batch = _kv_batch(q_start, lengths, page_table, T)
+    if not (_rows_fit(q, (T, q_heads, dim), dim, strides, cache)
+            and (out is None or _fits_cache(out, bf16, shape, cache))
+            and (lse is None or _fits_cache(lse, torch.float32, shape[:2], cache))):
+        _need_rows(q, T, q_heads, cache, "q")
+        for name, t, dtype, want in (("out", out, bf16, shape), ("lse", lse, torch.float32, shape[:2])):
+            if t is not None:
+                _need_cache(t, dtype, want, cache, name)
+    batch = _kv_batch(q_start, lengths, page_table, T, cache)
     if workspace is None:
         workspace = new_workspace(kv_attention_workspace_size(batch.B, T, q_heads, cache.heads, dim), cache.device)
     if out is None:

@@ -16,9 +16,14 @@
 // about 1 in 10^6 would differ by a step otherwise.
 //
 // Bound by HBM for a prompt (16-bit rows in, 8-bit pages and turned queries out), by
-// the latency of the lengths, the rows and the page's scale for single tokens.  A
-// block's task is one page run (the new tokens of one page), head and K or V: W warps
-// hold its values in registers, so that they are read and turned once.
+// the latency of the lengths, the rows and the page's scale for single tokens.  A task is
+// one page run (the new tokens of one page), head and K or V: W warps hold its values in
+// registers, so that they are read and turned once.  8192 tokens, 32 query and 8 key heads
+// of 128 channels (189 MB): 51 to 53 us, 0.53 of the copy's rate: each block has a chain of
+// dependent loads (lengths, rows, page), which four blocks an SM do not cover.  Measured on
+// the way: eight warps a task and its page looked up first 83; queries two units in flight,
+// three blocks an SM 64; four blocks 58; the page not waited for before the rows 55.  Pages
+// of 16 tokens: 99 with eight warps a task, 57 with two.  64 single tokens: 4.2 us.
 #include "block_dev.cuh"
 #include "kv_dev.cuh"
 

@@ -19,7 +19,30 @@
 //                    and values' scales
 //   warp 20          keys: TMA, a box a page
 //   warps 21, 22     MMA issuers, a tile each (21 also holds the tensor memory)
-// Work is dealt as in kv_attend_few.cu.  Every wait is bounded (ptx.cuh).
+// Work is dealt as in kv_attend_few.cu, a row tile counting kTcExtra steps more than it has.
+// Waits on mbarriers are bounded (ptx.cuh); the two warps of a row group meet at a hardware
+// barrier, which neither leaves alone (TcRow).
+//
+// What bounds it: a step of both tiles is 2560 clocks of MMAs (of which the scores' halves of
+// 64 keys read shared memory for 768, 512 with 128 keys) and takes about 4100 (1024 new
+// tokens, 32 heads on 8, 16384 keys: 105 steps a CTA in 255 us).  The tensor pipe is active
+// for half of that, and 60 % of the issue slots are taken: 2600 instructions a scheduler and
+// step, of which the weights themselves (multiply-add, exponential, sum, packing) are 620, the
+// maxima 110, the values' conversion 340 and the rest what a call, a wait and a barrier cost.
+// A prompt of 8192 tokens, 32 heads on 8 of 128 channels: 581 to 616 us (0.55 TFLOP of scores
+// and weighted values: 0.47 to 0.5 of the measured fp16 rate); without the softmax the same
+// loop takes two thirds of it.
+//
+// Measured on the way, that prompt and the case of 1024 new tokens (us): all 128 scores of a
+// row in registers, unrolled: 1530 (warps waited for instructions; 64-bit sums over row tiles
+// one by one at the start); short loops 857; MMAs issued under a predicate 828; scores a half
+// ahead of the softmax 759 and 240, by one warp a row group (two: the same by themselves, 610
+// against 665 once the deal counted what a row tile costs); barriers asked with a time for
+// which the thread may be suspended, 252 against 277.  Slower: a warp for both tiles' MMAs; a
+// row group's two warps with a half of the step each and no scores ahead, 757 and 339; the
+// weights before the maximum, 742 and 309; more registers for the softmax by setmaxnreg, one
+// unrolled pass over the scores (no change); pages prefetched to L2 (a chunk of 64 tokens on
+// 131072 keys 148 against 154, the others no change).
 #include <mutex>
 
 #include "block_dev.cuh"

@@ -28,6 +28,15 @@
 // values (4 channels of 4 keys, paired by byte permutes), without bank conflicts:
 // place(row, chunk) = chunk ^ (row & 7), lane's keys as in key_row().
 //
+// What it measured, 64 sequences of 2048 to 8192 keys, 32 heads on 8 of 128 channels, one token
+// each (684 MB): 126 to 130 us, 0.78 to 0.8 of the copy's rate; 2 of 131072 keys, 56 heads on 8
+// (537 MB): 105 to 110 us.  With rows as the MMAs' M: 154 and 111; 16 keys a step: 153 and 122;
+// 6 copies in the ring and 2 CTAs an SM: 138 and 102.  Bound by the memory's rate and, near it,
+// by instructions (about 500 a warp and 32 keys: conversions 190 of them).  With 16 rows
+// (two n-tiles) a warp has 245 registers and an SM two CTAs: 32 sequences of 4096 keys with
+// 16 rows each take 52 us (135 MB), which 3 CTAs of 168 registers (66) and one copy a step
+// (55 to 60) did not improve.
+//
 // Work: the batch's units of 128 keys (32 a warp) are dealt to the CTAs in equal runs,
 // whatever the lengths of the sequences (kv_plan.h); a run that starts or ends inside
 // a row tile leaves its part in the workspace, and kv_join_kernel adds the parts in
