@@ -561,8 +561,8 @@ MOE_W8A8_API moe_status_t moe_w8a8_norm_residual(const void* x, int x_fp32, cons
  *              position: they are not stored and see nothing
  *   page_table [B][table_stride]: the first max_pages of a row are the pages of
  *              the sequence, in order; entries behind its last page are not read.
- *              A page that is written belongs to one sequence; one that is only
- *              read may belong to several
+ *              A page that is written stands once in one sequence's row; one
+ *              that is only read may stand in several
  * The arrays are read on the device: a captured call follows their contents.
  * Lengths beyond max_pages * page count as that; page ids outside [0, n_pages)
  * are never followed: the tokens of such a page are not stored, or not seen, and

@@ -60,9 +60,10 @@ def test_parts_of_wider_rows():
     run(ONE, 32, 128, wide=272, seed=3)
 
 
-def test_many_sequences():
+@pytest.mark.parametrize("count,most", [(700, 4), (2500, 4), (1100, 60)])
+def test_many_sequences(count, most):
     g = torch.Generator().manual_seed(4)
-    run([(int(torch.randint(0, 4, (), generator=g)), int(torch.randint(4, 50, (), generator=g))) for _ in range(700)],
+    run([(int(torch.randint(0, most, (), generator=g)), int(torch.randint(4, 70, (), generator=g))) for _ in range(count)],
         16, 64, 1, 2, rope_dim=16, seed=4)
 
 

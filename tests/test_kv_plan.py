@@ -35,12 +35,11 @@ int main() {
         for (int b = 0; b < B; ++b) lengths[b] = wild ? rnd(100000) - 50000 : rnd(max_pages * page + 1);
         KvBatch bt{q_start.data(), lengths.data(), table.data(), max_pages, B, T, max_pages};
         // pages of new tokens
-        long long runs = 0;
+        std::vector<std::pair<int, int>> by_sequence, by_slot;
         for (int b = 0; b < B; ++b) {
             const KvSeq s = kv_seq(bt, b, page);
             CHECK(s.q0 >= 0 && s.n >= 0 && s.q0 + s.n <= T && s.len >= 0 && s.len <= max_pages * page);
             const int n = kv_run_pages(s, page), first = kv_first_page(s, page);
-            runs += n;
             int tokens = 0;
             for (int i = 0; i < n; ++i) {
                 CHECK(first + i < max_pages);
@@ -48,10 +47,22 @@ int main() {
                 CHECK(hi > lo);
                 CHECK(lo - (s.len - s.n) >= 0 && hi - (s.len - s.n) <= s.n);  // rows of the sequence
                 tokens += hi - lo;
+                by_sequence.push_back({b, first + i});
             }
             CHECK(tokens == kv_min(s.n, s.len));
         }
-        if (!wild) CHECK(runs <= kv_most_runs(B, T, page));
+        const bool by_token = kv_slot_by_token(B, T, page);
+        for (int slot = 0; slot < kv_slots(B, T, page); ++slot) {
+            int b = 0;  // the last sequence that begins at the slot or before; any one where they are wild
+            if (wild) b = rnd(B);
+            else while (b + 1 < B && kv_first_slot(bt, b + 1, page, by_token) <= slot) ++b;
+            const KvSeq s = kv_seq(bt, b, page);
+            const int at = kv_slot_page(s, slot - kv_first_slot(bt, b, page, by_token), page, by_token);
+            CHECK(at >= -1 && at < max_pages);
+            if (at >= 0) by_slot.push_back({b, at});
+            if (at >= 0) CHECK(at >= kv_first_page(s, page) && at < kv_first_page(s, page) + kv_run_pages(s, page));
+        }
+        if (!wild) CHECK(by_slot == by_sequence);
         // attention
         const int row_choice[2] = {16, 256}, tok_choice[2] = {64, 128};
         KvShape sh{1 + rnd(rnd(2) ? 20 : 3), row_choice[rnd(2)], tok_choice[rnd(2)], rnd(2) ? 0 : 1 + rnd(300), page, rnd(3) ? rnd(6) : 0};

@@ -31,6 +31,7 @@ struct KvAppendArgs {
     // set by the launch
     int q_tokens;       // tokens of a block that turns queries
     int store_blocks, task_blocks;
+    bool by_token;      // how a page of new tokens finds its slot (kv_plan.h)
 };
 cudaError_t launch_kv_append(KvAppendArgs a, cudaStream_t st, bool pdl);
 

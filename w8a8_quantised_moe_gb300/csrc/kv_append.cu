@@ -19,11 +19,12 @@
 // the latency of the lengths, the rows and the page's scale for single tokens.  A task is
 // one page run (the new tokens of one page), head and K or V: W warps hold its values in
 // registers, so that they are read and turned once.  8192 tokens, 32 query and 8 key heads
-// of 128 channels (189 MB): 51 to 53 us, 0.53 of the copy's rate: each block has a chain of
+// of 128 channels (189 MB): 47 us, 0.59 of the copy's rate: each block has a chain of
 // dependent loads (lengths, rows, page), which four blocks an SM do not cover.  Measured on
 // the way: eight warps a task and its page looked up first 83; queries two units in flight,
-// three blocks an SM 64; four blocks 58; the page not waited for before the rows 55.  Pages
-// of 16 tokens: 99 with eight warps a task, 57 with two.  64 single tokens: 4.2 us.
+// three blocks an SM 64; four blocks 58; the page not waited for before the rows 55; the
+// runs' sequences from a sum over the batch in each block 51.  Pages of 16 tokens: 99 with
+// eight warps a task, 57 with two.  64 single tokens: 4.7 us (5.0 with that sum).
 #include "block_dev.cuh"
 #include "kv_dev.cuh"
 
@@ -127,8 +128,8 @@ __device__ __forceinline__ uint32_t requant4(uint32_t w, float ratio) {
     return e4m3_pair(f[0], f[1]) | (e4m3_pair(f[2], f[3]) << 16);
 }
 
-// Queries: the block's tokens [t0, t1), every head; two units of a thread in flight (four: 55 us for
-// a prompt of 8192 tokens, two 53).
+// Queries: the block's tokens [t0, t1), every head; two units of a thread in flight (four: 2 us
+// more for a prompt of 8192 tokens).
 constexpr int kApTokens = 16;  // of such a block, at most
 __device__ __forceinline__ void turn_queries(const KvAppendArgs& a, int t0, int t1, int* pos) {
     // the tokens' positions; -1: none to turn
@@ -196,8 +197,7 @@ __device__ __forceinline__ void turn_queries(const KvAppendArgs& a, int t0, int 
 // second half of one of 128 tokens) are read twice.
 template <int W, int NU>
 __global__ void __launch_bounds__(kApThreads, 4) kv_append_kernel(const KvAppendArgs a) {
-    __shared__ int64_t red[kApThreads / 32];
-    __shared__ int run_b, run_page, pos[kApTokens];
+    __shared__ int pos[kApTokens];
     __shared__ float amax_s[kApThreads / 32];
     pdl_wait();
     pdl_trigger();
@@ -206,26 +206,21 @@ __global__ void __launch_bounds__(kApThreads, 4) kv_append_kernel(const KvAppend
         turn_queries(a, t0, kv_min(t0 + a.q_tokens, a.bt.T), pos);
         return;
     }
-    const int run = blockIdx.x / a.task_blocks, P = a.c.page, D = a.c.dim;
-    // the run's sequence and page
-    const int per = (a.bt.B + kApThreads - 1) / kApThreads;
-    const int b0 = kv_min((int)threadIdx.x * per, a.bt.B), b1 = kv_min(b0 + per, a.bt.B);
-    int64_t mine = 0, before;
-    for (int b = b0; b < b1; ++b) mine += kv_run_pages(kv_seq(a.bt, b, P), P);
-    if (run >= block_scan<kApThreads>(mine, before, red)) return;
-    if (run >= before && run < before + mine) {
-        int left = run - (int)before, b = b0;
-        for (;; ++b) {
-            const int n = kv_run_pages(kv_seq(a.bt, b, P), P);
-            if (left < n) break;
-            left -= n;
-        }
-        run_b = b;
-        run_page = left;
+    const int slot = blockIdx.x / a.task_blocks, P = a.c.page, D = a.c.dim;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the slot's sequence, found by each warp for itself, 32 candidates at once
+    int seq = 0;
+    for (int span = a.bt.B; span > 1;) {
+        const int step = (span + 31) / 32, i = lane * step;
+        const bool begun = i < span && kv_first_slot(a.bt, seq + i, P, a.by_token) <= slot;
+        const uint32_t all = __ballot_sync(0xffffffffu, begun);
+        const int last = all == 0 ? 0 : 31 - __clz(all);
+        seq += last * step;
+        span = kv_min(step, span - last * step);
     }
-    __syncthreads();
-    const KvSeq s = kv_seq(a.bt, run_b, P);
-    const int page = kv_first_page(s, P) + run_page;
+    const KvSeq s = kv_seq(a.bt, seq, P);
+    const int page = kv_slot_page(s, slot - kv_first_slot(a.bt, seq, P, a.by_token), P, a.by_token);
+    if (page < 0) return;
     // positions [lo, hi) of the page are new; those before lo are held already
     int lo = kv_max(page * P, kv_max(s.len - s.n, 0)), hi = kv_min(page * P + P, s.len);
     const int held = lo - page * P;
@@ -233,8 +228,7 @@ __global__ void __launch_bounds__(kApThreads, 4) kv_append_kernel(const KvAppend
         if (threadIdx.x == 0) atomicOr(a.error, kErrDevice);
         hi = a.rope_rows;
     }
-    const int id = a.bt.page_table[run_b * a.bt.table_stride + page];  // not waited for before the rows are there
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int id = a.bt.page_table[seq * a.bt.table_stride + page];  // not waited for before the rows are there
     const int task = (blockIdx.x % a.task_blocks) * (8 / W) + warp / W;
     // the warps of a task end as one, so that they meet at their barriers
     if (task >= 2 * a.c.heads || hi <= lo) return;
@@ -326,13 +320,13 @@ __global__ void __launch_bounds__(kApThreads, 4) kv_append_kernel(const KvAppend
 }  // namespace
 
 cudaError_t launch_kv_append(KvAppendArgs a, cudaStream_t st, bool pdl) {
-    const int64_t runs = kv_most_runs(a.bt.B, a.bt.T, a.c.page);
+    a.by_token = kv_slot_by_token(a.bt.B, a.bt.T, a.c.page);
     // A warp a task where a sequence brings a few tokens; else as many as hold a page of
     // new tokens, two units a thread.
     const int page_units = a.c.page * a.c.dim / 16;
     const int W = (int64_t)a.bt.T <= 4 * (int64_t)a.bt.B ? 1 : page_units <= 64 ? 1 : page_units <= 128 ? 2 : page_units <= 256 ? 4 : 8;
     a.task_blocks = (2 * a.c.heads * W + 7) / 8;
-    const int64_t store = runs * a.task_blocks;
+    const int64_t store = kv_slots(a.bt.B, a.bt.T, a.c.page) * a.task_blocks;
     a.q_tokens = 1;
     while (a.q_tokens < kApTokens && (int64_t)a.bt.T / (2 * a.q_tokens) >= 8 * num_sms()) a.q_tokens *= 2;
     const int64_t q_blocks = a.q != nullptr ? (a.bt.T + a.q_tokens - 1) / a.q_tokens : 0;

@@ -46,10 +46,23 @@ KV_HD int kv_first_page(const KvSeq& s, int page) { return kv_max(s.len - s.n, 0
 KV_HD int kv_run_pages(const KvSeq& s, int page) {
     return s.n == 0 || s.len == 0 ? 0 : (s.len - 1) / page - kv_first_page(s, page) + 1;
 }
-// The most that all sequences together can have (each touches at most n / page + 2).
-KV_HD int64_t kv_most_runs(int64_t B, int64_t T, int64_t page) {
-    const int64_t by_pages = T / page + 2 * (B < T ? B : T);
-    return by_pages < T ? by_pages : T;
+// Such a run has a slot: with few tokens a sequence its first token's, else sequence b's runs
+// have those from q_start[b] / page + 2 b on (n tokens touch at most n / page + 2 pages, so
+// that the next sequence's begin behind them).
+KV_HD bool kv_slot_by_token(int64_t B, int64_t T, int64_t page) { return T <= T / page + 2 * B; }
+KV_HD int64_t kv_slots(int64_t B, int64_t T, int64_t page) {
+    return kv_slot_by_token(B, T, page) ? T : T / page + 2 * B;
+}
+// The first slot of sequence b: the sequence of a slot is the last one that begins at it or before.
+KV_HD int kv_first_slot(const KvBatch& bt, int b, int page, bool by_token) {
+    const int q0 = kv_clamp(bt.q_start[b], 0, bt.T);
+    return by_token ? q0 : q0 / page + 2 * b;
+}
+// The page, counted in the sequence, of its i-th slot; -1: none.
+KV_HD int kv_slot_page(const KvSeq& s, int i, int page, bool by_token) {
+    if (!by_token) return i >= 0 && i < kv_run_pages(s, page) ? kv_first_page(s, page) + i : -1;
+    const int p = s.len - s.n + i;
+    return i >= 0 && i < s.n && p >= 0 && (i == 0 || p % page == 0) ? p / page : -1;
 }
 
 // Attention.  The rows of a sequence and key head are its new tokens times the
