@@ -243,6 +243,22 @@ def test_many_sequences():
     run(seqs, 16, 64, heads=1, q_heads=2, seed=13)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_row_tiles_with_one_tile_before_some_with_two(dim):
+    """The second tile's warps pass over row tiles of at most 128 rows; what they then read is their own step's."""
+    seqs = [(33, 2345), (290, 1500), (65, 3000), (288, 2100), (301, 301)]
+    batch = ref.Batch(seqs, 32, seed=18)
+    cache = ref.filled_cache(batch, 8, dim, 18, scales=(-8, 0))
+    q = queries(batch.T, 32, dim, 18)
+    first = moe.kv_attention(q, cache, *batch.args)
+    ref.check_attention(q, cache, batch, first)
+    lines = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(24):
+        if i % 3 == 0:
+            lines.fill_(i)  # the cache from memory, not from L2
+        assert torch.equal(moe.kv_attention(q, cache, *batch.args), first)
+
+
 def test_no_rows():
     batch = ref.Batch([], 16)
     cache = moe.new_kv_cache(1, 2, 64, 16)

@@ -37,7 +37,7 @@ def append(lib, **given):
 
 def attend(lib, short=0, **given):
     c, b = structs(given)
-    a = dict(q=FAKE, q_stride=512, q_heads=4, scale=0.1, window=0, out=FAKE, lse=None, ws=FAKE)
+    a = dict(q=FAKE, q_stride=512, q_heads=4, scale=0.1, window=0, out=2 * FAKE, lse=None, ws=FAKE)
     a.update(given)
     need = lib.moe_w8a8_kv_attention_workspace_size(b.B, b.T, a["q_heads"], c.heads, c.dim) or 1 << 40
     return lib.moe_w8a8_kv_attention(ctypes.addressof(c), ctypes.addressof(b), *a.values(), need - short, None)
@@ -83,13 +83,14 @@ def test_append_only(lib):
         assert append(lib, **bad) == SHAPE, bad
     assert append(lib, rope=None) == INVALID and append(lib, rope_dim=0) == INVALID
     assert append(lib, ws_bytes=255) == WS_SMALL
+    assert append(lib, q_stride=520) == INVALID  # in place, but not contiguous
 
 
 def test_attention_only(lib):
     for bad in (dict(q_heads=1), dict(q_heads=5), dict(q_heads=0)):
         assert attend(lib, **bad) == SHAPE, bad
     for bad in (dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
-                dict(window=-1), dict(lse=FAKE + 2), dict(ws=FAKE + 128)):
+                dict(window=-1), dict(lse=FAKE + 2), dict(ws=FAKE + 128), dict(out=FAKE)):
         assert attend(lib, **bad) == INVALID, bad
     assert attend(lib, short=1) == WS_SMALL
 

@@ -95,6 +95,7 @@ moe_status_t moe_w8a8_kv_append(const moe_w8a8_kv_cache_t* cache, const moe_w8a8
                   rope != nullptr ? static_cast<const void*>(rope) : k, workspace},
                  {cache->k_scale, cache->v_scale, batch->q_start, batch->lengths, batch->page_table}))
         return MOE_ERR_INVALID_ARG;
+    if (q != nullptr && q_out == q && q_stride != q_heads * D) return MOE_ERR_INVALID_ARG;  // in place: contiguous
     if (workspace_bytes < 256 || injected(kInjectWsShort)) return MOE_ERR_WORKSPACE_TOO_SMALL;
     KvAppendArgs a{};
     a.c = cache_of(*cache);
@@ -131,7 +132,7 @@ moe_status_t moe_w8a8_kv_attention(const moe_w8a8_kv_cache_t* cache, const moe_w
     if (B == 0 || T == 0) return MOE_OK;
     if (bad_ptrs({q, out, cache->k, cache->v, workspace},
                  {cache->k_scale, cache->v_scale, batch->q_start, batch->lengths, batch->page_table}) ||
-        !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        out == q || !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return MOE_ERR_INVALID_ARG;
     const AttendLayout L = attend_layout(T, q_heads, cache->heads, D);
     if (workspace_bytes < L.total || injected(kInjectWsShort)) return MOE_ERR_WORKSPACE_TOO_SMALL;

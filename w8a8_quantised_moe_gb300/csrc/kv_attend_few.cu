@@ -81,7 +81,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 template <int D, int NR>
 struct Few {
     static constexpr int kRows = 8 * NR;                      // of a row tile
-    static constexpr int kChunks = D / 16;                    // 16-byte pieces of a row
     static constexpr int kHalf = kFewKeys * D;                // bytes of a copy's keys (or values)
     static constexpr int kStage = 2 * kHalf + 16;             // and the two scales
     static constexpr int kRing = kFewStages * kStage;         // a warp's
@@ -101,6 +100,7 @@ struct Few {
 template <int D>
 struct FewCopies {
     using F = Few<D, 1>;  // (a copy is the same for any rows)
+    static constexpr int kChunks = D / 16;  // 16-byte pieces of a row
     KvPlace at;
     int64_t left;  // copies
     int id, half;
@@ -123,8 +123,8 @@ struct FewCopies {
         if (left > 0) {
             const int lane = threadIdx.x & 31, k0 = key0(), there_are = at.s.len - k0;
             const bool there = there_are > 0 && kv_page_ok(a.c, id, a.error);
-            constexpr int kPer = 32 / F::kChunks;  // rows of an instruction
-            const int c = lane % F::kChunks, row = lane / F::kChunks;
+            constexpr int kPer = 32 / kChunks;  // rows of an instruction
+            const int c = lane % kChunks, row = lane / kChunks;
             const int64_t off =
                 there ? id * a.c.page_stride + (((int64_t)at.head << a.c.page_bits) + (k0 & (a.c.page - 1)) + row) * D + c * 16
                       : 0;
