@@ -29,8 +29,8 @@
 // for half of that, and 60 % of the issue slots are taken: 2600 instructions a scheduler and
 // step, of which the weights themselves (multiply-add, exponential, sum, packing) are 620, the
 // maxima 110, the values' conversion 340 and the rest what a call, a wait and a barrier cost.
-// A prompt of 8192 tokens, 32 heads on 8 of 128 channels: 540 us (0.55 TFLOP of scores
-// and weighted values: 0.54 of the measured bf16 rate); without the softmax the same
+// A prompt of 8192 tokens, 32 heads on 8 of 128 channels: 561 us (0.55 TFLOP of scores
+// and weighted values: 0.52 of the measured bf16 rate); without the softmax the same
 // loop takes two thirds of it.
 //
 // Measured on the way, that prompt and the case of 1024 new tokens (us): all 128 scores of a
@@ -545,6 +545,7 @@ __device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& 
     TcRing v;
     uint32_t s_phase = 0;  // steps
     bool failed = false;   // a wait gave up
+    bool passed = false;   // over a row tile without rows of this tile
     TcRow<D> mine;
     TcWalk walk(work);
     auto start = [&](TcRow<D>& r, const TcWalk& w) {
@@ -559,19 +560,23 @@ __device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& 
         TcWalk next = walk;
         if (t >= walk.tiles(a)) {
             for (int j = 0; j < walk.n; ++j) v.step(kTcVS);
+            passed = true;
             next.next(a);
             start(mine, next);
             walk = next;
             continue;
         }
+        // Steps passed over have not been waited for here, but by the scores' issuer: with the first
+        // scores it is known that the stage's fill before this one is done, whose end has the parity
+        // that the wait below would take for this one's.  (v_full always waited for behind the
+        // step's scores: the prompt 2 % slower.)
+        if (passed) failed = !tc_wait(&bar.s_full[2 * t], s_phase, ctl) || failed;
+        passed = false;
         for (int j = 0; j < walk.n; ++j) {
+            failed = !tc_wait(&bar.v_full[v.stage], v.phase, ctl) || failed;  // its scales
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 failed = !tc_wait(&bar.s_full[2 * t + h], s_phase, ctl) || failed;
-                // The step's scales, after its scores: this warp has not waited for row tiles without
-                // rows of its tile, but the scores' issuer has, so that the stage's fill before this
-                // one is known to be done (its end has the parity that this wait would take for this one's).
-                if (h == 0) failed = !tc_wait(&bar.v_full[v.stage], v.phase, ctl) || failed;
                 tc_fence_after();
                 const float4* scales =
                     reinterpret_cast<const float4*>(smem + Tc<D>::kOffScales) + 8 * v.stage + 4 * h + 2 * part;
