@@ -29,7 +29,7 @@
 // for half of that, and 60 % of the issue slots are taken: 2600 instructions a scheduler and
 // step, of which the weights themselves (multiply-add, exponential, sum, packing) are 620, the
 // maxima 110, the values' conversion 340 and the rest what a call, a wait and a barrier cost.
-// A prompt of 8192 tokens, 32 heads on 8 of 128 channels: 561 us (0.55 TFLOP of scores
+// A prompt of 8192 tokens, 32 heads on 8 of 128 channels: 557 to 571 us (0.55 TFLOP of scores
 // and weighted values: 0.52 of the measured bf16 rate); without the softmax the same
 // loop takes two thirds of it.
 //
