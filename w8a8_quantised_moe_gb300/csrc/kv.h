@@ -49,7 +49,7 @@ struct KvAttendArgs {
     uint64_t timeout_ns;
     int stall;          // test hook (MOE_INJECT=stall)
     // workspace
-    int2* info;         // [T][q_heads]: where a row's parts are (kv_parts.cuh)
+    int2* info;         // [T][q_heads]: where a row's parts are (kv_dev.cuh)
     float* part_o;      // [slots][rows][dim]
     float2* part_ml;    // [slots][rows]
     int slots;          // two a CTA of the grid; set by the launch

@@ -648,9 +648,9 @@ __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& w
         }
         ks = 1.f;
         vs = 0.f;
-        if (there && lane < 8) {
-            ks = __ldg(a.c.k_scale + id * a.c.scale_stride + p.head);
-            vs = __ldg(a.c.v_scale + id * a.c.scale_stride + p.head);
+        if (there && lane < 8) {  // (no __ldg: an append before this launch writes parts of these lines from several SMs)
+            ks = a.c.k_scale[id * a.c.scale_stride + p.head];
+            vs = a.c.v_scale[id * a.c.scale_stride + p.head];
         }
         if (++j == walk.n) {
             walk.next(a);
