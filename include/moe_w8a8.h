@@ -564,9 +564,11 @@ MOE_W8A8_API moe_status_t moe_w8a8_norm_residual(const void* x, int x_fp32, cons
  *              A page that is written stands once in one sequence's row; one
  *              that is only read may stand in several
  * The arrays are read on the device: a captured call follows their contents.
- * Lengths beyond max_pages * page count as that; page ids outside [0, n_pages)
- * are never followed: the tokens of such a page are not stored, or not seen, and
- * the error word is set (MOE_ERR_DEVICE from moe_w8a8_device_error).
+ * Page ids outside [0, n_pages) are never followed: the tokens of such a page are
+ * not stored, or not seen, and the error word is set (MOE_ERR_DEVICE from
+ * moe_w8a8_device_error).  Of a sequence longer than max_pages * page the append
+ * leaves out the new tokens at the positions behind, their queries too, and sets the
+ * error word; attention takes it as one of max_pages * page tokens.
  * 0 <= B, T <= 2^20; max_pages * page <= 2^30.  B == 0 or T == 0 is a no-op.
  * Strides of q, k and v are elements from token to token, multiples of 8; a
  * token's heads are contiguous.  Pointers are 16-byte aligned, those of scales,

@@ -1,0 +1,92 @@
+"""The paged cache at the limits of what its calls are told, on the host: the tokens that an append
+stores, whatever the lengths say."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from w8a8_quantised_moe_gb300 import build
+
+STORED = r"""
+#include <climits>
+#include <cstdio>
+#include <set>
+#include <utility>
+#include <vector>
+#include "kv_plan.h"
+using namespace moe;
+static unsigned long long state = 1234567890123ull;
+static int rnd(int n) { state ^= state << 13; state ^= state >> 7; state ^= state << 17; return (int)(state % n); }
+#define CHECK(x) do { if (!(x)) { std::printf("line %d: %s (case %d)\n", __LINE__, #x, kase); return 1; } } while (0)
+int main() {
+    for (int kase = 0; kase < 6000; ++kase) {
+        const int pages[4] = {16, 32, 64, 128}, page = pages[rnd(4)];
+        const int B = 1 + rnd(6), max_pages = rnd(5), cap = max_pages * page;
+        std::vector<int> q_start(B + 1), lengths(B);
+        int at = rnd(3);
+        for (int b = 0; b <= B; ++b) {
+            q_start[b] = at;
+            at += rnd(3) ? rnd(5) : rnd(300);
+        }
+        const int T = q_start[B] + rnd(4);
+        for (int b = 0; b < B; ++b) {
+            const int n = q_start[b + 1] - q_start[b];
+            const int choice[8] = {rnd(cap + 1), cap, cap + 1, cap + rnd(n + 2), cap + n, cap + n + 1 + rnd(200), INT_MAX, -rnd(50)};
+            lengths[b] = choice[rnd(8)];
+        }
+        KvBatch bt{q_start.data(), lengths.data(), nullptr, max_pages, B, T, max_pages};
+        const bool by_token = kv_slot_by_token(B, T, page);
+        std::set<std::pair<int, int>> stored, want;
+        int reported = 0, reports = 0;
+        for (int slot = 0; slot < kv_slots(B, T, page); ++slot) {
+            int b = 0;
+            while (b + 1 < B && kv_first_slot(bt, b + 1, page, by_token) <= slot) ++b;
+            int over;
+            const KvSeq s = kv_seq_stored(bt, b, page, over);
+            const int run = slot - kv_first_slot(bt, b, page, by_token);
+            if (over > 0 && run == 0) ++reported;
+            const int p = kv_slot_page(s, run, page, by_token);
+            if (p < 0) continue;
+            CHECK(p < max_pages);
+            const int lo = kv_max(p * page, kv_max(s.len - s.n, 0)), hi = kv_min(p * page + page, s.len);
+            CHECK(hi > lo);
+            for (int pos = lo; pos < hi; ++pos) {
+                const int row = s.q0 + pos - (s.len - s.n);
+                CHECK(row >= q_start[b] && row < q_start[b + 1]);
+                CHECK(stored.insert({row, pos}).second);
+            }
+        }
+        for (int b = 0; b < B; ++b) {
+            const long long n = q_start[b + 1] - q_start[b], L = lengths[b] < 0 ? 0 : lengths[b];
+            for (int i = 0; i < n; ++i) {
+                const long long pos = L - n + i;
+                if (pos >= 0 && pos < cap) want.insert({q_start[b] + i, (int)pos});
+            }
+            reports += n > 0 && L > cap;
+            int over;
+            const KvSeq s = kv_seq_stored(bt, b, page, over);
+            CHECK(s.q0 == q_start[b] && s.n >= 0 && over >= 0 && s.n + over == n && s.len <= cap);
+            CHECK(s.n == 0 || (long long)s.len - s.n == L - n);
+        }
+        CHECK(stored == want);
+        CHECK(reported == reports);
+    }
+    std::printf("ok\n");
+    return 0;
+}
+"""
+
+
+def test_an_append_stores_each_token_at_its_position_or_not_at_all(tmp_path):
+    if shutil.which("g++") is None:
+        pytest.skip("g++ not found")
+    (tmp_path / "stored.cc").write_text(STORED)
+    exe = str(tmp_path / "stored")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover", "-I", build.CSRC,
+                    str(tmp_path / "stored.cc"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+    with open(os.path.join(build.CSRC, "kv_append.cu")) as f:
+        text = f.read()
+    assert "kv_seq_stored(" in text and "kv_seq(" not in text

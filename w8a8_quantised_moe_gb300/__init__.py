@@ -706,8 +706,10 @@ def kv_append(cache, k, v, q_start, lengths, page_table, q=None, rope=None, inte
     [B, pages] as in include/moe_w8a8.h, on the device; rope fp32 [positions,
     rope_dim]: cosines, then sines, of a position's angles, or None; interleaved:
     pairs are neighbours, not half a rope_dim apart.  Returns the turned queries, bf16
-    [T, q_heads, dim] (``q_out`` where given), or None without q.  A bad page id or a
-    position outside the table is reported by ``device_error(cache.status)``."""
+    [T, q_heads, dim] (``q_out`` where given), or None without q.  A bad page id, a length
+    beyond the page table or a position outside ``rope`` is reported by
+    ``device_error(cache.status)``; such tokens are left out, their rows of the queries as
+    they were."""
     if stream is not None and q is not None and q_out is None:
         with _on(stream):
             return kv_append(cache, k, v, q_start, lengths, page_table, q, rope, interleaved)

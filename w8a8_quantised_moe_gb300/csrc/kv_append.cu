@@ -7,6 +7,7 @@
 //     code = E4M3 nearest to value / s, ties to the even mantissa
 //   a page that holds tokens already: s' = max(s, the new tokens' s); where s' > s its
 //     codes are rounded again, E4M3(code s / s')
+//   a token at a position behind its sequence's pages, or the table of angles: left out, reported
 //
 // A power of two costs nothing: E4M3 keeps the same relative precision at any scale,
 // quotients by it are exact, and rounding codes again is exact but for subnormals, so
@@ -143,8 +144,9 @@ __device__ __forceinline__ void turn_queries(const KvAppendArgs& a, int t0, int 
         }
         int p = -1;
         if (lo < a.bt.B) {  // else a row behind the last sequence
-            const KvSeq s = kv_seq(a.bt, lo, a.c.page);
-            if (t >= s.q0) p = s.len - s.n + t - s.q0;
+            int over;
+            const KvSeq s = kv_seq_stored(a.bt, lo, a.c.page, over);
+            if (t >= s.q0 && t < s.q0 + s.n) p = s.len - s.n + t - s.q0;
         }
         if (a.rope_dim > 0 && p >= a.rope_rows) {
             atomicOr(a.error, kErrDevice);
@@ -218,8 +220,11 @@ __global__ void __launch_bounds__(kApThreads, 4) kv_append_kernel(const KvAppend
         seq += last * step;
         span = kv_min(step, span - last * step);
     }
-    const KvSeq s = kv_seq(a.bt, seq, P);
-    const int page = kv_slot_page(s, slot - kv_first_slot(a.bt, seq, P, a.by_token), P, a.by_token);
+    int over;
+    const KvSeq s = kv_seq_stored(a.bt, seq, P, over);
+    const int run = slot - kv_first_slot(a.bt, seq, P, a.by_token);
+    if (over > 0 && run == 0 && threadIdx.x == 0) atomicOr(a.error, kErrDevice);  // no pages for them
+    const int page = kv_slot_page(s, run, P, a.by_token);
     if (page < 0) return;
     // positions [lo, hi) of the page are new; those before lo are held already
     int lo = kv_max(page * P, kv_max(s.len - s.n, 0)), hi = kv_min(page * P + P, s.len);

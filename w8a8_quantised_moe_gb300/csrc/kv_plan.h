@@ -39,6 +39,15 @@ KV_HD KvSeq kv_seq(const KvBatch& bt, int b, int page) {
     s.len = kv_clamp(bt.lengths[b], 0, bt.max_pages * page);
     return s;
 }
+// The same for a call that stores the new tokens: those at positions behind the sequence's
+// pages are left out (`over` of them), so that the others keep theirs.  Reading alone, as above,
+// takes such a sequence as one that ends with its pages.
+KV_HD KvSeq kv_seq_stored(const KvBatch& bt, int b, int page, int& over) {
+    KvSeq s = kv_seq(bt, b, page);
+    over = kv_min(kv_max(bt.lengths[b], 0) - s.len, s.n);
+    s.n -= over;
+    return s;
+}
 
 // Pages that hold a sequence's new tokens (those at positions 0 and up): the
 // first of them and how many.
