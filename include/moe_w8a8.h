@@ -560,7 +560,9 @@ MOE_W8A8_API moe_status_t moe_w8a8_norm_residual(const void* x, int x_fp32, cons
  *              smaller than their number have, as far as they do not fit, no
  *              position: they are not stored and see nothing
  *   page_table [B][table_stride]: the first max_pages of a row are the pages of
- *              the sequence, in order; entries behind its last page are not read.
+ *              the sequence, in order; entries behind its last page are not read,
+ *              and pages whose tokens no row sees any more, before the window,
+ *              need not be the cache's.
  *              A page that is written stands once in one sequence's row; one
  *              that is only read may stand in several
  * The arrays are read on the device: a captured call follows their contents.

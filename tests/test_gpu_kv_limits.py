@@ -1,14 +1,21 @@
-"""The paged cache at the limits of what its calls are told: tokens behind the page table."""
+"""The paged cache at the limits of what its calls are told: tokens behind the page table, pages
+behind the window."""
 import pytest
 import torch
 
 import kv_reference as ref
 import w8a8_quantised_moe_gb300 as moe
 from test_gpu_kv_append import rows
+from test_gpu_kv_attention import queries
 
 pytestmark = pytest.mark.gpu
 
 INT_MAX = 2**31 - 1
+
+
+def space(batch, q_heads, cache):
+    return moe.new_workspace(
+        moe.kv_attention_workspace_size(len(batch.seqs), batch.T, q_heads, cache.heads, cache.dim))
 
 
 @pytest.mark.parametrize("over", [1, "some", "all", "past", INT_MAX])
@@ -73,3 +80,38 @@ def test_a_decoding_loop_that_runs_past_its_pages():
     assert moe.device_error(cache.status) == -7
     for name, was in zip(("k", "v", "k_scale", "v_scale"), full):
         assert torch.equal(getattr(cache, name), was), name
+
+
+def behind(batch, window):
+    """[first key that a row of the sequence sees]"""
+    return [max(0, length - n - window + 1) if window else 0 for n, length in batch.seqs]
+
+
+WINDOWED = [[(1, 700), (1, 300), (1, 40)], [(6, 701), (3, 299)], [(100, 702), (70, 300), (1, 500)]]
+
+
+@pytest.mark.parametrize("window", [1, 17, 100, 129])
+@pytest.mark.parametrize("seqs", WINDOWED, ids=["one", "few", "many"])
+@pytest.mark.parametrize("page,dim", [(16, 64), (64, 128), (128, 64)])
+def test_pages_behind_the_window_are_not_asked_for(page, dim, seqs, window):
+    """A serving loop takes pages back that no row sees any more: their entries are no pages, and no error."""
+    batch = ref.Batch(seqs, page, seed=20)
+    cache = ref.filled_cache(batch, 2, dim, 20)
+    q = queries(batch.T, 8, dim, 20)
+    ws = space(batch, 8, cache)
+    lse = torch.empty(batch.T, 8, device="cuda")
+    want = moe.kv_attention(q, cache, *batch.args, window=window, workspace=ws, lse=lse)
+    ref.check_attention(q, cache, batch, want, lse, window=window)
+    assert moe.device_error(ws) == 0
+    table, taken = batch.args[2].clone(), 0
+    for b, first in enumerate(behind(batch, window)):
+        table[b, :first // page] = -1
+        taken += first // page
+    assert taken > 0
+    got = moe.kv_attention(q, cache, *batch.args[:2], table, window=window, workspace=ws)
+    assert torch.equal(got, want) and moe.device_error(ws) == 0
+    # a page with a key that is seen is still asked for
+    b, first = max(enumerate(behind(batch, window)), key=lambda x: x[1])
+    table[b, first // page] = -1
+    moe.kv_attention(q, cache, *batch.args[:2], table, window=window, workspace=ws)
+    assert moe.device_error(ws) == -7

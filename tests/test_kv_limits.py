@@ -1,5 +1,5 @@
 """The paged cache at the limits of what its calls are told, on the host: the tokens that an append
-stores, whatever the lengths say."""
+stores, whatever the lengths say, and the first key that a row tile sees."""
 import os
 import shutil
 import subprocess
@@ -77,16 +77,55 @@ int main() {
 }
 """
 
+FIRST_KEY = r"""
+#include <cstdio>
+#include "kv_plan.h"
+using namespace moe;
+static unsigned long long state = 987654321987ull;
+static int rnd(int n) { state ^= state << 13; state ^= state >> 7; state ^= state << 17; return (int)(state % n); }
+#define CHECK(x) do { if (!(x)) { std::printf("line %d: %s (case %d)\n", __LINE__, #x, kase); return 1; } } while (0)
+int main() {
+    for (int kase = 0; kase < 20000; ++kase) {
+        const int rows[3] = {8, 16, 256};
+        const KvShape sh{1 + rnd(rnd(2) ? 40 : 3), rows[rnd(3)], 128, rnd(3) ? 1 + rnd(rnd(2) ? 20 : 400) : 0, 16, 0};
+        const KvSeq s{0, 1 + rnd(rnd(2) ? 5 : 300), rnd(900)};
+        for (int rt = 0; rt < kv_row_tiles(s, sh); ++rt) {
+            int unit, count;
+            kv_units(s, sh, rt, unit, count);
+            const int got = kv_first_key(s, sh, rt);
+            int first = 1 << 30;  // key that a row sees
+            const int end = kv_min((rt + 1) * sh.rows, s.n * sh.group);
+            for (int r = rt * sh.rows; r < end; ++r) {
+                const int pos = s.len - s.n + r / sh.group;
+                if (pos >= 0) first = kv_min(first, sh.window ? kv_max(pos - sh.window + 1, 0) : 0);
+            }
+            CHECK(first == 1 << 30 || got == first);
+            CHECK(got >= 0 && (got == 0 || got / sh.tokens == unit));
+        }
+    }
+    std::printf("ok\n");
+    return 0;
+}
+"""
 
-def test_an_append_stores_each_token_at_its_position_or_not_at_all(tmp_path):
+
+def compiled(tmp_path, text):
     if shutil.which("g++") is None:
         pytest.skip("g++ not found")
-    (tmp_path / "stored.cc").write_text(STORED)
-    exe = str(tmp_path / "stored")
+    (tmp_path / "program.cc").write_text(text)
+    exe = str(tmp_path / "program")
     subprocess.run(["g++", "-O1", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover", "-I", build.CSRC,
-                    str(tmp_path / "stored.cc"), "-o", exe], check=True)
+                    str(tmp_path / "program.cc"), "-o", exe], check=True)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+def test_the_first_key_that_a_row_tile_sees(tmp_path):
+    compiled(tmp_path, FIRST_KEY)
+
+
+def test_an_append_stores_each_token_at_its_position_or_not_at_all(tmp_path):
+    compiled(tmp_path, STORED)
     with open(os.path.join(build.CSRC, "kv_append.cu")) as f:
         text = f.read()
     assert "kv_seq_stored(" in text and "kv_seq(" not in text

@@ -17,7 +17,7 @@
 //                    rises by more than 2^8, by the same threads
 //   warps 16-19      values: codes from global memory to fp16 in shared memory, keys'
 //                    and values' scales
-//   warp 20          keys: TMA, a box a page
+//   warp 20          keys: TMA, a box a page; reports pages that are not the cache's
 //   warps 21, 22     MMA issuers, a tile each (21 also holds the tensor memory)
 // Work is dealt as in kv_attend_few.cu, a row tile counting kTcExtra steps more than it has.
 // Waits on mbarriers are bounded (ptx.cuh); the two warps of a row group meet at a hardware
@@ -631,7 +631,6 @@ __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& w
         const int k0 = (p.unit + j) * kTcTile, keys = p.s.len - k0;  // keys of the step that are there
         const int id = ids;
         const bool there = (unsigned)id < (unsigned)a.c.n_pages;
-        if (!there && lane < 8 && 16 * lane < keys) atomicOr(a.error, kErrDevice);
         // where this lane's group begins (a page that is not there: nothing)
         const int in_page = (16 * (lane & 7)) & (a.c.page - 1);
         const uint8_t* group = a.c.v + (there ? id * a.c.page_stride + ((p.head << a.c.page_bits) + in_page) * D : 0);
@@ -708,7 +707,12 @@ __device__ __forceinline__ void tc_keys(const KvAttendArgs& a, const KvWork& wor
         for (int j = 0; j < walk.n; ++j, ++it) {
             if (j == 0 && it != 0 && lane < boxes) id = tc_page(a, walk.at, walk.at.unit * kTcTile, lane * groups);
             // a page that is not there is read as one behind the last: zeros
-            const int page = (unsigned)id < (unsigned)a.c.n_pages ? id : no_page;
+            // (bad pages are reported here, the values' warps having no register for it: 7 % of a prompt's time)
+            const bool there = (unsigned)id < (unsigned)a.c.n_pages;
+            const int page = there ? id : no_page, from = (walk.at.unit + j) * kTcTile + lane * a.c.page;
+            if (!there && lane < boxes && from < walk.at.s.len &&
+                from + a.c.page > kv_first_key(walk.at.s, a.sh, walk.at.rt))
+                atomicOr(a.error, kErrDevice);
             if (lane < boxes && j + 1 < walk.n) id = tc_page(a, walk.at, (walk.at.unit + j + 1) * kTcTile, lane * groups);
             if (lane == 0) {
                 ok = mbar_wait(&bar.k_empty[k.stage], k.phase ^ 1u, ctl);

@@ -107,6 +107,7 @@ struct FewCopies {
     KvPlace at;
     int64_t left;  // copies
     int id, half;
+    int seen;  // the row tile's first seen key
     __device__ __forceinline__ int key0() const {
         return at.unit * kKvFewTokens + ((int)(threadIdx.x >> 5) * kFewStep + half) * kFewKeys;
     }
@@ -116,16 +117,17 @@ struct FewCopies {
     }
     __device__ __forceinline__ void start(const KvAttendArgs& a, const KvWork& w) {
         at = w.at;
+        seen = kv_first_key(at.s, a.sh, at.rt);
         left = (w.u1 - w.u0) * kFewStep;
         half = 0;
         if (left > 0) look_up(a);
     }
     // Copies 16 keys, their values and the two scales to `stage`; what is not there
-    // (behind the sequence, another's page) becomes 0, its scales too.
+    // (behind the sequence, another's page, before the window) becomes 0, its scales too.
     __device__ __forceinline__ void issue(const KvAttendArgs& a, uint8_t* stage) {
         if (left > 0) {
             const int lane = threadIdx.x & 31, k0 = key0(), there_are = at.s.len - k0;
-            const bool there = there_are > 0 && kv_page_ok(a.c, id, a.error);
+            const bool there = there_are > 0 && k0 + kFewKeys > seen && kv_page_ok(a.c, id, a.error);
             constexpr int kPer = 32 / kChunks;  // rows of an instruction
             const int c = lane % kChunks, row = lane / kChunks;
             const int64_t off =
@@ -159,6 +161,7 @@ struct FewCopies {
                 if (++half == kFewStep) {
                     half = 0;
                     kv_next(at, a.bt, a.sh, a.c.heads);
+                    if (at.unit == at.first) seen = kv_first_key(at.s, a.sh, at.rt);
                 }
                 look_up(a);
             }

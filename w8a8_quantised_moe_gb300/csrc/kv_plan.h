@@ -91,6 +91,11 @@ KV_HD void kv_units(const KvSeq& s, const KvShape& sh, int rt, int& first, int& 
     first = sh.window > 0 && p0 >= sh.window ? (p0 - sh.window + 1) / sh.tokens : 0;
     count = p1 < 0 ? 1 : p1 / sh.tokens + 1 - first;
 }
+// The first key that a row of the row tile sees.  Pages before it need not be there: a serving
+// loop takes back those that nobody sees any more.
+KV_HD int kv_first_key(const KvSeq& s, const KvShape& sh, int rt) {
+    return sh.window > 0 ? kv_max(s.len - s.n + rt * sh.rows / sh.group - sh.window + 1, 0) : 0;
+}
 
 // sum of floor((a i + b) / m) over 0 <= i < n, for a, b >= 0 and m > 0: the points of the
 // lattice under a line.  Whole parts of the slope and of b are counted at once; what
