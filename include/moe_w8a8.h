@@ -544,7 +544,10 @@ MOE_W8A8_API moe_status_t moe_w8a8_norm_residual(const void* x, int x_fp32, cons
  *
  * moe_w8a8_kv_cache_t: device memory of the caller.
  *   k, v       E4M3 codes [n_pages][heads][page][dim], page_stride bytes (a
- *              multiple of 16) from one page to the next, the rest contiguous
+ *              multiple of 16) from one page to the next, the rest contiguous.
+ *              Of tokens that a row sees they are numbers, as the append's are
+ *              (a NaN code of v can reach rows that do not see it); what is not
+ *              finite goes into the block's scale.  Other codes may be anything
  *   k_scale, v_scale  fp32 [n_pages][heads], scale_stride values from page to
  *              page; positive (values' scales below 2^-64 count as 2^-64; a
  *              value block whose scale is 0 is not seen)
@@ -561,8 +564,8 @@ MOE_W8A8_API moe_status_t moe_w8a8_norm_residual(const void* x, int x_fp32, cons
  *              position: they are not stored and see nothing
  *   page_table [B][table_stride]: the first max_pages of a row are the pages of
  *              the sequence, in order; entries behind its last page are not read,
- *              and pages whose tokens no row sees any more, before the window,
- *              need not be the cache's.
+ *              and those of pages whose tokens no row sees any more, before the
+ *              window, may name any page or none.
  *              A page that is written stands once in one sequence's row; one
  *              that is only read may stand in several
  * The arrays are read on the device: a captured call follows their contents.

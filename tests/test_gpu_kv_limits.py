@@ -1,5 +1,7 @@
 """The paged cache at the limits of what its calls are told: tokens behind the page table, pages
 behind the window."""
+import math
+
 import pytest
 import torch
 
@@ -115,3 +117,27 @@ def test_pages_behind_the_window_are_not_asked_for(page, dim, seqs, window):
     table[b, first // page] = -1
     moe.kv_attention(q, cache, *batch.args[:2], table, window=window, workspace=ws)
     assert moe.device_error(ws) == -7
+
+
+@pytest.mark.parametrize("window", [1, 17, 100, 129])
+@pytest.mark.parametrize("seqs", WINDOWED, ids=["one", "few", "many"])
+@pytest.mark.parametrize("page,dim", [(16, 64), (64, 128), (128, 64)])
+def test_what_is_behind_the_window_reaches_nobody(page, dim, seqs, window):
+    """Entries of pages that hold another sequence's tokens, or nothing yet (codes and scales of any bits), and
+    such codes before the first seen key of a page."""
+    batch = ref.Batch(seqs, page, seed=21)
+    cache = ref.filled_cache(batch, 2, dim, 21)
+    q = queries(batch.T, 8, dim, 21)
+    ws = space(batch, 8, cache)
+    want = moe.kv_attention(q, cache, *batch.args, window=window, workspace=ws)
+    ref.check_attention(q, cache, batch, want, window=window)
+    for scale in (math.nan, math.inf, -1.0):
+        cache.k_scale[batch.spare], cache.v_scale[batch.spare] = scale, scale
+        table = batch.args[2].clone()
+        for b, first in enumerate(behind(batch, window)):
+            table[b, :first // page] = batch.spare[0]  # NaN codes
+            p = int(batch.table[b, first // page])
+            cache.k[p, :, :first % page] = 0xFF
+            cache.v[p, :, :first % page] = 0x7F
+        got = moe.kv_attention(q, cache, *batch.args[:2], table, window=window, workspace=ws)
+        assert torch.equal(got, want) and moe.device_error(ws) == 0

@@ -610,7 +610,10 @@ __device__ __forceinline__ void tc_softmax(const KvAttendArgs& a, const KvWork& 
 }
 
 // ------------------------------------------------------------------ values
-template <int D>
+// WINDOW: the call has a window; values before it become 0, as those behind the sequence (a weight
+// of 0 does not undo a NaN).  A kernel of its own, as the bound costs the others 4 to 7 % of a
+// prompt (registers).
+template <int D, bool WINDOW>
 __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& work, uint8_t* smem, const TcBars& bar,
                                           const WaitCtl& ctl) {
     constexpr int kPerRow = D / 16, kRows = 128 / kPerRow, kPasses = kTcTile / kRows;  // rows of a pass
@@ -630,7 +633,8 @@ __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& w
         const KvPlace& p = walk.at;
         const int k0 = (p.unit + j) * kTcTile, keys = p.s.len - k0;  // keys of the step that are there
         const int id = ids;
-        const bool there = (unsigned)id < (unsigned)a.c.n_pages;
+        const int from = WINDOW ? kv_first_key(p.s, a.sh, p.rt) - k0 : 0;
+        const bool there = (unsigned)id < (unsigned)a.c.n_pages && (!WINDOW || 16 * (lane & 7) + 16 > from);
         // where this lane's group begins (a page that is not there: nothing)
         const int in_page = (16 * (lane & 7)) & (a.c.page - 1);
         const uint8_t* group = a.c.v + (there ? id * a.c.page_stride + ((p.head << a.c.page_bits) + in_page) * D : 0);
@@ -642,7 +646,7 @@ __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& w
             const int key = i * kRows + row, g = D == 128 ? i : key >> 4;
             const uint64_t at = (uint64_t)__shfl_sync(0xffffffffu, hi, g) << 32 | __shfl_sync(0xffffffffu, lo, g);
             w[i] = make_uint4(0, 0, 0, 0);
-            if ((ok >> g & 1) && key < keys)
+            if ((ok >> g & 1) && key < keys && (!WINDOW || key >= from))
                 w[i] = __ldg(reinterpret_cast<const uint4*>(at + ((key & 15) * D + c * 16)));
         }
         ks = 1.f;
@@ -867,7 +871,7 @@ __device__ __forceinline__ void tc_products(const KvAttendArgs& a, const KvWork&
     if (lane == 0) mbar_wait_drain(&bar.teardown[t], 0);
 }
 
-template <int D>
+template <int D, bool WINDOW>
 __global__ void __launch_bounds__(kTcThreads, 1)
     kv_attend_kernel(const __grid_constant__ CUtensorMap keys, const KvAttendArgs a, int no_page) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -920,7 +924,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (warp < kTcValues0)
             tc_softmax<D>(a, *work, smem, bar, tmem, ctl);
         else if (warp < kTcKeys0)
-            tc_values<D>(a, *work, smem, bar, ctl);
+            tc_values<D, WINDOW>(a, *work, smem, bar, ctl);
         else if (warp == kTcKeys0)
             tc_keys<D>(a, *work, smem, bar, &keys, no_page, ctl);
         else if (warp < kTcProducts0 + 2)
@@ -935,9 +939,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
 }
 
-template <int D>
+template <int D, bool WINDOW>
 cudaError_t launch_tc(const KvAttendArgs& a, cudaStream_t st, bool pdl) {
-    auto kern = kv_attend_kernel<D>;
+    auto kern = kv_attend_kernel<D, WINDOW>;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     std::call_once(once, [&] {
@@ -964,7 +968,9 @@ cudaError_t launch_kv_attend(KvAttendArgs a, cudaStream_t st, bool pdl) {
     a.sh.tokens = kTcTile;
     a.sh.extra = kTcExtra;
     a.slots = 2 * kv_tc_ctas();
-    const cudaError_t e = a.c.dim == 64 ? launch_tc<64>(a, st, pdl) : launch_tc<128>(a, st, pdl);
+    const bool d64 = a.c.dim == 64;
+    const cudaError_t e = a.sh.window > 0 ? (d64 ? launch_tc<64, true>(a, st, pdl) : launch_tc<128, true>(a, st, pdl))
+                                          : (d64 ? launch_tc<64, false>(a, st, pdl) : launch_tc<128, false>(a, st, pdl));
     return e != cudaSuccess ? e : launch_kv_join(a, st, pdl);
 }
 

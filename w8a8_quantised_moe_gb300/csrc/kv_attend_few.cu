@@ -99,8 +99,9 @@ struct Few {
 };
 
 // The steps of a CTA's run, as one warp copies them, 16 keys at a time: the page of the
-// next copy is looked up a copy ahead.
-template <int D>
+// next copy is looked up a copy ahead.  WINDOW: the call has a window; a kernel of its own, as
+// the first seen key costs the others 5 % of a batch with drafted tokens (registers).
+template <int D, bool WINDOW>
 struct FewCopies {
     using F = Few<D, 1>;  // (a copy is the same for any rows)
     static constexpr int kChunks = D / 16;  // 16-byte pieces of a row
@@ -117,24 +118,25 @@ struct FewCopies {
     }
     __device__ __forceinline__ void start(const KvAttendArgs& a, const KvWork& w) {
         at = w.at;
-        seen = kv_first_key(at.s, a.sh, at.rt);
+        seen = WINDOW ? kv_first_key(at.s, a.sh, at.rt) : 0;
         left = (w.u1 - w.u0) * kFewStep;
         half = 0;
         if (left > 0) look_up(a);
     }
     // Copies 16 keys, their values and the two scales to `stage`; what is not there
-    // (behind the sequence, another's page, before the window) becomes 0, its scales too.
+    // (behind the sequence, another's page, before the window) becomes 0, its scales too; so do
+    // the values before the window in a page that reaches into it: a weight of 0 does not undo a NaN.
     __device__ __forceinline__ void issue(const KvAttendArgs& a, uint8_t* stage) {
         if (left > 0) {
             const int lane = threadIdx.x & 31, k0 = key0(), there_are = at.s.len - k0;
-            const bool there = there_are > 0 && k0 + kFewKeys > seen && kv_page_ok(a.c, id, a.error);
+            const bool there = there_are > 0 && (!WINDOW || k0 + kFewKeys > seen) && kv_page_ok(a.c, id, a.error);
             constexpr int kPer = 32 / kChunks;  // rows of an instruction
             const int c = lane % kChunks, row = lane / kChunks;
             const int64_t off =
                 there ? id * a.c.page_stride + (((int64_t)at.head << a.c.page_bits) + (k0 & (a.c.page - 1)) + row) * D + c * 16
                       : 0;
             const uint8_t *k = a.c.k + off, *v = a.c.v + off;
-            if (there && there_are >= kFewKeys) {
+            if (there && there_are >= kFewKeys && (!WINDOW || k0 >= seen)) {
 #pragma unroll
                 for (int i = 0; i < kFewKeys / kPer; ++i) {
                     uint8_t* dst = stage + F::place(i * kPer + row, c);
@@ -147,7 +149,8 @@ struct FewCopies {
                     const bool valid = there && i * kPer + row < there_are;
                     uint8_t* dst = stage + F::place(i * kPer + row, c);
                     cp_async16_zfill(dst, k + (valid ? i * kPer * D : 0), valid);
-                    cp_async16_zfill(dst + F::kHalf, v + (valid ? i * kPer * D : 0), valid);
+                    const bool value = valid && (!WINDOW || k0 + i * kPer + row >= seen);
+                    cp_async16_zfill(dst + F::kHalf, v + (value ? i * kPer * D : 0), value);
                 }
             }
             if (lane < 2) {
@@ -161,7 +164,7 @@ struct FewCopies {
                 if (++half == kFewStep) {
                     half = 0;
                     kv_next(at, a.bt, a.sh, a.c.heads);
-                    if (at.unit == at.first) seen = kv_first_key(at.s, a.sh, at.rt);
+                    if (WINDOW && at.unit == at.first) seen = kv_first_key(at.s, a.sh, at.rt);
                 }
                 look_up(a);
             }
@@ -374,7 +377,7 @@ __device__ __forceinline__ void write_out4(const KvAttendArgs& a, int64_t row, i
     if (c == 0 && a.lse != nullptr) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-template <int D, int NR>
+template <int D, int NR, bool WINDOW>
 __global__ void __launch_bounds__(kFewThreads, Few<D, NR>::kCtas) kv_attend_few_kernel(const KvAttendArgs a) {
     using F = Few<D, NR>;
     constexpr int kRows = F::kRows;
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(kFewThreads, Few<D, NR>::kCtas) kv_attend_few_
     const int64_t units = work->u1 - work->u0;
     if (units <= 0) return;
 
-    FewCopies<D> copies;
+    FewCopies<D, WINDOW> copies;
     copies.start(a, *work);
 #pragma unroll
     for (int i = 0; i < kFewStages - kFewStep; ++i) copies.issue(a, ring + i * F::kStage);
@@ -585,10 +588,10 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttendArgs a, int 
     }
 }
 
-template <int D, int NR>
-cudaError_t launch_few(KvAttendArgs& a, cudaStream_t st, bool pdl) {
+template <int D, int NR, bool WINDOW>
+cudaError_t launch_few_kernel(KvAttendArgs& a, cudaStream_t st, bool pdl) {
     using F = Few<D, NR>;
-    auto kern = kv_attend_few_kernel<D, NR>;
+    auto kern = kv_attend_few_kernel<D, NR, WINDOW>;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     std::call_once(once, [&] {
@@ -598,6 +601,10 @@ cudaError_t launch_few(KvAttendArgs& a, cudaStream_t st, bool pdl) {
     a.sh.rows = F::kRows;
     a.slots = 2 * F::kCtas * num_sms();
     return launch_kernel(kern, dim3(F::kCtas * num_sms()), dim3(kFewThreads), F::kSmem, st, pdl, a);
+}
+template <int D, int NR>
+cudaError_t launch_few(KvAttendArgs& a, cudaStream_t st, bool pdl) {
+    return a.sh.window > 0 ? launch_few_kernel<D, NR, true>(a, st, pdl) : launch_few_kernel<D, NR, false>(a, st, pdl);
 }
 
 }  // namespace

@@ -91,8 +91,8 @@ KV_HD void kv_units(const KvSeq& s, const KvShape& sh, int rt, int& first, int& 
     first = sh.window > 0 && p0 >= sh.window ? (p0 - sh.window + 1) / sh.tokens : 0;
     count = p1 < 0 ? 1 : p1 / sh.tokens + 1 - first;
 }
-// The first key that a row of the row tile sees.  Pages before it need not be there: a serving
-// loop takes back those that nobody sees any more.
+// The first key that a row of the row tile sees.  What lies before it may be anything: a serving
+// loop takes back pages that nobody sees any more.
 KV_HD int kv_first_key(const KvSeq& s, const KvShape& sh, int rt) {
     return sh.window > 0 ? kv_max(s.len - s.n + rt * sh.rows / sh.group - sh.window + 1, 0) : 0;
 }
