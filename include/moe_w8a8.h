@@ -550,7 +550,8 @@ MOE_W8A8_API moe_status_t moe_w8a8_norm_residual(const void* x, int x_fp32, cons
  *              finite goes into the block's scale.  Other codes may be anything
  *   k_scale, v_scale  fp32 [n_pages][heads], scale_stride values from page to
  *              page; positive (values' scales below 2^-64 count as 2^-64; a
- *              value block whose scale is 0 is not seen)
+ *              value block whose scale is 0 is not seen; a scale that is not
+ *              finite makes every result NaN that sees a token of the block)
  *   page 16, 32, 64 or 128; dim 64 or 128; 1 <= heads <= 256.
  *
  * moe_w8a8_kv_batch_t: B sequences with T new tokens in all.

@@ -1,5 +1,5 @@
 """The paged cache at the limits of what its calls are told: tokens behind the page table, pages
-behind the window."""
+behind the window, scales that are not finite."""
 import math
 
 import pytest
@@ -141,3 +141,22 @@ def test_what_is_behind_the_window_reaches_nobody(page, dim, seqs, window):
             cache.v[p, :, :first % page] = 0x7F
         got = moe.kv_attention(q, cache, *batch.args[:2], table, window=window, workspace=ws)
         assert torch.equal(got, want) and moe.device_error(ws) == 0
+
+
+@pytest.mark.parametrize("n", [1, 140])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_scales_that_are_infinite(n, dim):
+    """They count as NaN: for the rows that see the block, and for no others."""
+    batch = ref.Batch([(n, 200), (n, 150)], 16, seed=9)
+    cache = ref.filled_cache(batch, 2, dim, 9)
+    q = queries(batch.T, 4, dim, 9)
+    clean = moe.kv_attention(q, cache, *batch.args)
+    page = int(batch.table[0, 12])  # tokens 192.., seen by the last 8 rows
+    for scales, head in ((cache.k_scale, 0), (cache.v_scale, 1)):
+        kept = scales[page].clone()
+        scales[page, head] = math.inf
+        got = moe.kv_attention(q, cache, *batch.args)
+        hit = torch.zeros(batch.T, 4, dtype=torch.bool, device="cuda")
+        hit[max(0, n - 8):n, 2 * head:2 * head + 2] = True
+        assert got[hit].isnan().all() and torch.equal(got[~hit], clean[~hit])
+        scales[page] = kept

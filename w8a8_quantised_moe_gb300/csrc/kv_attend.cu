@@ -685,7 +685,8 @@ __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& w
         if (tid < 8) {
             float lg, inv;
             value_scale(vs, lg, inv);
-            reinterpret_cast<float4*>(smem + Tc<D>::kOffScales)[8 * v.stage + tid] = make_float4(ks, lg, inv, 0.f);
+            reinterpret_cast<float4*>(smem + Tc<D>::kOffScales)[8 * v.stage + tid] =
+                make_float4(finite_scale(ks), lg, inv, 0.f);
         }
         fence_proxy_async_smem();
         __syncwarp();

@@ -270,12 +270,13 @@ struct FewRows {
         for (int b = 0; b < kFewStep; ++b) {
             const float2 sc = *reinterpret_cast<const float2*>(stage[b] + 2 * F::kHalf);
             float lg;
+            const float key = finite_scale(sc.x);
             value_scale(sc.y, lg, inv[b]);
             gone = gone || sc.y == 0.f;
 #pragma unroll
             for (int n = 0; n < NR; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[b][n][i] = fmaf(s[b][n][i], sc.x * factor[n][i & 1], lg);
+                for (int i = 0; i < 4; ++i) s[b][n][i] = fmaf(s[b][n][i], key * factor[n][i & 1], lg);
         }
         const int window = a.sh.window;
         if (k0 + kFewStep * kFewKeys - 1 > pos_min || (window > 0 && k0 <= pos_max - window) || gone) {

@@ -36,15 +36,19 @@ __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// A block's scale where it is finite, else NaN.
+__device__ __forceinline__ float finite_scale(float s) { return fabsf(s) < INFINITY ? s : __uint_as_float(0x7fffffffu); }
 // A value block's scale as the attention uses it: the exponent that the weights
 // take up, log2(scale), and 1 / scale, by which the sum of the weights is put right.
-// A scale of 0 stands for a block that is not seen.  NaN stays NaN.
+// A scale of 0 stands for a block that is not seen.  What is not finite counts as NaN: with an
+// infinite addend a hidden score of -inf would become NaN.
 __device__ __forceinline__ void value_scale(float s, float& lg, float& inv) {
     if (s == 0.f) {
         lg = -INFINITY;
         inv = 0.f;
     } else {
         if (s < kMinScale) s = kMinScale;
+        s = finite_scale(s);
         lg = log2f(s);
         inv = __frcp_rn(s);
     }
