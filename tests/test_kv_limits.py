@@ -1,6 +1,8 @@
 """The paged cache at the limits of what its calls are told, on the host: the tokens that an append
-stores, whatever the lengths say, and the first key that a row tile sees."""
+stores, whatever the lengths say, and the first key that a row tile sees; and no loads by the
+read-only path."""
 import os
+import re
 import shutil
 import subprocess
 
@@ -129,3 +131,13 @@ def test_an_append_stores_each_token_at_its_position_or_not_at_all(tmp_path):
     with open(os.path.join(build.CSRC, "kv_append.cu")) as f:
         text = f.read()
     assert "kv_seq_stored(" in text and "kv_seq(" not in text
+
+
+def test_no_load_by_the_read_only_path():
+    """Kernels that start before the one that writes their input has ended may not use it."""
+    names = [n for n in os.listdir(build.CSRC) if re.match(r"(api_)?kv.*\.(cu|cuh|h)$", n)]
+    assert {"kv_append.cu", "kv_attend.cu", "kv_attend_few.cu", "kv_dev.cuh"} <= set(names)
+    for name in names:
+        with open(os.path.join(build.CSRC, name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        assert not re.search(r"__ldg\b|\.nc\b|__restrict__", text), name

@@ -1,6 +1,10 @@
 // kv.h -- declarations of the paged 8-bit key/value cache: appending to it
 // (kv_append.cu) and attention over it (kv_attend_few.cu, kv_attend.cu).
 //
+// These kernels may start while the kernel before them on the stream still writes what they read
+// (an append its queries, codes and scales): every load is a coherent one, none goes by the
+// read-only path, whose data must not change while a kernel lives.
+//
 // A block of the cache is the tokens of one page and head: E4M3 codes [page][dim]
 // and one binary32 scale, for keys and for values.
 #pragma once

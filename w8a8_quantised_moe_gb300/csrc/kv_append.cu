@@ -72,7 +72,7 @@ template <bool ODD>
 __device__ __forceinline__ void turn_unit(float (&f)[16], const Unit& u, const float* row, int half) {
     const float4* pc = reinterpret_cast<const float4*>(row + u.angle);
     const float4* ps = reinterpret_cast<const float4*>(row + half + u.angle);
-    const float4 c0 = __ldg(pc), c1 = __ldg(pc + 1), s0 = __ldg(ps), s1 = __ldg(ps + 1);
+    const float4 c0 = pc[0], c1 = pc[1], s0 = ps[0], s1 = ps[1];
     const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
     const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
     auto turn = [&](float& a, float& b, int i) {

@@ -221,7 +221,7 @@ struct TcRing {
 // Pages of 16-key groups: group i of the step that begins at key k0; -1: none there.
 __device__ __forceinline__ int tc_page(const KvAttendArgs& a, const KvPlace& p, int k0, int i) {
     const int k = k0 + 16 * i;
-    return k < p.s.len ? __ldg(a.bt.page_table + p.b * a.bt.table_stride + (k >> a.c.page_bits)) : -1;
+    return k < p.s.len ? a.bt.page_table[p.b * a.bt.table_stride + (k >> a.c.page_bits)] : -1;
 }
 
 // max of three
@@ -305,7 +305,7 @@ struct TcRow {
         auto source = [&](int i) {
             const int rr = i * kRows + lane / kLanes;
             const uint16_t* src = a.q + of.q_row(rr) + part * kCols + lane % kLanes * 8;
-            return r0 + rr < rows ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+            return r0 + rr < rows ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
         };
         uint4 w[kLoads];
 #pragma unroll
@@ -647,11 +647,11 @@ __device__ __forceinline__ void tc_values(const KvAttendArgs& a, const KvWork& w
             const uint64_t at = (uint64_t)__shfl_sync(0xffffffffu, hi, g) << 32 | __shfl_sync(0xffffffffu, lo, g);
             w[i] = make_uint4(0, 0, 0, 0);
             if ((ok >> g & 1) && key < keys && (!WINDOW || key >= from))
-                w[i] = __ldg(reinterpret_cast<const uint4*>(at + ((key & 15) * D + c * 16)));
+                w[i] = __ldcg(reinterpret_cast<const uint4*>(at + ((key & 15) * D + c * 16)));
         }
         ks = 1.f;
         vs = 0.f;
-        if (there && lane < 8) {  // (no __ldg: an append before this launch writes parts of these lines from several SMs)
+        if (there && lane < 8) {
             ks = a.c.k_scale[id * a.c.scale_stride + p.head];
             vs = a.c.v_scale[id * a.c.scale_stride + p.head];
         }

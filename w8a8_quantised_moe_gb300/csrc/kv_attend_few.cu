@@ -114,7 +114,7 @@ struct FewCopies {
     }
     __device__ __forceinline__ void look_up(const KvAttendArgs& a) {
         const int k0 = key0();
-        id = k0 < at.s.len ? __ldg(a.bt.page_table + at.b * a.bt.table_stride + (k0 >> a.c.page_bits)) : -1;
+        id = k0 < at.s.len ? a.bt.page_table[at.b * a.bt.table_stride + (k0 >> a.c.page_bits)] : -1;
     }
     __device__ __forceinline__ void start(const KvAttendArgs& a, const KvWork& w) {
         at = w.at;
@@ -200,7 +200,7 @@ struct FewRows {
             uint32_t top = 0;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
-                w[s] = __ldg(reinterpret_cast<const uint2*>(row + (s >> 2) * 64 + 16 * t + 4 * (s & 3)));
+                w[s] = *reinterpret_cast<const uint2*>(row + (s >> 2) * 64 + 16 * t + 4 * (s & 3));
                 // magnitudes of bf16 pairs, compared as whole numbers
                 top = __vmaxu2(top, __vmaxu2(w[s].x & 0x7fff7fffu, w[s].y & 0x7fff7fffu));
             }
