@@ -590,7 +590,8 @@ MOE_W8A8_API moe_status_t moe_w8a8_norm_residual(const void* x, int x_fp32, cons
  *              rope_dim a multiple of 16, at most dim.  Tokens whose position is
  *              not in the table are left out, and the error word is set
  *   q, q_out   bf16 [T][q_heads][dim], q_out contiguous; q may be NULL (no
- *              queries), q_out may be q where q is contiguous
+ *              queries), q_out may be q where q is contiguous; else it shares no
+ *              memory with q, k or v
  *   workspace  256 bytes, zeroed once: the error word
  * Codes are those of the exact products with the table's values; queries are
  * turned in binary32 and rounded once.
@@ -600,7 +601,7 @@ MOE_W8A8_API moe_status_t moe_w8a8_norm_residual(const void* x, int x_fp32, cons
  *   p = L - n + i,  s_j = scale <q, k_j> for 0 <= j <= p (and j > p - window),
  *   out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)
  *   q          bf16, turned already; out bf16 [T][q_heads][dim], rounded once,
- *              not q's memory; lse fp32 [T][q_heads] or NULL
+ *              none of it in q's rows; lse fp32 [T][q_heads] or NULL
  *   scale      positive; window 0: every key up to p
  *   workspace  >= moe_w8a8_kv_attention_workspace_size(B, T, q_heads, heads,
  *              dim) bytes, which do not fall with B or T; 256-byte aligned, the

@@ -1,6 +1,6 @@
 """The paged cache at the limits of what its calls are told, on the host: the tokens that an append
 stores, whatever the lengths say, and the first key that a row tile sees; and no loads by the
-read-only path."""
+read-only path; and outputs in their inputs' memory."""
 import os
 import re
 import shutil
@@ -8,6 +8,7 @@ import subprocess
 
 import pytest
 
+from test_kv_abi import CUDA, FAKE, INVALID, append, attend, lib  # noqa: F401 (lib: the fixture)
 from w8a8_quantised_moe_gb300 import build
 
 STORED = r"""
@@ -141,3 +142,27 @@ def test_no_load_by_the_read_only_path():
         with open(os.path.join(build.CSRC, name)) as f:
             text = re.sub(r"//[^\n]*", "", f.read())
         assert not re.search(r"__ldg\b|\.nc\b|__restrict__", text), name
+
+
+def meets(out, width, rows, w, stride, T):
+    """Whether bytes [out, out + 2 width T) are in one of the T rows of 2 w bytes, 2 stride apart."""
+    return any(rows + 2 * i * stride < out + 2 * width * T and out < rows + 2 * (i * stride + w) for i in range(T))
+
+
+@pytest.mark.parametrize("T", [1, 5])
+@pytest.mark.parametrize("stride", [512, 520, 4096])
+def test_outputs_that_share_memory_with_their_inputs(lib, monkeypatch, T, stride):
+    """4 heads of 128 channels: rows of 1024 bytes."""
+    monkeypatch.setenv("MOE_INJECT", "launch_fail")  # what passes the checks ends there
+    far, seen = 1 << 28, set()
+    for off in [*range(-6 * 1024, 6 * 8192, 16 * 13), -1024 * T, -1024 * T - 16, -1024 * T + 16, 0, 16, -16, 1008, 1024, 1040]:
+        hit = meets(FAKE + off, 512, FAKE, 512, stride, T)
+        seen.add(hit)
+        assert attend(lib, T=T, q=FAKE, q_stride=stride, out=FAKE + off) == (INVALID if hit else CUDA), off
+        away = dict(T=T, key=far, value=far, q=2 * far, q_stride=stride, k_stride=stride, v_stride=stride)
+        want = CUDA if not hit or (off == 0 and stride == 512) else INVALID
+        assert append(lib, **{**away, "q": FAKE, "q_out": FAKE + off}) == want, off
+        for name in ("key", "value"):  # 2 heads: rows of 512 bytes
+            hit = meets(FAKE + off, 512, FAKE, 256, stride, T)
+            assert append(lib, **{**away, name: FAKE, "q_out": FAKE + off}) == (INVALID if hit else CUDA), (name, off)
+    assert seen == {False, True}

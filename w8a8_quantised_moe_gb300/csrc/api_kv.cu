@@ -28,6 +28,15 @@ bool row_stride_ok(int64_t stride, int64_t heads, int64_t D) {
 }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Whether T contiguous rows of `width` bf16 values at `out` share bytes with T rows of `w` at
+// `in`, `stride` values from one to the next (stride >= w).
+bool rows_meet(const uint16_t* out, int64_t width, const uint16_t* in, int64_t w, int64_t stride, int64_t T) {
+    const uint64_t o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in);
+    const uint64_t end = o + 2 * (uint64_t)(T * width), row = 2 * (uint64_t)w, step = 2 * (uint64_t)stride;
+    const uint64_t n = i + row > o ? 0 : (o - i - row) / step + 1;  // the first row that ends behind `o`
+    return n < (uint64_t)T && i + n * step < end;
+}
+
 bool bad_ptrs(std::initializer_list<const void*> by16, std::initializer_list<const void*> by4) {
     for (const void* p : by16)
         if (p == nullptr || !aligned16(p)) return true;
@@ -96,6 +105,11 @@ moe_status_t moe_w8a8_kv_append(const moe_w8a8_kv_cache_t* cache, const moe_w8a8
                  {cache->k_scale, cache->v_scale, batch->q_start, batch->lengths, batch->page_table}))
         return MOE_ERR_INVALID_ARG;
     if (q != nullptr && q_out == q && q_stride != q_heads * D) return MOE_ERR_INVALID_ARG;  // in place: contiguous
+    const int64_t T = batch->T, width = q_heads * D, kv = cache->heads * D;
+    if (q != nullptr && q_out != q &&
+        (rows_meet(q_out, width, q, width, q_stride, T) || rows_meet(q_out, width, k, kv, k_stride, T) ||
+         rows_meet(q_out, width, v, kv, v_stride, T)))
+        return MOE_ERR_INVALID_ARG;
     if (workspace_bytes < 256 || injected(kInjectWsShort)) return MOE_ERR_WORKSPACE_TOO_SMALL;
     KvAppendArgs a{};
     a.c = cache_of(*cache);
@@ -132,7 +146,7 @@ moe_status_t moe_w8a8_kv_attention(const moe_w8a8_kv_cache_t* cache, const moe_w
     if (B == 0 || T == 0) return MOE_OK;
     if (bad_ptrs({q, out, cache->k, cache->v, workspace},
                  {cache->k_scale, cache->v_scale, batch->q_start, batch->lengths, batch->page_table}) ||
-        out == q || !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        rows_meet(out, q_heads * D, q, q_heads * D, q_stride, T) || !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return MOE_ERR_INVALID_ARG;
     const AttendLayout L = attend_layout(T, q_heads, cache->heads, D);
     if (workspace_bytes < L.total || injected(kInjectWsShort)) return MOE_ERR_WORKSPACE_TOO_SMALL;
