@@ -610,8 +610,12 @@ cudaError_t launch_few(KvAttendArgs& a, cudaStream_t st, bool pdl) {
 
 }  // namespace
 
-// Rows of the parts that a grid of either form leaves, at most two a CTA.
-int64_t kv_few_part_rows() { return 2 * (int64_t)num_sms() * (3 * 8 > 2 * 16 ? 3 * 8 : 2 * 16); }
+// Rows of the parts that a grid of either form leaves, at most two a CTA (for any D).
+int64_t kv_few_part_rows() {
+    constexpr int k8 = Few<128, 1>::kCtas * Few<128, 1>::kRows, k16 = Few<128, 2>::kCtas * Few<128, 2>::kRows;
+    static_assert(k8 == Few<64, 1>::kCtas * Few<64, 1>::kRows && k16 == Few<64, 2>::kCtas * Few<64, 2>::kRows, "rows");
+    return 2 * (int64_t)num_sms() * (k8 > k16 ? k8 : k16);
+}
 
 cudaError_t launch_kv_attend_few(KvAttendArgs a, cudaStream_t st, bool pdl) {
     a.sh.tokens = kKvFewTokens;

@@ -27,7 +27,6 @@ struct KvBatch {
 KV_HD int kv_clamp(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 KV_HD int kv_min(int a, int b) { return a < b ? a : b; }
 KV_HD int kv_max(int a, int b) { return a > b ? a : b; }
-KV_HD int64_t kv_min64(int64_t a, int64_t b) { return a < b ? a : b; }
 
 struct KvSeq {
     int q0, n, len;  // first row, new tokens, cached tokens (the new ones included)
