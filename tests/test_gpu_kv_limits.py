@@ -1,10 +1,11 @@
 """The paged cache at the limits of what its calls are told: tokens behind the page table, pages
-behind the window, scales that are not finite."""
+behind the window, scales that are not finite, scores of thousands, bad pages."""
 import math
 
 import pytest
 import torch
 
+import block_reference as block
 import kv_reference as ref
 import w8a8_quantised_moe_gb300 as moe
 from test_gpu_kv_append import rows
@@ -160,3 +161,61 @@ def test_scales_that_are_infinite(n, dim):
         hit[max(0, n - 8):n, 2 * head:2 * head + 2] = True
         assert got[hit].isnan().all() and torch.equal(got[~hit], clean[~hit])
         scales[page] = kept
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("seqs", [[(1, 130), (1, 700)], [(70, 130), (33, 400)]], ids=["one", "many"])
+def test_scores_of_thousands_find_their_key(seqs, dim):
+    """Each query is one key's direction, 2^60 long: that key's score is ahead by thousands, so that the
+    output is its value (bf16 holds an E4M3 code times a power of two; a weight of any size cancels but for the
+    2^-12 by which fp16 holds it) and the log sum its score (all products positive: 2^-16 of it for the sums,
+    as much again for the query's parts and the exponent's argument)."""
+    batch = ref.Batch(seqs, 32, seed=22)
+    cache = ref.filled_cache(batch, 2, dim, 22)
+    cache.k_scale.copy_(torch.where(cache.k_scale.isnan(), cache.k_scale, 2.0**-6))
+    val = block.e4m3_values().cuda()
+    g = torch.Generator().manual_seed(22)
+    q = torch.zeros(batch.T, 4, dim, dtype=torch.float64, device="cuda")
+    want, want_lse = torch.zeros_like(q), torch.zeros(batch.T, 4, dtype=torch.float64, device="cuda")
+    scale = 2.0**-50
+    for b, (n, length) in enumerate(seqs):
+        pages = batch.args[2][b, : -(-length // 32)].long()
+        for h in range(4):
+            kv = h // 2
+            k = (val[cache.k[pages, kv].long()] * cache.k_scale[pages, kv].double()[:, None, None]).flatten(0, 1)
+            v = (val[cache.v[pages, kv].long()] * cache.v_scale[pages, kv].double()[:, None, None]).flatten(0, 1)
+            for i in range(n):
+                seen = length - n + i + 1
+                j = int(torch.randint(seen, (), generator=g))
+                x = k[j] * 2.0**60
+                s = scale * (k[:seen] @ x)
+                s[j], top = -math.inf, float(s[j])
+                assert float(s.max()) < top - 4000
+                r = batch.starts[b] + i
+                q[r, h], want[r, h], want_lse[r, h] = x, v[j], top
+    assert (q.bfloat16().double() == q).all() and (want.bfloat16().double() == want).all()
+    lse = torch.empty(batch.T, 4, device="cuda")
+    got = moe.kv_attention(q.bfloat16(), cache, *batch.args, scale=scale, lse=lse)
+    assert (got.double() == want).all()
+    assert ((lse.double() - want_lse).abs() <= 2.0**-14 * want_lse).all()
+
+
+@pytest.mark.parametrize("n", [1, 100])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_bad_pages_against_the_reference(n, dim):
+    """The other keys' attention, as if the bad pages' tokens had never been there."""
+    batch = ref.Batch([(n, 200), (n, 150)], 16, seed=23)
+    cache = ref.filled_cache(batch, 2, dim, 23)
+    q = queries(batch.T, 4, dim, 23)
+    table = batch.args[2].clone()
+    table[0, 2], table[0, 3] = -1, batch.n_pages
+    ws = space(batch, 4, cache)
+    lse = torch.empty(batch.T, 4, device="cuda")
+    got = moe.kv_attention(q, cache, *batch.args[:2], table, workspace=ws, lse=lse)
+    assert moe.device_error(ws) == -7
+    batch.seqs[0] = (n, 200 - 32)  # 32 tokens before the first row
+    whole = batch.args[2]
+    shorter = whole.clone()
+    shorter[0, 2:-2] = whole[0, 4:]
+    batch.args = (*batch.args[:2], shorter)
+    ref.check_attention(q, cache, batch, got, lse)
