@@ -535,9 +535,10 @@ MOE_W8A8_API moe_status_t moe_w8a8_norm_residual(const void* x, int x_fp32, cons
  * for values; a value is its code times its block's scale.  moe_w8a8_kv_append
  * gives a block the scale 2^E, E the least integer >= -64 with
  * max |value| <= 448 * 2^E, and the E4M3 codes nearest to value / 2^E (ties to
- * even).  Where new tokens come into a page that holds tokens of their sequence
- * already, the block keeps the larger of its scale and theirs, and where that
- * grows the codes that it holds are rounded again, to E4M3(code * old / new):
+ * even; where a caller's scale that is no power of two stays, to value * (1 / scale),
+ * rounded in binary32).  Where new tokens come into a page that holds tokens of
+ * their sequence already, the block keeps the larger of its scale and theirs, and
+ * where that grows the codes that it holds are rounded again, to E4M3(code * old / new):
  * exact but for codes that become subnormal.  A value that is not finite makes
  * its block's scale NaN (and the new codes 0) until the page is begun anew, and
  * with it every result that sees a token of the block, no other.
@@ -605,12 +606,18 @@ MOE_W8A8_API moe_status_t moe_w8a8_norm_residual(const void* x, int x_fp32, cons
  *   scale      positive; window 0: every key up to p
  *   workspace  >= moe_w8a8_kv_attention_workspace_size(B, T, q_heads, heads,
  *              dim) bytes, which do not fall with B or T; 256-byte aligned, the
- *              first 256 bytes zeroed once
+ *              first 256 bytes zeroed once; of its own for each call that may
+ *              overlap another on the GPU, replays of graphs included
  * A row that sees no key has out 0 and lse -inf.  Scores are binary32 sums of
  * exact products (of a query row to 2^-17 of its largest channel), weights fp16
- * (11 bits), sums binary32.  Results depend in their last bits on the batch:
- * where a sequence is cut into parts, and which form of row tiles its average
- * number of rows takes.  One launch, and one that joins the parts.
+ * (11 bits, at least 2^-31 of the row's largest), sums binary32.  A weight is taken
+ * together with its value block's scale: where the scales of a head's value
+ * blocks are more than 2^100 apart, keys of the smaller ones can be lost (blocks of
+ * zeros have an append's least, 2^-64: so values stay below 2^44).  Results depend in their
+ * last bits on the batch: where a sequence is cut into parts, and which form of row
+ * tiles its average number of rows takes; so does the time of a batch that mixes
+ * long prompts with many single tokens or empty places.  One launch, and one
+ * that joins the parts.
  * ------------------------------------------------------------------------- */
 typedef struct {
     uint8_t* k;

@@ -219,3 +219,18 @@ def test_bad_pages_against_the_reference(n, dim):
     shorter[0, 2:-2] = whole[0, 4:]
     batch.args = (*batch.args[:2], shorter)
     ref.check_attention(q, cache, batch, got, lse)
+
+
+@pytest.mark.parametrize("seqs", [[(1, 257), (1, 1000)], [(100, 100), (37, 400)]], ids=["one", "many"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_value_scales_up_to_2_to_100_apart(seqs, dim):
+    """A key's weight and its block's scale share one exponent.  A weight is lost where that product is 2^132
+    below the row's largest, so is 2^-32 of that key's weight or less where the scales are 2^100 apart: a
+    thousand such keys stay within the 2^-20 that the log sum has."""
+    batch = ref.Batch(seqs, 16, seed=24)
+    cache = ref.filled_cache(batch, 2, dim, 24, scales=(-64, 37))
+    cache.k_scale.copy_(torch.where(cache.k_scale.isnan(), cache.k_scale, 2.0**-6))
+    q = queries(batch.T, 4, dim, 24)
+    lse = torch.empty(batch.T, 4, device="cuda")
+    got = moe.kv_attention(q, cache, *batch.args, lse=lse)
+    ref.check_attention(q, cache, batch, got, lse)

@@ -58,9 +58,14 @@ struct AttendLayout {
     size_t info, part_ml, part_o, total;
 };
 // Rows (new token, query head of a key head) that B sequences have on average, beyond which
-// row tiles of 256 are taken.  32 sequences of 4096 keys, 4 key heads of 128 channels, us in
-// tiles of 8 or 16 and of 256: 16 rows 52 / 93, 32 rows 76 / 92, 48 rows 107 / 94, 64 rows
-// 131 / 96; 2 of 32768: 16 rows 37 / 49, 32 rows 46 / 49, 64 rows 74 / 49.
+// row tiles of 256 are taken.  32 sequences of 4096 keys, 4 key heads, us in tiles of 8 or 16
+// and of 256, with 128 channels: 16 rows 50 / 91, 32 rows 74 / 91, 48 rows 104 / 92, 64 rows
+// 130 / 94; with 64: 35 / 67, 55 / 68, 79 / 69, 98 / 68.  2 of 32768: 16 rows 37 / 46, 32 rows
+// 45 / 46, 64 rows 71 / 46; with 64: 30 / 41, 36 / 41, 55 / 40.
+// The average is the batch's, sequences without new tokens counted, and all of it takes one form:
+// batches whose sequences differ pay for it (63 single tokens with a chunk of 256, which by
+// themselves take 97 and 39 us: 234; a prompt of 8192 tokens in a batch of 1024 places, the
+// others empty: 5028, in tiles of 256 518).
 constexpr int64_t kManyRows = 32;
 bool many_rows(int64_t B, int64_t T, int64_t group) { return T * group > kManyRows * B; }
 

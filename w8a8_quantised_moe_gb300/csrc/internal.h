@@ -173,8 +173,9 @@ LinLayout lin_layout(int64_t M, int64_t N, int64_t K);
 // CTA of its predecessor is running, so no grid can hold the SMs that an
 // earlier one still needs.  The first kernel of each entry point of the layers
 // is launched without PDL (it then serialises like a plain launch); the
-// block-scaled linear layer, the block-scaled layer's form for a few tokens and
-// the norms launch their first with it, which waits like any other.  The dp4a
+// block-scaled linear layer, the block-scaled layer's form for a few tokens, the
+// norms, the paged cache's append and the attention over it launch their first with
+// it, which waits like any other.  The dp4a
 // GEMM reads the expert offsets and its weights before its wait, the few-row
 // block-scaled products their weights and the experts' ids or offsets (all
 // complete before its predecessor passed its own wait).  A kernel with tensor

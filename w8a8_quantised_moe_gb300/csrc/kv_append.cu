@@ -18,9 +18,10 @@
 //
 // Bound by HBM for a prompt (16-bit rows in, 8-bit pages and turned queries out), by
 // the latency of the lengths, the rows and the page's scale for single tokens.  A task is
-// one page run (the new tokens of one page), head and K or V: W warps hold its values in
-// registers, so that they are read and turned once.  8192 tokens, 32 query and 8 key heads
-// of 128 channels (189 MB): 47 us, 0.59 of the copy's rate: each block has a chain of
+// one page run (the new tokens of one page), head and K or V: W warps hold its values, two
+// units of 16 a thread, so that they are read and turned once.  (64 registers, for four blocks
+// an SM: the compiler spills 160 to 240 bytes a thread.)  8192 tokens, 32 query and 8 key heads
+// of 128 channels (189 MB): 48 us, 0.58 of the copy's rate: each block has a chain of
 // dependent loads (lengths, rows, page), which four blocks an SM do not cover.  Measured on
 // the way: eight warps a task and its page looked up first 83; queries two units in flight,
 // three blocks an SM 64; four blocks 58; the page not waited for before the rows 55; the

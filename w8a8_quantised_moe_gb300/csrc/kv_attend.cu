@@ -29,9 +29,11 @@
 // for half of that, and 60 % of the issue slots are taken: 2600 instructions a scheduler and
 // step, of which the weights themselves (multiply-add, exponential, sum, packing) are 620, the
 // maxima 110, the values' conversion 340 and the rest what a call, a wait and a barrier cost.
-// A prompt of 8192 tokens, 32 heads on 8 of 128 channels: 557 to 571 us (0.55 TFLOP of scores
-// and weighted values: 0.52 of the measured bf16 rate); without the softmax the same
-// loop takes two thirds of it.
+// A prompt of 8192 tokens, 32 heads on 8 of 128 channels: 555 to 562 us (0.55 TFLOP of scores
+// and weighted values: 0.53 of the measured bf16 rate); without the softmax the same
+// loop takes two thirds of it.  768 threads leave 80 registers each, of which the compiler
+// spills 160 to 190 bytes a thread: one more value held in the values' warps costs a prompt up to
+// 7 %.
 //
 // Measured on the way, that prompt and the case of 1024 new tokens (us): all 128 scores of a
 // row in registers, unrolled: 1530 (warps waited for instructions; 64-bit sums over row tiles
@@ -58,8 +60,9 @@ constexpr int kTcTile = 128;      // rows of a tile, keys of a step
 constexpr int kTcHalf = 64;       // keys of half a step, whose scores are one of a tile's two buffers
 constexpr int kTcKS = 2, kTcVS = 2;  // stages of keys, of values (three of keys: the same times)
 // What beginning and ending a row tile costs, in steps, for the deal.  A prompt of 8192
-// tokens, 0 / 2 / 4 / 6 / 8: 809 / 706 / 590 / 581 / 593 us (the CTAs with a head's first row
-// tiles have up to 29 of them).
+// tokens, 0 / 2 / 4 / 6 / 8: 809 / 706 / 590 / 581 / 593 us with 128 channels (before the join was
+// made faster), 519 / 439 / 437 / 447 / 453 with 64 (the CTAs with a head's first row tiles have up
+// to 29 of them).
 constexpr int kTcExtra = 6;
 constexpr float kTcHeadroom = 8.f, kTcWeightBits = 6.f;  // as in kv_attend_few.cu
 constexpr uint32_t kTcCols = 512;

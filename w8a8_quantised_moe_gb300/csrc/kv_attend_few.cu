@@ -29,12 +29,12 @@
 // place(row, chunk) = chunk ^ (row & 7), lane's keys as in key_row().
 //
 // What it measured, 64 sequences of 2048 to 8192 keys, 32 heads on 8 of 128 channels, one token
-// each (684 MB): 126 to 130 us, 0.78 to 0.8 of the copy's rate; 2 of 131072 keys, 56 heads on 8
+// each (684 MB): 124 to 130 us, 0.78 to 0.81 of the copy's rate; 2 of 131072 keys, 56 heads on 8
 // (537 MB): 105 to 110 us.  With rows as the MMAs' M: 154 and 111; 16 keys a step: 153 and 122;
 // 6 copies in the ring and 2 CTAs an SM: 138 and 102.  Bound by the memory's rate and, near it,
 // by instructions (about 500 a warp and 32 keys: conversions 190 of them).  With 16 rows
 // (two n-tiles) a warp has 245 registers and an SM two CTAs: 32 sequences of 4096 keys with
-// 16 rows each take 52 us (135 MB), which 3 CTAs of 168 registers (66) and one copy a step
+// 16 rows each take 50 us (135 MB), which 3 CTAs of 168 registers (66) and one copy a step
 // (55 to 60) did not improve.
 //
 // Work: the batch's units of 128 keys (32 a warp) are dealt to the CTAs in equal runs,
@@ -54,8 +54,8 @@ constexpr int kFewKeys = 16;      // keys of a copy: they lie in one page
 constexpr int kFewStep = 2;       // copies of a warp's step
 constexpr int kFewStages = 4;     // copies under way or in use
 // Units of a CTA, at least (where there are that many): more CTAs end sooner but have more parts
-// to join.  1 / 2 / 4 / 8, graphs of one call: a token on 4096 keys 20.7 / 18.5 / 16.7 / 21.2 us, 13
-// with a window of 500 14.5 / 16.6 / 18.6 / 26.8.
+// to join.  1 / 2 / 4 / 8, from graphs: a token on 4096 keys 19.4 / 15.7 / 15.4 / 19.6 us, 13
+// with a window of 500 11.2 / 14.5 / 16.6 / 24.0.
 constexpr int kFewLeast = 2;
 constexpr float kHeadroom = 8.f;  // the maximum may lag behind by this much (base 2)
 constexpr float kWeightBits = 6.f;  // weights are 2^6 at the maximum
