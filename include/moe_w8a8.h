@@ -612,12 +612,12 @@ MOE_W8A8_API moe_status_t moe_w8a8_norm_residual(const void* x, int x_fp32, cons
  * exact products (of a query row to 2^-17 of its largest channel), weights fp16
  * (11 bits, at least 2^-31 of the row's largest), sums binary32.  A weight is taken
  * together with its value block's scale: where the scales of a head's value
- * blocks are more than 2^100 apart, keys of the smaller ones can be lost (blocks of
- * zeros have an append's least, 2^-64: so values stay below 2^44).  Results depend in their
- * last bits on the batch: where a sequence is cut into parts, and which form of row
- * tiles its average number of rows takes; so does the time of a batch that mixes
- * long prompts with many single tokens or empty places.  One launch, and one
- * that joins the parts.
+ * blocks are more than 2^100 apart, keys of the smaller ones can be lost (an append
+ * gives blocks of zeros 2^-64: values of magnitudes below 2^44 are safe).  Results
+ * depend in their last bits on the batch: where a sequence is cut into parts, and
+ * which form of row tiles its average number of rows takes.  One form serves the
+ * whole batch: one that mixes a long prompt with many single tokens or empty
+ * places is slow.  One launch, and one that joins the parts.
  * ------------------------------------------------------------------------- */
 typedef struct {
     uint8_t* k;
